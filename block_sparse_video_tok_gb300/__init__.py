@@ -8,7 +8,13 @@
 
     from block_sparse_video_tok_gb300.autograd import block_sparse_attention
     o = block_sparse_attention(q, k, v, q2k_idx, q2k_num, vbs)   # differentiable in q, k, v
-"""
-from . import autograd, build, vsa, workloads  # noqa: F401
 
-__all__ = ["autograd", "build", "vsa", "workloads"]
+The operators around it in a video transformer layer (include/vsa_layer.h):
+
+    from block_sparse_video_tok_gb300.autograd import cross_attention, norm_rope
+    q, k, v = norm_rope(q, k, v, q_weight, k_weight, cos, sin, order)   # [B,S,H,D] -> [B,H,S',D]
+    o = cross_attention(q, k, v, kv_len)                         # to states of another length
+"""
+from . import autograd, build, layer, vsa, workloads  # noqa: F401
+
+__all__ = ["autograd", "build", "layer", "vsa", "workloads"]

@@ -13,7 +13,7 @@ Argument marshalling only: every step runs in libvsa.so's kernels through `vsa`.
 """
 import torch
 
-from . import vsa
+from . import layer, vsa
 
 
 class BlockSparseAttention(torch.autograd.Function):
@@ -56,3 +56,70 @@ def block_sparse_attention(q, k, v, q2k_idx, q2k_num, vbs, sm_scale=None, k2q=No
     o, _ = BlockSparseAttention.apply(q, k, v, q2k_idx, q2k_num, vbs, float(sm_scale), k2q_idx,
                                       k2q_num)
     return o
+
+
+class NormRope(torch.autograd.Function):
+    """vsa_norm_rope of layer.py; gradients flow to q, k, v and the weights."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, q_weight, k_weight, cos, sin, src, dst, halves, eps):
+        out = layer.vsa_norm_rope(q, k, v, q_weight, k_weight, cos, sin, src, halves, eps)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, dst)
+        ctx.halves, ctx.eps, ctx.rows = halves, eps, out[0].shape[2]
+        ctx.v_heads = None if v is None else v.shape[2]
+        return out
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out, dv_out):
+        q, k, q_weight, k_weight, cos, sin, dst = ctx.saved_tensors
+        grads = []
+        for g, heads in ((dq_out, q.shape[2]), (dk_out, None if k is None else k.shape[2]),
+                         (dv_out, ctx.v_heads)):
+            if g is None and heads is not None:      # an output that the loss does not reach
+                g = q.new_zeros((q.shape[0], heads, ctx.rows, q.shape[3]))
+            grads.append(g if g is None else _aligned(g))
+        need = ctx.needs_input_grad[3] or ctx.needs_input_grad[4]
+        return layer.vsa_norm_rope_bwd(*grads, q, k, q_weight, k_weight, cos, sin, dst, ctx.halves,
+                                       ctx.eps, need_dweight=need) + (None,) * 6
+
+
+class CrossAttention(torch.autograd.Function):
+    """vsa_cross of layer.py: (o, lse); gradients flow to q, k and v (lse is not differentiable)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, kv_len, sm_scale):
+        o, lse = layer.vsa_cross_fwd(q, k, v, kv_len, sm_scale)
+        ctx.save_for_backward(q, k, v, o, lse, kv_len)
+        ctx.sm_scale = sm_scale
+        ctx.mark_non_differentiable(lse)
+        return o, lse
+
+    @staticmethod
+    def backward(ctx, do, _dlse):
+        q, k, v, o, lse, kv_len = ctx.saved_tensors
+        return layer.vsa_cross_bwd(_aligned(do), q, k, v, o, lse, kv_len, ctx.sm_scale) + (None,) * 2
+
+
+def _aligned(g):
+    """g, copied where its strides are not the kernels' (an expanded or transposed gradient)."""
+    unit = 16 // g.element_size()
+    if g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and not any(s % unit for s in g.stride()[:-1]):
+        return g
+    return g.contiguous()
+
+
+def norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin=None, order=None,
+              halves=False, eps=1e-6):
+    """Differentiable layer.vsa_norm_rope: the per-head norm and rotation of q and k in the pass
+    that moves q, k and v [B, S, H, D] to [B, H, rows, D].  order: (src, dst) as from
+    layer.video_token_order, or None.  Returns (q, k, v) for block_sparse_attention."""
+    src, dst = order if order is not None else (None, None)
+    return NormRope.apply(q, k, v, q_weight, k_weight, cos, sin, src, dst, bool(halves), float(eps))
+
+
+def cross_attention(q, k, v, kv_len=None, sm_scale=None):
+    """O of the attention of q [B, H, Sq, 128] to the first kv_len[b] of the keys and values
+    [B, Hk, Sk, 128], differentiable in q, k and v (see layer.vsa_cross_fwd)."""
+    if sm_scale is None:
+        sm_scale = q.shape[-1] ** -0.5
+    return CrossAttention.apply(q, k, v, kv_len, float(sm_scale))[0]

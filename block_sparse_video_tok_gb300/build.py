@@ -17,8 +17,8 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libvsa.so")
 SOURCES = ["api.cu", "invert.cu", "prepost.cu", "tmap.cu", "bwd_main.cu", "fwd_main.cu",
-           "noalloc.cu"]
-HEADERS = ["ptx.cuh", "queue.cuh", "vsa_internal.cuh"]
+           "noalloc.cu", "layer_api.cu", "norm_rope.cu", "cross_fwd.cu", "cross_bwd.cu"]
+HEADERS = ["ptx.cuh", "queue.cuh", "vsa_internal.cuh", "layer_internal.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -33,7 +33,7 @@ def _nvcc():
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files.append(os.path.join(ROOT, "include", "vsa.h"))
+    files += [os.path.join(ROOT, "include", h) for h in ("vsa.h", "vsa_layer.h")]
     return files
 
 
