@@ -103,7 +103,7 @@ class CrossAttention(torch.autograd.Function):
 def _aligned(g):
     """g, copied where its strides are not the kernels' (an expanded or transposed gradient)."""
     unit = 16 // g.element_size()
-    if g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and not any(s % unit for s in g.stride()[:-1]):
+    if g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and all(s and s % unit == 0 for s in g.stride()[:-1]):
         return g
     return g.contiguous()
 

@@ -1,0 +1,137 @@
+// cross_common.cuh -- what the cross-attention kernels share: how query rows are laid out in
+// 128-row tiles, the tensor maps of operands of any strides, and small device helpers.
+#pragma once
+
+#include "layer_internal.cuh"
+#include "ptx.cuh"
+
+namespace vsa {
+
+constexpr int TILE = 128;                        // rows of a query tile, keys of a kv tile
+constexpr uint32_t TILE_BYTES = TILE * 128 * 2;  // one operand tile: two column halves of 16 KB
+
+// Query rows in tiles.  From 128 tokens on, a tile is 128 tokens of one head.  Below, a tile
+// packs all tokens of `pack` neighbouring heads that read the same key head, so that the keys
+// are read once for them: row r is token r % box of head r / box.  pack divides the number of
+// heads that share a key head, so no tile reaches into another key head's.
+struct QTiles {
+  int box;     // tokens of one head in a tile
+  int pack;    // heads in a tile
+  int blocks;  // tiles along the tokens of a head
+  int share;   // heads / kv_heads
+  int tiles;   // tiles of one (batch, key head)
+};
+
+inline QTiles q_tiles(int heads, int kv_heads, int q_tokens) {
+  QTiles t;
+  t.share = heads / kv_heads;
+  t.box = q_tokens < TILE ? q_tokens : TILE;
+  t.blocks = (q_tokens + TILE - 1) / TILE;
+  t.pack = 1;
+  for (int p = 2; p <= t.share && p * t.box <= TILE; ++p)
+    if (t.share % p == 0) t.pack = p;
+  t.tiles = t.blocks * (t.share / t.pack);
+  return t;
+}
+
+// Tensor map of x as (64 columns, tokens, heads, column half, batch), box (64, box_tokens,
+// box_heads, 2, 1), 128-byte swizzle: one copy lands a tile of 128 rows as two column halves of
+// box_heads x box_tokens rows of 128 bytes.  A box of fewer rows holds one column half (the
+// halves of a tile in shared memory are 16 KB apart) and a tile takes two copies.  A broadcast dimension (stride 0) has extent 1 in the
+// map, and its coordinate must be 0.
+cudaError_t make_tmap_heads(CUtensorMap* map, const HeadsView& x, int tokens, int batch,
+                            int box_tokens, int box_heads);
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns, int lane) {
+  int ok = 1;
+  if (lane == 0) ok = mbar_wait_bounded(bar, parity, abort, limit_ns) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+__device__ __forceinline__ void raise_abort(volatile int* abort, uint32_t* err) {
+  *abort = 1;
+  atomicOr(err, VSA_DEVERR_TIMEOUT);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Packed fp32 pairs: one instruction on both halves of a 64-bit register pair.
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Byte offset of 16-byte chunk c of row r in a column half of an operand tile.
+__device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
+  return r * 128u + ((c ^ (r & 7u)) << 4);
+}
+
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+// The rows [from, to) of an operand tile in shared memory become zero, for a whole warp to call;
+// the writes are ordered before later tensor-core reads.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int lane) {
+  for (int i = lane; i < (to - from) * 16; i += 32) {
+    const uint32_t r = static_cast<uint32_t>(from + (i >> 4)), c = static_cast<uint32_t>(i & 15);
+    st_shared_zero16(tile + (c >> 3) * (TILE_BYTES / 2) + r * 128u + (c & 7u) * 16u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+#endif
+
+}  // namespace vsa

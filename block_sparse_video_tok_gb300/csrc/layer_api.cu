@@ -121,6 +121,13 @@ vsa_status check_cross(const vsa_cross* op) {
   return VSA_OK;
 }
 
+// A cross-attention operand: heads and tokens must not be broadcast (a tile spans several).
+vsa_status cross_view(const vsa_heads* x, int batch, int tokens, bool output, vsa::HeadsView* v) {
+  const vsa_status st = view_of(x, batch, tokens, vsa::HEAD_DIM, 2, output, v);
+  if (st != VSA_OK) return st;
+  return (x->heads > 1 && v->head == 0) || (tokens > 1 && v->token == 0) ? VSA_ERR_INVALID_ARG : VSA_OK;
+}
+
 vsa_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   if (need == 0) return VSA_OK;
   return workspace && aligned(workspace, 256) && bytes >= need ? VSA_OK : VSA_ERR_WORKSPACE;
@@ -241,11 +248,11 @@ vsa_status vsa_cross_fwd(const vsa_cross* op, const vsa_heads* q, const vsa_head
   if (st != VSA_OK) return st;
   vsa::CrossArgs a{};
   fill_cross(op, &a);
-  const int B = op->batch, Sq = op->q_tokens, Sk = op->kv_tokens, D = vsa::HEAD_DIM;
-  if ((st = view_of(q, B, Sq, D, 2, false, &a.q)) != VSA_OK) return st;
-  if ((st = view_of(k, B, Sk, D, 2, false, &a.k)) != VSA_OK) return st;
-  if ((st = view_of(v, B, Sk, D, 2, false, &a.v)) != VSA_OK) return st;
-  if ((st = view_of(o, B, Sq, D, 2, true, &a.o)) != VSA_OK) return st;
+  const int B = op->batch, Sq = op->q_tokens, Sk = op->kv_tokens;
+  if ((st = cross_view(q, B, Sq, false, &a.q)) != VSA_OK) return st;
+  if ((st = cross_view(k, B, Sk, false, &a.k)) != VSA_OK) return st;
+  if ((st = cross_view(v, B, Sk, false, &a.v)) != VSA_OK) return st;
+  if ((st = cross_view(o, B, Sq, true, &a.o)) != VSA_OK) return st;
   if (a.q.heads != op->heads || a.o.heads != op->heads || a.k.heads != op->kv_heads || a.v.heads != op->kv_heads)
     return VSA_ERR_INVALID_ARG;
   if (!lse || !aligned(lse, 4)) return VSA_ERR_INVALID_ARG;
@@ -265,7 +272,7 @@ vsa_status vsa_cross_bwd(const vsa_cross* op, const vsa_heads* dout, const vsa_h
   if (st != VSA_OK) return st;
   vsa::CrossArgs a{};
   fill_cross(op, &a);
-  const int B = op->batch, Sq = op->q_tokens, Sk = op->kv_tokens, D = vsa::HEAD_DIM;
+  const int B = op->batch, Sq = op->q_tokens, Sk = op->kv_tokens;
   struct {
     const vsa_heads* x;
     int tokens, heads;
@@ -276,7 +283,7 @@ vsa_status vsa_cross_bwd(const vsa_cross* op, const vsa_heads* dout, const vsa_h
            {o, Sq, op->heads, false, &a.o},       {dq, Sq, op->heads, true, &a.dq},
            {dk, Sk, op->kv_heads, true, &a.dk},   {dv, Sk, op->kv_heads, true, &a.dv}};
   for (auto& x : t) {
-    if ((st = view_of(x.x, B, x.tokens, D, 2, x.output, x.view)) != VSA_OK) return st;
+    if ((st = cross_view(x.x, B, x.tokens, x.output, x.view)) != VSA_OK) return st;
     if (x.view->heads != x.heads) return VSA_ERR_INVALID_ARG;
   }
   if (!lse || !aligned(lse, 4)) return VSA_ERR_INVALID_ARG;

@@ -6,7 +6,7 @@
 // swizzle), which only the TMA reduce-add touches.
 #include <cudaTypedefs.h>
 
-#include "vsa_internal.cuh"
+#include "cross_common.cuh"
 
 namespace vsa {
 
@@ -83,6 +83,26 @@ cudaError_t make_tmap_rows128_f16_halves(CUtensorMap* map, const void* ptr, long
   const cuuint32_t estride[3] = {1u, 1u, 1u};
   CUresult r = encode(map, two_byte_type(bf16), 3, const_cast<void*>(ptr), gdim, gstride, box,
                       estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_heads(CUtensorMap* map, const HeadsView& x, int tokens, int batch,
+                            int box_tokens, int box_heads) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  // A dimension of stride 0 is one entry long; the stride of a single entry is never used.
+  auto extent = [](int n, int64_t stride) { return static_cast<cuuint64_t>(stride > 0 ? n : 1); };
+  auto bytes = [](int64_t stride) { return static_cast<cuuint64_t>(stride > 0 ? stride * 2 : 256); };
+  const cuuint64_t gdim[5] = {64u, extent(tokens, x.token), extent(x.heads, x.head), 2u,
+                              extent(batch, x.batch)};
+  const cuuint64_t gstride[4] = {bytes(x.token), bytes(x.head), 128u, bytes(x.batch)};
+  const cuuint32_t box[5] = {64u, static_cast<cuuint32_t>(box_tokens),
+                             static_cast<cuuint32_t>(box_heads),
+                             box_tokens * box_heads == TILE ? 2u : 1u, 1u};
+  const cuuint32_t estride[5] = {1u, 1u, 1u, 1u, 1u};
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, x.data, gdim, gstride, box, estride,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

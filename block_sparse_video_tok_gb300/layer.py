@@ -352,7 +352,10 @@ def _cross_op(q, k, kv_len, sm_scale):
 
 
 def _bf16(t, name, shape, device):
-    return _heads(t, name, shape, torch.bfloat16, device)
+    h = _heads(t, name, shape, torch.bfloat16, device)
+    if (shape[1] > 1 and h.head_stride == 0) or (shape[2] > 1 and h.token_stride == 0):
+        raise ValueError("%s must not be broadcast over its heads or tokens" % name)
+    return h
 
 
 def _lse(lse, B, H, Sq, device):

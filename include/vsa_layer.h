@@ -10,8 +10,8 @@
  * with these additions:
  *   - Tensors are described by vsa_heads: any strides with unit stride inside a head; the data
  *     pointer and the strides of dimensions longer than 1 must be multiples of 16 bytes.
- *     Strides count elements.  Input strides may be 0 (a broadcast dimension); an output must
- *     not overlap itself or an input.
+ *     Strides count elements.  Input strides may be 0 (a broadcast dimension; in vsa_cross
+ *     that of the batch only); an output must not overlap itself or an input.
  *   - Problems only visible on the device never trap: they are clamped or skipped and set a bit
  *     in a device error word.  These operators share one word per device inside the library,
  *     which collects bits until vsa_layer_device_error reads and clears it (with

@@ -134,6 +134,8 @@ def test_cross_refuses_bad_tensors(layer):
             args[i] = bad
             assert lib.vsa_cross_fwd(op, *args, p, p, 1 << 40, None) == 1
     assert lib.vsa_cross_fwd(op, *good, None, p, 1 << 40, None) == 1                    # lse
+    for dim in ("head_stride", "token_stride"):                                          # broadcast
+        assert lib.vsa_cross_fwd(op, heads(layer, **{dim: 0}), *good[1:], p, p, 1 << 40, None) == 1
     assert lib.vsa_cross_fwd(op, *good[:3], heads(layer, token_stride=0), p, p, 1 << 40, None) == 1
     q, k, v, o = good
     need = lib.vsa_cross_bwd_workspace_bytes(op)
