@@ -11,9 +11,10 @@ kernels on the caller's stream, and outputs and workspaces that are not passed a
 with torch (on that stream).  `autograd.norm_rope` and `autograd.cross_attention` are the
 differentiable forms.
 """
-import contextlib
 import ctypes
+import functools
 import math
+import struct
 
 import numpy as np
 import torch
@@ -68,7 +69,14 @@ SIGNATURES = {
     "vsa_layer_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _P]),
 }
 
+# The wrappers below hand structures over as packed bytes: a single call into C builds one, where
+# a ctypes.Structure converts field by field, which would cost more than a small kernel.
+_pack_heads = struct.Struct("@4Pi4x").pack
+_pack_norm = struct.Struct("@8if4PqP").pack
+_pack_cross = struct.Struct("@6ifP").pack
+
 _fns = None
+_calls = None
 
 
 def _lib():
@@ -84,24 +92,51 @@ def _lib():
     return _fns
 
 
+def _call(name, *args):
+    """The named function on packed structures."""
+    global _calls
+    if _calls is None:
+        lib, calls = _lib(), {}
+        for n, (res, types) in SIGNATURES.items():
+            fn = calls[n] = lib[n]              # a function object of its own
+            fn.restype = res
+            fn.argtypes = [ctypes.c_char_p if t in (_H, _N, _C) else t for t in types]
+        _calls = calls
+    status = _calls[name](*args)
+    if status != 0:
+        vsa._check(status, name)
+
+
 # ------------------------------------------------------------------------------- arguments
 
-def _heads(t, name, shape, dtype, device):
-    """The [B, H, S, D] view t as a VsaHeads, after checking it."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise TypeError("%s must be a tensor on %s" % (name, device))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+def _heads(t, name, shape, like, transposed=False, whole=False):
+    """The [B, H, S, D] tensor t (transposed: [B, S, H, D]) as a packed vsa_heads, after checking
+    it against `shape` (as t has it) and the type and device of `like`.  whole: its heads and tokens
+    must not be broadcast."""
+    try:
+        if t.dtype is not like.dtype:
+            raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+        if t.get_device() != like.get_device():
+            raise TypeError("%s must be a tensor on %s" % (name, like.device))
+    except AttributeError:
+        raise TypeError("%s must be a tensor on %s" % (name, like.device)) from None
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    sb, sh, ss, sd = t.stride()
-    unit = 16 // t.element_size()
-    B, H, S, D = shape
-    if sd != 1 or t.data_ptr() % 16 or (B > 1 and sb % unit) or (H > 1 and sh % unit) or \
-            (S > 1 and ss % unit):
+    ptr = t.data_ptr()
+    if transposed:
+        B, S, H, D = shape
+        sb, ss, sh, sd = t.stride()
+    else:
+        B, H, S, D = shape
+        sb, sh, ss, sd = t.stride()
+    # A dimension of length 1 may have any stride.
+    used = (sb if B > 1 else 0) | (sh if H > 1 else 0) | (ss if S > 1 else 0)
+    if sd != 1 or (ptr | used * t.element_size()) & 15:
         raise ValueError("%s: the last dimension must be contiguous, and the data and the other "
                          "strides multiples of 16 bytes (strides %s)" % (name, t.stride()))
-    return VsaHeads(t.data_ptr(), sb, sh, ss, H)
+    if whole and ((sh == 0 and H > 1) or (ss == 0 and S > 1)):
+        raise ValueError("%s must not be broadcast over its heads or tokens" % name)
+    return _pack_heads(ptr, sb, sh, ss, H)
 
 
 def _cuda(t, name):
@@ -111,90 +146,102 @@ def _cuda(t, name):
         raise ValueError("%s must be 4-D, got %s" % (name, tuple(t.shape)))
     if t.numel() == 0:
         raise ValueError("%s is empty: %s" % (name, tuple(t.shape)))
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError("%s is on %s, which is not the current device" % (name, t.device))
 
 
-def _vector(t, name, dtype, n, device):
+def _vector(t, name, dtype, n, like):
     """The address of a contiguous 1-D tensor, or None."""
     if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype:
-        raise TypeError("%s must be a %s tensor on %s" % (name, dtype, device))
+        return 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != like.get_device() or t.dtype is not dtype:
+        raise TypeError("%s must be a %s tensor on %s" % (name, dtype, like.device))
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be contiguous with shape (%d,), got %s" % (name, n, tuple(t.shape)))
     return t.data_ptr()
 
 
-def _on(stream):
-    """Context for allocations that are used on `stream` (None: the current one)."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+class _Stream:
+    """Where a call runs: its handle, and allocations made on it."""
+
+    __slots__ = ("stream", "handle")
+
+    def __init__(self, stream, like):
+        self.stream = stream
+        self.handle = torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None \
+            else stream.cuda_stream
+
+    def make(self, f, *args, **kwargs):
+        if self.stream is None:
+            return f(*args, **kwargs)
+        with torch.cuda.stream(self.stream):
+            return f(*args, **kwargs)
+
+    def workspace(self, given, need, like):
+        """(workspace tensor, address, bytes); allocated if not given."""
+        if need == 0:
+            return None, None, 0
+        if given is None:
+            given = self.make(torch.empty, need, dtype=torch.uint8, device=like.device)
+            return given, given.data_ptr(), need
+        if not isinstance(given, torch.Tensor) or given.get_device() != like.get_device() or \
+                not given.is_contiguous():
+            raise TypeError("workspace must be a contiguous tensor on %s" % like.device)
+        return given, given.data_ptr(), given.numel() * given.element_size()
 
 
-def _handle(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+@functools.lru_cache(maxsize=256)
+def _cross_workspace(name, device, *sizes):
+    """Workspace bytes of a cross attention of these sizes (a pure function of them)."""
+    return getattr(_lib(), name)(VsaCross(*sizes, 1.0, None))
 
 
-def _check(status, what):
-    if status != 0:
-        vsa._check(status, what)
-
-
-def _workspace(given, need, device, stream):
-    """(workspace tensor, address, bytes); allocated if not given."""
-    if need == 0:
-        return None, None, 0
-    if given is None:
-        with _on(stream):
-            given = torch.empty(need, dtype=torch.uint8, device=device)
-        return given, given.data_ptr(), need
-    if not isinstance(given, torch.Tensor) or given.device != device or not given.is_contiguous():
-        raise TypeError("workspace must be a contiguous tensor on %s" % device)
-    return given, given.data_ptr(), given.numel() * given.element_size()
+@functools.lru_cache(maxsize=64)
+def _norm_workspace(device, head_dim):
+    return _lib().vsa_norm_rope_bwd_workspace_bytes(
+        VsaNormRope(1, 1, 1, head_dim, 0, 0, 0, 0, 0.0, None, None, None, None, 0, None))
 
 
 # ------------------------------------------------------------------------------- norm_rope
 
-def _norm_rope_op(x, rows, weights, cos, sin, order, order_len, halves, eps):
-    """(VsaNormRope, kept tensors) for activations shaped and typed like x [B, S, H, D]."""
+def _norm_rope_op(x, rows, q_weight, k_weight, cos, sin, order, order_len, halves, eps):
+    """The packed vsa_norm_rope for activations shaped and typed like x [B, S, H, D]."""
     B, S, _, D = x.shape
-    dtype, device = x.dtype, x.device
-    if dtype not in _DTYPES:
+    dtype = x.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError("activations must be bf16, fp16 or fp32, got %s" % dtype)
     if D % 8 or not 8 <= D <= 256:
         raise ValueError("head_dim must be a multiple of 8 up to 256, got %d" % D)
-    wdtype = next((w.dtype for w in weights if isinstance(w, torch.Tensor)), dtype)
-    if wdtype not in (dtype, torch.float32):
+    w = k_weight if q_weight is None else q_weight
+    wdtype = dtype if w is None else getattr(w, "dtype", None)
+    if wdtype is not dtype and wdtype is not torch.float32:
         raise TypeError("weights must be fp32 or %s, got %s" % (dtype, wdtype))
-    wp = [_vector(w, n, wdtype, D, device) for w, n in zip(weights, ("q_weight", "k_weight"))]
-    rot, stride, cp, sp = 0, 0, None, None
+    wq = _vector(q_weight, "q_weight", wdtype, D, x)
+    wk = _vector(k_weight, "k_weight", wdtype, D, x)
+    rot = stride = cp = sp = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     if cos is not None:
         for t, n in ((cos, "cos"), (sin, "sin")):
-            if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32:
-                raise TypeError("%s must be an fp32 tensor on %s" % (n, device))
-            if t.dim() not in (2, 3) or t.shape != cos.shape or t.shape[-2] != S or \
-                    (t.dim() == 3 and t.shape[0] != B):
-                raise ValueError("%s must be [%d, rot / 2] or [%d, %d, rot / 2], got %s" %
-                                 (n, S, B, S, tuple(t.shape)))
-            if not t.is_contiguous() or t.data_ptr() % 16:
-                raise ValueError("%s must be contiguous and 16-byte aligned" % n)
-        rot = 2 * cos.shape[-1]
-        stride = S * cos.shape[-1] if cos.dim() == 3 else 0
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or \
+                    t.get_device() != x.get_device():
+                raise TypeError("%s must be an fp32 tensor on %s" % (n, x.device))
+        shape = cos.shape
+        if len(shape) not in (2, 3) or sin.shape != shape or shape[-2] != S or \
+                (len(shape) == 3 and shape[0] != B):
+            raise ValueError("cos and sin must be [%d, rot / 2] or [%d, %d, rot / 2], got %s and %s" %
+                             (S, B, S, tuple(shape), tuple(sin.shape)))
         cp, sp = cos.data_ptr(), sin.data_ptr()
+        if not cos.is_contiguous() or not sin.is_contiguous() or (cp | sp) & 15:
+            raise ValueError("cos and sin must be contiguous and 16-byte aligned")
+        rot = 2 * shape[-1]
+        stride = S * shape[-1] if len(shape) == 3 else 0
         if rot > D or rot % (16 if halves else 8):
             raise ValueError("cos and sin turn %d of %d elements of a head: at most all, in "
                              "multiples of %d" % (rot, D, 16 if halves else 8))
-    op = _vector(order, "the order", torch.int32, order_len, device)
-    return VsaNormRope(B, S, rows, D, _DTYPES[dtype], _DTYPES[wdtype], rot, 1 if halves else 0,
-                       eps, wp[0], wp[1], cp, sp, stride, op)
-
-
-def _tokens_view(t):
-    """[B, S, H, D] as [B, H, S, D]."""
-    return t.transpose(1, 2)
+    return _pack_norm(B, S, rows, D, code, _DTYPES[wdtype], rot, 1 if halves else 0, eps, wq, wk, cp,
+                      sp, stride, _vector(order, "the order", torch.int32, order_len, x))
 
 
 def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin=None, src=None,
@@ -211,9 +258,9 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
     _cuda(q, "q")
     B, S, _, D = q.shape
     rows = S if src is None else src.numel()
-    op = _norm_rope_op(q, rows, (q_weight, k_weight), cos, sin, src, rows, halves, eps)
-    ins, outs = [], []
-    res = []
+    op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, src, rows, halves, eps)
+    on = _Stream(stream, q)
+    ins, outs, res = [], [], []
     for x, y, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
         if x is None:
             if y is not None:
@@ -225,13 +272,13 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
         if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.shape[2] == 0:
             raise ValueError("%s must be [B, S, H, D]" % name)
         H = x.shape[2]
-        ins.append(_heads(_tokens_view(x), name, (B, H, S, D), q.dtype, q.device))
+        ins.append(_heads(x, name, (B, S, H, D), q, transposed=True))
+        shape = (B, H, rows, D)
         if y is None:
-            with _on(stream):
-                y = torch.empty((B, H, rows, D), dtype=q.dtype, device=q.device)
-        outs.append(_heads(y, name + "_out", (B, H, rows, D), q.dtype, q.device))
+            y = on.make(q.new_empty, shape)
+        outs.append(_heads(y, name + "_out", shape, q))
         res.append(y)
-    _check(_lib().vsa_norm_rope_fwd(op, *ins, *outs, _handle(stream)), "vsa_norm_rope_fwd")
+    _call("vsa_norm_rope_fwd", op, *ins, *outs, on.handle)
     return tuple(res)
 
 
@@ -251,7 +298,8 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
     rows = dq_out.shape[2]
     if dst is None and rows != S:
         raise ValueError("dq_out has %d rows for %d tokens, without dst" % (rows, S))
-    op = _norm_rope_op(q, rows, (q_weight, k_weight), cos, sin, dst, S, halves, eps)
+    op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, dst, S, halves, eps)
+    on = _Stream(stream, q)
     dys, xs, dxs, res, dws = [], [], [], [], []
     for dy, x, dx, w, name in ((dq_out, q, dq, q_weight, "q"), (dk_out, k, dk, k_weight, "k"),
                                (dv_out, None, dv, None, "v")):
@@ -268,26 +316,21 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
         if not isinstance(dy, torch.Tensor) or dy.dim() != 4 or dy.shape[1] == 0:
             raise ValueError("d%s_out must be [B, H, rows, D]" % name)
         H = dy.shape[1]
-        dys.append(_heads(dy, "d%s_out" % name, (B, H, rows, D), q.dtype, q.device))
-        if x is not None:
-            if x.dim() != 4:
-                raise ValueError("%s must be [B, S, H, D]" % name)
-            xs.append(_heads(_tokens_view(x), name, (B, H, S, D), q.dtype, q.device))
-        with _on(stream):
-            if dx is None:
-                dx = torch.empty((B, S, H, D), dtype=q.dtype, device=q.device)
-            if name != "v":
-                dws.append(torch.empty_like(w) if w is not None and need_dweight else None)
-        dxs.append(_heads(_tokens_view(dx), "d" + name, (B, H, S, D), q.dtype, q.device))
+        dys.append(_heads(dy, "d%s_out" % name, (B, H, rows, D), q))
+        shape = (B, S, H, D)
+        if name != "v":
+            xs.append(_heads(x, name, shape, q, transposed=True))
+            dws.append(on.make(torch.empty_like, w) if w is not None and need_dweight else None)
+        if dx is None:
+            dx = on.make(q.new_empty, shape)
+        dxs.append(_heads(dx, "d" + name, shape, q, transposed=True))
         res.append(dx)
-    need = 0
-    if any(w is not None for w in dws):
-        need = _lib().vsa_norm_rope_bwd_workspace_bytes(op)
-    keep, wp, wn = _workspace(workspace, need, q.device, stream)
-    _check(_lib().vsa_norm_rope_bwd(op, *dys, *xs, *dxs, *(None if w is None else w.data_ptr()
-                                                           for w in dws), wp, wn,
-                                    _handle(stream)), "vsa_norm_rope_bwd")
-    return (*res, *dws)
+    dwq, dwk = dws
+    need = 0 if dwq is None and dwk is None else _norm_workspace(q.get_device(), D)
+    keep, wp, wn = on.workspace(workspace, need, q)
+    _call("vsa_norm_rope_bwd", op, *dys, *xs, *dxs, None if dwq is None else dwq.data_ptr(),
+          None if dwk is None else dwk.data_ptr(), wp, wn, on.handle)
+    return (*res, dwq, dwk)
 
 
 def video_token_order(grid, cube=VIDEO_CUBE, device="cuda"):
@@ -335,10 +378,13 @@ def rotation_table(positions, rot, theta=10000.0, device="cuda"):
 # ------------------------------------------------------------------------- cross attention
 
 def _cross_op(q, k, kv_len, sm_scale):
+    """(packed vsa_cross, its sizes)."""
     _cuda(q, "q")
     _cuda(k, "k")
+    if q.dtype is not torch.bfloat16:
+        raise TypeError("q must be torch.bfloat16, got %s" % q.dtype)
     B, H, Sq, D = q.shape
-    Hk, Sk = k.shape[1], k.shape[2]
+    _, Hk, Sk, _ = k.shape
     if D != vsa.HEAD_DIM:
         raise ValueError("head_dim must be %d, got %d" % (vsa.HEAD_DIM, D))
     if H % Hk:
@@ -347,22 +393,16 @@ def _cross_op(q, k, kv_len, sm_scale):
         sm_scale = D ** -0.5
     if not math.isfinite(sm_scale):
         raise ValueError("sm_scale must be finite")
-    n = _vector(kv_len, "kv_len", torch.int32, B, q.device)
-    return VsaCross(B, H, Hk, Sq, Sk, D, sm_scale, n), (B, H, Sq, D), (B, Hk, Sk, D)
+    sizes = (B, H, Hk, Sq, Sk, D)
+    return _pack_cross(*sizes, sm_scale, _vector(kv_len, "kv_len", torch.int32, B, q)), sizes
 
 
-def _bf16(t, name, shape, device):
-    h = _heads(t, name, shape, torch.bfloat16, device)
-    if (shape[1] > 1 and h.head_stride == 0) or (shape[2] > 1 and h.token_stride == 0):
-        raise ValueError("%s must not be broadcast over its heads or tokens" % name)
-    return h
-
-
-def _lse(lse, B, H, Sq, device):
-    if not isinstance(lse, torch.Tensor) or lse.device != device or lse.dtype != torch.float32:
-        raise TypeError("lse must be an fp32 tensor on %s" % device)
-    if lse.shape != (B, H, Sq) or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous [%d, %d, %d], got %s" % (B, H, Sq, tuple(lse.shape)))
+def _lse(lse, shape, like):
+    if not isinstance(lse, torch.Tensor) or lse.get_device() != like.get_device() or \
+            lse.dtype is not torch.float32:
+        raise TypeError("lse must be an fp32 tensor on %s" % like.device)
+    if lse.shape != shape or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous %s, got %s" % (tuple(shape), tuple(lse.shape)))
     return lse.data_ptr()
 
 
@@ -371,18 +411,20 @@ def vsa_cross_fwd(q, k, v, kv_len=None, sm_scale=None, o=None, lse=None, workspa
     """Attention of q [B, H, Sq, 128] to k, v [B, Hk, Sk, 128] (bf16; H a multiple of Hk), over the
     first kv_len[b] keys (int32 [B]; None: all).  sm_scale defaults to 1/sqrt(128).  Returns (o in
     q's memory order, lse fp32 [B, H, Sq], base 2); without a visible key o = 0 and lse = -inf."""
-    op, qs, ks = _cross_op(q, k, kv_len, sm_scale)
-    dev = q.device
-    with _on(stream):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(qs[:3], dtype=torch.float32, device=dev)
-    args = (_bf16(q, "q", qs, dev), _bf16(k, "k", ks, dev), _bf16(v, "v", ks, dev),
-            _bf16(o, "o", qs, dev), _lse(lse, *qs[:3], dev))
-    lib = _lib()
-    keep, wp, wn = _workspace(workspace, lib.vsa_cross_fwd_workspace_bytes(op), dev, stream)
-    _check(lib.vsa_cross_fwd(op, *args, wp, wn, _handle(stream)), "vsa_cross_fwd")
+    op, sizes = _cross_op(q, k, kv_len, sm_scale)
+    B, H, Hk, Sq, Sk, D = sizes
+    on = _Stream(stream, q)
+    if o is None:
+        o = on.make(torch.empty_like, q)
+    if lse is None:
+        lse = on.make(q.new_empty, (B, H, Sq), dtype=torch.float32)
+    qs, ks = (B, H, Sq, D), (B, Hk, Sk, D)
+    args = (_heads(q, "q", qs, q, whole=True), _heads(k, "k", ks, q, whole=True),
+            _heads(v, "v", ks, q, whole=True), _heads(o, "o", qs, q, whole=True),
+            _lse(lse, qs[:3], q))
+    keep, wp, wn = on.workspace(workspace, _cross_workspace("vsa_cross_fwd_workspace_bytes",
+                                                            q.get_device(), *sizes), q)
+    _call("vsa_cross_fwd", op, *args, wp, wn, on.handle)
     return o, lse
 
 
@@ -391,18 +433,21 @@ def vsa_cross_bwd(dout, q, k, v, o, lse, kv_len=None, sm_scale=None, dq=None, dk
     """Gradients of vsa_cross_fwd from dout, its inputs, and the o and lse that it returned.
     Returns (dq, dk, dv), each in its input's memory order; rows of dk and dv at or past
     kv_len[b] are exact zeros."""
-    op, qs, ks = _cross_op(q, k, kv_len, sm_scale)
-    dev = q.device
-    with _on(stream):
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-    args = (_bf16(dout, "dout", qs, dev), _bf16(q, "q", qs, dev), _bf16(k, "k", ks, dev),
-            _bf16(v, "v", ks, dev), _bf16(o, "o", qs, dev), _lse(lse, *qs[:3], dev),
-            _bf16(dq, "dq", qs, dev), _bf16(dk, "dk", ks, dev), _bf16(dv, "dv", ks, dev))
-    lib = _lib()
-    keep, wp, wn = _workspace(workspace, lib.vsa_cross_bwd_workspace_bytes(op), dev, stream)
-    _check(lib.vsa_cross_bwd(op, *args, wp, wn, _handle(stream)), "vsa_cross_bwd")
+    op, sizes = _cross_op(q, k, kv_len, sm_scale)
+    B, H, Hk, Sq, Sk, D = sizes
+    on = _Stream(stream, q)
+    dq = on.make(torch.empty_like, q) if dq is None else dq
+    dk = on.make(torch.empty_like, k) if dk is None else dk
+    dv = on.make(torch.empty_like, v) if dv is None else dv
+    qs, ks = (B, H, Sq, D), (B, Hk, Sk, D)
+    args = (_heads(dout, "dout", qs, q, whole=True), _heads(q, "q", qs, q, whole=True),
+            _heads(k, "k", ks, q, whole=True), _heads(v, "v", ks, q, whole=True),
+            _heads(o, "o", qs, q, whole=True), _lse(lse, qs[:3], q),
+            _heads(dq, "dq", qs, q, whole=True), _heads(dk, "dk", ks, q, whole=True),
+            _heads(dv, "dv", ks, q, whole=True))
+    keep, wp, wn = on.workspace(workspace, _cross_workspace("vsa_cross_bwd_workspace_bytes",
+                                                            q.get_device(), *sizes), q)
+    _call("vsa_cross_bwd", op, *args, wp, wn, on.handle)
     return dq, dk, dv
 
 
@@ -410,6 +455,6 @@ def vsa_layer_device_error(stream=None):
     """Synchronise the stream; return and clear the device error bits that these operators have
     raised on the current device since the last call."""
     bits = ctypes.c_uint32(0)
-    _check(_lib().vsa_layer_device_error(ctypes.byref(bits), _handle(stream)),
-           "vsa_layer_device_error")
+    handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    vsa._check(_lib().vsa_layer_device_error(ctypes.byref(bits), handle), "vsa_layer_device_error")
     return int(bits.value)
