@@ -23,17 +23,35 @@ constexpr int THREADS = 256;
 constexpr int UNROLL = 4;  // heads in flight per group of lanes
 constexpr unsigned FULL = 0xffffffffu;
 
+// 8 elements as loaded (16 or 32 bytes), widened where they are used: a lane keeps several heads'
+// worth in flight.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* v);
+struct Raw {
+  uint4 u[sizeof(T) / 2];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+  }
+  __device__ __forceinline__ void widen(float* v) const;
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void Raw<float>::widen(float* v) const {
+  v[0] = __uint_as_float(u[0].x), v[1] = __uint_as_float(u[0].y), v[2] = __uint_as_float(u[0].z);
+  v[3] = __uint_as_float(u[0].w), v[4] = __uint_as_float(u[1].x), v[5] = __uint_as_float(u[1].y);
+  v[6] = __uint_as_float(u[1].z), v[7] = __uint_as_float(u[1].w);
 }
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void Raw<__nv_bfloat16>::widen(float* v) const {
+  const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
@@ -41,15 +59,21 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, flo
   }
 }
 template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float* v) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void Raw<__half>::widen(float* v) const {
+  const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
     v[2 * i] = f.x;
     v[2 * i + 1] = f.y;
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+  Raw<T> r;
+  r.load(p);
+  r.widen(v);
 }
 
 template <typename T>
@@ -186,32 +210,35 @@ __global__ void __launch_bounds__(THREADS) norm_rope_fwd_kernel(const Params p) 
     const T* src = static_cast<const T*>(a.in[x].data) + b * a.in[x].batch + t * a.in[x].token + e;
     T* dst = static_cast<T*>(a.out[x].data) + b * a.out[x].batch + row * a.out[x].token + e;
     for (int h = h0; h < h1; h += UNROLL) {
-      float v[UNROLL][8];
+      Raw<T> raw[UNROLL];
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-        if (has && h + u < h1) load8(src + (h + u) * a.in[x].head, v[u]);
+        raw[u].zero();
+        if (has && h + u < h1) raw[u].load(src + (h + u) * a.in[x].head);
       }
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
-        if (x < 2) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[u][i], v[u][i], ss);
-          const float r = rsqrtf(fmaf(group_sum<LPR>(ss), p.inv_dim, a.eps));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[u][i] = has ? v[u][i] * r * w[x & 1][i] : 0.f;
-          rot.template turn<false>(v[u]);
+        T* to = dst + (h + u) * a.out[x].head;
+        if (x == 2) {
+          if (active && h + u < h1) raw[u].store(to);
+          continue;
         }
-        if (active && h + u < h1) store8(dst + (h + u) * a.out[x].head, v[u]);
+        float v[8], ss = 0.f;
+        raw[u].widen(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+        const float r = rsqrtf(fmaf(group_sum<LPR>(ss), p.inv_dim, a.eps));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = has ? v[i] * r * w[x & 1][i] : 0.f;
+        rot.template turn<false>(v);
+        if (active && h + u < h1) store8(to, v);
       }
     }
   }
 }
 
 template <typename T, typename W, int LPR, bool HALVES>
-__global__ void __launch_bounds__(THREADS) norm_rope_bwd_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, 2) norm_rope_bwd_kernel(const Params p) {
   __shared__ float sums[THREADS / LPR][LPR * 8];
   grid_dependency_wait();
   const NormRopeArgs& a = p.a;
@@ -244,38 +271,42 @@ __global__ void __launch_bounds__(THREADS) norm_rope_bwd_kernel(const Params p) 
       const T* src = static_cast<const T*>(a.x[x & 1].data) + b * a.x[x & 1].batch +
                      t * a.x[x & 1].token + e;
       for (int h = h0; h < h1; h += UNROLL) {
-        float u[UNROLL][8], v[UNROLL][8];
+        Raw<T> ry[UNROLL], rx[UNROLL];
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[k][i] = v[k][i] = 0.f;
+          ry[k].zero();
+          rx[k].zero();
           if (has && h + k < h1) {
-            load8(dy + (h + k) * a.in[x].head, u[k]);
-            if (x < 2) load8(src + (h + k) * a.x[x & 1].head, v[k]);
+            ry[k].load(dy + (h + k) * a.in[x].head);
+            if (x < 2) rx[k].load(src + (h + k) * a.x[x & 1].head);
           }
         }
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
-          if (x < 2) {
-            rot.template turn<true>(u[k]);
-            float ss = 0.f, sg = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              ss = fmaf(v[k][i], v[k][i], ss);
-              sg = fmaf(u[k][i] * w[x & 1][i], v[k][i], sg);
-            }
-            const float r = rsqrtf(fmaf(group_sum<LPR>(ss), p.inv_dim, a.eps));
-            const float m = group_sum<LPR>(sg) * p.inv_dim * r;  // mean(u w n)
-            // Lanes without a row hold zeros, but r is infinite there when eps is 0.
-            const float rr = has ? r : 0.f, mm = has ? m : 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float nx = v[k][i] * rr;
-              dw[x & 1][i] = fmaf(u[k][i], nx, dw[x & 1][i]);
-              u[k][i] = rr * (u[k][i] * w[x & 1][i] - nx * mm);
-            }
+          T* to = dx + (h + k) * a.out[x].head;
+          if (x == 2) {
+            if (active && h + k < h1) ry[k].store(to);
+            continue;
           }
-          if (active && h + k < h1) store8(dx + (h + k) * a.out[x].head, u[k]);
+          float u[8], v[8], ss = 0.f, sg = 0.f;
+          ry[k].widen(u);
+          rx[k].widen(v);
+          rot.template turn<true>(u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            ss = fmaf(v[i], v[i], ss);
+            sg = fmaf(u[i] * w[x & 1][i], v[i], sg);
+          }
+          // Lanes without a row hold zeros, but the root is infinite there when eps is 0.
+          const float root = rsqrtf(fmaf(group_sum<LPR>(ss), p.inv_dim, a.eps)), r = has ? root : 0.f;
+          const float m = group_sum<LPR>(sg) * p.inv_dim * r;  // mean(u w n)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float n = v[i] * r;
+            dw[x & 1][i] = fmaf(u[i], n, dw[x & 1][i]);
+            u[i] = r * fmaf(-n, m, u[i] * w[x & 1][i]);
+          }
+          if (active && h + k < h1) store8(to, u);
         }
       }
     }

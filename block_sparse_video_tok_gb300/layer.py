@@ -275,7 +275,7 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
         ins.append(_heads(x, name, (B, S, H, D), q, transposed=True))
         shape = (B, H, rows, D)
         if y is None:
-            y = on.make(q.new_empty, shape)
+            y = on.make(torch.empty, shape, dtype=q.dtype, device=q.device)
         outs.append(_heads(y, name + "_out", shape, q))
         res.append(y)
     _call("vsa_norm_rope_fwd", op, *ins, *outs, on.handle)
@@ -322,7 +322,7 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
             xs.append(_heads(x, name, shape, q, transposed=True))
             dws.append(on.make(torch.empty_like, w) if w is not None and need_dweight else None)
         if dx is None:
-            dx = on.make(q.new_empty, shape)
+            dx = on.make(torch.empty, shape, dtype=q.dtype, device=q.device)
         dxs.append(_heads(dx, "d" + name, shape, q, transposed=True))
         res.append(dx)
     dwq, dwk = dws
@@ -417,7 +417,7 @@ def vsa_cross_fwd(q, k, v, kv_len=None, sm_scale=None, o=None, lse=None, workspa
     if o is None:
         o = on.make(torch.empty_like, q)
     if lse is None:
-        lse = on.make(q.new_empty, (B, H, Sq), dtype=torch.float32)
+        lse = on.make(torch.empty, (B, H, Sq), dtype=torch.float32, device=q.device)
     qs, ks = (B, H, Sq, D), (B, Hk, Sk, D)
     args = (_heads(q, "q", qs, q, whole=True), _heads(k, "k", ks, q, whole=True),
             _heads(v, "v", ks, q, whole=True), _heads(o, "o", qs, q, whole=True),
