@@ -45,32 +45,11 @@ struct Params {
                  // dkv: [split][batch * kv_heads * kv_tiles][dV, dK][128 columns][128 keys]
 };
 
-// D = A B^T, both operands K-major tiles of 128 columns in shared memory.
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-  umma_ss_elect<false>(d, a, b, idesc);
-#pragma unroll
-  for (int kk = 1; kk < 8; ++kk) {
-    const uint32_t off = (kk >> 2) * (TILE_BYTES / 2) + (kk & 3) * 32u;
-    umma_ss_elect<true>(d, sdesc_advance(a, off), sdesc_advance(b, off), idesc);
-  }
-}
-
-// D += A B: A of 16-bit pairs in tensor memory, `steps` of 16 along its columns (8 TMEM columns
+// D (+)= A B: A of 16-bit pairs in tensor memory, `steps` of 16 along its columns (8 TMEM columns
 // each; step 4 starts `half` columns after step 0), B an MN-major tile.
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t half, uint64_t b, bool fresh, int steps) {
-  if (fresh)
-    umma_ts_elect<false>(d, a, b, IDESC_ACC);
-  else
-    umma_ts_elect<true>(d, a, b, IDESC_ACC);
-  if (steps == 8) {
-#pragma unroll
-    for (int kk = 1; kk < 8; ++kk)
-      umma_ts_elect<true>(d, a + (kk >> 2) * half + (kk & 3) * 8u, sdesc_advance(b, kk * 2048u), IDESC_ACC);
-  } else {
-#pragma unroll 1
-    for (int kk = 1; kk < steps; ++kk)
-      umma_ts_elect<true>(d, a + (kk >> 2) * half + (kk & 3) * 8u, sdesc_advance(b, kk * 2048u), IDESC_ACC);
-  }
+__device__ __forceinline__ void product_acc(uint32_t d, uint32_t a, uint32_t half, uint64_t b, bool fresh, int steps) {
+  product_ts(d, a, b, IDESC_ACC, fresh ? 0u : 1u, min(steps, 4));
+  if (steps > 4) product_ts(d, a + half, sdesc_advance(b, 8192u), IDESC_ACC, 1u, steps - 4);
 }
 
 // A warp's 32 rows x 64 fp32 columns (one row per lane), scaled and rounded, to global memory in
@@ -246,18 +225,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
       if (u.count() == 0) continue;
-      ok = mbar_wait_warp(bar(Q_EMPTY), (qn & 1u) ^ 1u, abort, limit);
+      ok = warp_wait(bar(Q_EMPTY), (qn & 1u) ^ 1u, abort, limit);
       if (!ok) break;
       if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q, bar(Q_FULL), u.b, u.kh, u.tile);
       __syncwarp();
       ++qn;
-      ok = mbar_wait_warp(bar(DO_EMPTY), (dn & 1u) ^ 1u, abort, limit);
+      ok = warp_wait(bar(DO_EMPTY), (dn & 1u) ^ 1u, abort, limit);
       if (!ok) break;
       if (lane == 0) load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO, bar(DO_FULL), u.b, u.kh, u.tile);
       __syncwarp();
       ++dn;
       for (int j = 0; j < u.count(); ++j) {
-        ok = mbar_wait_warp(bar(V_EMPTY), (vn & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(V_EMPTY), (vn & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(V_FULL), TILE_BYTES);
@@ -283,7 +262,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Unit u = decode(p, w);
       for (int j = 0; j < u.count(); ++j) {
         const uint32_t s = kn % K_STAGES, tile = base + SM_K + s * TILE_BYTES;
-        ok = mbar_wait_warp(bar(K_EMPTY0 + s), ((kn / K_STAGES) & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(K_EMPTY0 + s), ((kn / K_STAGES) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         // Rows past the last visible key may hold anything and meet dS = 0 in dS K: they are
         // zeroed here unless the copy itself fills them.
@@ -297,7 +276,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (patch) {
           ++tails;
-          ok = mbar_wait_warp(full, (tails - 1) & 1u, abort, limit);
+          ok = warp_wait(full, (tails - 1) & 1u, abort, limit);
           if (!ok) break;
           tails_seen = tails;
           zero_rows(tile, n, ceil16(n), lane);
@@ -327,11 +306,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t dqn = 0;            // units whose dQ has begun
     auto issue_dq = [&]() {
       const uint32_t y = x - 1;
-      if (!mbar_wait_warp(bar(DS_READY0 + (y & 1u)), (y >> 1) & 1u, abort, limit)) return false;
-      if (prev_first && !mbar_wait_warp(bar(DQ_EMPTY), (dqn & 1u) ^ 1u, abort, limit)) return false;
+      if (!warp_wait(bar(DS_READY0 + (y & 1u)), (y >> 1) & 1u, abort, limit)) return false;
+      if (prev_first && !warp_wait(bar(DQ_EMPTY), (dqn & 1u) ^ 1u, abort, limit)) return false;
       if (prev_first) ++dqn;
       tc_fence_after_sync();
-      product_ts(tmem + TM_DQ, tmem + TM_DS + (y & 1u) * 64u, 32u,
+      product_acc(tmem + TM_DQ, tmem + TM_DS + (y & 1u) * 64u, 32u,
                  sdesc_advance(k_mn, (y % K_STAGES) * TILE_BYTES), prev_first, ceil16(prev_keys) / 16);
       umma_commit_elect(bar(K_EMPTY0 + y % K_STAGES));
       if (prev_last) umma_commit_elect(bar(DQ_FULL));
@@ -343,18 +322,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int j = 0; j < n && ok; ++j) {
         const int keys = u.keys_of(j);
         const uint32_t idesc = idesc_s(keys);
-        ok = mbar_wait_warp(bar(K_FULL0 + x % K_STAGES), (x / K_STAGES) & 1u, abort, limit) &&
-             (j != 0 || mbar_wait_warp(bar(Q_FULL), un & 1u, abort, limit)) &&
-             mbar_wait_warp(bar(S_FREE), (x & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(K_FULL0 + x % K_STAGES), (x / K_STAGES) & 1u, abort, limit) &&
+             (j != 0 || warp_wait(bar(Q_FULL), un & 1u, abort, limit)) &&
+             warp_wait(bar(S_FREE), (x & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
         product_ss(tmem + TM_S, q_desc, sdesc_advance(k_desc, (x % K_STAGES) * TILE_BYTES), idesc);
         umma_commit_elect(bar(S_FULL));
         issued = true;
         if (j + 1 == n) umma_commit_elect(bar(Q_EMPTY));
-        ok = mbar_wait_warp(bar(V_FULL), x & 1u, abort, limit) &&
-             (j != 0 || mbar_wait_warp(bar(DO_FULL), un & 1u, abort, limit)) &&
-             mbar_wait_warp(bar(DP_FREE), (x & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(V_FULL), x & 1u, abort, limit) &&
+             (j != 0 || warp_wait(bar(DO_FULL), un & 1u, abort, limit)) &&
+             warp_wait(bar(DP_FREE), (x & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
         product_ss(tmem + TM_DP, do_desc, v_desc, idesc);
@@ -414,7 +393,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(orow), rr);
         ov[i] = (rows >> rr) & 1u ? reinterpret_cast<const uint4*>(from)[lane & 7] : make_uint4(0u, 0u, 0u, 0u);
       }
-      ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit, lane);
+      ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit);
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -437,14 +416,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_arrive(bar(DO_EMPTY));
         mbar_arrive(bar(XCH0 + quarter));
       }
-      ok = warp_wait(bar(XCH0 + quarter), un & 1u, abort, limit, lane);
+      ok = warp_wait(bar(XCH0 + quarter), un & 1u, abort, limit);
       if (!ok) break;
       // The next unit's sums come after this one's dQ, for which both warps have read these.
       const float delta = xch[r] + xch[TILE + r];
       if (half == 0 && q.valid && u.t0 == 0) p.delta[row] = delta;
       const uint64_t nl2 = f2_pack(-lse, -lse), nd2 = f2_pack(-delta, -delta);
       for (int j = 0; j < u.count(); ++j) {
-        ok = warp_wait(bar(S_FULL), x & 1u, abort, limit, lane);
+        ok = warp_wait(bar(S_FULL), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
         uint32_t v[64];
@@ -460,7 +439,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           pr[i] = ex2(a0);
           pr[i + 1] = ex2(a1);
         }
-        ok = warp_wait(bar(DP_FULL), x & 1u, abort, limit, lane);
+        ok = warp_wait(bar(DP_FULL), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
         load64(t_dp, v);
@@ -493,7 +472,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++x;
       }
       if (!ok) break;
-      ok = warp_wait(bar(DQ_FULL), un & 1u, abort, limit, lane);
+      ok = warp_wait(bar(DQ_FULL), un & 1u, abort, limit);
       if (!ok) break;
       tc_fence_after_sync();
       uint32_t v[64];
@@ -659,7 +638,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
       if (u.count() == 0) continue;
-      ok = mbar_wait_warp(bar(KV_EMPTY), (un & 1u) ^ 1u, abort, limit);
+      ok = warp_wait(bar(KV_EMPTY), (un & 1u) ^ 1u, abort, limit);
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(bar(KV_FULL), 2 * TILE_BYTES);
@@ -670,13 +649,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ++un;
       for (int i = u.q0; i < u.q1; ++i) {
         uint32_t s = qn % Q_STAGES;
-        ok = mbar_wait_warp(bar(Q_EMPTY0 + s), ((qn / Q_STAGES) & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(Q_EMPTY0 + s), ((qn / Q_STAGES) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q + s * TILE_BYTES, bar(Q_FULL0 + s), u.b, u.kh, i);
         __syncwarp();
         ++qn;
         s = dn % DO_STAGES;
-        ok = mbar_wait_warp(bar(DO_EMPTY0 + s), ((dn / DO_STAGES) & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(DO_EMPTY0 + s), ((dn / DO_STAGES) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         if (lane == 0)
           load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO + s * TILE_BYTES, bar(DO_FULL0 + s), u.b, u.kh, i);
@@ -718,13 +697,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             nd[k] = -p.delta[row];
           }
         }
-        ok = mbar_wait_warp(bar(LSE_EMPTY0 + (x & 1u)), ((x >> 1) & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(LSE_EMPTY0 + (x & 1u)), ((x >> 1) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) lse[(x & 1u) * TILE + k * 32 + lane] = nl[k];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(LSE_FULL0 + (x & 1u)));
-        ok = mbar_wait_warp(bar(DELTA_EMPTY), (x & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(DELTA_EMPTY), (x & 1u) ^ 1u, abort, limit);
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) delta[k * 32 + lane] = nd[k];
@@ -746,7 +725,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true, issued = false;
     auto issue_s = [&](uint32_t y, int rows) {
       const uint32_t s = y % Q_STAGES;
-      if (!mbar_wait_warp(bar(Q_FULL0 + s), (y / Q_STAGES) & 1u, abort, limit)) return false;
+      if (!warp_wait(bar(Q_FULL0 + s), (y / Q_STAGES) & 1u, abort, limit)) return false;
       tc_fence_after_sync();
       product_ss(tmem + TM_S, k_desc, sdesc_advance(q_desc, s * TILE_BYTES), idesc_s(rows));
       umma_commit_elect(bar(S_FULL));
@@ -755,7 +734,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     };
     auto issue_dp = [&](uint32_t y, int rows) {
       const uint32_t s = y % DO_STAGES;
-      if (!mbar_wait_warp(bar(DO_FULL0 + s), (y / DO_STAGES) & 1u, abort, limit)) return false;
+      if (!warp_wait(bar(DO_FULL0 + s), (y / DO_STAGES) & 1u, abort, limit)) return false;
       tc_fence_after_sync();
       product_ss(tmem + TM_DP, v_desc, sdesc_advance(do_desc, s * TILE_BYTES), idesc_s(rows));
       umma_commit_elect(bar(DP_FULL));
@@ -765,21 +744,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Unit u = decode(p, w);
       if (u.count() == 0) continue;
       int rows = rows_of(p, u.q0);
-      ok = mbar_wait_warp(bar(KV_FULL), un & 1u, abort, limit) && issue_s(x, rows) && issue_dp(x, rows);
+      ok = warp_wait(bar(KV_FULL), un & 1u, abort, limit) && issue_s(x, rows) && issue_dp(x, rows);
       for (int i = u.q0; i < u.q1 && ok; ++i) {
         const bool more = i + 1 < u.q1, fresh = i == u.q0;
         const int steps = ceil16(rows) / 16, next = more ? rows_of(p, i + 1) : 0;
-        ok = mbar_wait_warp(bar(P_READY), x & 1u, abort, limit) &&
-             (!fresh || mbar_wait_warp(bar(ACC_EMPTY), (un & 1u) ^ 1u, abort, limit));
+        ok = warp_wait(bar(P_READY), x & 1u, abort, limit) &&
+             (!fresh || warp_wait(bar(ACC_EMPTY), (un & 1u) ^ 1u, abort, limit));
         if (!ok) break;
         tc_fence_after_sync();
-        product_ts(tmem + TM_DV, tmem + TM_S, 64u, sdesc_advance(do_mn, (x % DO_STAGES) * TILE_BYTES), fresh, steps);
+        product_acc(tmem + TM_DV, tmem + TM_S, 64u, sdesc_advance(do_mn, (x % DO_STAGES) * TILE_BYTES), fresh, steps);
         umma_commit_elect(bar(DO_EMPTY0 + x % DO_STAGES));
         if (more && !(ok = issue_s(x + 1, next))) break;
-        ok = mbar_wait_warp(bar(DS_READY), x & 1u, abort, limit);
+        ok = warp_wait(bar(DS_READY), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
-        product_ts(tmem + TM_DK, tmem + TM_DP, 64u, sdesc_advance(q_mn, (x % Q_STAGES) * TILE_BYTES), fresh, steps);
+        product_acc(tmem + TM_DK, tmem + TM_DP, 64u, sdesc_advance(q_mn, (x % Q_STAGES) * TILE_BYTES), fresh, steps);
         umma_commit_elect(bar(Q_EMPTY0 + x % Q_STAGES));
         if (more && !(ok = issue_dp(x + 1, next))) break;
         ++x;
@@ -826,8 +805,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int i = u.q0; i < u.q1; ++i) {
         const float* lse = reinterpret_cast<const float*>(gbase + SM_LSE) + (x & 1u) * TILE + half * 64;
         const float* delta = reinterpret_cast<const float*>(gbase + SM_DELTA) + half * 64;
-        ok = warp_wait(bar(LSE_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit, lane) &&
-             warp_wait(bar(S_FULL), x & 1u, abort, limit, lane);
+        ok = warp_wait(bar(LSE_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit) &&
+             warp_wait(bar(S_FULL), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
         uint32_t v[64], pk[32];
@@ -851,8 +830,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mbar_arrive(bar(P_READY));
           mbar_arrive(bar(LSE_EMPTY0 + (x & 1u)));
         }
-        ok = warp_wait(bar(DELTA_FULL), x & 1u, abort, limit, lane) &&
-             warp_wait(bar(DP_FULL), x & 1u, abort, limit, lane);
+        ok = warp_wait(bar(DELTA_FULL), x & 1u, abort, limit) &&
+             warp_wait(bar(DP_FULL), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
         load64(t_dp, v);
@@ -878,7 +857,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++x;
       }
       if (!ok) break;
-      ok = warp_wait(bar(ACC_FULL), un & 1u, abort, limit, lane);
+      ok = warp_wait(bar(ACC_FULL), un & 1u, abort, limit);
       if (!ok) break;
       tc_fence_after_sync();
       const unsigned rows = __ballot_sync(0xffffffffu, visible);

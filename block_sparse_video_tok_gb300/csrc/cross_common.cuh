@@ -44,11 +44,56 @@ cudaError_t make_tmap_heads(CUtensorMap* map, const HeadsView& x, int tokens, in
 
 #ifdef __CUDACC__
 
+// Wait of a converged warp for the phase of `bar` with the given parity; false if *abort was
+// raised or `limit_ns` of wall time passed.  Every lane polls, and the clock and *abort are looked
+// at once in POLLS probes: reading the global timer between probes held a warp for hundreds of
+// cycles after its barrier had completed (a hand-over from tensor core to softmax took 700).
+constexpr int POLLS = 64;
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          uint64_t limit_ns, int lane) {
-  int ok = 1;
-  if (lane == 0) ok = mbar_wait_bounded(bar, parity, abort, limit_ns) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+                                          uint64_t limit_ns) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    uint64_t t0 = 0;
+    while (true) {
+      int i = 0;
+      do {
+        ok = mbar_try_wait(bar, parity);
+      } while (!ok && ++i < POLLS);
+      if (ok || *abort) break;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > limit_ns) break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// warp_wait on several barriers at once: waits for those whose bit is set in `need`, and probes
+// those in `probe` once.  The probes go out together, so their round trips overlap.  Returns the
+// bits of the completed ones for all lanes; a missing bit of `need` means abort or timeout.
+template <int N>
+__device__ __forceinline__ uint32_t warp_wait_n(const uint32_t (&bar)[N], const uint32_t (&parity)[N], uint32_t need,
+                                                uint32_t probe, volatile int* abort, uint64_t limit_ns) {
+  uint32_t done = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (((need | probe) >> i) & 1u) done |= mbar_try_wait(bar[i], parity[i]) ? 1u << i : 0u;
+  if ((done & need) != need) {
+    uint64_t t0 = 0;
+    while (true) {
+      int k = 0;
+      do {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (((need & ~done) >> i) & 1u) done |= mbar_try_wait(bar[i], parity[i]) ? 1u << i : 0u;
+      } while ((done & need) != need && ++k < POLLS);
+      if ((done & need) == need || *abort) break;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > limit_ns) break;
+    }
+  }
+  return __reduce_and_sync(0xffffffffu, done);
 }
 
 __device__ __forceinline__ void raise_abort(volatile int* abort, uint32_t* err) {
@@ -130,6 +175,72 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int l
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// The UMMAs of a whole product in one block, issued by the lane elect.sync chooses of a converged
+// warp.  The issuing warp shares its scheduler with two softmax warps, so what counts is how few
+// instructions it takes: issued one by one, with an election and 64-bit descriptors each, a
+// product of 8 UMMAs took the warp about 870 cycles, for 520 of the tensor core.
+
+// D = A B^T over 128 columns: A, B K-major operand tiles (SWIZZLE_128B, column halves 16 KB apart).
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+      "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 1024;\n\tadd.u64 b, %2, 1024;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 1026;\n\tadd.u64 b, %2, 1026;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 1028;\n\tadd.u64 b, %2, 1028;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, %1, 1030;\n\tadd.u64 b, %2, 1030;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+
+// D (+)= A B over 64 rows of B: A 16-bit pairs in tensor memory (32 columns), B an MN-major tile
+// (SWIZZLE_128B).  accumulate = 0: D is overwritten.
+__device__ __forceinline__ void product_ts64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, c, t;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 c, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, c;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same over `steps` x 16 rows of B, 1 to 4 steps.
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate, int steps) {
+  if (steps == 4) {
+    product_ts64(d, a, b, idesc, accumulate);
+    return;
+  }
+  if (accumulate)
+    umma_ts_elect<true>(d, a, b, idesc);
+  else
+    umma_ts_elect<false>(d, a, b, idesc);
+#pragma unroll 1
+  for (int kk = 1; kk < steps; ++kk) umma_ts_elect<true>(d, a + kk * 8u, sdesc_advance(b, kk * 2048u), idesc);
 }
 
 #endif

@@ -22,9 +22,11 @@
 // When there are fewer units than SMs the keys are split: each part leaves its unnormalised O
 // and (m, l) in the workspace, and cross_combine_kernel joins them in part order.
 //
-// Roles (384 threads): warps 0-3 and 4-7 softmax groups; warp 8 TMEM owner and TMA producer of Q
-// and K; warp 9 UMMA issuer; warp 10 TMA producer of V.
-// Shared memory: a Q tile per group, 2 K and 2 V tiles, and 4 KB per softmax warp through which O
+// Roles (512 threads): warps 0-3 and 4-7 softmax groups; warps 8-11 output (one row of the tile
+// per thread: O / l, rounded, written), so that a group goes on to its next unit's scores while
+// its last O leaves; warp 12 TMEM owner and TMA producer of Q and K; warp 13 UMMA issuer; warp 14
+// TMA producer of V.
+// Shared memory: a Q tile per group, 2 K and 2 V tiles, and 4 KB per output warp through which O
 // leaves in whole 128-byte lines.  A Q tile is free as soon as its unit's last S has been
 // computed, a softmax and a P V before the next unit needs it, and its successor has been
 // prefetched into L2 by then.  TMEM: O x2 [0, 256), S x2 [256, 512).
@@ -34,35 +36,40 @@ namespace vsa {
 
 namespace {
 
-constexpr int NUM_THREADS = 384;  // warps are allocated in fours: the twelfth has no role
-constexpr int TMA_WARP = 8, MMA_WARP = 9, V_WARP = 10;
+constexpr int NUM_THREADS = 512;
+constexpr int TMA_WARP = 0, MMA_WARP = 1, V_WARP = 2, SOFTMAX_WARP = 4, OUT_WARP = 12;
 constexpr int KV_STAGES = 2;
 constexpr float RESCALE = 8.0f;  // log2 units
 
 constexpr uint32_t SM_Q = 0;
 constexpr uint32_t SM_K = 2 * TILE_BYTES;
 constexpr uint32_t SM_V = SM_K + KV_STAGES * TILE_BYTES;
-constexpr uint32_t SM_OUT = SM_V + KV_STAGES * TILE_BYTES;  // 8 warps x 32 rows x 128 bytes
-constexpr uint32_t SM_BAR = SM_OUT + TILE_BYTES;
+constexpr uint32_t SM_OUT = SM_V + KV_STAGES * TILE_BYTES;  // 4 warps x 32 rows x 128 bytes
+constexpr uint32_t SM_ML = SM_OUT + TILE_BYTES / 2;         // [group][128 rows] (m, l)
+constexpr uint32_t SM_BAR = SM_ML + 2 * TILE * 8;
 
 enum Bar : uint32_t {
   Q_FULL0 = 0,  // per group
   Q_EMPTY0 = Q_FULL0 + 2,
   K_FULL0 = Q_EMPTY0 + 2,
-  K_EMPTY0 = K_FULL0 + KV_STAGES,
-  V_FULL0 = K_EMPTY0 + KV_STAGES,
-  V_EMPTY0 = V_FULL0 + KV_STAGES,
-  S_FULL0 = V_EMPTY0 + KV_STAGES,  // per group: S_g of the next kv tile is in TMEM
-  P_READY0 = S_FULL0 + 2,          // per group: P_g is in TMEM
-  O_FULL0 = P_READY0 + 2,          // per group: O_g holds the unit's last product
-  O_EMPTY0 = O_FULL0 + 2,          // per group: O_g has been read
-  V_TAIL = O_EMPTY0 + 2,
+  V_FULL0 = K_FULL0 + KV_STAGES,
+  // The issuer's step x: the products with V tile x - 1, then those with K tile x.  Completed
+  // steps x = 0, 2, .. and x = 1, 3, .. arrive here, so K tile x + 2 may follow step x, and V tile
+  // x + 1.
+  STEP0 = V_FULL0 + KV_STAGES,
+  S_FULL0 = STEP0 + 2,     // per group: S_g of the next kv tile is in TMEM
+  P_READY0 = S_FULL0 + 2,  // per group: P_g is in TMEM
+  O_FULL0 = P_READY0 + 2,  // per group: O_g holds the unit's last product
+  O_EMPTY0 = O_FULL0 + 2,  // per group: O_g and (m, l) have been read
+  ML_READY0 = O_EMPTY0 + 2,  // per group: the unit's (m, l) are in shared memory
+  V_TAIL = ML_READY0 + 2,
   DRAIN,
   NUM_BARS
 };
 constexpr uint32_t SM_TMEM_SLOT = SM_BAR + NUM_BARS * 8;
 constexpr uint32_t SM_ABORT = SM_TMEM_SLOT + 4;
 constexpr uint32_t SMEM_BYTES = SM_ABORT + 4 + 1024;  // + alignment slack
+static_assert(KV_STAGES == 2, "two step barriers");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 constexpr uint32_t TM_O = 0, TM_S = 256;  // O_g at TM_O + 128 g, S_g at TM_S + 128 g
@@ -116,18 +123,15 @@ __device__ __forceinline__ void tile_origin(const Params& p, const Unit& u, int 
 
 __device__ __forceinline__ int ceil16(int n) { return (n + 15) & ~15; }
 
-// Maximum (or minimum) of 128 raw scores: four chains of 3-input instructions.
-template <bool MIN>
-__device__ __forceinline__ float extremum(const uint32_t* sv) {
-  constexpr float sign = MIN ? -1.f : 1.f;
-  float m[4];
+// max(m, x) over 32 raw scores: two chains of 3-input instructions.
+__device__ __forceinline__ float max32(const uint32_t* x, float m) {
+  float a = m, b = __uint_as_float(x[0]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    m[k] = fmaxf(sign * __uint_as_float(sv[2 * k]), sign * __uint_as_float(sv[2 * k + 1]));
-#pragma unroll
-  for (int u = 8; u < TILE; u += 2)
-    m[(u >> 1) & 3] = max3(m[(u >> 1) & 3], sign * __uint_as_float(sv[u]), sign * __uint_as_float(sv[u + 1]));
-  return sign * max3(fmaxf(m[0], m[1]), m[2], m[3]);
+  for (int i = 0; i < 30; i += 4) {
+    a = max3(a, __uint_as_float(x[i + 1]), __uint_as_float(x[i + 2]));
+    b = max3(b, __uint_as_float(x[i + 3]), __uint_as_float(x[(i + 4) & 31]));
+  }
+  return fmaxf(a, b);
 }
 
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -167,270 +171,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tile_rows_bytes = static_cast<uint32_t>(p.t.box * p.t.pack) * 256u;
 
-  if (warp == TMA_WARP) {
-    // ------------------------------------------------------------------ TMA producer: Q, K
-    uint32_t qn[2] = {0, 0}, kn = 0;  // tiles loaded
-    bool ok = true;
-    const int halves = p.t.box * p.t.pack == TILE ? 1 : 2;  // copies of a Q tile
-    auto load_k = [&](const Unit& u, int j) {
-      const uint32_t s = kn % KV_STAGES;
-      if (!mbar_wait_warp(bar(K_EMPTY0 + s), ((kn / KV_STAGES) & 1u) ^ 1u, abort, limit)) return false;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(K_FULL0 + s), TILE_BYTES);
-        tma_load_5d(base + SM_K + s * TILE_BYTES, &tm_k, bar(K_FULL0 + s), 0, (u.t0 + j) * TILE, u.kh, 0,
-                    p.a.k.batch ? u.b : 0);
-      }
-      __syncwarp();
-      ++kn;
-      return true;
-    };
-    for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-      const Unit u = decode(p, w);
-      if (u.count() == 0) continue;
-      ok = load_k(u, 0);
-      for (int g = 0; g < (u.second ? 2 : 1) && ok; ++g) {
-        ok = mbar_wait_warp(bar(Q_EMPTY0 + g), (qn[g] & 1u) ^ 1u, abort, limit);
-        if (!ok) break;
-        int head, token;
-        tile_origin(p, u, u.tile0 + g, &head, &token);
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(Q_FULL0 + g), tile_rows_bytes);
-          for (int h = 0; h < halves; ++h)
-            tma_load_5d(base + SM_Q + g * TILE_BYTES + h * (TILE_BYTES / 2), &tm_q, bar(Q_FULL0 + g), 0, token, head, h,
-                        p.a.q.batch ? u.b : 0);
-        }
-        __syncwarp();
-        ++qn[g];
-      }
-      if (ok && lane == 0 && w + gridDim.x < p.total) {
-        const Unit nu = decode(p, w + gridDim.x);
-        for (int g = 0; g < (nu.count() == 0 ? 0 : nu.second ? 2 : 1); ++g) {
-          int head, token;
-          tile_origin(p, nu, nu.tile0 + g, &head, &token);
-          for (int h = 0; h < halves; ++h) tma_prefetch_5d(&tm_q, 0, token, head, h, p.a.q.batch ? nu.b : 0);
-        }
-      }
-      __syncwarp();
-      for (int j = 1; j < u.count() && ok; ++j) ok = load_k(u, j);
-    }
-    if (!ok && lane == 0) {
-      raise_abort(abort, p.a.err);
-      // Let the copies already issued land before the CTA's shared memory goes away.
-      volatile int never = 0;
-      for (int g = 0; g < 2; ++g)
-        if (qn[g] > 0) mbar_wait_bounded(bar(Q_FULL0 + g), (qn[g] - 1) & 1u, &never, DRAIN_LIMIT_NS);
-      for (uint32_t i = kn > KV_STAGES ? kn - KV_STAGES : 0; i < kn; ++i)
-        mbar_wait_bounded(bar(K_FULL0 + i % KV_STAGES), (i / KV_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
-    }
-    __syncwarp();
-  } else if (warp == V_WARP) {
-    // ------------------------------------------------------------------ TMA producer: V
-    uint32_t vn = 0, tails = 0, tails_seen = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-      const Unit u = decode(p, w);
-      for (int j = 0; j < u.count() && ok; ++j) {
-        const uint32_t s = vn % KV_STAGES, tile = base + SM_V + s * TILE_BYTES;
-        ok = mbar_wait_warp(bar(V_EMPTY0 + s), ((vn / KV_STAGES) & 1u) ^ 1u, abort, limit);
-        if (!ok) break;
-        // Past kv_tokens the copy itself fills with zeros; rows between the last visible key and
-        // there are zeroed here, before the tile is handed on.
-        const int n = u.keys_of(j);
-        const bool patch = n < TILE && u.keys < p.a.kv_tokens;
-        const uint32_t full = patch ? bar(V_TAIL) : bar(V_FULL0 + s);
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full, TILE_BYTES);
-          tma_load_5d(tile, &tm_v, full, 0, (u.t0 + j) * TILE, u.kh, 0, p.a.v.batch ? u.b : 0);
-        }
-        __syncwarp();
-        if (patch) {
-          ++tails;
-          ok = mbar_wait_warp(full, (tails - 1) & 1u, abort, limit);
-          if (!ok) break;
-          tails_seen = tails;
-          zero_rows(tile, n, ceil16(n), lane);
-          if (lane == 0) mbar_arrive(bar(V_FULL0 + s));
-        }
-        ++vn;
-      }
-    }
-    if (!ok && lane == 0) {
-      raise_abort(abort, p.a.err);
-      volatile int never = 0;
-      if (tails > tails_seen) mbar_wait_bounded(bar(V_TAIL), (tails - 1) & 1u, &never, DRAIN_LIMIT_NS);
-      for (uint32_t i = vn > KV_STAGES ? vn - KV_STAGES : 0; i < vn; ++i)
-        mbar_wait_bounded(bar(V_FULL0 + i % KV_STAGES), (i / KV_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
-    }
-    __syncwarp();
-  } else if (warp == MMA_WARP) {
-    // ------------------------------------------------------------------ UMMA issuer
-    // The whole warp runs this role in lockstep; one elected lane issues.
-    uint32_t kn = 0, vn = 0;                               // K and V tiles consumed
-    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};  // per group: Q tiles, kv tiles, units
-    bool ok = true, issued = false;
-    const uint64_t q_desc = sdesc_sw128(base + SM_Q, 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(base + SM_K, 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(base + SM_V, TILE_BYTES / 2, 1024);
-    // S_g = Q_g K^T over `keys` columns (rounded up to 16), K in stage kn; `last`: of the unit.
-    auto issue_s = [&](int g, int keys, bool last) {
-      const uint64_t qa = sdesc_advance(q_desc, g * TILE_BYTES);
-      const uint64_t kd = sdesc_advance(k_desc, (kn % KV_STAGES) * TILE_BYTES);
-      const uint32_t ts = tmem + TM_S + g * 128u;
-      const uint32_t idesc = IDESC_S0 | (static_cast<uint32_t>(ceil16(keys) >> 3) << 17);
-      umma_ss_elect<false>(ts, qa, kd, idesc);
-#pragma unroll
-      for (int kk = 1; kk < 8; ++kk) {
-        const uint32_t off = (kk >> 2) * (TILE_BYTES / 2) + (kk & 3) * 32u;
-        umma_ss_elect<true>(ts, sdesc_advance(qa, off), sdesc_advance(kd, off), idesc);
-      }
-      umma_commit_elect(bar(S_FULL0 + g));
-      if (last) umma_commit_elect(bar(Q_EMPTY0 + g));
-      issued = true;
-    };
-    auto issue_pv = [&](int g, bool fresh, int keys) {
-      const uint64_t vd = sdesc_advance(v_desc, (vn % KV_STAGES) * TILE_BYTES);
-      const uint32_t to = tmem + TM_O + g * 128u, pa = tmem + TM_S + g * 128u;
-      if (fresh)
-        umma_ts_elect<false>(to, pa, vd, IDESC_PV);
-      else
-        umma_ts_elect<true>(to, pa, vd, IDESC_PV);
-      if (keys > TILE - 16) {
-#pragma unroll
-        for (int kk = 1; kk < 8; ++kk) umma_ts_elect<true>(to, pa + kk * 8u, sdesc_advance(vd, kk * 2048u), IDESC_PV);
-      } else {
-#pragma unroll 1
-        for (int kk = 1; kk * 16 < keys; ++kk)
-          umma_ts_elect<true>(to, pa + kk * 8u, sdesc_advance(vd, kk * 2048u), IDESC_PV);
-      }
-    };
-    // The next unit with keys, from w on (total: none).
-    auto next_unit = [&](int w, Unit* u) {
-      for (; w < p.total; w += gridDim.x) {
-        *u = decode(p, w);
-        if (u->count() > 0) break;
-      }
-      return w;
-    };
-    Unit u{};
-    int w = next_unit(blockIdx.x, &u);
-    // S of unit x's first kv tile for one group (group 0 first).
-    auto first_s = [&](const Unit& x, int g) {
-      if (!mbar_wait_warp(bar(Q_FULL0 + g), qn[g] & 1u, abort, limit)) return false;
-      if (g == 0 && !mbar_wait_warp(bar(K_FULL0 + kn % KV_STAGES), (kn / KV_STAGES) & 1u, abort, limit)) return false;
-      tc_fence_after_sync();
-      issue_s(g, x.keys_of(0), x.count() == 1);
-      ++qn[g];
-      return true;
-    };
-    if (w < p.total) {
-      ok = first_s(u, 0) && (!u.second || first_s(u, 1));
-      if (ok) {
-        umma_commit_elect(bar(K_EMPTY0 + kn % KV_STAGES));
-        ++kn;
-      }
-    }
-    while (ok && w < p.total) {
-      Unit nu{};
-      const int nw = next_unit(w + gridDim.x, &nu);
-      const int groups = u.second ? 2 : 1, n = u.count();
-      for (int j = 0; j < n && ok; ++j) {
-        const int keys = u.keys_of(j);
-        for (int g = 0; g < groups; ++g) {
-          ok = mbar_wait_warp(bar(P_READY0 + g), pn[g] & 1u, abort, limit) &&
-               (g != 0 || mbar_wait_warp(bar(V_FULL0 + vn % KV_STAGES), (vn / KV_STAGES) & 1u, abort, limit)) &&
-               (j != 0 || mbar_wait_warp(bar(O_EMPTY0 + g), (on[g] & 1u) ^ 1u, abort, limit));
-          if (!ok) break;
-          tc_fence_after_sync();
-          issue_pv(g, j == 0, keys);
-          ++pn[g];
-          if (j + 1 < n) {
-            if (g == 0 && !(ok = mbar_wait_warp(bar(K_FULL0 + kn % KV_STAGES), (kn / KV_STAGES) & 1u, abort, limit)))
-              break;
-            tc_fence_after_sync();
-            issue_s(g, u.keys_of(j + 1), j + 2 == n);
-          } else {
-            umma_commit_elect(bar(O_FULL0 + g));
-            ++on[g];
-            // The next unit's first S of this group, while the softmax reads O_g.
-            if (nw < p.total && (g == 0 || nu.second) && !(ok = first_s(nu, g))) break;
-          }
-        }
-        if (!ok) break;
-        // A unit without a second tile followed by one with: its first S is still to come.
-        if (j + 1 == n && groups == 1 && nw < p.total && nu.second && !(ok = first_s(nu, 1))) break;
-        umma_commit_elect(bar(V_EMPTY0 + vn % KV_STAGES));
-        ++vn;
-        if (j + 1 < n || nw < p.total) {
-          umma_commit_elect(bar(K_EMPTY0 + kn % KV_STAGES));
-          ++kn;
-        }
-      }
-      u = nu;
-      w = nw;
-    }
-    if (!ok && lane == 0) raise_abort(abort, p.a.err);
-    if (issued) {
-      // Every UMMA has completed before TMEM is released.
-      umma_commit_elect(bar(DRAIN));
-      volatile int never = 0;
-      if (lane == 0) mbar_wait_bounded(bar(DRAIN), 0, &never, DRAIN_LIMIT_NS);
-      __syncwarp();
-    }
-  } else if (warp < 8) {
+  if (warp >= SOFTMAX_WARP && warp < OUT_WARP) {
     // ------------------------------------------------------------------ softmax groups
-    const int quarter = warp & 3, g = warp >> 2;
+    const int quarter = warp & 3, g = (warp - SOFTMAX_WARP) >> 2;
     const int r = quarter * 32 + lane;  // row of the tile == TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_off + TM_S + g * 128u, t_o = tmem + lane_off + TM_O + g * 128u;
-    float c1 = p.a.sm_scale * LOG2E_F;
-    if (c1 == 0.f) c1 = 1e-30f;  // keeps 0 * -inf out of the mask; finite scores still give s = 0
-    const uint32_t pad = c1 > 0.f ? 0xff800000u : 0x7f800000u;  // scales to -inf
-    const uint32_t stage = base + SM_OUT + warp * 4096u;  // this warp's 32 rows x 64 columns
-    uint32_t sn = 0, on = 0;                              // kv tiles and units of this group
+    // S carries the sign of the scale.  Scale 0: 1e-30 keeps 0 * -inf out of the mask, and finite
+    // scores still give s = 0.
+    const float c1 = p.a.sm_scale == 0.f ? 1e-30f : fabsf(p.a.sm_scale) * LOG2E_F;
+    float2* ml = reinterpret_cast<float2*>(gbase + SM_ML) + g * TILE + r;
+    uint32_t sn = 0, on = 0;  // kv tiles and units of this group
     bool ok = true;
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
-      if (g == 1 && !u.second) continue;
-      int head, token;
-      tile_origin(p, u, u.tile0 + g, &head, &token);
-      const int rh = r / p.t.box;
-      head += rh;
-      token += r - rh * p.t.box;
-      const bool valid = rh < p.t.pack && token < p.a.q_tokens;
-      const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token;
-      const int64_t ptile =
-          ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile0 + g;
-      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch + head * p.a.o.head +
-                            token * p.a.o.token;
-      if (u.count() == 0) {
-        if (!valid) continue;
-        if (p.splits > 1) {
-          p.part_ml[ptile * TILE + r] = make_float2(-INFINITY, 0.f);
-          continue;
-        }
-        for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0u, 0u, 0u, 0u);
-        p.a.lse[row] = -INFINITY;
-        continue;
-      }
+      if (u.count() == 0 || (g == 1 && !u.second)) continue;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < u.count(); ++j) {
-        ok = warp_wait(bar(S_FULL0 + g), sn & 1u, abort, limit, lane);
+        ok = warp_wait(bar(S_FULL0 + g), sn & 1u, abort, limit);
         if (!ok) break;
         ++sn;
         tc_fence_after_sync();
-        uint32_t sv[TILE];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + c * 32u, sv + c * 32);
-        tmem_wait_ld();
-        const int n = u.keys_of(j);
-        if (n < TILE) {
-#pragma unroll
-          for (int i = 0; i < TILE; ++i)
-            if (i >= n) sv[i] = pad;
+        // Two passes over S in chunks of 32 columns, each chunk's load in flight while the one
+        // before is worked on.  The loops stay rolled: unrolled over the 128 columns they took 524
+        // us where they now take 400 (131040 x 512, 12 heads), waiting for instructions.
+        const int n = u.keys_of(j), cols = (n + 63) & ~63;
+        if (n < cols) {
+#pragma unroll 1
+          for (int c = n; c < cols; ++c) tmem_st_32x32b_x1(t_s + c, 0xff800000u);
+          tmem_wait_st();
         }
-        const float mb = c1 * (c1 > 0.f ? extremum<false>(sv) : extremum<true>(sv));
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(t_s, v[0]);
+        float mb = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 64) {
+          tmem_wait_ld_regs(v[0]);
+          tmem_ld_32x32b_x32(t_s + c + 32u, v[1]);
+          mb = max32(v[0], mb);
+          tmem_wait_ld_regs(v[1]);
+          tmem_ld_32x32b_x32(t_s + (c + 64 < cols ? c + 64 : 0), v[0]);  // after the last: the first again
+          mb = max32(v[1], mb);
+        }
+        mb *= c1;
         const bool need = mb > m + RESCALE;
-        if (__any_sync(0xffffffffu, need)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
           const float f = need ? ex2(m - mb) : 1.f;  // m = -inf: 0, nothing accumulated yet
           l *= f;
           if (need) m = mb;
@@ -450,87 +235,326 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const float off = m == -INFINITY ? 0.f : -m;
         const uint64_t c2 = f2_pack(c1, c1), o2 = f2_pack(off, off);
         uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        // P of the chunk from column c on goes over columns c / 2 .. c / 2 + 15, which earlier
+        // chunks and this one alone cover.
+        auto exps = [&](const uint32_t* x, int c) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float a0, a1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c * 32 + 2 * i]), __uint_as_float(sv[c * 32 + 2 * i + 1])),
-                             c2, o2),
-                      a0, a1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, o2), a0, a1);
             const float p0 = ex2(a0), p1 = ex2(a1);
             acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
             pk[i] = pack_bf162(p0, p1);
           }
-          tmem_st_32x32b_x16(t_s + c * 16u, pk);
+          tmem_st_32x32b_x16(t_s + c / 2, pk);
+        };
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 64) {
+          tmem_wait_ld_regs(v[0]);
+          tmem_ld_32x32b_x32(t_s + c + 32u, v[1]);
+          exps(v[0], c);
+          tmem_wait_ld_regs(v[1]);
+          if (c + 64 < cols) tmem_ld_32x32b_x32(t_s + c + 64u, v[0]);
+          exps(v[1], c + 32);
         }
-        float s0, s1;
-        f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
-        l += s0 + s1;
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P_READY0 + g));
+        float s0, s1;
+        f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
+        l += s0 + s1;
       }
       if (!ok) break;
-      ok = warp_wait(bar(O_FULL0 + g), on & 1u, abort, limit, lane);
+      ok = warp_wait(bar(O_EMPTY0 + g), (on & 1u) ^ 1u, abort, limit);  // the last unit's have been read
       if (!ok) break;
-      tc_fence_after_sync();
-      if (p.splits > 1) {
-        if (valid) p.part_ml[ptile * TILE + r] = make_float2(m, l);
-        float* po = p.part_o + ptile * TILE * TILE + r;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t ov[32];
-          tmem_ld_32x32b_x32(t_o + c * 32u, ov);
-          tmem_wait_ld();
-          if (valid) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) po[(c * 32 + i) * TILE] = __uint_as_float(ov[i]);
+      *ml = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(ML_READY0 + g));
+      ++on;
+    }
+    if (!ok && lane == 0) raise_abort(abort, p.a.err);
+    __syncwarp();
+  } else if (warp >= OUT_WARP) {
+    // ------------------------------------------------------------------ output
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t stage = base + SM_OUT + quarter * 4096u;  // this warp's 32 rows x 64 columns
+    uint32_t on[2] = {0, 0};
+    bool ok = true;
+    for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+      const Unit u = decode(p, w);
+      for (int g = 0; g < (u.second ? 2 : 1) && ok; ++g) {
+        int head, token;
+        tile_origin(p, u, u.tile0 + g, &head, &token);
+        const int rh = r / p.t.box;
+        head += rh;
+        token += r - rh * p.t.box;
+        const bool valid = rh < p.t.pack && token < p.a.q_tokens;
+        const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token;
+        const int64_t ptile =
+            ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile0 + g;
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch + head * p.a.o.head +
+                              token * p.a.o.token;
+        if (u.count() == 0) {
+          if (!valid) continue;
+          if (p.splits > 1) {
+            p.part_ml[ptile * TILE + r] = make_float2(-INFINITY, 0.f);
+            continue;
           }
+          for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0u, 0u, 0u, 0u);
+          p.a.lse[row] = -INFINITY;
+          continue;
         }
-      } else {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        ok = warp_wait(bar(ML_READY0 + g), on[g] & 1u, abort, limit) &&
+             warp_wait(bar(O_FULL0 + g), on[g] & 1u, abort, limit);
+        if (!ok) break;
+        ++on[g];
+        tc_fence_after_sync();
+        const float2 ml = reinterpret_cast<const float2*>(gbase + SM_ML)[g * TILE + r];
+        const uint32_t t_o = tmem + lane_off + TM_O + g * 128u;
+        if (p.splits > 1) {
+          if (valid) p.part_ml[ptile * TILE + r] = ml;
+          float* po = p.part_o + ptile * TILE * TILE + r;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t ov[32];
+            tmem_ld_32x32b_x32(t_o + c * 32u, ov);
+            tmem_wait_ld();
+            if (valid) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) po[(c * 32 + i) * TILE] = __uint_as_float(ov[i]);
+            }
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(O_EMPTY0 + g));
+          continue;
+        }
+        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
         const uint64_t inv2 = f2_pack(inv, inv);
         const unsigned rows = __ballot_sync(0xffffffffu, valid);
+        if (valid) p.a.lse[row] = ml.x + log2f(ml.y);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {  // column halves of 64, through the warp's staging rows
-          uint32_t ov[64];
-          tmem_ld_32x32b_x32(t_o + h * 64u, ov);
-          tmem_ld_32x32b_x32(t_o + h * 64u + 32u, ov + 32);
-          tmem_wait_ld();
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t ov[32];
+            tmem_ld_32x32b_x32(t_o + h * 64u + c * 32u, ov);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t pk[4];
+            for (int i = 0; i < 4; ++i) {
+              uint32_t pk[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float a0, a1;
-              f2_unpack(f2_mul(f2_pack(__uint_as_float(ov[8 * i + 2 * x]), __uint_as_float(ov[8 * i + 2 * x + 1])), inv2),
-                        a0, a1);
-              pk[x] = pack_bf162(a0, a1);
+              for (int x = 0; x < 4; ++x) {
+                float a0, a1;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(ov[8 * i + 2 * x]), __uint_as_float(ov[8 * i + 2 * x + 1])), inv2),
+                          a0, a1);
+                pk[x] = pack_bf162(a0, a1);
+              }
+              st_shared16(stage + swizzled(lane, c * 4 + i), pk[0], pk[1], pk[2], pk[3]);
             }
-            st_shared16(stage + swizzled(lane, i), pk[0], pk[1], pk[2], pk[3]);
           }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (h == 1 && lane == 0) mbar_arrive(bar(O_EMPTY0 + g));
+          uint4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = ld_shared16(stage + swizzled(i * 4 + (lane >> 3), lane & 7));
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {  // four rows of 128 bytes at a time
             const int rr = i * 4 + (lane >> 3);
             const uint64_t to = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(orow), rr);
-            const uint4 x = ld_shared16(stage + swizzled(rr, lane & 7));
-            if ((rows >> rr) & 1u) reinterpret_cast<uint4*>(to)[h * 8 + (lane & 7)] = x;
+            if ((rows >> rr) & 1u) reinterpret_cast<uint4*>(to)[h * 8 + (lane & 7)] = x[i];
           }
-          __syncwarp();
         }
-        if (valid) p.a.lse[row] = m + log2f(l);
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(O_EMPTY0 + g));
-      ++on;
     }
     if (!ok && lane == 0) raise_abort(abort, p.a.err);
     __syncwarp();
+  } else {
+    if (warp == TMA_WARP) {
+      // ------------------------------------------------------------------ TMA producer: Q, K
+      uint32_t qn[2] = {0, 0}, kn = 0;  // tiles loaded
+      bool ok = true;
+      const int halves = p.t.box * p.t.pack == TILE ? 1 : 2;  // copies of a Q tile
+      auto load_k = [&](const Unit& u, int j) {
+        const uint32_t s = kn % KV_STAGES;
+        if (!warp_wait(bar(STEP0 + s), ((kn / KV_STAGES) & 1u) ^ 1u, abort, limit)) return false;  // step kn - 2
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(K_FULL0 + s), TILE_BYTES);
+          tma_load_5d(base + SM_K + s * TILE_BYTES, &tm_k, bar(K_FULL0 + s), 0, (u.t0 + j) * TILE, u.kh, 0,
+                      p.a.k.batch ? u.b : 0);
+        }
+        __syncwarp();
+        ++kn;
+        return true;
+      };
+      for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+        const Unit u = decode(p, w);
+        if (u.count() == 0) continue;
+        ok = load_k(u, 0);
+        for (int g = 0; g < (u.second ? 2 : 1) && ok; ++g) {
+          ok = warp_wait(bar(Q_EMPTY0 + g), (qn[g] & 1u) ^ 1u, abort, limit);
+          if (!ok) break;
+          int head, token;
+          tile_origin(p, u, u.tile0 + g, &head, &token);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(Q_FULL0 + g), tile_rows_bytes);
+            for (int h = 0; h < halves; ++h)
+              tma_load_5d(base + SM_Q + g * TILE_BYTES + h * (TILE_BYTES / 2), &tm_q, bar(Q_FULL0 + g), 0, token, head, h,
+                          p.a.q.batch ? u.b : 0);
+          }
+          __syncwarp();
+          ++qn[g];
+        }
+        if (ok && lane == 0 && w + gridDim.x < p.total) {
+          const Unit nu = decode(p, w + gridDim.x);
+          for (int g = 0; g < (nu.count() == 0 ? 0 : nu.second ? 2 : 1); ++g) {
+            int head, token;
+            tile_origin(p, nu, nu.tile0 + g, &head, &token);
+            for (int h = 0; h < halves; ++h) tma_prefetch_5d(&tm_q, 0, token, head, h, p.a.q.batch ? nu.b : 0);
+          }
+        }
+        __syncwarp();
+        for (int j = 1; j < u.count() && ok; ++j) ok = load_k(u, j);
+      }
+      if (!ok && lane == 0) {
+        raise_abort(abort, p.a.err);
+        // Let the copies already issued land before the CTA's shared memory goes away.
+        volatile int never = 0;
+        for (int g = 0; g < 2; ++g)
+          if (qn[g] > 0) mbar_wait_bounded(bar(Q_FULL0 + g), (qn[g] - 1) & 1u, &never, DRAIN_LIMIT_NS);
+        for (uint32_t i = kn > KV_STAGES ? kn - KV_STAGES : 0; i < kn; ++i)
+          mbar_wait_bounded(bar(K_FULL0 + i % KV_STAGES), (i / KV_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
+      }
+      __syncwarp();
+    } else if (warp == V_WARP) {
+      // ------------------------------------------------------------------ TMA producer: V
+      uint32_t vn = 0, tails = 0, tails_seen = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+        const Unit u = decode(p, w);
+        for (int j = 0; j < u.count() && ok; ++j) {
+          const uint32_t s = vn % KV_STAGES, tile = base + SM_V + s * TILE_BYTES;
+          if (vn >= KV_STAGES) ok = warp_wait(bar(STEP0 + ((vn - 1) & 1u)), ((vn - 1) >> 1) & 1u, abort, limit);
+          if (!ok) break;
+          // Past kv_tokens the copy itself fills with zeros; rows between the last visible key and
+          // there are zeroed here, before the tile is handed on.
+          const int n = u.keys_of(j);
+          const bool patch = n < TILE && u.keys < p.a.kv_tokens;
+          const uint32_t full = patch ? bar(V_TAIL) : bar(V_FULL0 + s);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full, TILE_BYTES);
+            tma_load_5d(tile, &tm_v, full, 0, (u.t0 + j) * TILE, u.kh, 0, p.a.v.batch ? u.b : 0);
+          }
+          __syncwarp();
+          if (patch) {
+            ++tails;
+            ok = warp_wait(full, (tails - 1) & 1u, abort, limit);
+            if (!ok) break;
+            tails_seen = tails;
+            zero_rows(tile, n, ceil16(n), lane);
+            if (lane == 0) mbar_arrive(bar(V_FULL0 + s));
+          }
+          ++vn;
+        }
+      }
+      if (!ok && lane == 0) {
+        raise_abort(abort, p.a.err);
+        volatile int never = 0;
+        if (tails > tails_seen) mbar_wait_bounded(bar(V_TAIL), (tails - 1) & 1u, &never, DRAIN_LIMIT_NS);
+        for (uint32_t i = vn > KV_STAGES ? vn - KV_STAGES : 0; i < vn; ++i)
+          mbar_wait_bounded(bar(V_FULL0 + i % KV_STAGES), (i / KV_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
+      }
+      __syncwarp();
+    } else if (warp == MMA_WARP) {
+      // ------------------------------------------------------------------ UMMA issuer
+      // The whole warp runs this role in lockstep; one elected lane issues.
+      uint32_t x = 0;                                        // step: K tile x, V tile x - 1
+      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};  // per group: Q tiles, kv tiles, units
+      bool ok = true, issued = false;
+      // The products are negated (of A, bit 13) where the scale is negative.
+      const uint32_t idesc_s = IDESC_S0 | (p.a.sm_scale < 0.f ? 1u << 13 : 0u);
+      const uint64_t q_desc = sdesc_sw128(base + SM_Q, 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(base + SM_K, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(base + SM_V, TILE_BYTES / 2, 1024);
+      // The next unit with keys, from w on (total: none).
+      auto next_unit = [&](int w, Unit* u) {
+        for (; w < p.total; w += gridDim.x) {
+          *u = decode(p, w);
+          if (u->count() > 0) break;
+        }
+        return w;
+      };
+      // Step x: per group, O_g += P_g V with the kv tile of step x - 1 (pj of unit pu), then S_g of
+      // the step's own (j of unit u).  One copy of the code for both groups and all steps: the
+      // roles' code has to share the instruction caches, and with a copy per case this warp
+      // waited for its instructions longer than the tensor core for it.
+      Unit u{}, pu{};
+      int w = next_unit(blockIdx.x, &u), j = 0, pj = 0;
+      bool s = w < p.total, pv = false;  // S and P V of this step
+      while (s || pv) {
+        const uint32_t vx = x - 1;
+        const int pkeys = pv ? pu.keys_of(pj) : 0, psteps = ceil16(pkeys) / 16;
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          if (pv && (g == 0 || pu.second)) {
+            const uint32_t bars[3] = {bar(P_READY0 + g), bar(V_FULL0 + (vx & 1u)), bar(O_EMPTY0 + g)};
+            const uint32_t par[3] = {pn[g] & 1u, (vx >> 1) & 1u, (on[g] & 1u) ^ 1u};
+            const uint32_t need = pj == 0 ? 7u : 3u;
+            if (!(ok = warp_wait_n(bars, par, need, 0u, abort, limit) == need)) break;
+            tc_fence_after_sync();
+            const uint64_t vd = sdesc_advance(v_desc, (vx & 1u) * TILE_BYTES);
+            const uint32_t to = tmem + TM_O + g * 128u, pa = tmem + TM_S + g * 128u;
+#pragma unroll 1
+            for (int h = 0; h < 2 && h * 4 < psteps; ++h)
+              product_ts(to, pa + h * 32u, sdesc_advance(vd, h * 8192u), IDESC_PV, pj == 0 && h == 0 ? 0u : 1u,
+                         min(psteps - h * 4, 4));
+            ++pn[g];
+            if (pj + 1 == pu.count()) {
+              umma_commit_elect(bar(O_FULL0 + g));
+              ++on[g];
+            }
+          }
+          if (s && (g == 0 || u.second)) {
+            const uint32_t bars[2] = {bar(K_FULL0 + (x & 1u)), bar(Q_FULL0 + g)};
+            const uint32_t par[2] = {(x >> 1) & 1u, qn[g] & 1u};
+            const uint32_t need = j == 0 ? 3u : 1u;
+            if (!(ok = warp_wait_n(bars, par, need, 0u, abort, limit) == need)) break;
+            tc_fence_after_sync();
+            product_ss(tmem + TM_S + g * 128u, sdesc_advance(q_desc, g * TILE_BYTES),
+                       sdesc_advance(k_desc, (x & 1u) * TILE_BYTES),
+                       idesc_s | (static_cast<uint32_t>(ceil16(u.keys_of(j)) >> 3) << 17));
+            umma_commit_elect(bar(S_FULL0 + g));
+            if (j == 0) ++qn[g];
+            if (j + 1 == u.count()) umma_commit_elect(bar(Q_EMPTY0 + g));
+            issued = true;
+          }
+        }
+        if (!ok) break;
+        umma_commit_elect(bar(STEP0 + (x & 1u)));
+        ++x;
+        pv = s;
+        pu = u;
+        pj = j;
+        if (s && ++j == u.count()) {
+          w = next_unit(w + gridDim.x, &u);
+          j = 0;
+          s = w < p.total;
+        }
+      }
+      if (!ok && lane == 0) raise_abort(abort, p.a.err);
+      if (issued) {
+        // Every UMMA has completed before TMEM is released.
+        umma_commit_elect(bar(DRAIN));
+        volatile int never = 0;
+        if (lane == 0) mbar_wait_bounded(bar(DRAIN), 0, &never, DRAIN_LIMIT_NS);
+        __syncwarp();
+      }
+    }
   }
 
   tc_fence_before_sync();

@@ -393,6 +393,11 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One column: thread i of the warp writes lane (addr.lane + i).
+__device__ __forceinline__ void tmem_st_32x32b_x1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+}
+
 // The store counterparts of tmem_ld_32x32b_x32: thread i of the warp writes lane (addr.lane + i),
 // columns addr.col .. addr.col+15 (x16) or +31 (x32) from v.
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* v) {
