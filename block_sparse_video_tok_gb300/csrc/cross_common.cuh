@@ -10,6 +10,24 @@ namespace vsa {
 constexpr int TILE = 128;                        // rows of a query tile, keys of a kv tile
 constexpr uint32_t TILE_BYTES = TILE * 128 * 2;  // one operand tile: two column halves of 16 KB
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiply and a shift (the persistent kernels
+// decode their units in every role, and the code of a 32-bit division there counts): with
+// 2^s >= d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, m) + n) >> s.
+struct Divisor {
+  uint32_t d, m, s;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int quotient(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), m) + static_cast<uint32_t>(n)) >> s);
+  }
+#endif
+};
+inline Divisor make_divisor(uint32_t d) {
+  Divisor x{d, 0, 0};
+  while ((1ull << x.s) < d) ++x.s;
+  x.m = static_cast<uint32_t>((1ull << 32) * ((1ull << x.s) - d) / d + 1);
+  return x;
+}
+
 // Query rows in tiles.  From 128 tokens on, a tile is 128 tokens of one head.  Below, a tile
 // packs all tokens of `pack` neighbouring heads that read the same key head, so that the keys
 // are read once for them: row r is token r % box of head r / box.  pack divides the number of
@@ -44,56 +62,34 @@ cudaError_t make_tmap_heads(CUtensorMap* map, const HeadsView& x, int tokens, in
 
 #ifdef __CUDACC__
 
+// x, which all lanes hold alike, in a form that the compiler knows to be the same for the whole
+// warp: what depends on it alone stays in uniform registers, where the tensor-core instructions
+// take their operands from.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Wait of a converged warp for the phase of `bar` with the given parity; false if *abort was
 // raised or `limit_ns` of wall time passed.  Every lane polls, and the clock and *abort are looked
 // at once in POLLS probes: reading the global timer between probes held a warp for hundreds of
-// cycles after its barrier had completed (a hand-over from tensor core to softmax took 700).
+// cycles after its barrier had completed.  The loop is a function of its own, not a copy in each
+// of some twenty places: the code of all roles shares the instruction caches.
 constexpr int POLLS = 64;
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          uint64_t limit_ns) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    uint64_t t0 = 0;
-    while (true) {
-      int i = 0;
-      do {
-        ok = mbar_try_wait(bar, parity);
-      } while (!ok && ++i < POLLS);
-      if (ok || *abort) break;
-      const uint64_t t = globaltimer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > limit_ns) break;
-    }
+static __device__ __noinline__ bool warp_poll(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  while (true) {
+    bool ok;
+    int i = 0;
+    do {
+      ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+    } while (!ok && ++i < POLLS);
+    if (ok) return true;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (__any_sync(0xffffffffu, *abort != 0 || t - t0 > limit_ns)) return false;
   }
-  return __all_sync(0xffffffffu, ok);
 }
-
-// warp_wait on several barriers at once: waits for those whose bit is set in `need`, and probes
-// those in `probe` once.  The probes go out together, so their round trips overlap.  Returns the
-// bits of the completed ones for all lanes; a missing bit of `need` means abort or timeout.
-template <int N>
-__device__ __forceinline__ uint32_t warp_wait_n(const uint32_t (&bar)[N], const uint32_t (&parity)[N], uint32_t need,
-                                                uint32_t probe, volatile int* abort, uint64_t limit_ns) {
-  uint32_t done = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (((need | probe) >> i) & 1u) done |= mbar_try_wait(bar[i], parity[i]) ? 1u << i : 0u;
-  if ((done & need) != need) {
-    uint64_t t0 = 0;
-    while (true) {
-      int k = 0;
-      do {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (((need & ~done) >> i) & 1u) done |= mbar_try_wait(bar[i], parity[i]) ? 1u << i : 0u;
-      } while ((done & need) != need && ++k < POLLS);
-      if ((done & need) == need || *abort) break;
-      const uint64_t t = globaltimer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > limit_ns) break;
-    }
-  }
-  return __reduce_and_sync(0xffffffffu, done);
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_poll(bar, parity, abort, limit_ns);
 }
 
 __device__ __forceinline__ void raise_abort(volatile int* abort, uint32_t* err) {

@@ -15,9 +15,9 @@
 // bf16; l adds up the unrounded values.  The rounding is of the size of O's own (2^-9 relative,
 // independent per key).
 //
-// The last kv tile multiplies only ceil16(keys left) columns; its other columns are masked in
-// registers, and rows of V past the last key, which may hold anything, are zeroed in shared
-// memory before P (0 there) meets them.
+// The last kv tile multiplies only as many columns as have keys (S in steps of 16, P V of 64);
+// scores past the last key are overwritten with -inf, and rows of V past it, which may hold
+// anything, are zeroed in shared memory before P (0 there) meets them.
 //
 // When there are fewer units than SMs the keys are split: each part leaves its unnormalised O
 // and (m, l) in the workspace, and cross_combine_kernel joins them in part order.
@@ -82,6 +82,7 @@ struct Params {
   int pairs;   // units along the tiles of one (batch, key head)
   int splits;  // parts of the keys
   int total;   // units * splits
+  Divisor by_pairs, by_kv_heads, by_batch, by_splits, by_blocks;
   float* part_o;    // [split][batch * kv_heads * tiles][128 columns][128 rows]
   float2* part_ml;  // [split][batch * kv_heads * tiles][128 rows]
 };
@@ -98,16 +99,16 @@ struct Unit {
 
 __device__ __forceinline__ Unit decode(const Params& p, int w) {
   Unit u;
-  const int x = w % p.pairs;
-  w /= p.pairs;
-  u.kh = w % p.a.kv_heads;
-  w /= p.a.kv_heads;
-  u.b = w % p.a.batch;
-  u.split = w / p.a.batch;
-  u.tile0 = 2 * x;
-  u.second = 2 * x + 1 < p.t.tiles;
-  u.keys = visible_keys(p.a.kv_len, u.b, p.a.kv_tokens, p.a.err);
-  const int n = (u.keys + TILE - 1) / TILE, per = (n + p.splits - 1) / p.splits;
+  int q = p.by_pairs.quotient(w);
+  u.tile0 = 2 * (w - q * p.pairs);
+  w = q;
+  q = p.by_kv_heads.quotient(w);
+  u.kh = w - q * p.a.kv_heads;
+  u.split = p.by_batch.quotient(q);
+  u.b = q - u.split * p.a.batch;
+  u.second = u.tile0 + 1 < p.t.tiles;
+  u.keys = uniform(visible_keys(p.a.kv_len, u.b, p.a.kv_tokens, p.a.err));
+  const int n = (u.keys + TILE - 1) / TILE, per = p.by_splits.quotient(n + p.splits - 1);
   u.t0 = min(u.split * per, n);
   u.t1 = min(u.t0 + per, n);
   return u;
@@ -116,12 +117,13 @@ __device__ __forceinline__ Unit decode(const Params& p, int w) {
 // First head and token of tile `tile` of the unit's (batch, key head).
 __device__ __forceinline__ void tile_origin(const Params& p, const Unit& u, int tile, int* head,
                                             int* token) {
-  const int g = tile / p.t.blocks;
+  const int g = p.by_blocks.quotient(tile);
   *head = u.kh * p.t.share + g * p.t.pack;
   *token = (tile - g * p.t.blocks) * p.t.box;
 }
 
 __device__ __forceinline__ int ceil16(int n) { return (n + 15) & ~15; }
+__device__ __forceinline__ int ceil64(int n) { return (n + 63) & ~63; }
 
 // max(m, x) over 32 raw scores: two chains of 3-input instructions.
 __device__ __forceinline__ float max32(const uint32_t* x, float m) {
@@ -142,9 +144,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + SM_ABORT);
-  const uint32_t* tmem_slot = reinterpret_cast<const uint32_t*>(gbase + SM_TMEM_SLOT);
   auto bar = [&](uint32_t b) { return base + SM_BAR + 8u * b; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint64_t limit = p.a.wait_ns;
 
   if (threadIdx.x == 0) {
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they start at 0
   const uint32_t tile_rows_bytes = static_cast<uint32_t>(p.t.box * p.t.pack) * 256u;
 
   if (warp >= SOFTMAX_WARP && warp < OUT_WARP) {
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // Two passes over S in chunks of 32 columns, each chunk's load in flight while the one
         // before is worked on.  The loops stay rolled: unrolled over the 128 columns they took 524
         // us where they now take 400 (131040 x 512, 12 heads), waiting for instructions.
-        const int n = u.keys_of(j), cols = (n + 63) & ~63;
+        const int n = u.keys_of(j), cols = ceil64(n);
         if (n < cols) {
 #pragma unroll 1
           for (int c = n; c < cols; ++c) tmem_st_32x32b_x1(t_s + c, 0xff800000u);
@@ -278,98 +279,95 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else if (warp >= OUT_WARP) {
     // ------------------------------------------------------------------ output
+    // Row r of a tile lies at the same distance from its first row in every tile.
     const int quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_o = (static_cast<uint32_t>(quarter * 32) << 16) + TM_O;
     const uint32_t stage = base + SM_OUT + quarter * 4096u;  // this warp's 32 rows x 64 columns
-    uint32_t on[2] = {0, 0};
+    int64_t to[8];  // of rows 4 i + lane / 8 of the warp, and the lane's 8 columns
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = quarter * 32 + i * 4 + (lane >> 3), h = x / p.t.box;
+      to[i] = h * p.a.o.head + (x - h * p.t.box) * p.a.o.token + (lane & 7) * 8;
+    }
+    const int64_t lse_at = static_cast<int64_t>(r / p.t.box) * p.a.q_tokens + r % p.t.box;
+    uint32_t on = 0;  // units of each group, a bit each
     bool ok = true;
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
-      for (int g = 0; g < (u.second ? 2 : 1) && ok; ++g) {
+#pragma unroll 1
+      for (int g = 0; g < (u.second ? 2 : 1); ++g) {
         int head, token;
         tile_origin(p, u, u.tile0 + g, &head, &token);
-        const int rh = r / p.t.box;
-        head += rh;
-        token += r - rh * p.t.box;
-        const bool valid = rh < p.t.pack && token < p.a.q_tokens;
-        const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token;
-        const int64_t ptile =
-            ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile0 + g;
-        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch + head * p.a.o.head +
-                              token * p.a.o.token;
-        if (u.count() == 0) {
-          if (!valid) continue;
-          if (p.splits > 1) {
-            p.part_ml[ptile * TILE + r] = make_float2(-INFINITY, 0.f);
-            continue;
-          }
-          for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0u, 0u, 0u, 0u);
-          p.a.lse[row] = -INFINITY;
-          continue;
+        const int rows = p.t.pack > 1 ? p.t.pack * p.t.box : min(p.t.box, p.a.q_tokens - token);
+        float* lse = p.a.lse + (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token + lse_at;
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch + head * p.a.o.head +
+                           token * p.a.o.token;
+        const int64_t part =
+            (((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile0 + g) * TILE;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (u.count() > 0) {
+          ok = warp_wait(bar(ML_READY0 + g), (on >> g) & 1u, abort, limit) &&
+               warp_wait(bar(O_FULL0 + g), (on >> g) & 1u, abort, limit);
+          if (!ok) break;
+          on ^= 1u << g;
+          tc_fence_after_sync();
+          ml = reinterpret_cast<const float2*>(gbase + SM_ML)[g * TILE + r];
         }
-        ok = warp_wait(bar(ML_READY0 + g), on[g] & 1u, abort, limit) &&
-             warp_wait(bar(O_FULL0 + g), on[g] & 1u, abort, limit);
-        if (!ok) break;
-        ++on[g];
-        tc_fence_after_sync();
-        const float2 ml = reinterpret_cast<const float2*>(gbase + SM_ML)[g * TILE + r];
-        const uint32_t t_o = tmem + lane_off + TM_O + g * 128u;
         if (p.splits > 1) {
-          if (valid) p.part_ml[ptile * TILE + r] = ml;
-          float* po = p.part_o + ptile * TILE * TILE + r;
+          if (r < rows) p.part_ml[part + r] = ml;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t ov[32];
-            tmem_ld_32x32b_x32(t_o + c * 32u, ov);
+          for (int c = 0; c < TILE && u.count() > 0; c += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(t_o + g * 128u + c, v);
             tmem_wait_ld();
-            if (valid) {
+            float* po = p.part_o + (part + c) * TILE + r;
+            if (r < rows) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) po[(c * 32 + i) * TILE] = __uint_as_float(ov[i]);
+              for (int i = 0; i < 16; ++i) po[i * TILE] = __uint_as_float(v[i]);
             }
           }
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(O_EMPTY0 + g));
-          continue;
-        }
-        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-        const uint64_t inv2 = f2_pack(inv, inv);
-        const unsigned rows = __ballot_sync(0xffffffffu, valid);
-        if (valid) p.a.lse[row] = ml.x + log2f(ml.y);
+        } else {
+          if (r < rows) *lse = ml.x + log2f(ml.y);
+          const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+          const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {  // column halves of 64, through the warp's staging rows
+          for (int h = 0; h < 2; ++h) {  // column halves of 64, through the warp's staging rows
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t ov[32];
-            tmem_ld_32x32b_x32(t_o + h * 64u + c * 32u, ov);
-            tmem_wait_ld();
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[32];
+              if (u.count() > 0) {
+                tmem_ld_32x32b_x32(t_o + g * 128u + h * 64u + c * 32u, v);
+                tmem_wait_ld();
+              } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                float a0, a1;
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(ov[8 * i + 2 * x]), __uint_as_float(ov[8 * i + 2 * x + 1])), inv2),
-                          a0, a1);
-                pk[x] = pack_bf162(a0, a1);
+                for (int i = 0; i < 32; ++i) v[i] = 0u;
               }
-              st_shared16(stage + swizzled(lane, c * 4 + i), pk[0], pk[1], pk[2], pk[3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  float a0, a1;
+                  f2_unpack(f2_mul(f2_pack(__uint_as_float(v[8 * i + 2 * x]), __uint_as_float(v[8 * i + 2 * x + 1])), inv2),
+                            a0, a1);
+                  pk[x] = pack_bf162(a0, a1);
+                }
+                st_shared16(stage + swizzled(lane, c * 4 + i), pk[0], pk[1], pk[2], pk[3]);
+              }
             }
-          }
-          tc_fence_before_sync();
-          __syncwarp();
-          if (h == 1 && lane == 0) mbar_arrive(bar(O_EMPTY0 + g));
-          uint4 x[8];
+            __syncwarp();
+            uint4 x[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = ld_shared16(stage + swizzled(i * 4 + (lane >> 3), lane & 7));
-          __syncwarp();
+            for (int i = 0; i < 8; ++i) x[i] = ld_shared16(stage + swizzled(i * 4 + (lane >> 3), lane & 7));
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {  // four rows of 128 bytes at a time
-            const int rr = i * 4 + (lane >> 3);
-            const uint64_t to = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(orow), rr);
-            if ((rows >> rr) & 1u) reinterpret_cast<uint4*>(to)[h * 8 + (lane & 7)] = x[i];
+            for (int i = 0; i < 8; ++i)  // four rows of 128 bytes at a time
+              if (quarter * 32 + i * 4 + (lane >> 3) < rows) *reinterpret_cast<uint4*>(o + to[i] + h * 64) = x[i];
           }
         }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0 && u.count() > 0) mbar_arrive(bar(O_EMPTY0 + g));
       }
     }
     if (!ok && lane == 0) raise_abort(abort, p.a.err);
@@ -410,12 +408,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           __syncwarp();
           ++qn[g];
         }
-        if (ok && lane == 0 && w + gridDim.x < p.total) {
+        if (ok && w + gridDim.x < p.total) {
           const Unit nu = decode(p, w + gridDim.x);
           for (int g = 0; g < (nu.count() == 0 ? 0 : nu.second ? 2 : 1); ++g) {
             int head, token;
             tile_origin(p, nu, nu.tile0 + g, &head, &token);
-            for (int h = 0; h < halves; ++h) tma_prefetch_5d(&tm_q, 0, token, head, h, p.a.q.batch ? nu.b : 0);
+            if (lane == 0) {
+              for (int h = 0; h < halves; ++h) tma_prefetch_5d(&tm_q, 0, token, head, h, p.a.q.batch ? nu.b : 0);
+            }
           }
         }
         __syncwarp();
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ok = warp_wait(full, (tails - 1) & 1u, abort, limit);
             if (!ok) break;
             tails_seen = tails;
-            zero_rows(tile, n, ceil16(n), lane);
+            zero_rows(tile, n, ceil64(n), lane);
             if (lane == 0) mbar_arrive(bar(V_FULL0 + s));
           }
           ++vn;
@@ -498,21 +498,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool s = w < p.total, pv = false;  // S and P V of this step
       while (s || pv) {
         const uint32_t vx = x - 1;
-        const int pkeys = pv ? pu.keys_of(pj) : 0, psteps = ceil16(pkeys) / 16;
+        const int pkeys = pv ? pu.keys_of(pj) : 0;
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
           if (pv && (g == 0 || pu.second)) {
-            const uint32_t bars[3] = {bar(P_READY0 + g), bar(V_FULL0 + (vx & 1u)), bar(O_EMPTY0 + g)};
-            const uint32_t par[3] = {pn[g] & 1u, (vx >> 1) & 1u, (on[g] & 1u) ^ 1u};
-            const uint32_t need = pj == 0 ? 7u : 3u;
-            if (!(ok = warp_wait_n(bars, par, need, 0u, abort, limit) == need)) break;
+            ok = warp_wait(bar(P_READY0 + g), pn[g] & 1u, abort, limit) &&
+                 (g != 0 || warp_wait(bar(V_FULL0 + (vx & 1u)), (vx >> 1) & 1u, abort, limit)) &&
+                 (pj != 0 || warp_wait(bar(O_EMPTY0 + g), (on[g] & 1u) ^ 1u, abort, limit));
+            if (!ok) break;
             tc_fence_after_sync();
             const uint64_t vd = sdesc_advance(v_desc, (vx & 1u) * TILE_BYTES);
-            const uint32_t to = tmem + TM_O + g * 128u, pa = tmem + TM_S + g * 128u;
 #pragma unroll 1
-            for (int h = 0; h < 2 && h * 4 < psteps; ++h)
-              product_ts(to, pa + h * 32u, sdesc_advance(vd, h * 8192u), IDESC_PV, pj == 0 && h == 0 ? 0u : 1u,
-                         min(psteps - h * 4, 4));
+            for (int h = 0; h * 64 < pkeys; ++h)
+              product_ts64(tmem + TM_O + g * 128u, tmem + TM_S + g * 128u + h * 32u, sdesc_advance(vd, h * 8192u), IDESC_PV,
+                           static_cast<uint32_t>(pj | h));
             ++pn[g];
             if (pj + 1 == pu.count()) {
               umma_commit_elect(bar(O_FULL0 + g));
@@ -520,10 +519,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
           if (s && (g == 0 || u.second)) {
-            const uint32_t bars[2] = {bar(K_FULL0 + (x & 1u)), bar(Q_FULL0 + g)};
-            const uint32_t par[2] = {(x >> 1) & 1u, qn[g] & 1u};
-            const uint32_t need = j == 0 ? 3u : 1u;
-            if (!(ok = warp_wait_n(bars, par, need, 0u, abort, limit) == need)) break;
+            ok = (g != 0 || warp_wait(bar(K_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit)) &&
+                 (j != 0 || warp_wait(bar(Q_FULL0 + g), qn[g] & 1u, abort, limit));
+            if (!ok) break;
             tc_fence_after_sync();
             product_ss(tmem + TM_S + g * 128u, sdesc_advance(q_desc, g * TILE_BYTES),
                        sdesc_advance(k_desc, (x & 1u) * TILE_BYTES),
@@ -636,6 +634,11 @@ cudaError_t launch_cross_fwd(const CrossArgs& a, cudaStream_t stream) {
   p.pairs = plan.pairs;
   p.splits = plan.splits;
   p.total = a.batch * a.kv_heads * plan.pairs * plan.splits;
+  p.by_pairs = make_divisor(p.pairs);
+  p.by_kv_heads = make_divisor(a.kv_heads);
+  p.by_batch = make_divisor(a.batch);
+  p.by_splits = make_divisor(p.splits);
+  p.by_blocks = make_divisor(p.t.blocks);
   p.part_o = reinterpret_cast<float*>(a.workspace);
   p.part_ml = reinterpret_cast<float2*>(a.workspace + plan.ml_off);
   CUtensorMap tq, tk, tv;
