@@ -89,7 +89,16 @@ static __device__ __noinline__ bool warp_poll(uint32_t bar, uint32_t parity, vol
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return warp_poll(bar, parity, abort, limit_ns);
+  // (The vote tells the compiler that the result is the same for all lanes.)
+  return __all_sync(0xffffffffu, warp_poll(bar, parity, abort, limit_ns));
+}
+
+// After an abort: the last `stages` of `count` copies, copy i counted on the barrier at full0 + 8
+// (i % stages), have landed (one thread; gives up after DRAIN_LIMIT_NS).
+static __device__ __noinline__ void drain_copies(uint32_t full0, uint32_t stages, uint32_t count) {
+  volatile int never = 0;
+  for (uint32_t i = count > stages ? count - stages : 0; i < count; ++i)
+    mbar_wait_bounded(full0 + 8u * (i % stages), (i / stages) & 1u, &never, DRAIN_LIMIT_NS);
 }
 
 __device__ __forceinline__ void raise_abort(volatile int* abort, uint32_t* err) {

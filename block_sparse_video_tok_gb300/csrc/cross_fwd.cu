@@ -375,60 +375,63 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else {
     if (warp == TMA_WARP) {
       // ------------------------------------------------------------------ TMA producer: Q, K
-      uint32_t qn[2] = {0, 0}, kn = 0;  // tiles loaded
+      uint32_t qn = 0, begun = 0, kn = 0;  // per group (a bit each): parity of the Q tiles, any; K tiles
       bool ok = true;
       const int halves = p.t.box * p.t.pack == TILE ? 1 : 2;  // copies of a Q tile
-      auto load_k = [&](const Unit& u, int j) {
-        const uint32_t s = kn % KV_STAGES;
-        if (!warp_wait(bar(STEP0 + s), ((kn / KV_STAGES) & 1u) ^ 1u, abort, limit)) return false;  // step kn - 2
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(K_FULL0 + s), TILE_BYTES);
-          tma_load_5d(base + SM_K + s * TILE_BYTES, &tm_k, bar(K_FULL0 + s), 0, (u.t0 + j) * TILE, u.kh, 0,
-                      p.a.k.batch ? u.b : 0);
-        }
-        __syncwarp();
-        ++kn;
-        return true;
-      };
-      for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-        const Unit u = decode(p, w);
-        if (u.count() == 0) continue;
-        ok = load_k(u, 0);
-        for (int g = 0; g < (u.second ? 2 : 1) && ok; ++g) {
-          ok = warp_wait(bar(Q_EMPTY0 + g), (qn[g] & 1u) ^ 1u, abort, limit);
+      Unit u{}, next{};
+      for (int w = blockIdx.x; ok; w += gridDim.x) {  // unit u, and the one after it
+        u = next;
+        next = w < p.total ? decode(p, w) : Unit{};
+        const int n = u.count();
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const uint32_t s = kn & 1u;
+          ok = warp_wait(bar(STEP0 + s), ((kn >> 1) & 1u) ^ 1u, abort, limit);  // step kn - 2
           if (!ok) break;
-          int head, token;
-          tile_origin(p, u, u.tile0 + g, &head, &token);
           if (lane == 0) {
-            mbar_arrive_expect_tx(bar(Q_FULL0 + g), tile_rows_bytes);
-            for (int h = 0; h < halves; ++h)
-              tma_load_5d(base + SM_Q + g * TILE_BYTES + h * (TILE_BYTES / 2), &tm_q, bar(Q_FULL0 + g), 0, token, head, h,
-                          p.a.q.batch ? u.b : 0);
+            mbar_arrive_expect_tx(bar(K_FULL0 + s), TILE_BYTES);
+            tma_load_5d(base + SM_K + s * TILE_BYTES, &tm_k, bar(K_FULL0 + s), 0, (u.t0 + j) * TILE, u.kh, 0,
+                        p.a.k.batch ? u.b : 0);
           }
           __syncwarp();
-          ++qn[g];
-        }
-        if (ok && w + gridDim.x < p.total) {
-          const Unit nu = decode(p, w + gridDim.x);
-          for (int g = 0; g < (nu.count() == 0 ? 0 : nu.second ? 2 : 1); ++g) {
-            int head, token;
-            tile_origin(p, nu, nu.tile0 + g, &head, &token);
-            if (lane == 0) {
-              for (int h = 0; h < halves; ++h) tma_prefetch_5d(&tm_q, 0, token, head, h, p.a.q.batch ? nu.b : 0);
+          ++kn;
+          if (j > 0) continue;
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {  // Q of both groups; then the next unit's, into L2
+            const int g = x & 1;
+            const Unit& v = x < 2 ? u : next;
+            if (v.count() == 0 || (g == 1 && !v.second)) continue;
+            if (x < 2) {
+              ok = warp_wait(bar(Q_EMPTY0 + g), ((qn >> g) & 1u) ^ 1u, abort, limit);
+              if (!ok) break;
+              qn ^= 1u << g;
+              begun |= 1u << g;
             }
+            int head, token;
+            tile_origin(p, v, v.tile0 + g, &head, &token);
+            if (lane == 0) {
+              if (x < 2) mbar_arrive_expect_tx(bar(Q_FULL0 + g), tile_rows_bytes);
+#pragma unroll 1
+              for (int h = 0; h < halves; ++h) {
+                if (x < 2)
+                  tma_load_5d(base + SM_Q + g * TILE_BYTES + h * (TILE_BYTES / 2), &tm_q, bar(Q_FULL0 + g), 0, token,
+                              head, h, p.a.q.batch ? v.b : 0);
+                else
+                  tma_prefetch_5d(&tm_q, 0, token, head, h, p.a.q.batch ? v.b : 0);
+              }
+            }
+            __syncwarp();
           }
+          if (!ok) break;
         }
-        __syncwarp();
-        for (int j = 1; j < u.count() && ok; ++j) ok = load_k(u, j);
+        if (w >= p.total) break;
       }
       if (!ok && lane == 0) {
         raise_abort(abort, p.a.err);
         // Let the copies already issued land before the CTA's shared memory goes away.
-        volatile int never = 0;
-        for (int g = 0; g < 2; ++g)
-          if (qn[g] > 0) mbar_wait_bounded(bar(Q_FULL0 + g), (qn[g] - 1) & 1u, &never, DRAIN_LIMIT_NS);
-        for (uint32_t i = kn > KV_STAGES ? kn - KV_STAGES : 0; i < kn; ++i)
-          mbar_wait_bounded(bar(K_FULL0 + i % KV_STAGES), (i / KV_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
+        drain_copies(bar(K_FULL0), KV_STAGES, kn);
+        if (begun & 1u) drain_copies(bar(Q_FULL0), 1, (qn & 1u) ? 1 : 2);
+        if (begun & 2u) drain_copies(bar(Q_FULL0 + 1), 1, (qn & 2u) ? 1 : 2);
       }
       __syncwarp();
     } else if (warp == V_WARP) {
@@ -464,47 +467,47 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok && lane == 0) {
         raise_abort(abort, p.a.err);
-        volatile int never = 0;
-        if (tails > tails_seen) mbar_wait_bounded(bar(V_TAIL), (tails - 1) & 1u, &never, DRAIN_LIMIT_NS);
-        for (uint32_t i = vn > KV_STAGES ? vn - KV_STAGES : 0; i < vn; ++i)
-          mbar_wait_bounded(bar(V_FULL0 + i % KV_STAGES), (i / KV_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
+        if (tails > tails_seen) drain_copies(bar(V_TAIL), 1, tails);
+        drain_copies(bar(V_FULL0), KV_STAGES, vn);
       }
       __syncwarp();
     } else if (warp == MMA_WARP) {
       // ------------------------------------------------------------------ UMMA issuer
       // The whole warp runs this role in lockstep; one elected lane issues.
-      uint32_t x = 0;                                        // step: K tile x, V tile x - 1
-      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};  // per group: Q tiles, kv tiles, units
+      uint32_t x = 0;                    // step: K tile x, V tile x - 1
+      uint32_t qn = 0, pn = 0, on = 0;   // parity of Q tiles, kv tiles and units, a bit per group
       bool ok = true, issued = false;
       // The products are negated (of A, bit 13) where the scale is negative.
       const uint32_t idesc_s = IDESC_S0 | (p.a.sm_scale < 0.f ? 1u << 13 : 0u);
       const uint64_t q_desc = sdesc_sw128(base + SM_Q, 16, 1024);
       const uint64_t k_desc = sdesc_sw128(base + SM_K, 16, 1024);
       const uint64_t v_desc = sdesc_sw128(base + SM_V, TILE_BYTES / 2, 1024);
-      // The next unit with keys, from w on (total: none).
-      auto next_unit = [&](int w, Unit* u) {
-        for (; w < p.total; w += gridDim.x) {
-          *u = decode(p, w);
-          if (u->count() > 0) break;
-        }
-        return w;
-      };
       // Step x: per group, O_g += P_g V with the kv tile of step x - 1 (pj of unit pu), then S_g of
       // the step's own (j of unit u).  One copy of the code for both groups and all steps: the
       // roles' code has to share the instruction caches, and with a copy per case this warp
       // waited for its instructions longer than the tensor core for it.
       Unit u{}, pu{};
-      int w = next_unit(blockIdx.x, &u), j = 0, pj = 0;
-      bool s = w < p.total, pv = false;  // S and P V of this step
-      while (s || pv) {
+      int w = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x), j = 0, pj = 0;
+      bool pv = false;  // P V of this step; S: unless w is past the last unit
+      while (true) {
+        if (j == u.count()) {  // to the next unit with keys
+          j = 0;
+#pragma unroll 1
+          for (w += gridDim.x; w < p.total; w += gridDim.x) {
+            u = decode(p, w);
+            if (u.count() > 0) break;
+          }
+        }
+        const bool s = w < p.total;
+        if (!s && !pv) break;
         const uint32_t vx = x - 1;
         const int pkeys = pv ? pu.keys_of(pj) : 0;
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
           if (pv && (g == 0 || pu.second)) {
-            ok = warp_wait(bar(P_READY0 + g), pn[g] & 1u, abort, limit) &&
+            ok = warp_wait(bar(P_READY0 + g), (pn >> g) & 1u, abort, limit) &&
                  (g != 0 || warp_wait(bar(V_FULL0 + (vx & 1u)), (vx >> 1) & 1u, abort, limit)) &&
-                 (pj != 0 || warp_wait(bar(O_EMPTY0 + g), (on[g] & 1u) ^ 1u, abort, limit));
+                 (pj != 0 || warp_wait(bar(O_EMPTY0 + g), ((on >> g) & 1u) ^ 1u, abort, limit));
             if (!ok) break;
             tc_fence_after_sync();
             const uint64_t vd = sdesc_advance(v_desc, (vx & 1u) * TILE_BYTES);
@@ -512,22 +515,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int h = 0; h * 64 < pkeys; ++h)
               product_ts64(tmem + TM_O + g * 128u, tmem + TM_S + g * 128u + h * 32u, sdesc_advance(vd, h * 8192u), IDESC_PV,
                            static_cast<uint32_t>(pj | h));
-            ++pn[g];
+            pn ^= 1u << g;
             if (pj + 1 == pu.count()) {
               umma_commit_elect(bar(O_FULL0 + g));
-              ++on[g];
+              on ^= 1u << g;
             }
           }
           if (s && (g == 0 || u.second)) {
             ok = (g != 0 || warp_wait(bar(K_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit)) &&
-                 (j != 0 || warp_wait(bar(Q_FULL0 + g), qn[g] & 1u, abort, limit));
+                 (j != 0 || warp_wait(bar(Q_FULL0 + g), (qn >> g) & 1u, abort, limit));
             if (!ok) break;
             tc_fence_after_sync();
             product_ss(tmem + TM_S + g * 128u, sdesc_advance(q_desc, g * TILE_BYTES),
                        sdesc_advance(k_desc, (x & 1u) * TILE_BYTES),
                        idesc_s | (static_cast<uint32_t>(ceil16(u.keys_of(j)) >> 3) << 17));
             umma_commit_elect(bar(S_FULL0 + g));
-            if (j == 0) ++qn[g];
+            if (j == 0) qn ^= 1u << g;
             if (j + 1 == u.count()) umma_commit_elect(bar(Q_EMPTY0 + g));
             issued = true;
           }
@@ -537,12 +540,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++x;
         pv = s;
         pu = u;
-        pj = j;
-        if (s && ++j == u.count()) {
-          w = next_unit(w + gridDim.x, &u);
-          j = 0;
-          s = w < p.total;
-        }
+        pj = j++;
+        if (!s) break;
       }
       if (!ok && lane == 0) raise_abort(abort, p.a.err);
       if (issued) {
