@@ -24,15 +24,16 @@ namespace vsa {
 
 namespace {
 
-constexpr int NUM_THREADS = 384;  // warps are allocated in fours: the twelfth has no role
-constexpr int SOFTMAX_WARPS = 8;
+// 20 warps: 0 TMEM owner and TMA producer, 1 UMMA issuer, 2 a second producer, 3 idle, 4-19 softmax.
+// Softmax warp (quarter, col) has rows 32 quarter .. + 31 of a tile of scores, one per lane, and
+// columns 32 col .. + 31.
+constexpr int NUM_THREADS = 640;
+constexpr int SOFTMAX_WARP = 4, SOFTMAX_WARPS = 16;
 constexpr uint32_t IDESC_S0 = idesc_f16_f32acc(128, 0, false, false, true);  // N is added
 constexpr uint32_t IDESC_ACC = idesc_f16_f32acc(128, 128, false, true, true);
 
-__device__ __forceinline__ int ceil16(int n) { return (n + 15) & ~15; }
-__device__ __forceinline__ uint32_t idesc_s(int n) {
-  return IDESC_S0 | (static_cast<uint32_t>(ceil16(n) >> 3) << 17);
-}
+__device__ __forceinline__ int ceil64(int n) { return (n + 63) & ~63; }
+__device__ __forceinline__ uint32_t idesc_s(int n) { return IDESC_S0 | (static_cast<uint32_t>(n >> 3) << 17); }
 
 struct Params {
   CrossArgs a;
@@ -40,49 +41,57 @@ struct Params {
   int kv_tiles;  // of kv_tokens
   int splits;    // parts of the inner axis
   int total;     // units
+  Divisor by_tiles, by_kv_tiles, by_kv_heads, by_batch, by_splits, by_blocks;
   float* delta;  // [batch, heads, q_tokens]
   float* part;   // dq: [split][batch * kv_heads * tiles][128 columns][128 rows];
                  // dkv: [split][batch * kv_heads * kv_tiles][dV, dK][128 columns][128 keys]
 };
 
-// D (+)= A B: A of 16-bit pairs in tensor memory, `steps` of 16 along its columns (8 TMEM columns
-// each; step 4 starts `half` columns after step 0), B an MN-major tile.
-__device__ __forceinline__ void product_acc(uint32_t d, uint32_t a, uint32_t half, uint64_t b, bool fresh, int steps) {
-  product_ts(d, a, b, IDESC_ACC, fresh ? 0u : 1u, min(steps, 4));
-  if (steps > 4) product_ts(d, a + half, sdesc_advance(b, 8192u), IDESC_ACC, 1u, steps - 4);
+__device__ __forceinline__ void load32(uint32_t taddr, uint32_t* v) {
+  tmem_ld_32x32b_x32(taddr, v);
+  tmem_wait_ld();
 }
 
-// A warp's 32 rows x 64 fp32 columns (one row per lane), scaled and rounded, to global memory in
-// whole lines through 4 KB of shared memory; `out` is each lane's row, written where `rows` has its bit.
+// A softmax warp's 32 rows x 32 columns of sums, scaled and rounded, to global memory: through 2
+// KB of shared memory, so that 64 consecutive bytes of a row leave together.  `at`: distance of
+// rows 8 i + lane / 4 from `out`, in elements; rows from `rows` on are not written.
 __device__ __forceinline__ void write_rows(uint32_t stage, const uint32_t* v, float scale, __nv_bfloat16* out,
-                                           unsigned rows, int lane) {
+                                           const int64_t* at, int rows, int lane) {
   const uint64_t s2 = f2_pack(scale, scale);
+  const uint32_t row = stage + lane * 64u, x = (lane >> 1) & 3u;  // chunks of 16 bytes, swizzled by row
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     uint32_t pk[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int k = 0; k < 4; ++k) {
       float a0, a1;
-      f2_unpack(f2_mul(f2_pack(__uint_as_float(v[8 * i + 2 * x]), __uint_as_float(v[8 * i + 2 * x + 1])), s2), a0, a1);
-      pk[x] = pack_bf162(a0, a1);
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(v[8 * i + 2 * k]), __uint_as_float(v[8 * i + 2 * k + 1])), s2), a0, a1);
+      pk[k] = pack_bf162(a0, a1);
     }
-    st_shared16(stage + swizzled(lane, i), pk[0], pk[1], pk[2], pk[3]);
+    st_shared16(row + ((i ^ x) << 4), pk[0], pk[1], pk[2], pk[3]);
+  }
+  __syncwarp();
+  uint4 w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t rr = i * 8 + (lane >> 2);
+    w[i] = ld_shared16(stage + rr * 64u + (((lane & 3u) ^ ((rr >> 1) & 3u)) << 4));
   }
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int rr = i * 4 + (lane >> 3);
-    const uint64_t to = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), rr);
-    const uint4 x = ld_shared16(stage + swizzled(rr, lane & 7));
-    if ((rows >> rr) & 1u) reinterpret_cast<uint4*>(to)[lane & 7] = x;
-  }
-  __syncwarp();
+  for (int i = 0; i < 4; ++i)
+    if (i * 8 + (lane >> 2) < rows) reinterpret_cast<uint4*>(out + at[i])[lane & 3] = w[i];
 }
 
-__device__ __forceinline__ void load64(uint32_t taddr, uint32_t* v) {
-  tmem_ld_32x32b_x32(taddr, v);
-  tmem_ld_32x32b_x32(taddr + 32u, v + 32);
-  tmem_wait_ld();
+// First head and token of a query tile, and how many rows it has (fewer in the last block of a
+// head's tokens).
+__device__ __forceinline__ void tile_origin(const Params& p, int kh, int tile, int* head, int* token) {
+  const int g = p.by_blocks.quotient(tile);
+  *head = kh * p.t.share + g * p.t.pack;
+  *token = (tile - g * p.t.blocks) * p.t.box;
+}
+__device__ __forceinline__ int tile_rows(const Params& p, int token) {
+  return p.t.pack > 1 ? p.t.pack * p.t.box : min(p.t.box, p.a.q_tokens - token);
 }
 
 // Row (head, token) of row r of a query tile, and whether it exists.
@@ -99,13 +108,12 @@ __device__ __forceinline__ QRow q_row(const Params& p, int kh, int tile, int r) 
   return x;
 }
 
-// One query-side tile (rows packed as in QTiles) into shared memory, by one thread.
+// One query-side tile into shared memory, by one thread.
 __device__ __forceinline__ void load_q_tile(const Params& p, const CUtensorMap* map, int64_t batch_stride, uint32_t dst,
-                                            uint32_t full, int b, int kh, int tile) {
-  const int g = tile / p.t.blocks;
-  const int head = kh * p.t.share + g * p.t.pack, token = (tile - g * p.t.blocks) * p.t.box;
+                                            uint32_t full, int b, int head, int token) {
   const int rows = p.t.box * p.t.pack;
   mbar_arrive_expect_tx(full, static_cast<uint32_t>(rows) * 256u);
+#pragma unroll 1
   for (int h = 0; h < (rows == TILE ? 1 : 2); ++h)
     tma_load_5d(dst + h * (TILE_BYTES / 2), map, full, 0, token, head, h, batch_stride ? b : 0);
 }
@@ -118,21 +126,20 @@ namespace dq {
 // three of them; a V tile serves one product.
 constexpr int K_STAGES = 3;
 constexpr uint32_t SM_Q = 0, SM_DO = TILE_BYTES, SM_K = 2 * TILE_BYTES, SM_V = SM_K + K_STAGES * TILE_BYTES;
-constexpr uint32_t SM_OUT = SM_V + TILE_BYTES;       // 8 warps x 4 KB
-constexpr uint32_t SM_XCH = SM_OUT + TILE_BYTES;     // [column half][128 rows] fp32
-constexpr uint32_t SM_BAR = SM_XCH + 2 * TILE * 4;
+constexpr uint32_t SM_OUT = SM_V + TILE_BYTES;    // 16 warps x 2 KB
+constexpr uint32_t SM_XCH = SM_OUT + TILE_BYTES;  // [128 rows][4 column groups] fp32
+constexpr uint32_t SM_BAR = SM_XCH + 4 * TILE * 4;
 enum Bar : uint32_t {
   Q_FULL = 0,
   Q_EMPTY,
   DO_FULL,
-  DO_EMPTY,  // the tensor core and the 8 warps that sum O dO
+  DO_EMPTY,  // the tensor core and the warps that sum O dO
   K_FULL0,
   K_EMPTY0 = K_FULL0 + K_STAGES,
   V_FULL = K_EMPTY0 + K_STAGES,
-  V_EMPTY,
   S_FULL,
-  S_FREE,  // S has been read
-  DP_FULL,
+  S_FREE,   // S has been read
+  DP_FULL,  // (and the V tile is free)
   DP_FREE,
   DS_READY0,  // two buffers
   DQ_FULL = DS_READY0 + 2,
@@ -144,7 +151,7 @@ enum Bar : uint32_t {
 };
 constexpr uint32_t SM_TMEM_SLOT = SM_BAR + NUM_BARS * 8;
 constexpr uint32_t SM_ABORT = SM_TMEM_SLOT + 4;
-constexpr uint32_t SMEM_BYTES = SM_ABORT + 4 + 1024;
+constexpr uint32_t SMEM_BYTES = SM_ABORT + 4;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 256, TM_DS = 384;  // dS: two buffers of 64 columns
 
@@ -156,39 +163,29 @@ struct Unit {
 
 __device__ __forceinline__ Unit decode(const Params& p, int w) {
   Unit u;
-  u.tile = w % p.t.tiles;
-  w /= p.t.tiles;
-  u.kh = w % p.a.kv_heads;
-  w /= p.a.kv_heads;
-  u.b = w % p.a.batch;
-  u.split = w / p.a.batch;
-  u.keys = visible_keys(p.a.kv_len, u.b, p.a.kv_tokens, p.a.err);
-  const int n = (u.keys + TILE - 1) / TILE, per = (n + p.splits - 1) / p.splits;
+  int q = p.by_tiles.quotient(w);
+  u.tile = w - q * p.t.tiles;
+  w = q;
+  q = p.by_kv_heads.quotient(w);
+  u.kh = w - q * p.a.kv_heads;
+  u.split = p.by_batch.quotient(q);
+  u.b = q - u.split * p.a.batch;
+  u.keys = uniform(visible_keys(p.a.kv_len, u.b, p.a.kv_tokens, p.a.err));
+  const int n = (u.keys + TILE - 1) / TILE, per = p.by_splits.quotient(n + p.splits - 1);
   u.t0 = min(u.split * per, n);
   u.t1 = min(u.t0 + per, n);
   return u;
-}
-
-__device__ __forceinline__ int next_unit(const Params& p, int w, Unit* u) {
-  for (; w < p.total; w += gridDim.x) {
-    *u = decode(p, w);
-    if (u->count() > 0) break;
-  }
-  return w;
 }
 
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
-  volatile int* abort = reinterpret_cast<volatile int*>(gbase + SM_ABORT);
-  const uint32_t* tmem_slot = reinterpret_cast<const uint32_t*>(gbase + SM_TMEM_SLOT);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + SM_ABORT);
   auto bar = [&](uint32_t b) { return base + SM_BAR + 8u * b; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint64_t limit = p.a.wait_ns;
 
   if (threadIdx.x == 0) {
@@ -197,12 +194,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t count = 1;
       if (b == S_FREE || b == DP_FREE || b == DS_READY0 || b == DS_READY0 + 1 || b == DQ_EMPTY) count = SOFTMAX_WARPS;
       if (b == DO_EMPTY) count = SOFTMAX_WARPS + 1;
-      if (b >= XCH0 && b < K_TAIL) count = 2;
+      if (b >= XCH0 && b < K_TAIL) count = 4;
       mbar_init(bar(b), count);
     }
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == 0) {
     tmem_alloc(base + SM_TMEM_SLOT, 512);
     tmem_relinquish();
     if (lane == 0) {
@@ -216,27 +213,172 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they start at 0
 
-  if (warp == 8) {
-    // ------------------------------------------------------------------ TMA producer: Q, dO, V
-    uint32_t qn = 0, dn = 0, vn = 0;
+  if (warp >= SOFTMAX_WARP) {
+    // ------------------------------------------------------------------ P, dS, Delta, output
+    const int quarter = warp & 3, col = (warp - SOFTMAX_WARP) >> 2, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t t_s = lanes + TM_S + col * 32u, t_dp = lanes + TM_DP + col * 32u;
+    const uint32_t t_ds = lanes + TM_DS + col * 16u, t_dq = lanes + TM_DQ + col * 32u;
+    const uint32_t stage = base + SM_OUT + (warp - SOFTMAX_WARP) * 2048u;
+    float* xch = reinterpret_cast<float*>(smem + SM_XCH);
+    const float c1 = p.a.sm_scale * LOG2E_F;
+    const uint64_t c2 = f2_pack(c1, c1);
+    // Rows 8 i + lane / 4 of the warp lie at the same distance from the first in every tile.
+    int64_t out_at[4], o_at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int y = quarter * 32 + i * 8 + (lane >> 2), h = y / p.t.box, t = y - h * p.t.box;
+      out_at[i] = h * p.a.dq.head + t * p.a.dq.token;
+      o_at[i] = h * p.a.o.head + t * p.a.o.token;
+    }
+    const int64_t lse_at = static_cast<int64_t>(r / p.t.box) * p.a.q_tokens + r % p.t.box;
+    uint32_t x = 0, un = 0;
     bool ok = true;
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
-      if (u.count() == 0) continue;
-      ok = warp_wait(bar(Q_EMPTY), (qn & 1u) ^ 1u, abort, limit);
+      int head, token;
+      tile_origin(p, u.kh, u.tile, &head, &token);
+      const int rows = tile_rows(p, token);
+      const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token + lse_at;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.dq.data) + u.b * p.a.dq.batch + head * p.a.dq.head +
+                           token * p.a.dq.token + col * 32;
+      uint32_t v[32];
+      if (u.count() == 0) {  // (with several parts the join kernel writes)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0u;
+        if (p.splits == 1) write_rows(stage, v, 1.f, out, out_at, rows - quarter * 32, lane);
+        continue;
+      }
+      const float lse = r < rows ? p.a.lse[row] : 0.f;
+      // This warp's share of Delta: 32 columns of 8 rows at a time, 8 columns a lane.
+      const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch + head * p.a.o.head +
+                               token * p.a.o.token + col * 32 + (lane & 3) * 8;
+      uint4 ov[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        ov[i] = quarter * 32 + i * 8 + (lane >> 2) < rows ? *reinterpret_cast<const uint4*>(o + o_at[i])
+                                                          : make_uint4(0u, 0u, 0u, 0u);
+      ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit);
       if (!ok) break;
-      if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q, bar(Q_FULL), u.b, u.kh, u.tile);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int y = quarter * 32 + i * 8 + (lane >> 2);
+        const uint4 d = ld_shared16(base + SM_DO + (col >> 1) * (TILE_BYTES / 2) + swizzled(y, (col & 1) * 4 + (lane & 3)));
+        const uint32_t ow[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w}, dw[4] = {d.x, d.y, d.z, d.w};
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s = fmaf(__uint_as_float(ow[k] << 16), __uint_as_float(dw[k] << 16), s);
+          s = fmaf(__uint_as_float(ow[k] & 0xffff0000u), __uint_as_float(dw[k] & 0xffff0000u), s);
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        if ((lane & 3) == 0) xch[y * 4 + col] = s;
+      }
       __syncwarp();
-      ++qn;
-      ok = warp_wait(bar(DO_EMPTY), (dn & 1u) ^ 1u, abort, limit);
+      if (lane == 0) {
+        mbar_arrive(bar(DO_EMPTY));
+        mbar_arrive(bar(XCH0 + quarter));
+      }
+      ok = warp_wait(bar(XCH0 + quarter), un & 1u, abort, limit);
       if (!ok) break;
-      if (lane == 0) load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO, bar(DO_FULL), u.b, u.kh, u.tile);
-      __syncwarp();
-      ++dn;
+      // The next unit's sums come after this one's dQ, for which all four warps have read these.
+      const float4 parts = reinterpret_cast<const float4*>(xch)[r];
+      const float delta = (parts.x + parts.y) + (parts.z + parts.w);
+      if (col == 0 && r < rows && u.t0 == 0) p.delta[row] = delta;
+      const float nl = lse == -INFINITY ? 0.f : -lse;  // a row whose scores are all -inf: P = 2^-inf = 0
+      const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(-delta, -delta);
+#pragma unroll 1
       for (int j = 0; j < u.count(); ++j) {
-        ok = warp_wait(bar(V_EMPTY), (vn & 1u) ^ 1u, abort, limit);
+        ok = warp_wait(bar(S_FULL), x & 1u, abort, limit);
+        if (!ok) break;
+        tc_fence_after_sync();
+        load32(t_s, v);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S_FREE));
+        float pr[32];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float a0, a1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, nl2), a0, a1);
+          pr[i] = ex2(a0);
+          pr[i + 1] = ex2(a1);
+        }
+        ok = warp_wait(bar(DP_FULL), x & 1u, abort, limit);
+        if (!ok) break;
+        tc_fence_after_sync();
+        load32(t_dp, v);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(DP_FREE));
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float a0, a1;
+          f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), nd2),
+                           f2_pack(pr[i], pr[i + 1])),
+                    a0, a1);
+          pk[i >> 1] = pack_bf162(a0, a1);
+        }
+        const int n = u.keys_of(j) - col * 32;  // columns of the warp that are visible
+        if (__builtin_expect(n < 32, 0)) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = 2 * i + 1 < n ? pk[i] : 2 * i < n ? pk[i] & 0xffffu : 0u;
+        }
+        // The buffer's last reader, dQ of two steps ago, was issued before this dP.
+        tmem_st_32x32b_x16(t_ds + (x & 1u) * 64u, pk);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(DS_READY0 + (x & 1u)));
+        ++x;
+      }
+      if (!ok) break;
+      ok = warp_wait(bar(DQ_FULL), un & 1u, abort, limit);
+      if (!ok) break;
+      tc_fence_after_sync();
+      load32(t_dq, v);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(DQ_EMPTY));
+      if (p.splits == 1) {
+        write_rows(stage, v, p.a.sm_scale, out, out_at, rows - quarter * 32, lane);
+      } else if (r < rows) {
+        const int64_t at = ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile;
+        float* to = p.part + (at * TILE + col * 32) * TILE + r;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) to[i * TILE] = __uint_as_float(v[i]);
+      }
+      ++un;
+    }
+    if (!ok && lane == 0) raise_abort(abort, p.a.err);
+    __syncwarp();
+  } else if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer: Q, dO, V
+    uint32_t un = 0, vn = 0;
+    bool ok = true, half = false;  // half: Q of a unit is loaded, its dO not
+    for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+      const Unit u = decode(p, w);
+      if (u.count() == 0) continue;
+      int head, token;
+      tile_origin(p, u.kh, u.tile, &head, &token);
+      ok = warp_wait(bar(Q_EMPTY), (un & 1u) ^ 1u, abort, limit);
+      if (!ok) break;
+      if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q, bar(Q_FULL), u.b, head, token);
+      __syncwarp();
+      half = true;
+      ok = warp_wait(bar(DO_EMPTY), (un & 1u) ^ 1u, abort, limit);
+      if (!ok) break;
+      if (lane == 0) load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO, bar(DO_FULL), u.b, head, token);
+      __syncwarp();
+      half = false;
+      ++un;
+#pragma unroll 1
+      for (int j = 0; j < u.count(); ++j) {
+        ok = vn == 0 || warp_wait(bar(DP_FULL), (vn - 1) & 1u, abort, limit);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(V_FULL), TILE_BYTES);
@@ -248,18 +390,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     if (!ok && lane == 0) {
       raise_abort(abort, p.a.err);
-      volatile int never = 0;  // let the copies already issued land
-      if (qn > 0) mbar_wait_bounded(bar(Q_FULL), (qn - 1) & 1u, &never, DRAIN_LIMIT_NS);
-      if (dn > 0) mbar_wait_bounded(bar(DO_FULL), (dn - 1) & 1u, &never, DRAIN_LIMIT_NS);
-      if (vn > 0) mbar_wait_bounded(bar(V_FULL), (vn - 1) & 1u, &never, DRAIN_LIMIT_NS);
+      drain_copies(bar(Q_FULL), 1, un + (half ? 1 : 0));  // let the copies already issued land
+      drain_copies(bar(DO_FULL), 1, un);
+      drain_copies(bar(V_FULL), 1, vn);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------------ TMA producer: K
     uint32_t kn = 0, tails = 0, tails_seen = 0;
     bool ok = true;
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
+#pragma unroll 1
       for (int j = 0; j < u.count(); ++j) {
         const uint32_t s = kn % K_STAGES, tile = base + SM_K + s * TILE_BYTES;
         ok = warp_wait(bar(K_EMPTY0 + s), ((kn / K_STAGES) & 1u) ^ 1u, abort, limit);
@@ -279,7 +421,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = warp_wait(full, (tails - 1) & 1u, abort, limit);
           if (!ok) break;
           tails_seen = tails;
-          zero_rows(tile, n, ceil16(n), lane);
+          zero_rows(tile, n, ceil64(n), lane);
           if (lane == 0) mbar_arrive(bar(K_FULL0 + s));
         }
         ++kn;
@@ -287,50 +429,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     if (!ok && lane == 0) {
       raise_abort(abort, p.a.err);
-      volatile int never = 0;
-      if (tails > tails_seen) mbar_wait_bounded(bar(K_TAIL), (tails - 1) & 1u, &never, DRAIN_LIMIT_NS);
-      for (uint32_t i = kn > K_STAGES ? kn - K_STAGES : 0; i < kn; ++i)
-        mbar_wait_bounded(bar(K_FULL0 + i % K_STAGES), (i / K_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
+      if (tails > tails_seen) drain_copies(bar(K_TAIL), 1, tails);
+      drain_copies(bar(K_FULL0), K_STAGES, kn);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------------ UMMA issuer
-    // Per step: S(x+1), dP(x+1), then dQ(x), across units.
+    // Step x: S(x), dP(x), then dQ(x - 1), across units.
     const uint64_t q_desc = sdesc_sw128(base + SM_Q, 16, 1024), do_desc = sdesc_sw128(base + SM_DO, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(base + SM_K, 16, 1024), v_desc = sdesc_sw128(base + SM_V, 16, 1024);
     const uint64_t k_mn = sdesc_sw128(base + SM_K, TILE_BYTES / 2, 1024);
-    uint32_t x = 0, un = 0;  // steps issued (S and dP); units begun
-    bool ok = true, issued = false;
-    int prev_keys = 0;           // step x - 1: its dQ is to come if prev_keys > 0
-    bool prev_first = false, prev_last = false;
-    uint32_t dqn = 0;            // units whose dQ has begun
-    auto issue_dq = [&]() {
-      const uint32_t y = x - 1;
-      if (!warp_wait(bar(DS_READY0 + (y & 1u)), (y >> 1) & 1u, abort, limit)) return false;
-      if (prev_first && !warp_wait(bar(DQ_EMPTY), (dqn & 1u) ^ 1u, abort, limit)) return false;
-      if (prev_first) ++dqn;
-      tc_fence_after_sync();
-      product_acc(tmem + TM_DQ, tmem + TM_DS + (y & 1u) * 64u, 32u,
-                 sdesc_advance(k_mn, (y % K_STAGES) * TILE_BYTES), prev_first, ceil16(prev_keys) / 16);
-      umma_commit_elect(bar(K_EMPTY0 + y % K_STAGES));
-      if (prev_last) umma_commit_elect(bar(DQ_FULL));
-      return true;
-    };
+    uint32_t x = 0, un = 0, dqn = 0;        // steps; units begun; units whose dQ has begun
+    uint32_t ks = 0, kph = 0, pks = 0;      // K stage and its phase; the last step's stage
+    int prev_keys = 0;                      // the last step: its dQ is to come if > 0
+    bool prev_first = false, prev_last = false, ok = true, issued = false;
     Unit u{};
-    for (int w = next_unit(p, blockIdx.x, &u); w < p.total && ok; w = next_unit(p, w + gridDim.x, &u)) {
-      const int n = u.count();
-      for (int j = 0; j < n && ok; ++j) {
-        const int keys = u.keys_of(j);
-        const uint32_t idesc = idesc_s(keys);
-        ok = warp_wait(bar(K_FULL0 + x % K_STAGES), (x / K_STAGES) & 1u, abort, limit) &&
+    int w = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x), j = 0;
+    while (true) {
+      if (j == u.count()) {  // to the next unit with keys
+        j = 0;
+#pragma unroll 1
+        for (w += gridDim.x; w < p.total; w += gridDim.x) {
+          u = decode(p, w);
+          if (u.count() > 0) break;
+        }
+      }
+      const bool s = w < p.total;
+      if (!s && prev_keys == 0) break;
+      const int keys = s ? u.keys_of(j) : 0;
+      const bool last = j + 1 == u.count();
+      if (s) {
+        const uint32_t idesc = idesc_s((keys + 15) & ~15);
+        ok = warp_wait(bar(K_FULL0 + ks), kph, abort, limit) &&
              (j != 0 || warp_wait(bar(Q_FULL), un & 1u, abort, limit)) &&
              warp_wait(bar(S_FREE), (x & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
-        product_ss(tmem + TM_S, q_desc, sdesc_advance(k_desc, (x % K_STAGES) * TILE_BYTES), idesc);
+        product_ss(tmem + TM_S, q_desc, sdesc_advance(k_desc, ks * TILE_BYTES), idesc);
         umma_commit_elect(bar(S_FULL));
         issued = true;
-        if (j + 1 == n) umma_commit_elect(bar(Q_EMPTY));
+        if (last) umma_commit_elect(bar(Q_EMPTY));
         ok = warp_wait(bar(V_FULL), x & 1u, abort, limit) &&
              (j != 0 || warp_wait(bar(DO_FULL), un & 1u, abort, limit)) &&
              warp_wait(bar(DP_FREE), (x & 1u) ^ 1u, abort, limit);
@@ -338,166 +476,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after_sync();
         product_ss(tmem + TM_DP, do_desc, v_desc, idesc);
         umma_commit_elect(bar(DP_FULL));
-        umma_commit_elect(bar(V_EMPTY));
-        if (j + 1 == n) umma_commit_elect(bar(DO_EMPTY));
-        if (prev_keys > 0 && !(ok = issue_dq())) break;
-        ++x;
-        prev_keys = keys;
-        prev_first = j == 0;
-        prev_last = j + 1 == n;
+        if (last) {
+          umma_commit_elect(bar(DO_EMPTY));
+          ++un;
+        }
       }
-      ++un;
+      if (prev_keys > 0) {
+        const uint32_t y = x - 1;
+        ok = warp_wait(bar(DS_READY0 + (y & 1u)), (y >> 1) & 1u, abort, limit) &&
+             (!prev_first || warp_wait(bar(DQ_EMPTY), (dqn & 1u) ^ 1u, abort, limit));
+        if (!ok) break;
+        if (prev_first) ++dqn;
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int h = 0; h * 64 < prev_keys; ++h)
+          product_ts64<16>(tmem + TM_DQ, tmem + TM_DS + (y & 1u) * 64u + h * 32u,
+                           sdesc_advance(k_mn, pks * TILE_BYTES + h * 8192u), IDESC_ACC, prev_first && h == 0 ? 0u : 1u);
+        umma_commit_elect(bar(K_EMPTY0 + pks));
+        if (prev_last) umma_commit_elect(bar(DQ_FULL));
+      }
+      if (!s) break;
+      ++x;
+      prev_keys = keys;
+      prev_first = j == 0;
+      prev_last = last;
+      pks = ks;
+      if (++ks == K_STAGES) {
+        ks = 0;
+        kph ^= 1u;
+      }
+      ++j;
     }
-    if (ok && prev_keys > 0) ok = issue_dq();
     if (!ok && lane == 0) raise_abort(abort, p.a.err);
     if (issued) {
       umma_commit_elect(bar(DRAIN));  // every UMMA has completed before TMEM is released
-      volatile int never = 0;
-      if (lane == 0) mbar_wait_bounded(bar(DRAIN), 0, &never, DRAIN_LIMIT_NS);
+      if (lane == 0) drain_copies(bar(DRAIN), 1, 1);
       __syncwarp();
     }
-  } else if (warp < SOFTMAX_WARPS) {
-    // ------------------------------------------------------------------ P, dS, Delta, output
-    // Warp (quarter, half): rows 32 quarter .. + 31, one per lane; columns 64 half .. + 63.
-    const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + TM_S + half * 64u, t_dp = tmem + lane_off + TM_DP + half * 64u;
-    const uint32_t t_ds = tmem + lane_off + TM_DS + half * 32u, t_dq = tmem + lane_off + TM_DQ + half * 64u;
-    const uint32_t stage = base + SM_OUT + warp * 4096u;
-    float* xch = reinterpret_cast<float*>(gbase + SM_XCH);
-    const float c1 = p.a.sm_scale * LOG2E_F;
-    const uint64_t c2 = f2_pack(c1, c1);
-    uint32_t x = 0, un = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-      const Unit u = decode(p, w);
-      const QRow q = q_row(p, u.kh, u.tile, r);
-      const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + q.head) * p.a.q_tokens + q.token;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.dq.data) + u.b * p.a.dq.batch + q.head * p.a.dq.head +
-                           q.token * p.a.dq.token + half * 64;
-      if (u.count() == 0) {
-        if (q.valid && u.split == 0 && p.splits == 1)
-          for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0u, 0u, 0u, 0u);
-        continue;
-      }
-      const unsigned rows = __ballot_sync(0xffffffffu, q.valid);
-      float lse = q.valid ? p.a.lse[row] : 0.f;
-      if (lse == -INFINITY) lse = 0.f;  // a row whose scores are all -inf: P = 2^-inf = 0
-      // This warp's share of Delta: 4 rows x 8 chunks of O at a time.
-      const __nv_bfloat16* orow = static_cast<const __nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch +
-                                  q.head * p.a.o.head + q.token * p.a.o.token + half * 64;
-      uint4 ov[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = i * 4 + (lane >> 3);
-        const uint64_t from = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(orow), rr);
-        ov[i] = (rows >> rr) & 1u ? reinterpret_cast<const uint4*>(from)[lane & 7] : make_uint4(0u, 0u, 0u, 0u);
-      }
-      ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit);
-      if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = i * 4 + (lane >> 3);
-        const uint4 d = ld_shared16(base + SM_DO + half * (TILE_BYTES / 2) + swizzled(quarter * 32 + rr, lane & 7));
-        const uint32_t ow[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w}, dw[4] = {d.x, d.y, d.z, d.w};
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          s = fmaf(__uint_as_float(ow[k] << 16), __uint_as_float(dw[k] << 16), s);
-          s = fmaf(__uint_as_float(ow[k] & 0xffff0000u), __uint_as_float(dw[k] & 0xffff0000u), s);
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        s += __shfl_xor_sync(0xffffffffu, s, 4);
-        if ((lane & 7) == 0) xch[half * TILE + quarter * 32 + rr] = s;
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(DO_EMPTY));
-        mbar_arrive(bar(XCH0 + quarter));
-      }
-      ok = warp_wait(bar(XCH0 + quarter), un & 1u, abort, limit);
-      if (!ok) break;
-      // The next unit's sums come after this one's dQ, for which both warps have read these.
-      const float delta = xch[r] + xch[TILE + r];
-      if (half == 0 && q.valid && u.t0 == 0) p.delta[row] = delta;
-      const uint64_t nl2 = f2_pack(-lse, -lse), nd2 = f2_pack(-delta, -delta);
-      for (int j = 0; j < u.count(); ++j) {
-        ok = warp_wait(bar(S_FULL), x & 1u, abort, limit);
-        if (!ok) break;
-        tc_fence_after_sync();
-        uint32_t v[64];
-        load64(t_s, v);
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(S_FREE));
-        float pr[64];
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          float a0, a1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, nl2), a0, a1);
-          pr[i] = ex2(a0);
-          pr[i + 1] = ex2(a1);
-        }
-        ok = warp_wait(bar(DP_FULL), x & 1u, abort, limit);
-        if (!ok) break;
-        tc_fence_after_sync();
-        load64(t_dp, v);
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(DP_FREE));
-        const int n = u.keys_of(j) - half * 64;  // columns of this half that are visible
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          float a0, a1;
-          f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), nd2),
-                           f2_pack(pr[i], pr[i + 1])),
-                    a0, a1);
-          pk[i >> 1] = pack_bf162(a0, a1);
-        }
-        if (n < 64) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (2 * i >= n) pk[i] = 0u;
-            else if (2 * i + 1 >= n) pk[i] &= 0xffffu;
-          }
-        }
-        // The buffer's last reader, dQ of two steps ago, was issued before this dP.
-        tmem_st_32x32b_x32(t_ds + (x & 1u) * 64u, pk);
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(DS_READY0 + (x & 1u)));
-        ++x;
-      }
-      if (!ok) break;
-      ok = warp_wait(bar(DQ_FULL), un & 1u, abort, limit);
-      if (!ok) break;
-      tc_fence_after_sync();
-      uint32_t v[64];
-      load64(t_dq, v);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(DQ_EMPTY));
-      if (p.splits == 1) {
-        write_rows(stage, v, p.a.sm_scale, out, rows, lane);
-      } else if (q.valid) {
-        const int64_t at = ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile;
-        float* to = p.part + (at * TILE + half * 64) * TILE + r;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) to[i * TILE] = __uint_as_float(v[i]);
-      }
-      ++un;
-    }
-    if (!ok && lane == 0) raise_abort(abort, p.a.err);
-    __syncwarp();
   }
 
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 // dQ of split tiles: the parts' sums in part order; a thread has one row and 8 columns.
@@ -537,7 +558,7 @@ constexpr uint32_t SM_DELTA = SM_LSE + 2 * TILE * 4;         // -Delta of 128 ro
 constexpr uint32_t SM_BAR = SM_DELTA + TILE * 4;
 enum Bar : uint32_t {
   KV_FULL = 0,
-  KV_EMPTY,  // the 8 warps that write the unit out (through K's and V's space)
+  KV_EMPTY,  // the warps that write the unit out (through K's space)
   Q_FULL0,
   Q_EMPTY0 = Q_FULL0 + Q_STAGES,
   DO_FULL0 = Q_EMPTY0 + Q_STAGES,
@@ -557,7 +578,7 @@ enum Bar : uint32_t {
 };
 constexpr uint32_t SM_TMEM_SLOT = SM_BAR + NUM_BARS * 8;
 constexpr uint32_t SM_ABORT = SM_TMEM_SLOT + 4;
-constexpr uint32_t SMEM_BYTES = SM_ABORT + 4 + 1024;
+constexpr uint32_t SMEM_BYTES = SM_ABORT + 4;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 384;
 
@@ -568,49 +589,41 @@ struct Unit {
 
 __device__ __forceinline__ Unit decode(const Params& p, int w) {
   Unit u;
-  u.j = w % p.kv_tiles;
-  w /= p.kv_tiles;
-  u.split = w % p.splits;
-  w /= p.splits;
-  u.kh = w % p.a.kv_heads;
-  u.b = w / p.a.kv_heads;
-  const int per = (p.t.tiles + p.splits - 1) / p.splits;
+  int q = p.by_kv_tiles.quotient(w);
+  u.j = w - q * p.kv_tiles;
+  w = q;
+  q = p.by_splits.quotient(w);
+  u.split = w - q * p.splits;
+  u.b = p.by_kv_heads.quotient(q);
+  u.kh = q - u.b * p.a.kv_heads;
+  const int per = p.by_splits.quotient(p.t.tiles + p.splits - 1);
   u.q0 = min(u.split * per, p.t.tiles);
   u.q1 = min(u.q0 + per, p.t.tiles);
-  u.keys = max(0, min(TILE, visible_keys(p.a.kv_len, u.b, p.a.kv_tokens, p.a.err) - u.j * TILE));
+  u.keys = max(0, min(TILE, uniform(visible_keys(p.a.kv_len, u.b, p.a.kv_tokens, p.a.err)) - u.j * TILE));
   return u;
-}
-
-// Rows of a query tile: fewer in the last block of a head's tokens.
-__device__ __forceinline__ int rows_of(const Params& p, int tile) {
-  if (p.t.pack > 1) return p.t.box * p.t.pack;
-  return min(p.t.box, p.a.q_tokens - tile % p.t.blocks * p.t.box);
 }
 
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     cross_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
-  volatile int* abort = reinterpret_cast<volatile int*>(gbase + SM_ABORT);
-  const uint32_t* tmem_slot = reinterpret_cast<const uint32_t*>(gbase + SM_TMEM_SLOT);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + SM_ABORT);
   auto bar = [&](uint32_t b) { return base + SM_BAR + 8u * b; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint64_t limit = p.a.wait_ns;
 
   if (threadIdx.x == 0) {
     *abort = 0;
     for (uint32_t b = 0; b < NUM_BARS; ++b) {
-      const bool eight = b == KV_EMPTY || b == P_READY || b == DS_READY || b == ACC_EMPTY ||
-                         (b >= LSE_EMPTY0 && b < S_FULL);
-      mbar_init(bar(b), eight ? SOFTMAX_WARPS : 1);
+      const bool many = b == KV_EMPTY || b == P_READY || b == DS_READY || b == ACC_EMPTY ||
+                        (b >= LSE_EMPTY0 && b < S_FULL);
+      mbar_init(bar(b), many ? SOFTMAX_WARPS : 1);
     }
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == 0) {
     tmem_alloc(base + SM_TMEM_SLOT, 512);
     tmem_relinquish();
     if (lane == 0) {
@@ -620,18 +633,146 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tma_prefetch_desc(&tm_v);
     }
   }
-  // Short tiles: the rows up to the next multiple of 16, which no copy writes, are multiplied as
-  // zeros in dV and dK.
+  // Short tiles: the rows up to the next multiple of 64, which no copy writes, are multiplied as
+  // zeros.
   const int full_rows = p.t.box * p.t.pack;
-  if (full_rows % 16 != 0 && warp < Q_STAGES + DO_STAGES)
-    zero_rows(base + SM_Q + warp * TILE_BYTES, full_rows, ceil16(full_rows), lane);
+  if (full_rows % 64 != 0 && warp >= SOFTMAX_WARP && warp < SOFTMAX_WARP + Q_STAGES + DO_STAGES)
+    zero_rows(base + SM_Q + (warp - SOFTMAX_WARP) * TILE_BYTES, full_rows, ceil64(full_rows), lane);
   grid_dependency_wait();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they start at 0
 
-  if (warp == 8) {
+  if (warp >= SOFTMAX_WARP) {
+    // ------------------------------------------------------------------ P^T, dS^T, output
+    // Rows are keys, columns query rows.
+    const int quarter = warp & 3, col = (warp - SOFTMAX_WARP) >> 2, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col * 32u;
+    const uint32_t stage = base + SM_K + (warp - SOFTMAX_WARP) * 2048u;
+    const float c1 = p.a.sm_scale * LOG2E_F;
+    const uint64_t c2 = f2_pack(c1, c1);
+    uint32_t x = 0, un = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+      const Unit u = decode(p, w);
+      const int n = u.count();
+      uint32_t v[32];
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const float4* lse = reinterpret_cast<const float4*>(smem + SM_LSE) + (x & 1u) * (TILE / 4) + col * 8;
+        ok = warp_wait(bar(LSE_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit) &&
+             warp_wait(bar(S_FULL), x & 1u, abort, limit);
+        if (!ok) break;
+        tc_fence_after_sync();
+        uint32_t pk[16];
+        load32(lanes + TM_S, v);
+        float pr[32];
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 nl = lse[c / 4];
+          float a0, a1, a2, a3;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c2, f2_pack(nl.x, nl.y)), a0, a1);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), c2, f2_pack(nl.z, nl.w)), a2, a3);
+          pr[c] = ex2(a0), pr[c + 1] = ex2(a1), pr[c + 2] = ex2(a2), pr[c + 3] = ex2(a3);
+          pk[c >> 1] = pack_bf162(pr[c], pr[c + 1]);
+          pk[(c >> 1) + 1] = pack_bf162(pr[c + 2], pr[c + 3]);
+        }
+        tmem_st_32x32b_x16(lanes + TM_S, pk);  // over the warp's own columns
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(P_READY));
+          mbar_arrive(bar(LSE_EMPTY0 + (x & 1u)));
+        }
+        ok = warp_wait(bar(DELTA_FULL), x & 1u, abort, limit) && warp_wait(bar(DP_FULL), x & 1u, abort, limit);
+        if (!ok) break;
+        tc_fence_after_sync();
+        load32(lanes + TM_DP, v);
+        const float4* delta = reinterpret_cast<const float4*>(smem + SM_DELTA) + col * 8;
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 nd = delta[c / 4];
+          float a0, a1, a2, a3;
+          f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f2_pack(nd.x, nd.y)),
+                           f2_pack(pr[c], pr[c + 1])), a0, a1);
+          f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), f2_pack(nd.z, nd.w)),
+                           f2_pack(pr[c + 2], pr[c + 3])), a2, a3);
+          pk[c >> 1] = pack_bf162(a0, a1);
+          pk[(c >> 1) + 1] = pack_bf162(a2, a3);
+        }
+        tmem_st_32x32b_x16(lanes + TM_DP, pk);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(DS_READY));
+          mbar_arrive(bar(DELTA_EMPTY));
+        }
+        ++x;
+      }
+      if (!ok) break;
+      if (n > 0) {
+        ok = warp_wait(bar(ACC_FULL), un & 1u, abort, limit);
+        if (!ok) break;
+        tc_fence_after_sync();
+      } else if (p.splits > 1) {
+        continue;  // the join kernel writes
+      }
+      // Keys past the visible ones get exact zeros.  (Without a visible key the warp must not stage:
+      // K's space may hold the next unit's already.)
+      const int exist = min(TILE, p.a.kv_tokens - u.j * TILE);
+      const int64_t part = ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.kv_tiles + u.j;
+#pragma unroll 1
+      for (int y = 0; y < 2; ++y) {
+        if (n > 0) {
+          load32(lanes + (y == 0 ? TM_DV : TM_DK), v);
+        } else {
+          const HeadsView& out = y == 0 ? p.a.dv : p.a.dk;
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(out.data) + u.b * out.batch + u.kh * out.head +
+                              (static_cast<int64_t>(u.j) * TILE + r) * out.token + col * 32;
+          if (r < exist) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(to)[c] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          continue;
+        }
+        if (p.splits > 1) {
+          float* to = p.part + ((part * 2 + y) * TILE + col * 32) * TILE + r;
+          if (r < u.keys) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) to[c * TILE] = __uint_as_float(v[c]);
+          }
+          continue;
+        }
+        const HeadsView& out = y == 0 ? p.a.dv : p.a.dk;
+        if (r >= u.keys) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = 0u;
+        }
+        int64_t at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = (quarter * 32 + i * 8 + (lane >> 2)) * out.token;
+        // (A negative scale would turn the zeros into -0.)
+        write_rows(stage, v, y == 0 || r >= u.keys ? 1.f : p.a.sm_scale,
+                   static_cast<__nv_bfloat16*>(out.data) + u.b * out.batch + u.kh * out.head +
+                       static_cast<int64_t>(u.j) * TILE * out.token + col * 32,
+                   at, exist - quarter * 32, lane);
+      }
+      if (n == 0) continue;
+      fence_proxy_async_smem();  // the staging writes before the next unit's copies
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(ACC_EMPTY));
+        mbar_arrive(bar(KV_EMPTY));
+      }
+      ++un;
+    }
+    if (!ok && lane == 0) raise_abort(abort, p.a.err);
+    __syncwarp();
+  } else if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     uint32_t un = 0, qn = 0, dn = 0;
     bool ok = true;
@@ -647,54 +788,63 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       __syncwarp();
       ++un;
+#pragma unroll 1
       for (int i = u.q0; i < u.q1; ++i) {
+        int head, token;
+        tile_origin(p, u.kh, i, &head, &token);
         uint32_t s = qn % Q_STAGES;
         ok = warp_wait(bar(Q_EMPTY0 + s), ((qn / Q_STAGES) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
-        if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q + s * TILE_BYTES, bar(Q_FULL0 + s), u.b, u.kh, i);
+        if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q + s * TILE_BYTES, bar(Q_FULL0 + s), u.b, head, token);
         __syncwarp();
         ++qn;
         s = dn % DO_STAGES;
         ok = warp_wait(bar(DO_EMPTY0 + s), ((dn / DO_STAGES) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         if (lane == 0)
-          load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO + s * TILE_BYTES, bar(DO_FULL0 + s), u.b, u.kh, i);
+          load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO + s * TILE_BYTES, bar(DO_FULL0 + s), u.b, head, token);
         __syncwarp();
         ++dn;
       }
     }
     if (!ok && lane == 0) {
       raise_abort(abort, p.a.err);
-      volatile int never = 0;  // let the copies already issued land
-      if (un > 0) mbar_wait_bounded(bar(KV_FULL), (un - 1) & 1u, &never, DRAIN_LIMIT_NS);
-      for (uint32_t i = qn > Q_STAGES ? qn - Q_STAGES : 0; i < qn; ++i)
-        mbar_wait_bounded(bar(Q_FULL0 + i % Q_STAGES), (i / Q_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
-      for (uint32_t i = dn > DO_STAGES ? dn - DO_STAGES : 0; i < dn; ++i)
-        mbar_wait_bounded(bar(DO_FULL0 + i % DO_STAGES), (i / DO_STAGES) & 1u, &never, DRAIN_LIMIT_NS);
+      drain_copies(bar(KV_FULL), 1, un);  // let the copies already issued land
+      drain_copies(bar(Q_FULL0), Q_STAGES, qn);
+      drain_copies(bar(DO_FULL0), DO_STAGES, dn);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------------ -lse and -Delta of the rows
     // A row that does not exist gets -lse = -inf: its P is 0.
-    float* lse = reinterpret_cast<float*>(gbase + SM_LSE);
-    float* delta = reinterpret_cast<float*>(gbase + SM_DELTA);
+    float* lse = reinterpret_cast<float*>(smem + SM_LSE);
+    float* delta = reinterpret_cast<float*>(smem + SM_DELTA);
+    int64_t at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int y = k * 32 + lane, h = y / p.t.box;
+      at[k] = static_cast<int64_t>(h) * p.a.q_tokens + y - h * p.t.box;
+    }
     uint32_t x = 0;
     bool ok = true;
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
       if (u.count() == 0) continue;
+#pragma unroll 1
       for (int i = u.q0; i < u.q1; ++i) {
+        int head, token;
+        tile_origin(p, u.kh, i, &head, &token);
+        const int rows = tile_rows(p, token);
+        const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token;
         float nl[4], nd[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const QRow q = q_row(p, u.kh, i, k * 32 + lane);
-          const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + q.head) * p.a.q_tokens + q.token;
           nl[k] = -INFINITY;
           nd[k] = 0.f;
-          if (q.valid) {
-            const float l = p.a.lse[row];
+          if (k * 32 + lane < rows) {
+            const float l = p.a.lse[row + at[k]];
             nl[k] = l == -INFINITY ? 0.f : -l;  // all scores -inf: P = 2^-inf = 0
-            nd[k] = -p.delta[row];
+            nd[k] = -p.delta[row + at[k]];
           }
         }
         ok = warp_wait(bar(LSE_EMPTY0 + (x & 1u)), ((x >> 1) & 1u) ^ 1u, abort, limit);
@@ -714,55 +864,74 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     if (!ok && lane == 0) raise_abort(abort, p.a.err);
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------------ UMMA issuer
-    // Per step: dV(g), S^T(g+1), dK(g), dP^T(g+1).  P^T lies over S^T and dS^T over dP^T (each
-    // half of the query columns over its own columns), and products of one thread run in order.
+    // Turn i of a unit: dV(i - 1), S^T(i), dK(i - 1), dP^T(i).  P^T lies over S^T and dS^T over
+    // dP^T, and products of one thread run in order.  Columns and rows count in halves of 64.
     const uint64_t k_desc = sdesc_sw128(base + SM_K, 16, 1024), v_desc = sdesc_sw128(base + SM_V, 16, 1024);
     const uint64_t q_desc = sdesc_sw128(base + SM_Q, 16, 1024), do_desc = sdesc_sw128(base + SM_DO, 16, 1024);
     const uint64_t q_mn = sdesc_sw128(base + SM_Q, TILE_BYTES / 2, 1024), do_mn = sdesc_sw128(base + SM_DO, TILE_BYTES / 2, 1024);
-    uint32_t x = 0, un = 0;  // steps begun with S^T; units
+    uint32_t x = 0, un = 0;                 // steps begun; units
+    uint32_t qs = 0, qph = 0, pqs = 0;      // Q stage and its phase; the last step's stage
     bool ok = true, issued = false;
-    auto issue_s = [&](uint32_t y, int rows) {
-      const uint32_t s = y % Q_STAGES;
-      if (!warp_wait(bar(Q_FULL0 + s), (y / Q_STAGES) & 1u, abort, limit)) return false;
-      tc_fence_after_sync();
-      product_ss(tmem + TM_S, k_desc, sdesc_advance(q_desc, s * TILE_BYTES), idesc_s(rows));
-      umma_commit_elect(bar(S_FULL));
-      issued = true;
-      return true;
-    };
-    auto issue_dp = [&](uint32_t y, int rows) {
-      const uint32_t s = y % DO_STAGES;
-      if (!warp_wait(bar(DO_FULL0 + s), (y / DO_STAGES) & 1u, abort, limit)) return false;
-      tc_fence_after_sync();
-      product_ss(tmem + TM_DP, v_desc, sdesc_advance(do_desc, s * TILE_BYTES), idesc_s(rows));
-      umma_commit_elect(bar(DP_FULL));
-      return true;
-    };
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
       if (u.count() == 0) continue;
-      int rows = rows_of(p, u.q0);
-      ok = warp_wait(bar(KV_FULL), un & 1u, abort, limit) && issue_s(x, rows) && issue_dp(x, rows);
-      for (int i = u.q0; i < u.q1 && ok; ++i) {
-        const bool more = i + 1 < u.q1, fresh = i == u.q0;
-        const int steps = ceil16(rows) / 16, next = more ? rows_of(p, i + 1) : 0;
-        ok = warp_wait(bar(P_READY), x & 1u, abort, limit) &&
-             (!fresh || warp_wait(bar(ACC_EMPTY), (un & 1u) ^ 1u, abort, limit));
-        if (!ok) break;
-        tc_fence_after_sync();
-        product_acc(tmem + TM_DV, tmem + TM_S, 64u, sdesc_advance(do_mn, (x % DO_STAGES) * TILE_BYTES), fresh, steps);
-        umma_commit_elect(bar(DO_EMPTY0 + x % DO_STAGES));
-        if (more && !(ok = issue_s(x + 1, next))) break;
-        ok = warp_wait(bar(DS_READY), x & 1u, abort, limit);
-        if (!ok) break;
-        tc_fence_after_sync();
-        product_acc(tmem + TM_DK, tmem + TM_DP, 64u, sdesc_advance(q_mn, (x % Q_STAGES) * TILE_BYTES), fresh, steps);
-        umma_commit_elect(bar(Q_EMPTY0 + x % Q_STAGES));
-        if (more && !(ok = issue_dp(x + 1, next))) break;
-        ++x;
-        rows = next;
+      ok = warp_wait(bar(KV_FULL), un & 1u, abort, limit);
+      int prev = 0;  // rows (in halves of 64) of the last step
+#pragma unroll 1
+      for (int i = u.q0; ok && i <= u.q1; ++i) {
+        const uint32_t y = x - 1;  // the last step
+        int rows = 0;
+        if (i < u.q1) {
+          int head, token;
+          tile_origin(p, u.kh, i, &head, &token);
+          rows = ceil64(tile_rows(p, token));
+        }
+        const uint32_t idesc = idesc_s(rows);
+        if (prev > 0) {
+          ok = warp_wait(bar(P_READY), y & 1u, abort, limit) &&
+               (i != u.q0 + 1 || warp_wait(bar(ACC_EMPTY), (un & 1u) ^ 1u, abort, limit));
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int h = 0; h * 64 < prev; ++h)
+            product_ts64<32>(tmem + TM_DV, tmem + TM_S + h * 64u, sdesc_advance(do_mn, (y & 1u) * TILE_BYTES + h * 8192u),
+                             IDESC_ACC, i == u.q0 + 1 && h == 0 ? 0u : 1u);
+          umma_commit_elect(bar(DO_EMPTY0 + (y & 1u)));
+        }
+        if (rows > 0) {
+          ok = warp_wait(bar(Q_FULL0 + qs), qph, abort, limit);
+          if (!ok) break;
+          tc_fence_after_sync();
+          product_ss(tmem + TM_S, k_desc, sdesc_advance(q_desc, qs * TILE_BYTES), idesc);
+          umma_commit_elect(bar(S_FULL));
+          issued = true;
+        }
+        if (prev > 0) {
+          ok = warp_wait(bar(DS_READY), y & 1u, abort, limit);
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int h = 0; h * 64 < prev; ++h)
+            product_ts64<32>(tmem + TM_DK, tmem + TM_DP + h * 64u, sdesc_advance(q_mn, pqs * TILE_BYTES + h * 8192u),
+                             IDESC_ACC, i == u.q0 + 1 && h == 0 ? 0u : 1u);
+          umma_commit_elect(bar(Q_EMPTY0 + pqs));
+        }
+        if (rows > 0) {
+          ok = warp_wait(bar(DO_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit);
+          if (!ok) break;
+          tc_fence_after_sync();
+          product_ss(tmem + TM_DP, v_desc, sdesc_advance(do_desc, (x & 1u) * TILE_BYTES), idesc);
+          umma_commit_elect(bar(DP_FULL));
+          ++x;
+          pqs = qs;
+          if (++qs == Q_STAGES) {
+            qs = 0;
+            qph ^= 1u;
+          }
+        }
+        prev = rows;
       }
       if (!ok) break;
       umma_commit_elect(bar(ACC_FULL));
@@ -771,126 +940,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (!ok && lane == 0) raise_abort(abort, p.a.err);
     if (issued) {
       umma_commit_elect(bar(DRAIN));  // every UMMA has completed before TMEM is released
-      volatile int never = 0;
-      if (lane == 0) mbar_wait_bounded(bar(DRAIN), 0, &never, DRAIN_LIMIT_NS);
+      if (lane == 0) drain_copies(bar(DRAIN), 1, 1);
       __syncwarp();
     }
-  } else if (warp < SOFTMAX_WARPS) {
-    // ------------------------------------------------------------------ P^T, dS^T, output
-    // Warp (quarter, half): keys 32 quarter .. + 31, one per lane; query columns 64 half .. + 63.
-    const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + TM_S + half * 64u, t_dp = tmem + lane_off + TM_DP + half * 64u;
-    const uint32_t t_dv = tmem + lane_off + TM_DV + half * 64u, t_dk = tmem + lane_off + TM_DK + half * 64u;
-    const uint32_t stage = base + (warp < 4 ? SM_K : SM_V) + (warp & 3) * 4096u;
-    const float c1 = p.a.sm_scale * LOG2E_F;
-    const uint64_t c2 = f2_pack(c1, c1);
-    uint32_t x = 0, un = 0;
-    bool ok = true;
-    for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-      const Unit u = decode(p, w);
-      const int key = u.j * TILE + r;
-      const bool exists = key < p.a.kv_tokens, visible = r < u.keys;
-      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.a.dk.data) + u.b * p.a.dk.batch + u.kh * p.a.dk.head +
-                          key * p.a.dk.token + half * 64;
-      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.a.dv.data) + u.b * p.a.dv.batch + u.kh * p.a.dv.head +
-                          key * p.a.dv.token + half * 64;
-      if (p.splits == 1 && exists && !visible) {
-        for (int c = 0; c < 8; ++c) {
-          reinterpret_cast<uint4*>(dk)[c] = make_uint4(0u, 0u, 0u, 0u);
-          reinterpret_cast<uint4*>(dv)[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-      if (u.count() == 0) continue;
-      for (int i = u.q0; i < u.q1; ++i) {
-        const float* lse = reinterpret_cast<const float*>(gbase + SM_LSE) + (x & 1u) * TILE + half * 64;
-        const float* delta = reinterpret_cast<const float*>(gbase + SM_DELTA) + half * 64;
-        ok = warp_wait(bar(LSE_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit) &&
-             warp_wait(bar(S_FULL), x & 1u, abort, limit);
-        if (!ok) break;
-        tc_fence_after_sync();
-        uint32_t v[64], pk[32];
-        load64(t_s, v);
-        float pr[64];
-#pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 nl = *reinterpret_cast<const float4*>(lse + c);
-          float a0, a1, a2, a3;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c2, f2_pack(nl.x, nl.y)), a0, a1);
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), c2, f2_pack(nl.z, nl.w)), a2, a3);
-          pr[c] = ex2(a0), pr[c + 1] = ex2(a1), pr[c + 2] = ex2(a2), pr[c + 3] = ex2(a3);
-          pk[c >> 1] = pack_bf162(pr[c], pr[c + 1]);
-          pk[(c >> 1) + 1] = pack_bf162(pr[c + 2], pr[c + 3]);
-        }
-        tmem_st_32x32b_x32(t_s, pk);
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(P_READY));
-          mbar_arrive(bar(LSE_EMPTY0 + (x & 1u)));
-        }
-        ok = warp_wait(bar(DELTA_FULL), x & 1u, abort, limit) &&
-             warp_wait(bar(DP_FULL), x & 1u, abort, limit);
-        if (!ok) break;
-        tc_fence_after_sync();
-        load64(t_dp, v);
-#pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 nd = *reinterpret_cast<const float4*>(delta + c);
-          float a0, a1, a2, a3;
-          f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f2_pack(nd.x, nd.y)),
-                           f2_pack(pr[c], pr[c + 1])), a0, a1);
-          f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), f2_pack(nd.z, nd.w)),
-                           f2_pack(pr[c + 2], pr[c + 3])), a2, a3);
-          pk[c >> 1] = pack_bf162(a0, a1);
-          pk[(c >> 1) + 1] = pack_bf162(a2, a3);
-        }
-        tmem_st_32x32b_x32(t_dp, pk);
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(DS_READY));
-          mbar_arrive(bar(DELTA_EMPTY));
-        }
-        ++x;
-      }
-      if (!ok) break;
-      ok = warp_wait(bar(ACC_FULL), un & 1u, abort, limit);
-      if (!ok) break;
-      tc_fence_after_sync();
-      const unsigned rows = __ballot_sync(0xffffffffu, visible);
-      const int64_t at = ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.kv_tiles + u.j;
-#pragma unroll 1
-      for (int y = 0; y < 2; ++y) {
-        uint32_t v[64];
-        load64(y == 0 ? t_dv : t_dk, v);
-        if (p.splits == 1) {
-          write_rows(stage, v, y == 0 ? 1.f : p.a.sm_scale, y == 0 ? dv : dk, rows, lane);
-        } else if (visible) {
-          float* to = p.part + ((at * 2 + y) * TILE + half * 64) * TILE + r;
-#pragma unroll
-          for (int c = 0; c < 64; ++c) to[c * TILE] = __uint_as_float(v[c]);
-        }
-      }
-      fence_proxy_async_smem();  // the staging writes before the next unit's copies
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(ACC_EMPTY));
-        mbar_arrive(bar(KV_EMPTY));
-      }
-      ++un;
-    }
-    if (!ok && lane == 0) raise_abort(abort, p.a.err);
-    __syncwarp();
   }
 
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 // dV, dK of split tiles: the parts' sums in part order; a thread has one key and 8 columns.
@@ -984,7 +1042,13 @@ cudaError_t launch_cross_bwd(const CrossArgs& a, cudaStream_t stream) {
   if ((e = ensure_smem_limit(dq::cross_dq_kernel, static_cast<int>(dq::SMEM_BYTES), dq_smem)) != cudaSuccess) return e;
   if ((e = ensure_smem_limit(dkv::cross_dkv_kernel, static_cast<int>(dkv::SMEM_BYTES), dkv_smem)) != cudaSuccess) return e;
   const int sms = device_sm_count(), bk = a.batch * a.kv_heads;
+  p.by_tiles = make_divisor(p.t.tiles);
+  p.by_kv_tiles = make_divisor(p.kv_tiles);
+  p.by_kv_heads = make_divisor(a.kv_heads);
+  p.by_batch = make_divisor(a.batch);
+  p.by_blocks = make_divisor(p.t.blocks);
   p.splits = plan.dq_splits;
+  p.by_splits = make_divisor(p.splits);
   p.total = bk * p.t.tiles * p.splits;
   e = launch_dependent(dq::cross_dq_kernel, dim3(p.total < sms ? p.total : sms), dim3(NUM_THREADS), dq::SMEM_BYTES, stream,
                        tq, td, tk, tv, p);
@@ -993,6 +1057,7 @@ cudaError_t launch_cross_bwd(const CrossArgs& a, cudaStream_t stream) {
       (e = launch_dependent(dq::cross_dq_join_kernel, dim3(bk * p.t.tiles, 16), dim3(TILE), 0, stream, p)) != cudaSuccess)
     return e;
   p.splits = plan.dkv_splits;
+  p.by_splits = make_divisor(p.splits);
   p.total = bk * p.kv_tiles * p.splits;
   e = launch_dependent(dkv::cross_dkv_kernel, dim3(p.total < sms ? p.total : sms), dim3(NUM_THREADS), dkv::SMEM_BYTES, stream,
                        tq, td, tk, tv, p);

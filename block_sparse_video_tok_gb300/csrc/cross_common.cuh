@@ -213,8 +213,10 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
-// D (+)= A B over 64 rows of B: A 16-bit pairs in tensor memory (32 columns), B an MN-major tile
-// (SWIZZLE_128B).  accumulate = 0: D is overwritten.
+// D (+)= A B over 64 rows of B: A 16-bit pairs in tensor memory, 16 columns for 32 rows of B and the
+// next 16 columns PAIR after them; B an MN-major tile (SWIZZLE_128B).  accumulate = 0: D is
+// overwritten.
+template <int PAIR>
 __device__ __forceinline__ void product_ts64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                              uint32_t accumulate) {
   asm volatile(
@@ -222,30 +224,15 @@ __device__ __forceinline__ void product_ts64(uint32_t d, uint32_t a, uint64_t b,
       "setp.ne.b32 c, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, c;\n\t"
-      "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 128;\n\t"
+      "add.u32 a, %1, %5;\n\tadd.u64 b, %2, 128;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
-      "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 256;\n\t"
+      "add.u32 a, %1, %6;\n\tadd.u64 b, %2, 256;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
-      "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 384;\n\t"
+      "add.u32 a, %1, %7;\n\tadd.u64 b, %2, 384;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
       "}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(8), "n"(PAIR), "n"(PAIR + 8)
       : "memory");
-}
-
-// The same over `steps` x 16 rows of B, 1 to 4 steps.
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t accumulate, int steps) {
-  if (steps == 4) {
-    product_ts64(d, a, b, idesc, accumulate);
-    return;
-  }
-  if (accumulate)
-    umma_ts_elect<true>(d, a, b, idesc);
-  else
-    umma_ts_elect<false>(d, a, b, idesc);
-#pragma unroll 1
-  for (int kk = 1; kk < steps; ++kk) umma_ts_elect<true>(d, a + kk * 8u, sdesc_advance(b, kk * 2048u), idesc);
 }
 
 #endif

@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint64_t vd = sdesc_advance(v_desc, (vx & 1u) * TILE_BYTES);
 #pragma unroll 1
             for (int h = 0; h * 64 < pkeys; ++h)
-              product_ts64(tmem + TM_O + g * 128u, tmem + TM_S + g * 128u + h * 32u, sdesc_advance(vd, h * 8192u), IDESC_PV,
+              product_ts64<16>(tmem + TM_O + g * 128u, tmem + TM_S + g * 128u + h * 32u, sdesc_advance(vd, h * 8192u), IDESC_PV,
                            static_cast<uint32_t>(pj | h));
             pn ^= 1u << g;
             if (pj + 1 == pu.count()) {
