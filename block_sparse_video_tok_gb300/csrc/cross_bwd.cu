@@ -24,10 +24,9 @@ namespace vsa {
 
 namespace {
 
-// 20 warps: 0 TMEM owner and TMA producer, 1 UMMA issuer, 2 a second producer, 3 idle, 4-19 softmax.
-// Softmax warp (quarter, col) has rows 32 quarter .. + 31 of a tile of scores, one per lane, and
-// columns 32 col .. + 31.
-constexpr int NUM_THREADS = 640;
+// Warps: 0 TMEM owner and TMA producer, 1 UMMA issuer, 2 a second producer, 3 idle, 4-19 softmax;
+// dq has 20-23 for what belongs to a unit and not to a step.  Softmax warp (quarter, col) has rows
+// 32 quarter .. + 31 of a tile of scores, one per lane, and columns 32 col .. + 31.
 constexpr int SOFTMAX_WARP = 4, SOFTMAX_WARPS = 16;
 constexpr uint32_t IDESC_S0 = idesc_f16_f32acc(128, 0, false, false, true);  // N is added
 constexpr uint32_t IDESC_ACC = idesc_f16_f32acc(128, 128, false, true, true);
@@ -41,7 +40,7 @@ struct Params {
   int kv_tiles;  // of kv_tokens
   int splits;    // parts of the inner axis
   int total;     // units
-  Divisor by_tiles, by_kv_tiles, by_kv_heads, by_batch, by_splits, by_blocks;
+  Divisor by_tiles, by_kv_tiles, by_kv_heads, by_batch, by_splits, by_blocks, by_box;
   float* delta;  // [batch, heads, q_tokens]
   float* part;   // dq: [split][batch * kv_heads * tiles][128 columns][128 rows];
                  // dkv: [split][batch * kv_heads * kv_tiles][dV, dK][128 columns][128 keys]
@@ -126,14 +125,16 @@ namespace dq {
 // three of them; a V tile serves one product.
 constexpr int K_STAGES = 3;
 constexpr uint32_t SM_Q = 0, SM_DO = TILE_BYTES, SM_K = 2 * TILE_BYTES, SM_V = SM_K + K_STAGES * TILE_BYTES;
-constexpr uint32_t SM_OUT = SM_V + TILE_BYTES;    // 16 warps x 2 KB
-constexpr uint32_t SM_XCH = SM_OUT + TILE_BYTES;  // [128 rows][4 column groups] fp32
-constexpr uint32_t SM_BAR = SM_XCH + 4 * TILE * 4;
+constexpr uint32_t SM_OUT = SM_V + TILE_BYTES;  // 4 warps x 2 KB
+constexpr uint32_t SM_LSE = SM_OUT + 4 * 2048;  // [unit parity][128 rows] -lse, then -Delta, fp32
+constexpr uint32_t SM_DELTA = SM_LSE + 2 * TILE * 4;
+constexpr uint32_t SM_BAR = SM_DELTA + 2 * TILE * 4;
+constexpr int NUM_THREADS = 768, AUX_WARP = 20;
 enum Bar : uint32_t {
   Q_FULL = 0,
   Q_EMPTY,
   DO_FULL,
-  DO_EMPTY,  // the tensor core and the warps that sum O dO
+  DO_EMPTY,  // the tensor core and the 4 warps that sum O dO
   K_FULL0,
   K_EMPTY0 = K_FULL0 + K_STAGES,
   V_FULL = K_EMPTY0 + K_STAGES,
@@ -144,8 +145,9 @@ enum Bar : uint32_t {
   DS_READY0,  // two buffers
   DQ_FULL = DS_READY0 + 2,
   DQ_EMPTY,
-  XCH0,  // per lane quarter
-  K_TAIL = XCH0 + 4,
+  LSE_FULL,    // per unit, 4 warps
+  DELTA_FULL,
+  K_TAIL,
   DRAIN,
   NUM_BARS
 };
@@ -180,7 +182,7 @@ __device__ __forceinline__ Unit decode(const Params& p, int w) {
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __grid_constant__ Params p) {
+                    const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM_ABORT);
@@ -192,9 +194,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     *abort = 0;
     for (uint32_t b = 0; b < NUM_BARS; ++b) {
       uint32_t count = 1;
-      if (b == S_FREE || b == DP_FREE || b == DS_READY0 || b == DS_READY0 + 1 || b == DQ_EMPTY) count = SOFTMAX_WARPS;
-      if (b == DO_EMPTY) count = SOFTMAX_WARPS + 1;
-      if (b >= XCH0 && b < K_TAIL) count = 4;
+      if (b == S_FREE || b == DP_FREE || b == DS_READY0 || b == DS_READY0 + 1) count = SOFTMAX_WARPS;
+      if (b == DO_EMPTY) count = 5;
+      if (b == DQ_EMPTY || b == LSE_FULL || b == DELTA_FULL) count = 4;
       mbar_init(bar(b), count);
     }
     fence_barrier_init();
@@ -215,86 +217,153 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after_sync();
   constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they start at 0
 
-  if (warp >= SOFTMAX_WARP) {
-    // ------------------------------------------------------------------ P, dS, Delta, output
+  if (warp >= AUX_WARP) {
+    // ------------------------------------------------------------------ lse, Delta, output
+    // Off the softmax warps' path: a unit's -lse and -Delta are there before its first dP, and its
+    // dQ leaves while the next unit is under way.
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t t_dq = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_DQ;
+    const uint32_t stage = base + SM_OUT + quarter * 2048u;
+    const int64_t lse_at = static_cast<int64_t>(r / p.t.box) * p.a.q_tokens + r % p.t.box;
+    uint32_t un = 0;
+    bool ok = true;
+    // dQ of unit u, the on-th of this CTA (zeros without keys: with several parts the join kernel
+    // writes those).
+    auto output = [&](const Unit& u, uint32_t on) {
+      int head, token;
+      tile_origin(p, u.kh, u.tile, &head, &token);
+      const int rows = tile_rows(p, token);
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.dq.data) + u.b * p.a.dq.batch + head * p.a.dq.head +
+                           token * p.a.dq.token;
+      int64_t at[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int y = quarter * 32 + i * 8 + (lane >> 2), h = p.by_box.quotient(y);
+        at[i] = h * p.a.dq.head + (y - h * p.t.box) * p.a.dq.token;
+      }
+      const bool any = u.count() > 0;
+      if (any) {
+        if (!warp_wait(bar(DQ_FULL), on & 1u, abort, limit)) return false;
+        tc_fence_after_sync();
+      } else if (p.splits > 1) {
+        return true;
+      }
+      const int64_t part = ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile;
+#pragma unroll 1
+      for (int c = 0; c < TILE; c += 32) {
+        uint32_t v[32];
+        if (any) {
+          load32(t_dq + c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+        if (p.splits == 1) {
+          write_rows(stage, v, any ? p.a.sm_scale : 1.f, out + c, at, rows - quarter * 32, lane);
+        } else if (r < rows) {
+          float* to = p.part + (part * TILE + c) * TILE + r;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) to[i * TILE] = __uint_as_float(v[i]);
+        }
+      }
+      if (!any) return true;
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(DQ_EMPTY));
+      return true;
+    };
+    Unit u{}, prev{};
+    bool pending = false;  // dQ of `prev` is to be written
+    for (int w = blockIdx.x; ok; w += gridDim.x) {
+      const bool more = w < p.total;
+      if (more) u = decode(p, w);
+      if (more && u.count() > 0) {
+        int head, token;
+        tile_origin(p, u.kh, u.tile, &head, &token);
+        const int rows = tile_rows(p, token);
+        const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token + lse_at;
+        const float lse = r < rows ? p.a.lse[row] : 0.f;
+        float* to_lse = reinterpret_cast<float*>(smem + SM_LSE) + (un & 1u) * TILE;
+        float* to_delta = reinterpret_cast<float*>(smem + SM_DELTA) + (un & 1u) * TILE;
+        // The buffers' last readers are done: dQ of the unit before the last has been put out.
+        to_lse[r] = lse == -INFINITY ? 0.f : -lse;  // all scores -inf: P = 2^-inf = 0
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(LSE_FULL));
+        // Delta: four rows at a time, 8 lanes a row, 8 columns of each half a lane.
+        const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch +
+                                 head * p.a.o.head + token * p.a.o.token + (lane & 7) * 8;
+#pragma unroll 1
+        for (int k = 0; k < 32; k += 16) {
+          uint4 ov[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int y = quarter * 32 + k + i * 4 + (lane >> 3), h = p.by_box.quotient(y);
+            const uint4* from = reinterpret_cast<const uint4*>(o + h * p.a.o.head + (y - h * p.t.box) * p.a.o.token);
+            ov[2 * i] = y < rows ? from[0] : make_uint4(0u, 0u, 0u, 0u);
+            ov[2 * i + 1] = y < rows ? from[8] : make_uint4(0u, 0u, 0u, 0u);
+          }
+          if (k == 0 && !(ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit))) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int y = quarter * 32 + k + i * 4 + (lane >> 3);
+            float s = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 d = ld_shared16(base + SM_DO + h * (TILE_BYTES / 2) + swizzled(y, lane & 7));
+              const uint4 x = ov[2 * i + h];
+              const uint32_t ow[4] = {x.x, x.y, x.z, x.w}, dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(dw[e] << 16), s);
+                s = fmaf(__uint_as_float(ow[e] & 0xffff0000u), __uint_as_float(dw[e] & 0xffff0000u), s);
+              }
+            }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s += __shfl_xor_sync(0xffffffffu, s, 4);
+            if ((lane & 7) == 0) to_delta[y] = -s;
+          }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(DO_EMPTY));
+          mbar_arrive(bar(DELTA_FULL));
+        }
+        if (r < rows && u.t0 == 0) p.delta[row] = -to_delta[r];
+        ++un;
+      }
+      if (pending) ok = output(prev, un - 1 - (more && u.count() > 0 ? 1 : 0));
+      if (!more) break;
+      prev = u;
+      pending = true;
+    }
+    if (!ok && lane == 0) raise_abort(abort, p.a.err);
+    __syncwarp();
+  } else if (warp >= SOFTMAX_WARP) {
+    // ------------------------------------------------------------------ P, dS
     const int quarter = warp & 3, col = (warp - SOFTMAX_WARP) >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t t_s = lanes + TM_S + col * 32u, t_dp = lanes + TM_DP + col * 32u;
-    const uint32_t t_ds = lanes + TM_DS + col * 16u, t_dq = lanes + TM_DQ + col * 32u;
-    const uint32_t stage = base + SM_OUT + (warp - SOFTMAX_WARP) * 2048u;
-    float* xch = reinterpret_cast<float*>(smem + SM_XCH);
+    const uint32_t t_s = lanes + TM_S + col * 32u, t_dp = lanes + TM_DP + col * 32u, t_ds = lanes + TM_DS + col * 16u;
     const float c1 = p.a.sm_scale * LOG2E_F;
     const uint64_t c2 = f2_pack(c1, c1);
-    // Rows 8 i + lane / 4 of the warp lie at the same distance from the first in every tile.
-    int64_t out_at[4], o_at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int y = quarter * 32 + i * 8 + (lane >> 2), h = y / p.t.box, t = y - h * p.t.box;
-      out_at[i] = h * p.a.dq.head + t * p.a.dq.token;
-      o_at[i] = h * p.a.o.head + t * p.a.o.token;
-    }
-    const int64_t lse_at = static_cast<int64_t>(r / p.t.box) * p.a.q_tokens + r % p.t.box;
     uint32_t x = 0, un = 0;
     bool ok = true;
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
-      int head, token;
-      tile_origin(p, u.kh, u.tile, &head, &token);
-      const int rows = tile_rows(p, token);
-      const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token + lse_at;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.dq.data) + u.b * p.a.dq.batch + head * p.a.dq.head +
-                           token * p.a.dq.token + col * 32;
-      uint32_t v[32];
-      if (u.count() == 0) {  // (with several parts the join kernel writes)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0u;
-        if (p.splits == 1) write_rows(stage, v, 1.f, out, out_at, rows - quarter * 32, lane);
-        continue;
-      }
-      const float lse = r < rows ? p.a.lse[row] : 0.f;
-      // This warp's share of Delta: 32 columns of 8 rows at a time, 8 columns a lane.
-      const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch + head * p.a.o.head +
-                               token * p.a.o.token + col * 32 + (lane & 3) * 8;
-      uint4 ov[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        ov[i] = quarter * 32 + i * 8 + (lane >> 2) < rows ? *reinterpret_cast<const uint4*>(o + o_at[i])
-                                                          : make_uint4(0u, 0u, 0u, 0u);
-      ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit);
+      const int n = u.count();
+      if (n == 0) continue;
+      ok = warp_wait(bar(LSE_FULL), un & 1u, abort, limit);
       if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int y = quarter * 32 + i * 8 + (lane >> 2);
-        const uint4 d = ld_shared16(base + SM_DO + (col >> 1) * (TILE_BYTES / 2) + swizzled(y, (col & 1) * 4 + (lane & 3)));
-        const uint32_t ow[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w}, dw[4] = {d.x, d.y, d.z, d.w};
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          s = fmaf(__uint_as_float(ow[k] << 16), __uint_as_float(dw[k] << 16), s);
-          s = fmaf(__uint_as_float(ow[k] & 0xffff0000u), __uint_as_float(dw[k] & 0xffff0000u), s);
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        if ((lane & 3) == 0) xch[y * 4 + col] = s;
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(DO_EMPTY));
-        mbar_arrive(bar(XCH0 + quarter));
-      }
-      ok = warp_wait(bar(XCH0 + quarter), un & 1u, abort, limit);
-      if (!ok) break;
-      // The next unit's sums come after this one's dQ, for which all four warps have read these.
-      const float4 parts = reinterpret_cast<const float4*>(xch)[r];
-      const float delta = (parts.x + parts.y) + (parts.z + parts.w);
-      if (col == 0 && r < rows && u.t0 == 0) p.delta[row] = delta;
-      const float nl = lse == -INFINITY ? 0.f : -lse;  // a row whose scores are all -inf: P = 2^-inf = 0
-      const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(-delta, -delta);
+      const float nl = reinterpret_cast<const float*>(smem + SM_LSE)[(un & 1u) * TILE + r];
+      float nd = 0.f;
+      const uint64_t nl2 = f2_pack(nl, nl);
 #pragma unroll 1
-      for (int j = 0; j < u.count(); ++j) {
+      for (int j = 0; j < n; ++j) {
         ok = warp_wait(bar(S_FULL), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
+        uint32_t v[32];
         load32(t_s, v);
         tc_fence_before_sync();
         __syncwarp();
@@ -307,14 +376,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           pr[i] = ex2(a0);
           pr[i + 1] = ex2(a1);
         }
+        if (j == 0) {
+          ok = warp_wait(bar(DELTA_FULL), un & 1u, abort, limit);
+          if (!ok) break;
+          nd = reinterpret_cast<const float*>(smem + SM_DELTA)[(un & 1u) * TILE + r];
+        }
+        const uint64_t nd2 = f2_pack(nd, nd);
         ok = warp_wait(bar(DP_FULL), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
-        load32(t_dp, v);
+        uint32_t pk[16];
+        tmem_ld_32x32b_x16(t_dp, v);
+        tmem_ld_32x32b_x16(t_dp + 16u, v + 16);
+        tmem_wait_ld();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(DP_FREE));
-        uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
           float a0, a1;
@@ -323,10 +400,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     a0, a1);
           pk[i >> 1] = pack_bf162(a0, a1);
         }
-        const int n = u.keys_of(j) - col * 32;  // columns of the warp that are visible
-        if (__builtin_expect(n < 32, 0)) {
+        const int c = u.keys_of(j) - col * 32;  // columns of the warp that are visible
+        if (__builtin_expect(c < 32, 0)) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = 2 * i + 1 < n ? pk[i] : 2 * i < n ? pk[i] & 0xffffu : 0u;
+          for (int i = 0; i < 16; ++i) pk[i] = 2 * i + 1 < c ? pk[i] : 2 * i < c ? pk[i] & 0xffffu : 0u;
         }
         // The buffer's last reader, dQ of two steps ago, was issued before this dP.
         tmem_st_32x32b_x16(t_ds + (x & 1u) * 64u, pk);
@@ -336,22 +413,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0) mbar_arrive(bar(DS_READY0 + (x & 1u)));
         ++x;
       }
-      if (!ok) break;
-      ok = warp_wait(bar(DQ_FULL), un & 1u, abort, limit);
-      if (!ok) break;
-      tc_fence_after_sync();
-      load32(t_dq, v);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(DQ_EMPTY));
-      if (p.splits == 1) {
-        write_rows(stage, v, p.a.sm_scale, out, out_at, rows - quarter * 32, lane);
-      } else if (r < rows) {
-        const int64_t at = ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile;
-        float* to = p.part + (at * TILE + col * 32) * TILE + r;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) to[i * TILE] = __uint_as_float(v[i]);
-      }
       ++un;
     }
     if (!ok && lane == 0) raise_abort(abort, p.a.err);
@@ -360,24 +421,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------------ TMA producer: Q, dO, V
     uint32_t un = 0, vn = 0;
     bool ok = true, half = false;  // half: Q of a unit is loaded, its dO not
-    for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-      const Unit u = decode(p, w);
-      if (u.count() == 0) continue;
-      int head, token;
-      tile_origin(p, u.kh, u.tile, &head, &token);
-      ok = warp_wait(bar(Q_EMPTY), (un & 1u) ^ 1u, abort, limit);
-      if (!ok) break;
-      if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q, bar(Q_FULL), u.b, head, token);
-      __syncwarp();
-      half = true;
-      ok = warp_wait(bar(DO_EMPTY), (un & 1u) ^ 1u, abort, limit);
-      if (!ok) break;
-      if (lane == 0) load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO, bar(DO_FULL), u.b, head, token);
-      __syncwarp();
-      half = false;
-      ++un;
+    Unit u{}, next{};
+    for (int w = blockIdx.x; ok; w += gridDim.x) {  // unit u, and the one after it
+      u = next;
+      next = w < p.total ? decode(p, w) : Unit{};
+      const int n = u.count();
 #pragma unroll 1
-      for (int j = 0; j < u.count(); ++j) {
+      for (int j = 0; j < n; ++j) {
+        if (j == 0) {
+          int head, token;
+          tile_origin(p, u.kh, u.tile, &head, &token);
+          ok = warp_wait(bar(Q_EMPTY), (un & 1u) ^ 1u, abort, limit);
+          if (!ok) break;
+          if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q, bar(Q_FULL), u.b, head, token);
+          __syncwarp();
+          half = true;
+          ok = warp_wait(bar(DO_EMPTY), (un & 1u) ^ 1u, abort, limit);
+          if (!ok) break;
+          if (lane == 0) load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO, bar(DO_FULL), u.b, head, token);
+          __syncwarp();
+          half = false;
+          ++un;
+          if (next.count() > 0 && lane == 0) {  // the next unit's tiles, into L2
+            tile_origin(p, next.kh, next.tile, &head, &token);
+#pragma unroll 1
+            for (int h = 0; h < (p.t.box * p.t.pack == TILE ? 1 : 2); ++h) {
+              tma_prefetch_5d(&tm_q, 0, token, head, h, p.a.q.batch ? next.b : 0);
+              tma_prefetch_5d(&tm_do, 0, token, head, h, p.a.dout.batch ? next.b : 0);
+              tma_prefetch_5d(&tm_o, 0, token, head, h, p.a.o.batch ? next.b : 0);
+            }
+          }
+          __syncwarp();
+        }
         ok = vn == 0 || warp_wait(bar(DP_FULL), (vn - 1) & 1u, abort, limit);
         if (!ok) break;
         if (lane == 0) {
@@ -387,6 +462,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         ++vn;
       }
+      if (w >= p.total) break;
     }
     if (!ok && lane == 0) {
       raise_abort(abort, p.a.err);
@@ -435,13 +511,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ UMMA issuer
-    // Step x: S(x), dP(x), then dQ(x - 1), across units.
+    // Step x: S(x), dP(x), then dQ(x - 1); the first step of a unit: dQ(x - 1) of the last one first,
+    // while Q and dO are on their way.
     const uint64_t q_desc = sdesc_sw128(base + SM_Q, 16, 1024), do_desc = sdesc_sw128(base + SM_DO, 16, 1024);
     const uint64_t k_desc = sdesc_sw128(base + SM_K, 16, 1024), v_desc = sdesc_sw128(base + SM_V, 16, 1024);
     const uint64_t k_mn = sdesc_sw128(base + SM_K, TILE_BYTES / 2, 1024);
-    uint32_t x = 0, un = 0, dqn = 0;        // steps; units begun; units whose dQ has begun
-    uint32_t ks = 0, kph = 0, pks = 0;      // K stage and its phase; the last step's stage
-    int prev_keys = 0;                      // the last step: its dQ is to come if > 0
+    uint32_t x = 0, un = 0, dqn = 0;    // steps; units begun; units whose dQ has begun
+    uint32_t ks = 0, kph = 0, pks = 0;  // K stage and its phase; the last step's stage
+    int prev_keys = 0;                  // the last step: its dQ is to come if > 0
     bool prev_first = false, prev_last = false, ok = true, issued = false;
     Unit u{};
     int w = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x), j = 0;
@@ -455,48 +532,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       const bool s = w < p.total;
-      if (!s && prev_keys == 0) break;
       const int keys = s ? u.keys_of(j) : 0;
       const bool last = j + 1 == u.count();
-      if (s) {
-        const uint32_t idesc = idesc_s((keys + 15) & ~15);
-        ok = warp_wait(bar(K_FULL0 + ks), kph, abort, limit) &&
-             (j != 0 || warp_wait(bar(Q_FULL), un & 1u, abort, limit)) &&
-             warp_wait(bar(S_FREE), (x & 1u) ^ 1u, abort, limit);
-        if (!ok) break;
-        tc_fence_after_sync();
-        product_ss(tmem + TM_S, q_desc, sdesc_advance(k_desc, ks * TILE_BYTES), idesc);
-        umma_commit_elect(bar(S_FULL));
-        issued = true;
-        if (last) umma_commit_elect(bar(Q_EMPTY));
-        ok = warp_wait(bar(V_FULL), x & 1u, abort, limit) &&
-             (j != 0 || warp_wait(bar(DO_FULL), un & 1u, abort, limit)) &&
-             warp_wait(bar(DP_FREE), (x & 1u) ^ 1u, abort, limit);
-        if (!ok) break;
-        tc_fence_after_sync();
-        product_ss(tmem + TM_DP, do_desc, v_desc, idesc);
-        umma_commit_elect(bar(DP_FULL));
-        if (last) {
-          umma_commit_elect(bar(DO_EMPTY));
-          ++un;
+#pragma unroll 1
+      for (int turn = 0; turn < 2; ++turn) {
+        if (prev_keys > 0 && turn == (s && j > 0 ? 1 : 0)) {
+          // The step before this one, whose number is x - 1 until this one's S has been issued.
+          const uint32_t y = x - 1 - turn;
+          ok = warp_wait(bar(DS_READY0 + (y & 1u)), (y >> 1) & 1u, abort, limit) &&
+               (!prev_first || warp_wait(bar(DQ_EMPTY), (dqn & 1u) ^ 1u, abort, limit));
+          if (!ok) break;
+          if (prev_first) ++dqn;
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int h = 0; h * 64 < prev_keys; ++h)
+            product_ts64<16>(tmem + TM_DQ, tmem + TM_DS + (y & 1u) * 64u + h * 32u,
+                             sdesc_advance(k_mn, pks * TILE_BYTES + h * 8192u), IDESC_ACC, prev_first && h == 0 ? 0u : 1u);
+          umma_commit_elect(bar(K_EMPTY0 + pks));
+          if (prev_last) umma_commit_elect(bar(DQ_FULL));
+        }
+        if (s && turn == 0) {
+          const uint32_t idesc = idesc_s((keys + 15) & ~15);
+          ok = warp_wait(bar(K_FULL0 + ks), kph, abort, limit) &&
+               (j != 0 || warp_wait(bar(Q_FULL), un & 1u, abort, limit)) &&
+               warp_wait(bar(S_FREE), (x & 1u) ^ 1u, abort, limit);
+          if (!ok) break;
+          tc_fence_after_sync();
+          product_ss(tmem + TM_S, q_desc, sdesc_advance(k_desc, ks * TILE_BYTES), idesc);
+          umma_commit_elect(bar(S_FULL));
+          issued = true;
+          if (last) umma_commit_elect(bar(Q_EMPTY));
+          ok = warp_wait(bar(V_FULL), x & 1u, abort, limit) &&
+               (j != 0 || warp_wait(bar(DO_FULL), un & 1u, abort, limit)) &&
+               warp_wait(bar(DP_FREE), (x & 1u) ^ 1u, abort, limit);
+          if (!ok) break;
+          tc_fence_after_sync();
+          product_ss(tmem + TM_DP, do_desc, v_desc, idesc);
+          umma_commit_elect(bar(DP_FULL));
+          if (last) {
+            umma_commit_elect(bar(DO_EMPTY));
+            ++un;
+          }
+          ++x;
         }
       }
-      if (prev_keys > 0) {
-        const uint32_t y = x - 1;
-        ok = warp_wait(bar(DS_READY0 + (y & 1u)), (y >> 1) & 1u, abort, limit) &&
-             (!prev_first || warp_wait(bar(DQ_EMPTY), (dqn & 1u) ^ 1u, abort, limit));
-        if (!ok) break;
-        if (prev_first) ++dqn;
-        tc_fence_after_sync();
-#pragma unroll 1
-        for (int h = 0; h * 64 < prev_keys; ++h)
-          product_ts64<16>(tmem + TM_DQ, tmem + TM_DS + (y & 1u) * 64u + h * 32u,
-                           sdesc_advance(k_mn, pks * TILE_BYTES + h * 8192u), IDESC_ACC, prev_first && h == 0 ? 0u : 1u);
-        umma_commit_elect(bar(K_EMPTY0 + pks));
-        if (prev_last) umma_commit_elect(bar(DQ_FULL));
-      }
-      if (!s) break;
-      ++x;
+      if (!ok || !s) break;
       prev_keys = keys;
       prev_first = j == 0;
       prev_last = last;
@@ -531,7 +611,8 @@ __global__ void __launch_bounds__(TILE) cross_dq_join_kernel(const __grid_consta
   const int keys = visible_keys(p.a.kv_len, b, p.a.kv_tokens, p.a.err);
   const int n = (keys + TILE - 1) / TILE, per = (n + p.splits - 1) / p.splits;
   float s[8] = {};
-  for (int x = 0; x < p.splits && x * per < n; ++x) {
+#pragma unroll 4
+  for (int x = 0; x < min(p.splits, per > 0 ? (n + per - 1) / per : 0); ++x) {
     const float* from = p.part + ((static_cast<int64_t>(x) * tiles + blockIdx.x) * TILE + c0) * TILE + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] += from[i * TILE];
@@ -551,6 +632,7 @@ namespace dkv {
 
 // A Q tile is held from S^T to dK of the same step (with the next S^T in between), a dO tile from
 // dP^T to dV.
+constexpr int NUM_THREADS = 640;
 constexpr int Q_STAGES = 3, DO_STAGES = 2;
 constexpr uint32_t SM_K = 0, SM_V = TILE_BYTES, SM_Q = 2 * TILE_BYTES, SM_DO = SM_Q + Q_STAGES * TILE_BYTES;
 constexpr uint32_t SM_LSE = SM_DO + DO_STAGES * TILE_BYTES;  // 2 stages of -lse of 128 rows, fp32
@@ -961,7 +1043,8 @@ __global__ void __launch_bounds__(TILE) cross_dkv_join_kernel(const __grid_const
   const bool visible = key < visible_keys(p.a.kv_len, b, p.a.kv_tokens, p.a.err);
   const int per = (p.t.tiles + p.splits - 1) / p.splits;
   float s[8] = {};
-  for (int x = 0; x < p.splits && x * per < p.t.tiles && visible; ++x) {
+#pragma unroll 4
+  for (int x = 0; x < (visible ? min(p.splits, (p.t.tiles + per - 1) / per) : 0); ++x) {
     const float* from = p.part + (((static_cast<int64_t>(x) * tiles + blockIdx.x) * 2 + y) * TILE + c0) * TILE + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] += from[i * TILE];
@@ -1032,10 +1115,11 @@ cudaError_t launch_cross_bwd(const CrossArgs& a, cudaStream_t stream) {
   p.kv_tiles = plan.kv_tiles;
   p.delta = reinterpret_cast<float*>(a.workspace);
   p.part = reinterpret_cast<float*>(a.workspace + plan.part_off);
-  CUtensorMap tq, td, tk, tv;
+  CUtensorMap tq, td, to, tk, tv;
   cudaError_t e;
   if ((e = make_tmap_heads(&tq, a.q, a.q_tokens, a.batch, p.t.box, p.t.pack)) != cudaSuccess) return e;
   if ((e = make_tmap_heads(&td, a.dout, a.q_tokens, a.batch, p.t.box, p.t.pack)) != cudaSuccess) return e;
+  if ((e = make_tmap_heads(&to, a.o, a.q_tokens, a.batch, p.t.box, p.t.pack)) != cudaSuccess) return e;
   if ((e = make_tmap_heads(&tk, a.k, a.kv_tokens, a.batch, TILE, 1)) != cudaSuccess) return e;
   if ((e = make_tmap_heads(&tv, a.v, a.kv_tokens, a.batch, TILE, 1)) != cudaSuccess) return e;
   static std::atomic<uint64_t> dq_smem{0}, dkv_smem{0};
@@ -1047,11 +1131,12 @@ cudaError_t launch_cross_bwd(const CrossArgs& a, cudaStream_t stream) {
   p.by_kv_heads = make_divisor(a.kv_heads);
   p.by_batch = make_divisor(a.batch);
   p.by_blocks = make_divisor(p.t.blocks);
+  p.by_box = make_divisor(p.t.box);
   p.splits = plan.dq_splits;
   p.by_splits = make_divisor(p.splits);
   p.total = bk * p.t.tiles * p.splits;
-  e = launch_dependent(dq::cross_dq_kernel, dim3(p.total < sms ? p.total : sms), dim3(NUM_THREADS), dq::SMEM_BYTES, stream,
-                       tq, td, tk, tv, p);
+  e = launch_dependent(dq::cross_dq_kernel, dim3(p.total < sms ? p.total : sms), dim3(dq::NUM_THREADS), dq::SMEM_BYTES, stream,
+                       tq, td, tk, tv, to, p);
   if (e != cudaSuccess) return e;
   if (p.splits > 1 &&
       (e = launch_dependent(dq::cross_dq_join_kernel, dim3(bk * p.t.tiles, 16), dim3(TILE), 0, stream, p)) != cudaSuccess)
@@ -1059,7 +1144,7 @@ cudaError_t launch_cross_bwd(const CrossArgs& a, cudaStream_t stream) {
   p.splits = plan.dkv_splits;
   p.by_splits = make_divisor(p.splits);
   p.total = bk * p.kv_tiles * p.splits;
-  e = launch_dependent(dkv::cross_dkv_kernel, dim3(p.total < sms ? p.total : sms), dim3(NUM_THREADS), dkv::SMEM_BYTES, stream,
+  e = launch_dependent(dkv::cross_dkv_kernel, dim3(p.total < sms ? p.total : sms), dim3(dkv::NUM_THREADS), dkv::SMEM_BYTES, stream,
                        tq, td, tk, tv, p);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_dependent(dkv::cross_dkv_join_kernel, dim3(bk * p.kv_tiles, 16, 2), dim3(TILE), 0, stream, p);
