@@ -25,7 +25,7 @@ namespace vsa {
 namespace {
 
 // Warps: 0 TMEM owner and TMA producer, 1 UMMA issuer, 2 a second producer, 3 idle, 4-19 softmax;
-// dq has 20-23 for what belongs to a unit and not to a step.  Softmax warp (quarter, col) has rows
+// dq has 20-27 for what belongs to a unit and not to a step.  Softmax warp (quarter, col) has rows
 // 32 quarter .. + 31 of a tile of scores, one per lane, and columns 32 col .. + 31.
 constexpr int SOFTMAX_WARP = 4, SOFTMAX_WARPS = 16;
 constexpr uint32_t IDESC_S0 = idesc_f16_f32acc(128, 0, false, false, true);  // N is added
@@ -107,6 +107,43 @@ __device__ __forceinline__ QRow q_row(const Params& p, int kh, int tile, int r) 
   return x;
 }
 
+// Lane i of four neighbours has chunks 0 .. 3 of row i (chunk k: v[4 k] .. v[4 k + 3]) and gets chunk
+// i of rows 0 .. 3.
+__device__ __forceinline__ void transpose4(uint32_t* v, int lane) {
+#pragma unroll
+  for (int m = 1; m <= 2; m *= 2) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & m) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t& lo = v[4 * k + i];
+        uint32_t& hi = v[4 * (k + m) + i];
+        const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? lo : hi, m);
+        lo = up ? t : lo;
+        hi = up ? hi : t;
+      }
+    }
+  }
+}
+
+// s += the parts' 8 columns of a row, in part order; four parts' loads at a time.
+__device__ __forceinline__ void add_parts(float* s, const float* part, int64_t stride, int parts) {
+#pragma unroll 1
+  for (int x = 0; x < parts; x += 4) {
+    float t[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[k][i] = x + k < parts ? part[(x + k) * stride + i * TILE] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += t[k][i];
+  }
+}
+
 // One query-side tile into shared memory, by one thread.
 __device__ __forceinline__ void load_q_tile(const Params& p, const CUtensorMap* map, int64_t batch_stride, uint32_t dst,
                                             uint32_t full, int b, int head, int token) {
@@ -122,30 +159,30 @@ __device__ __forceinline__ void load_q_tile(const Params& p, const CUtensorMap* 
 namespace dq {
 
 // K tiles are held from S to dQ of the same step, with the next step's S and dP in between, so
-// three of them; a V tile serves one product.
-constexpr int K_STAGES = 3;
+// three of them.  (With one V tile, its way from L2, 2000 cycles when all SMs load, set the pace.)
+constexpr int K_STAGES = 3, V_STAGES = 2;
 constexpr uint32_t SM_Q = 0, SM_DO = TILE_BYTES, SM_K = 2 * TILE_BYTES, SM_V = SM_K + K_STAGES * TILE_BYTES;
-constexpr uint32_t SM_OUT = SM_V + TILE_BYTES;  // 4 warps x 2 KB
-constexpr uint32_t SM_LSE = SM_OUT + 4 * 2048;  // [unit parity][128 rows] -lse, then -Delta, fp32
+constexpr uint32_t SM_LSE = SM_V + V_STAGES * TILE_BYTES;  // [unit parity][128 rows] -lse, -Delta
 constexpr uint32_t SM_DELTA = SM_LSE + 2 * TILE * 4;
 constexpr uint32_t SM_BAR = SM_DELTA + 2 * TILE * 4;
-constexpr int NUM_THREADS = 768, AUX_WARP = 20;
+constexpr int NUM_THREADS = 896, AUX_WARP = 20;
 enum Bar : uint32_t {
   Q_FULL = 0,
   Q_EMPTY,
   DO_FULL,
-  DO_EMPTY,  // the tensor core and the 4 warps that sum O dO
+  DO_EMPTY,  // the tensor core and the 8 warps that sum O dO
   K_FULL0,
   K_EMPTY0 = K_FULL0 + K_STAGES,
-  V_FULL = K_EMPTY0 + K_STAGES,
-  S_FULL,
-  S_FREE,   // S has been read
-  DP_FULL,  // (and the V tile is free)
+  V_FULL0 = K_EMPTY0 + K_STAGES,
+  V_EMPTY0 = V_FULL0 + V_STAGES,
+  S_FULL = V_EMPTY0 + V_STAGES,
+  S_FREE,  // S has been read
+  DP_FULL,
   DP_FREE,
   DS_READY0,  // two buffers
   DQ_FULL = DS_READY0 + 2,
   DQ_EMPTY,
-  LSE_FULL,    // per unit, 4 warps
+  LSE_FULL,    // per unit
   DELTA_FULL,
   K_TAIL,
   DRAIN,
@@ -154,6 +191,7 @@ enum Bar : uint32_t {
 constexpr uint32_t SM_TMEM_SLOT = SM_BAR + NUM_BARS * 8;
 constexpr uint32_t SM_ABORT = SM_TMEM_SLOT + 4;
 constexpr uint32_t SMEM_BYTES = SM_ABORT + 4;
+static_assert(V_STAGES == 2, "stage = step & 1");
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 256, TM_DS = 384;  // dS: two buffers of 64 columns
 
@@ -195,8 +233,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (uint32_t b = 0; b < NUM_BARS; ++b) {
       uint32_t count = 1;
       if (b == S_FREE || b == DP_FREE || b == DS_READY0 || b == DS_READY0 + 1) count = SOFTMAX_WARPS;
-      if (b == DO_EMPTY) count = 5;
-      if (b == DQ_EMPTY || b == LSE_FULL || b == DELTA_FULL) count = 4;
+      if (b == DO_EMPTY) count = 9;
+      if (b == DQ_EMPTY || b == DELTA_FULL) count = 8;
+      if (b == LSE_FULL) count = 4;
       mbar_init(bar(b), count);
     }
     fence_barrier_init();
@@ -219,121 +258,140 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (warp >= AUX_WARP) {
     // ------------------------------------------------------------------ lse, Delta, output
-    // Off the softmax warps' path: a unit's -lse and -Delta are there before its first dP, and its
-    // dQ leaves while the next unit is under way.
-    const int quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t t_dq = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_DQ;
-    const uint32_t stage = base + SM_OUT + quarter * 2048u;
-    const int64_t lse_at = static_cast<int64_t>(r / p.t.box) * p.a.q_tokens + r % p.t.box;
+    // Off the softmax warps' path: a unit's -lse and -Delta are there before its first dS, and its
+    // dQ leaves while the next unit is under way, straight from registers (shared memory has no
+    // room left).
+    const int quarter = warp & 3, half = (warp - AUX_WARP) >> 2, r = quarter * 32 + lane;
+    const uint32_t t_dq = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_DQ + half * 64u;
+    const int rh = r / p.t.box, rt = r - rh * p.t.box;
+    int64_t at[4];  // of the four rows that the lane writes, and its 8 columns
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int y = (r & ~3) + i, h = p.by_box.quotient(y);
+      at[i] = h * p.a.dq.head + (y - h * p.t.box) * p.a.dq.token + half * 64 + (lane & 3) * 8;
+    }
     uint32_t un = 0;
     bool ok = true;
-    // dQ of unit u, the on-th of this CTA (zeros without keys: with several parts the join kernel
-    // writes those).
-    auto output = [&](const Unit& u, uint32_t on) {
-      int head, token;
-      tile_origin(p, u.kh, u.tile, &head, &token);
-      const int rows = tile_rows(p, token);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.dq.data) + u.b * p.a.dq.batch + head * p.a.dq.head +
-                           token * p.a.dq.token;
-      int64_t at[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int y = quarter * 32 + i * 8 + (lane >> 2), h = p.by_box.quotient(y);
-        at[i] = h * p.a.dq.head + (y - h * p.t.box) * p.a.dq.token;
-      }
-      const bool any = u.count() > 0;
-      if (any) {
-        if (!warp_wait(bar(DQ_FULL), on & 1u, abort, limit)) return false;
-        tc_fence_after_sync();
-      } else if (p.splits > 1) {
-        return true;
-      }
-      const int64_t part = ((static_cast<int64_t>(u.split) * p.a.batch + u.b) * p.a.kv_heads + u.kh) * p.t.tiles + u.tile;
-#pragma unroll 1
-      for (int c = 0; c < TILE; c += 32) {
-        uint32_t v[32];
-        if (any) {
-          load32(t_dq + c, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-        }
-        if (p.splits == 1) {
-          write_rows(stage, v, any ? p.a.sm_scale : 1.f, out + c, at, rows - quarter * 32, lane);
-        } else if (r < rows) {
-          float* to = p.part + (part * TILE + c) * TILE + r;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) to[i * TILE] = __uint_as_float(v[i]);
-        }
-      }
-      if (!any) return true;
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(DQ_EMPTY));
-      return true;
-    };
     Unit u{}, prev{};
     bool pending = false;  // dQ of `prev` is to be written
     for (int w = blockIdx.x; ok; w += gridDim.x) {
       const bool more = w < p.total;
       if (more) u = decode(p, w);
-      if (more && u.count() > 0) {
+      const bool now = more && u.count() > 0;
+      if (now) {
         int head, token;
         tile_origin(p, u.kh, u.tile, &head, &token);
         const int rows = tile_rows(p, token);
-        const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token + lse_at;
-        const float lse = r < rows ? p.a.lse[row] : 0.f;
+        const int64_t row = (static_cast<int64_t>(u.b) * p.a.heads + head) * p.a.q_tokens + token;
+        // The buffers' last readers are done: dQ of the unit before the last has been put out.
         float* to_lse = reinterpret_cast<float*>(smem + SM_LSE) + (un & 1u) * TILE;
         float* to_delta = reinterpret_cast<float*>(smem + SM_DELTA) + (un & 1u) * TILE;
-        // The buffers' last readers are done: dQ of the unit before the last has been put out.
-        to_lse[r] = lse == -INFINITY ? 0.f : -lse;  // all scores -inf: P = 2^-inf = 0
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(LSE_FULL));
-        // Delta: four rows at a time, 8 lanes a row, 8 columns of each half a lane.
+        // Delta of 16 rows a warp: four at a time, 8 lanes a row, 8 columns of each half a lane.
         const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.a.o.data) + u.b * p.a.o.batch +
                                  head * p.a.o.head + token * p.a.o.token + (lane & 7) * 8;
-#pragma unroll 1
-        for (int k = 0; k < 32; k += 16) {
-          uint4 ov[8];
+        const int y0 = quarter * 32 + half * 16 + (lane >> 3);
+        uint4 ov[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int y = quarter * 32 + k + i * 4 + (lane >> 3), h = p.by_box.quotient(y);
-            const uint4* from = reinterpret_cast<const uint4*>(o + h * p.a.o.head + (y - h * p.t.box) * p.a.o.token);
-            ov[2 * i] = y < rows ? from[0] : make_uint4(0u, 0u, 0u, 0u);
-            ov[2 * i + 1] = y < rows ? from[8] : make_uint4(0u, 0u, 0u, 0u);
-          }
-          if (k == 0 && !(ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit))) break;
+        for (int i = 0; i < 4; ++i) {
+          const int y = y0 + i * 4, h = p.by_box.quotient(y);
+          const uint4* from = reinterpret_cast<const uint4*>(o + h * p.a.o.head + (y - h * p.t.box) * p.a.o.token);
+          ov[2 * i] = y < rows ? from[0] : make_uint4(0u, 0u, 0u, 0u);
+          ov[2 * i + 1] = y < rows ? from[8] : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (half == 0) {
+          const float lse = r < rows ? p.a.lse[row + static_cast<int64_t>(rh) * p.a.q_tokens + rt] : 0.f;
+          to_lse[r] = lse == -INFINITY ? 0.f : -lse;  // all scores -inf: P = 2^-inf = 0
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(LSE_FULL));
+        }
+        ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit);
+        if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int y = quarter * 32 + k + i * 4 + (lane >> 3);
-            float s = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const int y = y0 + i * 4;
+          float s = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 d = ld_shared16(base + SM_DO + h * (TILE_BYTES / 2) + swizzled(y, lane & 7));
-              const uint4 x = ov[2 * i + h];
-              const uint32_t ow[4] = {x.x, x.y, x.z, x.w}, dw[4] = {d.x, d.y, d.z, d.w};
+          for (int h = 0; h < 2; ++h) {
+            const uint4 d = ld_shared16(base + SM_DO + h * (TILE_BYTES / 2) + swizzled(y, lane & 7));
+            const uint4 x = ov[2 * i + h];
+            const uint32_t ow[4] = {x.x, x.y, x.z, x.w}, dw[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                s = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(dw[e] << 16), s);
-                s = fmaf(__uint_as_float(ow[e] & 0xffff0000u), __uint_as_float(dw[e] & 0xffff0000u), s);
-              }
+            for (int e = 0; e < 4; ++e) {
+              s = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(dw[e] << 16), s);
+              s = fmaf(__uint_as_float(ow[e] & 0xffff0000u), __uint_as_float(dw[e] & 0xffff0000u), s);
             }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            s += __shfl_xor_sync(0xffffffffu, s, 4);
-            if ((lane & 7) == 0) to_delta[y] = -s;
+          }
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          s += __shfl_xor_sync(0xffffffffu, s, 4);
+          if ((lane & 7) == 0) {
+            to_delta[y] = -s;
+            const int h = p.by_box.quotient(y);
+            if (y < rows && u.t0 == 0) p.delta[row + static_cast<int64_t>(h) * p.a.q_tokens + y - h * p.t.box] = s;
           }
         }
-        if (!ok) break;
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(DO_EMPTY));
           mbar_arrive(bar(DELTA_FULL));
         }
-        if (r < rows && u.t0 == 0) p.delta[row] = -to_delta[r];
         ++un;
       }
-      if (pending) ok = output(prev, un - 1 - (more && u.count() > 0 ? 1 : 0));
+      if (pending && (prev.count() > 0 || p.splits == 1)) {  // (split: the join kernel writes zeros)
+        int head, token;
+        tile_origin(p, prev.kh, prev.tile, &head, &token);
+        const int rows = tile_rows(p, token);
+        const bool any = prev.count() > 0;
+        if (any) {
+          ok = warp_wait(bar(DQ_FULL), (un - 1 - (now ? 1 : 0)) & 1u, abort, limit);
+          if (!ok) break;
+          tc_fence_after_sync();
+        }
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.dq.data) + prev.b * p.a.dq.batch + head * p.a.dq.head +
+                             token * p.a.dq.token;
+        const int64_t part =
+            ((static_cast<int64_t>(prev.split) * p.a.batch + prev.b) * p.a.kv_heads + prev.kh) * p.t.tiles + prev.tile;
+        const float scale = any ? p.a.sm_scale : 1.f;
+        const uint64_t s2 = f2_pack(scale, scale);
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t v[32];
+          if (any) {
+            load32(t_dq + c, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+          if (p.splits > 1) {
+            float* to = p.part + (part * TILE + half * 64 + c) * TILE + r;
+            if (r < rows) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) to[i * TILE] = __uint_as_float(v[i]);
+            }
+            continue;
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a0, a1;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2), a0, a1);
+            pk[i] = pack_bf162(a0, a1);
+          }
+          // Four lanes turn their four rows of four 16-byte chunks over, so that each writes the
+          // same chunk of all four: 64 bytes of a row in one piece (16 bytes of 32 rows at a time
+          // took the load-store unit 4000 cycles a tile).
+          transpose4(pk, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((r & ~3) + i < rows)
+              *reinterpret_cast<uint4*>(out + at[i] + c) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
+        if (any) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(DQ_EMPTY));
+        }
+      }
       if (!more) break;
       prev = u;
       pending = true;
@@ -386,9 +444,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         tc_fence_after_sync();
         uint32_t pk[16];
-        tmem_ld_32x32b_x16(t_dp, v);
-        tmem_ld_32x32b_x16(t_dp + 16u, v + 16);
-        tmem_wait_ld();
+        load32(t_dp, v);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(DP_FREE));
@@ -453,11 +509,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           __syncwarp();
         }
-        ok = vn == 0 || warp_wait(bar(DP_FULL), (vn - 1) & 1u, abort, limit);
+        const uint32_t s = vn & 1u;
+        ok = warp_wait(bar(V_EMPTY0 + s), ((vn >> 1) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(V_FULL), TILE_BYTES);
-          tma_load_5d(base + SM_V, &tm_v, bar(V_FULL), 0, (u.t0 + j) * TILE, u.kh, 0, p.a.v.batch ? u.b : 0);
+          mbar_arrive_expect_tx(bar(V_FULL0 + s), TILE_BYTES);
+          tma_load_5d(base + SM_V + s * TILE_BYTES, &tm_v, bar(V_FULL0 + s), 0, (u.t0 + j) * TILE, u.kh, 0,
+                      p.a.v.batch ? u.b : 0);
         }
         __syncwarp();
         ++vn;
@@ -468,7 +526,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       raise_abort(abort, p.a.err);
       drain_copies(bar(Q_FULL), 1, un + (half ? 1 : 0));  // let the copies already issued land
       drain_copies(bar(DO_FULL), 1, un);
-      drain_copies(bar(V_FULL), 1, vn);
+      drain_copies(bar(V_FULL0), V_STAGES, vn);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -562,13 +620,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           umma_commit_elect(bar(S_FULL));
           issued = true;
           if (last) umma_commit_elect(bar(Q_EMPTY));
-          ok = warp_wait(bar(V_FULL), x & 1u, abort, limit) &&
+          ok = warp_wait(bar(V_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit) &&
                (j != 0 || warp_wait(bar(DO_FULL), un & 1u, abort, limit)) &&
                warp_wait(bar(DP_FREE), (x & 1u) ^ 1u, abort, limit);
           if (!ok) break;
           tc_fence_after_sync();
-          product_ss(tmem + TM_DP, do_desc, v_desc, idesc);
+          product_ss(tmem + TM_DP, do_desc, sdesc_advance(v_desc, (x & 1u) * TILE_BYTES), idesc);
           umma_commit_elect(bar(DP_FULL));
+          umma_commit_elect(bar(V_EMPTY0 + (x & 1u)));
           if (last) {
             umma_commit_elect(bar(DO_EMPTY));
             ++un;
@@ -611,12 +670,8 @@ __global__ void __launch_bounds__(TILE) cross_dq_join_kernel(const __grid_consta
   const int keys = visible_keys(p.a.kv_len, b, p.a.kv_tokens, p.a.err);
   const int n = (keys + TILE - 1) / TILE, per = (n + p.splits - 1) / p.splits;
   float s[8] = {};
-#pragma unroll 4
-  for (int x = 0; x < min(p.splits, per > 0 ? (n + per - 1) / per : 0); ++x) {
-    const float* from = p.part + ((static_cast<int64_t>(x) * tiles + blockIdx.x) * TILE + c0) * TILE + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] += from[i * TILE];
-  }
+  add_parts(s, p.part + (static_cast<int64_t>(blockIdx.x) * TILE + c0) * TILE + threadIdx.x,
+            static_cast<int64_t>(tiles) * TILE * TILE, per > 0 ? (n + per - 1) / per : 0);
   const float c = p.a.sm_scale;
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.dq.data) + b * p.a.dq.batch + q.head * p.a.dq.head +
                             q.token * p.a.dq.token + c0) =
@@ -1043,12 +1098,8 @@ __global__ void __launch_bounds__(TILE) cross_dkv_join_kernel(const __grid_const
   const bool visible = key < visible_keys(p.a.kv_len, b, p.a.kv_tokens, p.a.err);
   const int per = (p.t.tiles + p.splits - 1) / p.splits;
   float s[8] = {};
-#pragma unroll 4
-  for (int x = 0; x < (visible ? min(p.splits, (p.t.tiles + per - 1) / per) : 0); ++x) {
-    const float* from = p.part + (((static_cast<int64_t>(x) * tiles + blockIdx.x) * 2 + y) * TILE + c0) * TILE + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] += from[i * TILE];
-  }
+  add_parts(s, p.part + ((static_cast<int64_t>(blockIdx.x) * 2 + y) * TILE + c0) * TILE + threadIdx.x,
+            static_cast<int64_t>(tiles) * 2 * TILE * TILE, visible ? (p.t.tiles + per - 1) / per : 0);
   const HeadsView& out = y == 0 ? p.a.dv : p.a.dk;
   const float c = y == 0 || !visible ? 1.f : p.a.sm_scale;  // a hidden key's rows are +0
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.data) + b * out.batch + kh * out.head + key * out.token + c0) =
