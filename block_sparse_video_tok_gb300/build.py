@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libvsa.so")
 SOURCES = ["api.cu", "invert.cu", "prepost.cu", "tmap.cu", "bwd_main.cu", "fwd_main.cu",
-           "noalloc.cu", "layer_api.cu", "norm_rope.cu", "cross_fwd.cu", "cross_bwd.cu"]
+           "noalloc.cu", "layer_api.cu", "norm_rope.cu", "cross_fwd.cu", "cross_token.cu",
+           "cross_bwd.cu"]
 HEADERS = ["ptx.cuh", "queue.cuh", "vsa_internal.cuh", "layer_internal.cuh",
            "cross_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

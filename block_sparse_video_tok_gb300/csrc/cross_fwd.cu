@@ -572,18 +572,29 @@ __global__ void __launch_bounds__(128) cross_combine_kernel(const __grid_constan
   const int head = kh * p.t.share + x / p.t.blocks * p.t.pack + rh;
   const int token = x % p.t.blocks * p.t.box + r - rh * p.t.box;
   if (rh >= p.t.pack || token >= p.a.q_tokens) return;
+  // The maximum over the parts first, so that the sums have no order of their own to wait for.
+  const float2* part_ml = p.part_ml + static_cast<int64_t>(tile) * TILE + r;
+  const float* part_o = p.part_o + (static_cast<int64_t>(tile) * TILE + c0) * TILE + r;
+  const int64_t step = static_cast<int64_t>(tiles) * TILE;
   float mm = -INFINITY, l = 0.f, o[8] = {};
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t at = static_cast<int64_t>(s) * tiles + tile;
-    const float2 ml = p.part_ml[at * TILE + r];
-    if (ml.y == 0.f) continue;  // NaN is kept
-    const float mn = fmaxf(mm, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(mm - ref), w = ex2(ml.x - ref);
-    mm = mn;
-    l = l * f + ml.y * w;
-    const float* po = p.part_o + (at * TILE + c0) * TILE + r;
+#pragma unroll 8
+  for (int s = 0; s < p.splits; ++s) mm = fmaxf(mm, part_ml[s * step].x);
+  const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 1
+  for (int s0 = 0; s0 < p.splits; s0 += 4) {
+    float x[4][8], w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * f + po[i * TILE] * w;
+    for (int k = 0; k < 4; ++k) {
+      const float2 ml = s0 + k < p.splits ? part_ml[(s0 + k) * step] : make_float2(-INFINITY, 0.f);
+      w[k] = ml.y == 0.f ? 0.f : ex2(ml.x - ref);  // NaN is kept
+      l += ml.y * w[k];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[k][i] = ml.y == 0.f ? 0.f : part_o[(s0 + k) * step * TILE + i * TILE];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] += x[k][i] * w[k];
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.o.data) + b * p.a.o.batch + head * p.a.o.head +
@@ -622,10 +633,13 @@ Plan plan_of(int batch, int heads, int kv_heads, int q_tokens, int kv_tokens) {
 }  // namespace
 
 size_t cross_fwd_workspace(int batch, int heads, int kv_heads, int q_tokens, int kv_tokens) {
+  if (use_cross_token(heads, kv_heads, q_tokens))
+    return cross_token_workspace(batch, heads, kv_heads, q_tokens, kv_tokens);
   return plan_of(batch, heads, kv_heads, q_tokens, kv_tokens).total;
 }
 
 cudaError_t launch_cross_fwd(const CrossArgs& a, cudaStream_t stream) {
+  if (use_cross_token(a.heads, a.kv_heads, a.q_tokens)) return launch_cross_token(a, stream);
   const Plan plan = plan_of(a.batch, a.heads, a.kv_heads, a.q_tokens, a.kv_tokens);
   Params p{};
   p.a = a;

@@ -55,6 +55,10 @@ struct CrossArgs {
 
 cudaError_t launch_cross_fwd(const CrossArgs& a, cudaStream_t stream);
 cudaError_t launch_cross_bwd(const CrossArgs& a, cudaStream_t stream);
+// The forward for a few query rows per key head, and whether it is the one to use.
+cudaError_t launch_cross_token(const CrossArgs& a, cudaStream_t stream);
+bool use_cross_token(int heads, int kv_heads, int q_tokens);
+size_t cross_token_workspace(int batch, int heads, int kv_heads, int q_tokens, int kv_tokens);
 size_t cross_fwd_workspace(int batch, int heads, int kv_heads, int q_tokens, int kv_tokens);
 size_t cross_bwd_workspace(int batch, int heads, int kv_heads, int q_tokens, int kv_tokens);
 
