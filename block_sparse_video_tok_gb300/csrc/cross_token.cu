@@ -203,12 +203,13 @@ __global__ void __launch_bounds__(512) cross_token_join_kernel(const __grid_cons
 
 constexpr int MAX_ROWS = 4;
 
-// Parts of the keys: one while a CTA has few keys or the pairs fill the SMs; else two CTAs per SM,
-// with at least MIN_KEYS keys each (fewer, and the join costs more than it saves).
+// Parts of the keys: one while a CTA has few keys or the pairs fill the SMs; else two CTAs per SM
+// with at least 256 keys each.  (96 pairs of 512 keys: in two parts the second launch and the
+// workspace cost the host more than the GPU saves.)
 int token_splits(int64_t pairs, int kv_tokens) {
-  constexpr int MIN_KEYS = 256;
   int64_t s = 2LL * device_sm_count() / pairs;
-  if (s > kv_tokens / MIN_KEYS) s = kv_tokens / MIN_KEYS;
+  if (s > kv_tokens / 256) s = kv_tokens / 256;
+  if (kv_tokens < 1024) s = 1;
   return s < 2 ? 1 : static_cast<int>(s);
 }
 

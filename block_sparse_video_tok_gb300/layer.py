@@ -109,29 +109,26 @@ def _call(name, *args):
 
 # ------------------------------------------------------------------------------- arguments
 
-def _heads(t, name, shape, like, transposed=False, whole=False):
-    """The [B, H, S, D] tensor t (transposed: [B, S, H, D]) as a packed vsa_heads, after checking
-    it against `shape` (as t has it) and the type and device of `like`.  whole: its heads and tokens
+def _heads(t, name, shape, dtype, device, transposed=False, whole=False):
+    """The [B, H, S, D] tensor t (transposed: [B, S, H, D]) as a packed vsa_heads, after checking it
+    against `shape` (as t has it), its type and its device's index.  whole: its heads and tokens
     must not be broadcast."""
-    try:
-        if t.dtype is not like.dtype:
-            raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
-        if t.get_device() != like.get_device():
-            raise TypeError("%s must be a tensor on %s" % (name, like.device))
-    except AttributeError:
-        raise TypeError("%s must be a tensor on %s" % (name, like.device)) from None
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise TypeError("%s must be a tensor on cuda:%d" % (name, device))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     ptr = t.data_ptr()
     if transposed:
-        B, S, H, D = shape
+        B, S, H, _ = shape
         sb, ss, sh, sd = t.stride()
     else:
-        B, H, S, D = shape
+        B, H, S, _ = shape
         sb, sh, ss, sd = t.stride()
-    # A dimension of length 1 may have any stride.
+    # A dimension of length 1 may have any stride.  (16 bytes: 4 fp32 or 8 16-bit elements.)
     used = (sb if B > 1 else 0) | (sh if H > 1 else 0) | (ss if S > 1 else 0)
-    if sd != 1 or (ptr | used * t.element_size()) & 15:
+    if sd != 1 or ptr & 15 or used & (3 if dtype is torch.float32 else 7):
         raise ValueError("%s: the last dimension must be contiguous, and the data and the other "
                          "strides multiples of 16 bytes (strides %s)" % (name, t.stride()))
     if whole and ((sh == 0 and H > 1) or (ss == 0 and S > 1)):
@@ -260,6 +257,7 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
     rows = S if src is None else src.numel()
     op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, src, rows, halves, eps)
     on = _Stream(stream, q)
+    dtype, device = q.dtype, q.get_device()
     ins, outs, res = [], [], []
     for x, y, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
         if x is None:
@@ -272,11 +270,11 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
         if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.shape[2] == 0:
             raise ValueError("%s must be [B, S, H, D]" % name)
         H = x.shape[2]
-        ins.append(_heads(x, name, (B, S, H, D), q, transposed=True))
+        ins.append(_heads(x, name, (B, S, H, D), dtype, device, True))
         shape = (B, H, rows, D)
         if y is None:
-            y = on.make(torch.empty, shape, dtype=q.dtype, device=q.device)
-        outs.append(_heads(y, name + "_out", shape, q))
+            y = on.make(torch.empty, shape, dtype=dtype, device=q.device)
+        outs.append(_heads(y, name + "_out", shape, dtype, device))
         res.append(y)
     _call("vsa_norm_rope_fwd", op, *ins, *outs, on.handle)
     return tuple(res)
@@ -300,6 +298,7 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
         raise ValueError("dq_out has %d rows for %d tokens, without dst" % (rows, S))
     op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, dst, S, halves, eps)
     on = _Stream(stream, q)
+    dtype, device = q.dtype, q.get_device()
     dys, xs, dxs, res, dws = [], [], [], [], []
     for dy, x, dx, w, name in ((dq_out, q, dq, q_weight, "q"), (dk_out, k, dk, k_weight, "k"),
                                (dv_out, None, dv, None, "v")):
@@ -316,17 +315,17 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
         if not isinstance(dy, torch.Tensor) or dy.dim() != 4 or dy.shape[1] == 0:
             raise ValueError("d%s_out must be [B, H, rows, D]" % name)
         H = dy.shape[1]
-        dys.append(_heads(dy, "d%s_out" % name, (B, H, rows, D), q))
+        dys.append(_heads(dy, "d%s_out" % name, (B, H, rows, D), dtype, device))
         shape = (B, S, H, D)
         if name != "v":
-            xs.append(_heads(x, name, shape, q, transposed=True))
+            xs.append(_heads(x, name, shape, dtype, device, True))
             dws.append(on.make(torch.empty_like, w) if w is not None and need_dweight else None)
         if dx is None:
-            dx = on.make(torch.empty, shape, dtype=q.dtype, device=q.device)
-        dxs.append(_heads(dx, "d" + name, shape, q, transposed=True))
+            dx = on.make(torch.empty, shape, dtype=dtype, device=q.device)
+        dxs.append(_heads(dx, "d" + name, shape, dtype, device, True))
         res.append(dx)
     dwq, dwk = dws
-    need = 0 if dwq is None and dwk is None else _norm_workspace(q.get_device(), D)
+    need = 0 if dwq is None and dwk is None else _norm_workspace(device, D)
     keep, wp, wn = on.workspace(workspace, need, q)
     _call("vsa_norm_rope_bwd", op, *dys, *xs, *dxs, None if dwq is None else dwq.data_ptr(),
           None if dwk is None else dwk.data_ptr(), wp, wn, on.handle)
@@ -380,9 +379,8 @@ def rotation_table(positions, rot, theta=10000.0, device="cuda"):
 def _cross_op(q, k, kv_len, sm_scale):
     """(packed vsa_cross, its sizes)."""
     _cuda(q, "q")
-    _cuda(k, "k")
-    if q.dtype is not torch.bfloat16:
-        raise TypeError("q must be torch.bfloat16, got %s" % q.dtype)
+    if not isinstance(k, torch.Tensor) or k.dim() != 4 or k.numel() == 0:
+        raise ValueError("k must be a 4-D tensor with elements")
     B, H, Sq, D = q.shape
     _, Hk, Sk, _ = k.shape
     if D != vsa.HEAD_DIM:
@@ -395,6 +393,10 @@ def _cross_op(q, k, kv_len, sm_scale):
         raise ValueError("sm_scale must be finite")
     sizes = (B, H, Hk, Sq, Sk, D)
     return _pack_cross(*sizes, sm_scale, _vector(kv_len, "kv_len", torch.int32, B, q)), sizes
+
+
+def _operand(t, name, shape, device):
+    return _heads(t, name, shape, torch.bfloat16, device, False, True)
 
 
 def _lse(lse, shape, like):
@@ -418,12 +420,11 @@ def vsa_cross_fwd(q, k, v, kv_len=None, sm_scale=None, o=None, lse=None, workspa
         o = on.make(torch.empty_like, q)
     if lse is None:
         lse = on.make(torch.empty, (B, H, Sq), dtype=torch.float32, device=q.device)
-    qs, ks = (B, H, Sq, D), (B, Hk, Sk, D)
-    args = (_heads(q, "q", qs, q, whole=True), _heads(k, "k", ks, q, whole=True),
-            _heads(v, "v", ks, q, whole=True), _heads(o, "o", qs, q, whole=True),
-            _lse(lse, qs[:3], q))
+    qs, ks, device = (B, H, Sq, D), (B, Hk, Sk, D), q.get_device()
+    args = (_operand(q, "q", qs, device), _operand(k, "k", ks, device), _operand(v, "v", ks, device),
+            _operand(o, "o", qs, device), _lse(lse, qs[:3], q))
     keep, wp, wn = on.workspace(workspace, _cross_workspace("vsa_cross_fwd_workspace_bytes",
-                                                            q.get_device(), *sizes), q)
+                                                            device, *sizes), q)
     _call("vsa_cross_fwd", op, *args, wp, wn, on.handle)
     return o, lse
 
@@ -439,14 +440,13 @@ def vsa_cross_bwd(dout, q, k, v, o, lse, kv_len=None, sm_scale=None, dq=None, dk
     dq = on.make(torch.empty_like, q) if dq is None else dq
     dk = on.make(torch.empty_like, k) if dk is None else dk
     dv = on.make(torch.empty_like, v) if dv is None else dv
-    qs, ks = (B, H, Sq, D), (B, Hk, Sk, D)
-    args = (_heads(dout, "dout", qs, q, whole=True), _heads(q, "q", qs, q, whole=True),
-            _heads(k, "k", ks, q, whole=True), _heads(v, "v", ks, q, whole=True),
-            _heads(o, "o", qs, q, whole=True), _lse(lse, qs[:3], q),
-            _heads(dq, "dq", qs, q, whole=True), _heads(dk, "dk", ks, q, whole=True),
-            _heads(dv, "dv", ks, q, whole=True))
+    qs, ks, device = (B, H, Sq, D), (B, Hk, Sk, D), q.get_device()
+    args = (_operand(dout, "dout", qs, device), _operand(q, "q", qs, device),
+            _operand(k, "k", ks, device), _operand(v, "v", ks, device),
+            _operand(o, "o", qs, device), _lse(lse, qs[:3], q), _operand(dq, "dq", qs, device),
+            _operand(dk, "dk", ks, device), _operand(dv, "dv", ks, device))
     keep, wp, wn = on.workspace(workspace, _cross_workspace("vsa_cross_bwd_workspace_bytes",
-                                                            q.get_device(), *sizes), q)
+                                                            device, *sizes), q)
     _call("vsa_cross_bwd", op, *args, wp, wn, on.handle)
     return dq, dk, dv
 
