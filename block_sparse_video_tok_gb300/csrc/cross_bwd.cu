@@ -685,22 +685,30 @@ __global__ void __launch_bounds__(TILE) cross_dq_join_kernel(const __grid_consta
 
 namespace dkv {
 
-// A Q tile is held from S^T to dK of the same step (with the next S^T in between), a dO tile from
-// dP^T to dV.
 constexpr int NUM_THREADS = 640;
-constexpr int Q_STAGES = 3, DO_STAGES = 2;
-constexpr uint32_t SM_K = 0, SM_V = TILE_BYTES, SM_Q = 2 * TILE_BYTES, SM_DO = SM_Q + Q_STAGES * TILE_BYTES;
-constexpr uint32_t SM_LSE = SM_DO + DO_STAGES * TILE_BYTES;  // 2 stages of -lse of 128 rows, fp32
-constexpr uint32_t SM_DELTA = SM_LSE + 2 * TILE * 4;         // -Delta of 128 rows
+
+// How the seven tiles of shared memory are used.  Many query tiles a unit: a Q tile is held from
+// S^T to dK of the same step (with the next S^T in between), a dO tile from dP^T to dV, and the
+// unit's output goes through K's space.  One query tile a unit (FEW; with one Q buffer a second
+// S^T would wait for the first dK, which comes after it): what counts is the next unit's K and V,
+// which get a second buffer, and the output has a space of its own.
+template <bool FEW>
+struct Stages {
+  static constexpr int KV = FEW ? 2 : 1, Q = FEW ? 1 : 3, DO = FEW ? 1 : 2;
+  static constexpr uint32_t SM_K = 0, SM_V = KV * TILE_BYTES, SM_Q = 2 * KV * TILE_BYTES, SM_DO = SM_Q + Q * TILE_BYTES;
+  static constexpr uint32_t SM_OUT = FEW ? SM_DO + DO * TILE_BYTES : SM_K;  // 16 warps x 2 KB
+};
+constexpr uint32_t SM_LSE = 7 * TILE_BYTES;           // 2 stages of -lse of 128 rows, fp32
+constexpr uint32_t SM_DELTA = SM_LSE + 2 * TILE * 4;  // -Delta of 128 rows
 constexpr uint32_t SM_BAR = SM_DELTA + TILE * 4;
 enum Bar : uint32_t {
-  KV_FULL = 0,
-  KV_EMPTY,  // the warps that write the unit out (through K's space)
-  Q_FULL0,
-  Q_EMPTY0 = Q_FULL0 + Q_STAGES,
-  DO_FULL0 = Q_EMPTY0 + Q_STAGES,
-  DO_EMPTY0 = DO_FULL0 + DO_STAGES,
-  LSE_FULL0 = DO_EMPTY0 + DO_STAGES,
+  KV_FULL0 = 0,
+  KV_EMPTY0 = KV_FULL0 + 2,  // FEW: the tensor core; else the warps that write the unit out
+  Q_FULL0 = KV_EMPTY0 + 2,
+  Q_EMPTY0 = Q_FULL0 + 3,
+  DO_FULL0 = Q_EMPTY0 + 3,
+  DO_EMPTY0 = DO_FULL0 + 2,
+  LSE_FULL0 = DO_EMPTY0 + 2,
   DELTA_FULL = LSE_FULL0 + 2,
   LSE_EMPTY0,
   DELTA_EMPTY = LSE_EMPTY0 + 2,
@@ -740,10 +748,12 @@ __device__ __forceinline__ Unit decode(const Params& p, int w) {
   return u;
 }
 
+template <bool FEW>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     cross_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ Params p) {
+  using T = Stages<FEW>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM_ABORT);
@@ -754,7 +764,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (threadIdx.x == 0) {
     *abort = 0;
     for (uint32_t b = 0; b < NUM_BARS; ++b) {
-      const bool many = b == KV_EMPTY || b == P_READY || b == DS_READY || b == ACC_EMPTY ||
+      const bool many = (!FEW && b >= KV_EMPTY0 && b < Q_FULL0) || b == P_READY || b == DS_READY || b == ACC_EMPTY ||
                         (b >= LSE_EMPTY0 && b < S_FULL);
       mbar_init(bar(b), many ? SOFTMAX_WARPS : 1);
     }
@@ -773,8 +783,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // Short tiles: the rows up to the next multiple of 64, which no copy writes, are multiplied as
   // zeros.
   const int full_rows = p.t.box * p.t.pack;
-  if (full_rows % 64 != 0 && warp >= SOFTMAX_WARP && warp < SOFTMAX_WARP + Q_STAGES + DO_STAGES)
-    zero_rows(base + SM_Q + (warp - SOFTMAX_WARP) * TILE_BYTES, full_rows, ceil64(full_rows), lane);
+  if (full_rows % 64 != 0 && warp >= SOFTMAX_WARP && warp < SOFTMAX_WARP + T::Q + T::DO)
+    zero_rows(base + T::SM_Q + (warp - SOFTMAX_WARP) * TILE_BYTES, full_rows, ceil64(full_rows), lane);
   grid_dependency_wait();
   tc_fence_before_sync();
   __syncthreads();
@@ -786,7 +796,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // Rows are keys, columns query rows.
     const int quarter = warp & 3, col = (warp - SOFTMAX_WARP) >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col * 32u;
-    const uint32_t stage = base + SM_K + (warp - SOFTMAX_WARP) * 2048u;
+    const uint32_t stage = base + T::SM_OUT + (warp - SOFTMAX_WARP) * 2048u;
     const float c1 = p.a.sm_scale * LOG2E_F;
     const uint64_t c2 = f2_pack(c1, c1);
     uint32_t x = 0, un = 0;
@@ -903,7 +913,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(ACC_EMPTY));
-        mbar_arrive(bar(KV_EMPTY));
+        if (!FEW) mbar_arrive(bar(KV_EMPTY0));
       }
       ++un;
     }
@@ -916,12 +926,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
       if (u.count() == 0) continue;
-      ok = warp_wait(bar(KV_EMPTY), (un & 1u) ^ 1u, abort, limit);
+      const uint32_t kv = un % T::KV;
+      ok = warp_wait(bar(KV_EMPTY0 + kv), ((un / T::KV) & 1u) ^ 1u, abort, limit);
       if (!ok) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar(KV_FULL), 2 * TILE_BYTES);
-        tma_load_5d(base + SM_K, &tm_k, bar(KV_FULL), 0, u.j * TILE, u.kh, 0, p.a.k.batch ? u.b : 0);
-        tma_load_5d(base + SM_V, &tm_v, bar(KV_FULL), 0, u.j * TILE, u.kh, 0, p.a.v.batch ? u.b : 0);
+        mbar_arrive_expect_tx(bar(KV_FULL0 + kv), 2 * TILE_BYTES);
+        tma_load_5d(base + T::SM_K + kv * TILE_BYTES, &tm_k, bar(KV_FULL0 + kv), 0, u.j * TILE, u.kh, 0,
+                    p.a.k.batch ? u.b : 0);
+        tma_load_5d(base + T::SM_V + kv * TILE_BYTES, &tm_v, bar(KV_FULL0 + kv), 0, u.j * TILE, u.kh, 0,
+                    p.a.v.batch ? u.b : 0);
       }
       __syncwarp();
       ++un;
@@ -929,26 +942,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int i = u.q0; i < u.q1; ++i) {
         int head, token;
         tile_origin(p, u.kh, i, &head, &token);
-        uint32_t s = qn % Q_STAGES;
-        ok = warp_wait(bar(Q_EMPTY0 + s), ((qn / Q_STAGES) & 1u) ^ 1u, abort, limit);
+        uint32_t s = qn % T::Q;
+        ok = warp_wait(bar(Q_EMPTY0 + s), ((qn / T::Q) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
-        if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + SM_Q + s * TILE_BYTES, bar(Q_FULL0 + s), u.b, head, token);
+        if (lane == 0) load_q_tile(p, &tm_q, p.a.q.batch, base + T::SM_Q + s * TILE_BYTES, bar(Q_FULL0 + s), u.b, head, token);
         __syncwarp();
         ++qn;
-        s = dn % DO_STAGES;
-        ok = warp_wait(bar(DO_EMPTY0 + s), ((dn / DO_STAGES) & 1u) ^ 1u, abort, limit);
+        s = dn % T::DO;
+        ok = warp_wait(bar(DO_EMPTY0 + s), ((dn / T::DO) & 1u) ^ 1u, abort, limit);
         if (!ok) break;
         if (lane == 0)
-          load_q_tile(p, &tm_do, p.a.dout.batch, base + SM_DO + s * TILE_BYTES, bar(DO_FULL0 + s), u.b, head, token);
+          load_q_tile(p, &tm_do, p.a.dout.batch, base + T::SM_DO + s * TILE_BYTES, bar(DO_FULL0 + s), u.b, head, token);
         __syncwarp();
         ++dn;
       }
     }
     if (!ok && lane == 0) {
       raise_abort(abort, p.a.err);
-      drain_copies(bar(KV_FULL), 1, un);  // let the copies already issued land
-      drain_copies(bar(Q_FULL0), Q_STAGES, qn);
-      drain_copies(bar(DO_FULL0), DO_STAGES, dn);
+      drain_copies(bar(KV_FULL0), T::KV, un);  // let the copies already issued land
+      drain_copies(bar(Q_FULL0), T::Q, qn);
+      drain_copies(bar(DO_FULL0), T::DO, dn);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -1005,16 +1018,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------------ UMMA issuer
     // Turn i of a unit: dV(i - 1), S^T(i), dK(i - 1), dP^T(i).  P^T lies over S^T and dS^T over
     // dP^T, and products of one thread run in order.  Columns and rows count in halves of 64.
-    const uint64_t k_desc = sdesc_sw128(base + SM_K, 16, 1024), v_desc = sdesc_sw128(base + SM_V, 16, 1024);
-    const uint64_t q_desc = sdesc_sw128(base + SM_Q, 16, 1024), do_desc = sdesc_sw128(base + SM_DO, 16, 1024);
-    const uint64_t q_mn = sdesc_sw128(base + SM_Q, TILE_BYTES / 2, 1024), do_mn = sdesc_sw128(base + SM_DO, TILE_BYTES / 2, 1024);
+    const uint64_t k_desc = sdesc_sw128(base + T::SM_K, 16, 1024), v_desc = sdesc_sw128(base + T::SM_V, 16, 1024);
+    const uint64_t q_desc = sdesc_sw128(base + T::SM_Q, 16, 1024), do_desc = sdesc_sw128(base + T::SM_DO, 16, 1024);
+    const uint64_t q_mn = sdesc_sw128(base + T::SM_Q, TILE_BYTES / 2, 1024), do_mn = sdesc_sw128(base + T::SM_DO, TILE_BYTES / 2, 1024);
     uint32_t x = 0, un = 0;                 // steps begun; units
     uint32_t qs = 0, qph = 0, pqs = 0;      // Q stage and its phase; the last step's stage
     bool ok = true, issued = false;
     for (int w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
       const Unit u = decode(p, w);
       if (u.count() == 0) continue;
-      ok = warp_wait(bar(KV_FULL), un & 1u, abort, limit);
+      const uint32_t kv = un % T::KV;
+      ok = warp_wait(bar(KV_FULL0 + kv), (un / T::KV) & 1u, abort, limit);
       int prev = 0;  // rows (in halves of 64) of the last step
 #pragma unroll 1
       for (int i = u.q0; ok && i <= u.q1; ++i) {
@@ -1033,15 +1047,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tc_fence_after_sync();
 #pragma unroll 1
           for (int h = 0; h * 64 < prev; ++h)
-            product_ts64<32>(tmem + TM_DV, tmem + TM_S + h * 64u, sdesc_advance(do_mn, (y & 1u) * TILE_BYTES + h * 8192u),
+            product_ts64<32>(tmem + TM_DV, tmem + TM_S + h * 64u, sdesc_advance(do_mn, (y % T::DO) * TILE_BYTES + h * 8192u),
                              IDESC_ACC, i == u.q0 + 1 && h == 0 ? 0u : 1u);
-          umma_commit_elect(bar(DO_EMPTY0 + (y & 1u)));
+          umma_commit_elect(bar(DO_EMPTY0 + y % T::DO));
         }
         if (rows > 0) {
           ok = warp_wait(bar(Q_FULL0 + qs), qph, abort, limit);
           if (!ok) break;
           tc_fence_after_sync();
-          product_ss(tmem + TM_S, k_desc, sdesc_advance(q_desc, qs * TILE_BYTES), idesc);
+          product_ss(tmem + TM_S, sdesc_advance(k_desc, kv * TILE_BYTES), sdesc_advance(q_desc, qs * TILE_BYTES), idesc);
           umma_commit_elect(bar(S_FULL));
           issued = true;
         }
@@ -1056,14 +1070,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           umma_commit_elect(bar(Q_EMPTY0 + pqs));
         }
         if (rows > 0) {
-          ok = warp_wait(bar(DO_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit);
+          ok = warp_wait(bar(DO_FULL0 + x % T::DO), (x / T::DO) & 1u, abort, limit);
           if (!ok) break;
           tc_fence_after_sync();
-          product_ss(tmem + TM_DP, v_desc, sdesc_advance(do_desc, (x & 1u) * TILE_BYTES), idesc);
+          product_ss(tmem + TM_DP, sdesc_advance(v_desc, kv * TILE_BYTES),
+                     sdesc_advance(do_desc, (x % T::DO) * TILE_BYTES), idesc);
           umma_commit_elect(bar(DP_FULL));
           ++x;
           pqs = qs;
-          if (++qs == Q_STAGES) {
+          if (++qs == T::Q) {
             qs = 0;
             qph ^= 1u;
           }
@@ -1072,6 +1087,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
       umma_commit_elect(bar(ACC_FULL));
+      if (FEW) umma_commit_elect(bar(KV_EMPTY0 + kv));
       ++un;
     }
     if (!ok && lane == 0) raise_abort(abort, p.a.err);
@@ -1173,9 +1189,11 @@ cudaError_t launch_cross_bwd(const CrossArgs& a, cudaStream_t stream) {
   if ((e = make_tmap_heads(&to, a.o, a.q_tokens, a.batch, p.t.box, p.t.pack)) != cudaSuccess) return e;
   if ((e = make_tmap_heads(&tk, a.k, a.kv_tokens, a.batch, TILE, 1)) != cudaSuccess) return e;
   if ((e = make_tmap_heads(&tv, a.v, a.kv_tokens, a.batch, TILE, 1)) != cudaSuccess) return e;
-  static std::atomic<uint64_t> dq_smem{0}, dkv_smem{0};
+  static std::atomic<uint64_t> dq_smem{0}, dkv_smem{0}, dkv_few_smem{0};
   if ((e = ensure_smem_limit(dq::cross_dq_kernel, static_cast<int>(dq::SMEM_BYTES), dq_smem)) != cudaSuccess) return e;
-  if ((e = ensure_smem_limit(dkv::cross_dkv_kernel, static_cast<int>(dkv::SMEM_BYTES), dkv_smem)) != cudaSuccess) return e;
+  if ((e = ensure_smem_limit(dkv::cross_dkv_kernel<false>, static_cast<int>(dkv::SMEM_BYTES), dkv_smem)) != cudaSuccess ||
+      (e = ensure_smem_limit(dkv::cross_dkv_kernel<true>, static_cast<int>(dkv::SMEM_BYTES), dkv_few_smem)) != cudaSuccess)
+    return e;
   const int sms = device_sm_count(), bk = a.batch * a.kv_heads;
   p.by_tiles = make_divisor(p.t.tiles);
   p.by_kv_tiles = make_divisor(p.kv_tiles);
@@ -1195,7 +1213,8 @@ cudaError_t launch_cross_bwd(const CrossArgs& a, cudaStream_t stream) {
   p.splits = plan.dkv_splits;
   p.by_splits = make_divisor(p.splits);
   p.total = bk * p.kv_tiles * p.splits;
-  e = launch_dependent(dkv::cross_dkv_kernel, dim3(p.total < sms ? p.total : sms), dim3(dkv::NUM_THREADS), dkv::SMEM_BYTES, stream,
+  const bool few = p.t.tiles <= p.splits && p.total > sms;  // one query tile a unit, several units a CTA
+  e = launch_dependent(few ? dkv::cross_dkv_kernel<true> : dkv::cross_dkv_kernel<false>, dim3(p.total < sms ? p.total : sms), dim3(dkv::NUM_THREADS), dkv::SMEM_BYTES, stream,
                        tq, td, tk, tv, p);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_dependent(dkv::cross_dkv_join_kernel, dim3(bk * p.kv_tiles, 16, 2), dim3(TILE), 0, stream, p);
