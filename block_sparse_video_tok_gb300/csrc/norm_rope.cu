@@ -19,8 +19,12 @@ namespace vsa {
 
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int UNROLL = 4;  // heads in flight per group of lanes
+// Heads in flight per group of lanes, and what the backward's registers leave room for: 6 heads and
+// four CTAs of 128 threads per SM.  (12 heads of 128, bf16: forward of 131040 tokens 388 us, 99 % of
+// the measured copy rate, with 4 heads 394; backward of 2 x 32760 266 us, 90 %, with 4 heads 287,
+// with 8 heads 340.)
+constexpr int THREADS = 128, BWD_CTAS = 4;
+constexpr int UNROLL = 6;
 constexpr unsigned FULL = 0xffffffffu;
 
 // 8 elements as loaded (16 or 32 bytes), widened where they are used: a lane keeps several heads'
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(THREADS) norm_rope_fwd_kernel(const Params p) 
 }
 
 template <typename T, typename W, int LPR, bool HALVES>
-__global__ void __launch_bounds__(THREADS, 2) norm_rope_bwd_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, BWD_CTAS) norm_rope_bwd_kernel(const Params p) {
   __shared__ float sums[THREADS / LPR][LPR * 8];
   grid_dependency_wait();
   const NormRopeArgs& a = p.a;
@@ -362,9 +366,10 @@ int head_chunks(int64_t blocks, int heads) {
   return static_cast<int>(c < heads ? c : heads);
 }
 
-// CTAs of the backward: four resident per SM, each leaving one partial sum of dw.  head_chunks
+// CTAs of the backward: as many as are resident, each leaving one partial sum of dw.  head_chunks
 // keeps within it too: x blocks < 2 SMs become x ceil(2 SMs / x) < x + 2 SMs < 4 SMs.
-int max_ctas() { return 4 * device_sm_count(); }
+int max_ctas() { return BWD_CTAS * device_sm_count(); }
+static_assert(BWD_CTAS >= 4, "head_chunks");
 
 struct BwdGrid {
   int x, y, chunk;
