@@ -68,24 +68,17 @@ cudaError_t make_tmap_heads(CUtensorMap* map, const HeadsView& x, int tokens, in
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Wait of a converged warp for the phase of `bar` with the given parity; false if *abort was
-// raised or `limit_ns` of wall time passed.  Every lane polls, and the clock and *abort are looked
-// at once in POLLS probes: reading the global timer between probes held a warp for hundreds of
-// cycles after its barrier had completed.  The loop is a function of its own, not a copy in each
-// of some twenty places: the code of all roles shares the instruction caches.
-constexpr int POLLS = 64;
+// raised or `limit_ns` of wall time passed (a probe that fails has been suspended for a while, so
+// the clock is read seldom).  The loop is a function of its own, not a copy in each of some twenty
+// places: the code of all roles shares the instruction caches.
 static __device__ __noinline__ bool warp_poll(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   uint64_t t0 = 0;
-  while (true) {
-    bool ok;
-    int i = 0;
-    do {
-      ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
-    } while (!ok && ++i < POLLS);
-    if (ok) return true;
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
     if (__any_sync(0xffffffffu, *abort != 0 || t - t0 > limit_ns)) return false;
   }
+  return true;
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
