@@ -182,9 +182,11 @@ enum Bar : uint32_t {
   DS_READY0,  // two buffers
   DQ_FULL = DS_READY0 + 2,
   DQ_EMPTY,
-  LSE_FULL,    // per unit
-  DELTA_FULL,
-  K_TAIL,
+  // One for even and one for odd units: a warp that fills may be a unit ahead of another that fills
+  // or of one that waits, and two phases ahead of neither.
+  LSE_FULL0,
+  DELTA_FULL0 = LSE_FULL0 + 2,
+  K_TAIL = DELTA_FULL0 + 2,
   DRAIN,
   NUM_BARS
 };
@@ -234,8 +236,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t count = 1;
       if (b == S_FREE || b == DP_FREE || b == DS_READY0 || b == DS_READY0 + 1) count = SOFTMAX_WARPS;
       if (b == DO_EMPTY) count = 9;
-      if (b == DQ_EMPTY || b == DELTA_FULL) count = 8;
-      if (b == LSE_FULL) count = 4;
+      if (b == DQ_EMPTY || b == DELTA_FULL0 || b == DELTA_FULL0 + 1) count = 8;
+      if (b == LSE_FULL0 || b == LSE_FULL0 + 1) count = 4;
       mbar_init(bar(b), count);
     }
     fence_barrier_init();
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const float lse = r < rows ? p.a.lse[row + static_cast<int64_t>(rh) * p.a.q_tokens + rt] : 0.f;
           to_lse[r] = lse == -INFINITY ? 0.f : -lse;  // all scores -inf: P = 2^-inf = 0
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(LSE_FULL));
+          if (lane == 0) mbar_arrive(bar(LSE_FULL0 + (un & 1u)));
         }
         ok = warp_wait(bar(DO_FULL), un & 1u, abort, limit);
         if (!ok) break;
@@ -332,8 +334,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         __syncwarp();
         if (lane == 0) {
+          mbar_arrive(bar(DELTA_FULL0 + (un & 1u)));
           mbar_arrive(bar(DO_EMPTY));
-          mbar_arrive(bar(DELTA_FULL));
         }
         ++un;
       }
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Unit u = decode(p, w);
       const int n = u.count();
       if (n == 0) continue;
-      ok = warp_wait(bar(LSE_FULL), un & 1u, abort, limit);
+      ok = warp_wait(bar(LSE_FULL0 + (un & 1u)), (un >> 1) & 1u, abort, limit);
       if (!ok) break;
       const float nl = reinterpret_cast<const float*>(smem + SM_LSE)[(un & 1u) * TILE + r];
       float nd = 0.f;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           pr[i + 1] = ex2(a1);
         }
         if (j == 0) {
-          ok = warp_wait(bar(DELTA_FULL), un & 1u, abort, limit);
+          ok = warp_wait(bar(DELTA_FULL0 + (un & 1u)), (un >> 1) & 1u, abort, limit);
           if (!ok) break;
           nd = reinterpret_cast<const float*>(smem + SM_DELTA)[(un & 1u) * TILE + r];
         }
