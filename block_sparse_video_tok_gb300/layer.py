@@ -25,6 +25,8 @@ from .workloads import VIDEO_CUBE
 DEVERR_ORDER = 0x40
 DEVERR_KV_LEN = 0x80
 
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # device index -> stream handle
+
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
@@ -158,33 +160,23 @@ def _vector(t, name, dtype, n, like):
     return t.data_ptr()
 
 
-class _Stream:
-    """Where a call runs: its handle, and allocations made on it."""
+def _on(stream, f, *args, **kwargs):
+    """f with `stream` as the current one, so that what it allocates belongs to it."""
+    with torch.cuda.stream(stream):
+        return f(*args, **kwargs)
 
-    __slots__ = ("stream", "handle")
 
-    def __init__(self, stream, like):
-        self.stream = stream
-        self.handle = torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None \
-            else stream.cuda_stream
-
-    def make(self, f, *args, **kwargs):
-        if self.stream is None:
-            return f(*args, **kwargs)
-        with torch.cuda.stream(self.stream):
-            return f(*args, **kwargs)
-
-    def workspace(self, given, need, like):
-        """(workspace tensor, address, bytes); allocated if not given."""
-        if need == 0:
-            return None, None, 0
-        if given is None:
-            given = self.make(torch.empty, need, dtype=torch.uint8, device=like.device)
-            return given, given.data_ptr(), need
-        if not isinstance(given, torch.Tensor) or given.get_device() != like.get_device() or \
-                not given.is_contiguous():
-            raise TypeError("workspace must be a contiguous tensor on %s" % like.device)
-        return given, given.data_ptr(), given.numel() * given.element_size()
+def _workspace(given, need, like):
+    """(workspace tensor, address, bytes); allocated if not given."""
+    if need == 0:
+        return None, None, 0
+    if given is None:
+        given = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return given, given.data_ptr(), need
+    if not isinstance(given, torch.Tensor) or given.get_device() != like.get_device() or \
+            not given.is_contiguous():
+        raise TypeError("workspace must be a contiguous tensor on %s" % like.device)
+    return given, given.data_ptr(), given.numel() * given.element_size()
 
 
 @functools.lru_cache(maxsize=256)
@@ -252,12 +244,14 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
     first rot elements of a head are turned, in pairs (2i, 2i + 1) or, with halves, (i, i + rot/2).
     src: int32 [rows], the token of each output row, -1 for a row of zeros (None: row t is token
     t).  Returns (q_out, k_out, v_out), [B, H, rows, D]; None where the input is None."""
+    if stream is not None:
+        return _on(stream, vsa_norm_rope, q, k, v, q_weight, k_weight, cos, sin, src, halves, eps,
+                   q_out, k_out, v_out)
     _cuda(q, "q")
     B, S, _, D = q.shape
     rows = S if src is None else src.numel()
     op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, src, rows, halves, eps)
-    on = _Stream(stream, q)
-    dtype, device = q.dtype, q.get_device()
+    dtype, where, device = q.dtype, q.device, q.get_device()
     ins, outs, res = [], [], []
     for x, y, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
         if x is None:
@@ -271,12 +265,13 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
             raise ValueError("%s must be [B, S, H, D]" % name)
         H = x.shape[2]
         ins.append(_heads(x, name, (B, S, H, D), dtype, device, True))
-        shape = (B, H, rows, D)
         if y is None:
-            y = on.make(torch.empty, shape, dtype=dtype, device=q.device)
-        outs.append(_heads(y, name + "_out", shape, dtype, device))
+            y = torch.empty((B, H, rows, D), dtype=dtype, device=where)
+            outs.append(_pack_heads(y.data_ptr(), H * rows * D, rows * D, D, H))
+        else:
+            outs.append(_heads(y, name + "_out", (B, H, rows, D), dtype, device))
         res.append(y)
-    _call("vsa_norm_rope_fwd", op, *ins, *outs, on.handle)
+    _call("vsa_norm_rope_fwd", op, *ins, *outs, _current(device))
     return tuple(res)
 
 
@@ -288,6 +283,9 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
     each token, -1 for a token that no row takes (None: row t).  Returns (dq, dk, dv, dq_weight,
     dk_weight): dq, dk, dv in token order [B, S, H, D]; weight gradients in the weights' type, None
     for a weight that is None (or with need_dweight false)."""
+    if stream is not None:
+        return _on(stream, vsa_norm_rope_bwd, dq_out, dk_out, dv_out, q, k, q_weight, k_weight, cos,
+                   sin, dst, halves, eps, dq, dk, dv, need_dweight, workspace)
     _cuda(q, "q")
     _cuda(dq_out, "dq_out")
     if (k is None) != (dk_out is None):
@@ -297,8 +295,7 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
     if dst is None and rows != S:
         raise ValueError("dq_out has %d rows for %d tokens, without dst" % (rows, S))
     op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, dst, S, halves, eps)
-    on = _Stream(stream, q)
-    dtype, device = q.dtype, q.get_device()
+    dtype, where, device = q.dtype, q.device, q.get_device()
     dys, xs, dxs, res, dws = [], [], [], [], []
     for dy, x, dx, w, name in ((dq_out, q, dq, q_weight, "q"), (dk_out, k, dk, k_weight, "k"),
                                (dv_out, None, dv, None, "v")):
@@ -319,16 +316,18 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
         shape = (B, S, H, D)
         if name != "v":
             xs.append(_heads(x, name, shape, dtype, device, True))
-            dws.append(on.make(torch.empty_like, w) if w is not None and need_dweight else None)
+            dws.append(torch.empty_like(w) if w is not None and need_dweight else None)
         if dx is None:
-            dx = on.make(torch.empty, shape, dtype=dtype, device=q.device)
-        dxs.append(_heads(dx, "d" + name, shape, dtype, device, True))
+            dx = torch.empty(shape, dtype=dtype, device=where)
+            dxs.append(_pack_heads(dx.data_ptr(), S * H * D, D, H * D, H))
+        else:
+            dxs.append(_heads(dx, "d" + name, shape, dtype, device, True))
         res.append(dx)
     dwq, dwk = dws
     need = 0 if dwq is None and dwk is None else _norm_workspace(device, D)
-    keep, wp, wn = on.workspace(workspace, need, q)
+    keep, wp, wn = _workspace(workspace, need, q)
     _call("vsa_norm_rope_bwd", op, *dys, *xs, *dxs, None if dwq is None else dwq.data_ptr(),
-          None if dwk is None else dwk.data_ptr(), wp, wn, on.handle)
+          None if dwk is None else dwk.data_ptr(), wp, wn, _current(device))
     return (*res, dwq, dwk)
 
 
@@ -413,19 +412,20 @@ def vsa_cross_fwd(q, k, v, kv_len=None, sm_scale=None, o=None, lse=None, workspa
     """Attention of q [B, H, Sq, 128] to k, v [B, Hk, Sk, 128] (bf16; H a multiple of Hk), over the
     first kv_len[b] keys (int32 [B]; None: all).  sm_scale defaults to 1/sqrt(128).  Returns (o in
     q's memory order, lse fp32 [B, H, Sq], base 2); without a visible key o = 0 and lse = -inf."""
+    if stream is not None:
+        return _on(stream, vsa_cross_fwd, q, k, v, kv_len, sm_scale, o, lse, workspace)
     op, sizes = _cross_op(q, k, kv_len, sm_scale)
     B, H, Hk, Sq, Sk, D = sizes
-    on = _Stream(stream, q)
     if o is None:
-        o = on.make(torch.empty_like, q)
+        o = torch.empty_like(q)
     if lse is None:
-        lse = on.make(torch.empty, (B, H, Sq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
     qs, ks, device = (B, H, Sq, D), (B, Hk, Sk, D), q.get_device()
     args = (_operand(q, "q", qs, device), _operand(k, "k", ks, device), _operand(v, "v", ks, device),
             _operand(o, "o", qs, device), _lse(lse, qs[:3], q))
-    keep, wp, wn = on.workspace(workspace, _cross_workspace("vsa_cross_fwd_workspace_bytes",
-                                                            device, *sizes), q)
-    _call("vsa_cross_fwd", op, *args, wp, wn, on.handle)
+    keep, wp, wn = _workspace(workspace, _cross_workspace("vsa_cross_fwd_workspace_bytes", device,
+                                                          *sizes), q)
+    _call("vsa_cross_fwd", op, *args, wp, wn, _current(device))
     return o, lse
 
 
@@ -434,20 +434,22 @@ def vsa_cross_bwd(dout, q, k, v, o, lse, kv_len=None, sm_scale=None, dq=None, dk
     """Gradients of vsa_cross_fwd from dout, its inputs, and the o and lse that it returned.
     Returns (dq, dk, dv), each in its input's memory order; rows of dk and dv at or past
     kv_len[b] are exact zeros."""
+    if stream is not None:
+        return _on(stream, vsa_cross_bwd, dout, q, k, v, o, lse, kv_len, sm_scale, dq, dk, dv,
+                   workspace)
     op, sizes = _cross_op(q, k, kv_len, sm_scale)
     B, H, Hk, Sq, Sk, D = sizes
-    on = _Stream(stream, q)
-    dq = on.make(torch.empty_like, q) if dq is None else dq
-    dk = on.make(torch.empty_like, k) if dk is None else dk
-    dv = on.make(torch.empty_like, v) if dv is None else dv
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
     qs, ks, device = (B, H, Sq, D), (B, Hk, Sk, D), q.get_device()
     args = (_operand(dout, "dout", qs, device), _operand(q, "q", qs, device),
             _operand(k, "k", ks, device), _operand(v, "v", ks, device),
             _operand(o, "o", qs, device), _lse(lse, qs[:3], q), _operand(dq, "dq", qs, device),
             _operand(dk, "dk", ks, device), _operand(dv, "dv", ks, device))
-    keep, wp, wn = on.workspace(workspace, _cross_workspace("vsa_cross_bwd_workspace_bytes",
-                                                            device, *sizes), q)
-    _call("vsa_cross_bwd", op, *args, wp, wn, on.handle)
+    keep, wp, wn = _workspace(workspace, _cross_workspace("vsa_cross_bwd_workspace_bytes", device,
+                                                          *sizes), q)
+    _call("vsa_cross_bwd", op, *args, wp, wn, _current(device))
     return dq, dk, dv
 
 
