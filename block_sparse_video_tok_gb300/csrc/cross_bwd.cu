@@ -17,7 +17,18 @@
 //
 // Where the tiles are fewer than the SMs, the inner axis is split over CTAs (dq: the kv tiles,
 // dkv: the query tiles): each part leaves fp32 sums in the workspace, and join kernels add them in
-// part order.
+// part order (2 x 8 heads, 64 queries on 8191 keys: 52 us, without parts 103; 2 x 32 heads on 4 key
+// heads, 16 queries: 38 us, without parts 94, without packing the heads that share keys 91).
+//
+// Measured: 32760 queries on 512 keys, 12 heads: 246 us in short bursts (1.07 PFLOP/s of the five
+// products that the formulas have, 1.50 of the seven that are done), 266 us in a long run under
+// the power cap; dQ 132 us, dK and dV 113 us, the join 7 us.
+// What bounds dQ (tensor pipe 49 % active): an SM takes copies in at 34 to 45 bytes a cycle, and a
+// step's 64 KB of K and V with its share of a unit's Q, dO and O are 2000 to 2500 cycles against
+// 1554 of products; and its softmax warps are as long as its products (about 1580 cycles a step).
+// Tried without gain: K and V multicast to pairs of CTAs (137 us), fewer and larger hand-overs
+// (139), S, dQ, dP in this order, which frees a K tile earlier (148).
+// What bounds dK and dV (tensor pipe 76 % active): the four products, and copies of 64 KB a step.
 #include "cross_common.cuh"
 
 namespace vsa {
@@ -51,7 +62,7 @@ __device__ __forceinline__ void load32(uint32_t taddr, uint32_t* v) {
   tmem_wait_ld();
 }
 
-// A softmax warp's 32 rows x 32 columns of sums, scaled and rounded, to global memory: through 2
+// A dkv softmax warp's 32 rows x 32 columns of sums, scaled and rounded, to global memory: through 2
 // KB of shared memory, so that 64 consecutive bytes of a row leave together.  `at`: distance of
 // rows 8 i + lane / 4 from `out`, in elements; rows from `rows` on are not written.
 __device__ __forceinline__ void write_rows(uint32_t stage, const uint32_t* v, float scale, __nv_bfloat16* out,
@@ -693,7 +704,8 @@ constexpr int NUM_THREADS = 640;
 // S^T to dK of the same step (with the next S^T in between), a dO tile from dP^T to dV, and the
 // unit's output goes through K's space.  One query tile a unit (FEW; with one Q buffer a second
 // S^T would wait for the first dK, which comes after it): what counts is the next unit's K and V,
-// which get a second buffer, and the output has a space of its own.
+// which get a second buffer, and the output has a space of its own (2 x 8 heads, 64 queries on 8191
+// keys: the whole backward 52 us, with the other use of the tiles 59).
 template <bool FEW>
 struct Stages {
   static constexpr int KV = FEW ? 2 : 1, Q = FEW ? 1 : 3, DO = FEW ? 1 : 2;

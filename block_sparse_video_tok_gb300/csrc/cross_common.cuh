@@ -105,6 +105,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Softmax statistics (m, l) and O += weight of another part: f scales the old, w the new.
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2, float* f, float* w) {
+  const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
+  *f = ex2(m - ref);
+  *w = ex2(m2 - ref);
+  m = mn;
+  l = l * *f + l2 * *w;
+}
+
 // Packed fp32 pairs: one instruction on both halves of a 64-bit register pair.
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
   uint64_t r;

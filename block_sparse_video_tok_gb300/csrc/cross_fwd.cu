@@ -20,16 +20,26 @@
 // anything, are zeroed in shared memory before P (0 there) meets them.
 //
 // When there are fewer units than SMs the keys are split: each part leaves its unnormalised O
-// and (m, l) in the workspace, and cross_combine_kernel joins them in part order.
+// and (m, l) in the workspace, and cross_combine_kernel joins them in part order (2 x 8 heads, 64
+// queries on 8191 keys: 23 us, without parts 89).
 //
-// Roles (512 threads): warps 0-3 and 4-7 softmax groups; warps 8-11 output (one row of the tile
-// per thread: O / l, rounded, written), so that a group goes on to its next unit's scores while
-// its last O leaves; warp 12 TMEM owner and TMA producer of Q and K; warp 13 UMMA issuer; warp 14
-// TMA producer of V.
+// Roles (512 threads): warp 0 TMEM owner and TMA producer of Q and K; warp 1 UMMA issuer; warp 2 TMA
+// producer of V; warp 3 idle; warps 4-7 and 8-11 softmax groups; warps 12-15 output (one row of
+// the tile per thread: O / l, rounded, written), so that a group goes on to its next unit's scores
+// while its last O leaves.
 // Shared memory: a Q tile per group, 2 K and 2 V tiles, and 4 KB per output warp through which O
 // leaves in whole 128-byte lines.  A Q tile is free as soon as its unit's last S has been
 // computed, a softmax and a P V before the next unit needs it, and its successor has been
 // prefetched into L2 by then.  TMEM: O x2 [0, 256), S x2 [256, 512).
+//
+// Measured: 131040 queries on 512 keys, 12 heads: 277 us in short bursts (1.49 PFLOP/s, 78 % of the
+// measured burst peak), 307 us in a long run under the power cap (1.34, 78 % of the sustained
+// peak).  What bounds it: of the 1630 cycles that a kv tile of a group takes, its two products fill
+// 1036 of the tensor core (54 % active by counter, start and end included), its exponentials 512
+// of the special function units; the rest is the way from S through the softmax back to P V, which
+// the other group's products cover in part, and the copies at a unit's start (64 KB of Q, at 34 to
+// 45 bytes a cycle into an SM).  Tried without gain: P handed over in halves, registers moved
+// between the roles, K and V multicast to pairs of CTAs.
 #include "cross_common.cuh"
 
 namespace vsa {
@@ -560,49 +570,99 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == TMA_WARP) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of the keys: per row, M = max m, w = 2^(m - M), O = sum w O / sum w l.  A warp
-// handles 32 rows x 8 columns of a tile; a part without a visible key (l = 0) is not read.
-__global__ void __launch_bounds__(128) cross_combine_kernel(const __grid_constant__ Params p) {
+constexpr int JOIN_THREADS = 512;
+
+// Threads for the rows of a tile, and groups of them for `splits` parts: one for up to 12 parts
+// (three waits for loads), else as many as have 6 to 12 each.
+__host__ __device__ inline int join_width(const QTiles& t) {
+  const int rows = t.box * t.pack;
+  return rows > 64 ? 128 : rows > 32 ? 64 : 32;
+}
+inline int join_threads(const QTiles& t, int splits) {
+  int n = join_width(t);
+  while (n < JOIN_THREADS && n * 12 < splits * join_width(t)) n *= 2;
+  return n;
+}
+
+// Joins the parts of the keys: a CTA has 8 columns of a tile's rows.  Its threads are groups of as
+// many as the tile has rows (in 32, 64 or 128); group g takes parts g, g + groups, .., four parts'
+// loads at a time, and the groups are joined in shared memory in group order.  A part without a
+// visible key (l = 0) is not read.  (The latency of the loads is what counts: with all parts of a
+// row in one thread a single token of 8 heads on 32768 keys, 64 parts, took 8 us longer.)
+__global__ void __launch_bounds__(JOIN_THREADS) cross_combine_kernel(const __grid_constant__ Params p) {
+  __shared__ float sh_o[8][JOIN_THREADS];
+  __shared__ float2 sh_ml[JOIN_THREADS];
   grid_dependency_wait();
-  const int tile = blockIdx.x, lane = threadIdx.x & 31;
-  const int r = (threadIdx.x >> 5) * 32 + lane, c0 = blockIdx.y * 8;
+  const int width = join_width(p.t), groups = blockDim.x / width;
+  const int tile = blockIdx.x, r = threadIdx.x & (width - 1), g = threadIdx.x / width, c0 = blockIdx.y * 8;
   const int tiles = p.a.batch * p.a.kv_heads * p.t.tiles;
   const int x = tile % p.t.tiles, bk = tile / p.t.tiles, b = bk / p.a.kv_heads, kh = bk % p.a.kv_heads;
   const int rh = r / p.t.box;
   const int head = kh * p.t.share + x / p.t.blocks * p.t.pack + rh;
   const int token = x % p.t.blocks * p.t.box + r - rh * p.t.box;
-  if (rh >= p.t.pack || token >= p.a.q_tokens) return;
-  // The maximum over the parts first, so that the sums have no order of their own to wait for.
+  const bool valid = rh < p.t.pack && token < p.a.q_tokens;
   const float2* part_ml = p.part_ml + static_cast<int64_t>(tile) * TILE + r;
   const float* part_o = p.part_o + (static_cast<int64_t>(tile) * TILE + c0) * TILE + r;
   const int64_t step = static_cast<int64_t>(tiles) * TILE;
-  float mm = -INFINITY, l = 0.f, o[8] = {};
-#pragma unroll 8
-  for (int s = 0; s < p.splits; ++s) mm = fmaxf(mm, part_ml[s * step].x);
-  const float ref = mm == -INFINITY ? 0.f : mm;
+  float m = -INFINITY, l = 0.f, o[8] = {};
 #pragma unroll 1
-  for (int s0 = 0; s0 < p.splits; s0 += 4) {
-    float x[4][8], w[4];
+  for (int s0 = g; s0 < p.splits && valid; s0 += 4 * groups) {
+    float y[4][8];
+    float2 ml[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 ml = s0 + k < p.splits ? part_ml[(s0 + k) * step] : make_float2(-INFINITY, 0.f);
-      w[k] = ml.y == 0.f ? 0.f : ex2(ml.x - ref);  // NaN is kept
-      l += ml.y * w[k];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[k][i] = ml.y == 0.f ? 0.f : part_o[(s0 + k) * step * TILE + i * TILE];
+      const int s = s0 + k * groups;
+      ml[k] = s < p.splits ? part_ml[s * step] : make_float2(-INFINITY, 0.f);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] += x[k][i] * w[k];
+      for (int i = 0; i < 8; ++i) y[k][i] = ml[k].y == 0.f ? 0.f : part_o[(s0 + k * groups) * step * TILE + i * TILE];
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mn = fmaxf(mn, ml[k].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, f = ex2(m - ref);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = ml[k].y == 0.f ? 0.f : ex2(ml[k].x - ref);  // NaN is kept
+      l = fmaf(ml[k].y, w, l);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(y[k][i], w, o[i]);
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.o.data) + b * p.a.o.batch + head * p.a.o.head +
-                            token * p.a.o.token + c0) =
-      make_uint4(pack_bf162(o[0] * inv, o[1] * inv), pack_bf162(o[2] * inv, o[3] * inv),
-                 pack_bf162(o[4] * inv, o[5] * inv), pack_bf162(o[6] * inv, o[7] * inv));
-  if (c0 == 0)
-    p.a.lse[(static_cast<int64_t>(b) * p.a.heads + head) * p.a.q_tokens + token] = mm + log2f(l);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.o.data) + b * p.a.o.batch + head * p.a.o.head +
+                       token * p.a.o.token + c0;
+  float* lse = p.a.lse + (static_cast<int64_t>(b) * p.a.heads + head) * p.a.q_tokens + token;
+  if (groups == 1) {
+    if (!valid) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf162(o[0] * inv, o[1] * inv), pack_bf162(o[2] * inv, o[3] * inv),
+                                                pack_bf162(o[4] * inv, o[5] * inv), pack_bf162(o[6] * inv, o[7] * inv));
+    if (c0 == 0) *lse = m + log2f(l);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sh_o[i][threadIdx.x] = o[i];
+  sh_ml[threadIdx.x] = make_float2(m, l);
+  __syncthreads();
+  if (!valid) return;
+  for (int i = g; i < 8; i += groups) {
+    m = -INFINITY, l = 0.f;
+    float sum = 0.f;
+    for (int k = 0; k < groups; ++k) {
+      const float2 ml = sh_ml[k * width + r];
+      if (ml.y == 0.f) continue;
+      float f, w;
+      join(m, l, ml.x, ml.y, &f, &w);
+      sum = sum * f + sh_o[i][k * width + r] * w;
+    }
+    out[i] = __float2bfloat16_rn(l == 0.f ? 0.f : sum / l);
+    if (c0 + i == 0) *lse = m + log2f(l);
+  }
 }
 
 struct Plan {
@@ -665,7 +725,8 @@ cudaError_t launch_cross_fwd(const CrossArgs& a, cudaStream_t stream) {
   e = launch_dependent(cross_fwd_kernel, dim3(p.total < sms ? p.total : sms), dim3(NUM_THREADS), SMEM_BYTES, stream,
                        tq, tk, tv, p);
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_dependent(cross_combine_kernel, dim3(a.batch * a.kv_heads * p.t.tiles, 16), dim3(128), 0, stream, p);
+  return launch_dependent(cross_combine_kernel, dim3(a.batch * a.kv_heads * p.t.tiles, 16), dim3(join_threads(p.t, p.splits)), 0,
+                          stream, p);
 }
 
 }  // namespace vsa

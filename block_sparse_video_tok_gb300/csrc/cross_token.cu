@@ -1,12 +1,15 @@
-// cross_token.cu -- cross attention forward for a few query rows per key head (single tokens in
-// serving: one token, or the tokens of up to MAX_ROWS query heads that share a key head).
+// cross_token.cu -- cross attention forward for one or two query rows per key head (single tokens in
+// serving).
 //
 // Bound by the read of K and V, 512 bytes a key: each key is loaded once for all its rows, and the
 // arithmetic (about 20 instructions a row and two keys) stays on the CUDA cores, where fp32
 // products need no tile of 128 rows.  Half a warp holds a key's 128 columns, 8 a lane (16 bytes
 // of K and V each), with its own online softmax and O; KEYS keys per half-warp are in flight.  The
 // halves' results are joined in shared memory in a fixed order.  Where the (batch, key head) pairs
-// are fewer than the SMs, the keys are split over CTAs and a second kernel joins the parts.
+// are fewer than the SMs, the keys are split over CTAs and a second kernel joins the parts: 2 key
+// heads of 32768 keys take 12 us, in one part each 338.  Short calls are bound by latency (8 x 12
+// heads of 512 keys: 7.6 us), long ones by instructions and HBM (64 x
+// 8 heads of 2048 keys: 102 us, 5.3 TB/s).
 #include "cross_common.cuh"
 
 namespace vsa {
@@ -30,15 +33,6 @@ __device__ __forceinline__ void widen8(uint4 u, float* v) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
-}
-
-// (m, l) and O += weight of another part: f scales the old, w the new.
-__device__ __forceinline__ void join(float& m, float& l, float m2, float l2, float* f, float* w) {
-  const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
-  *f = ex2(m - ref);
-  *w = ex2(m2 - ref);
-  m = mn;
-  l = l * *f + l2 * *w;
 }
 
 template <int ROWS>
@@ -201,11 +195,14 @@ __global__ void __launch_bounds__(512) cross_token_join_kernel(const __grid_cons
   if (d == 0) p.a.lse[(static_cast<int64_t>(b) * p.a.heads + h) * p.a.q_tokens + t] = m + log2f(l);
 }
 
-constexpr int MAX_ROWS = 4;
+// Query rows of a key head that this kernel takes; more go to the kernel of 128-row tiles, whose
+// time does not depend on them.  (8 x 12 key heads of 512 keys: 1, 2, 4 rows 7.7, 9.1, 14.0 us here,
+// 10.5 there; 64 x 8 key heads of 2048 keys: 103, 102, 142 us here, 98 there; 2 of 32768 keys: 12.6
+// us here for one row, 24 there.)
+constexpr int MAX_ROWS = 2;
 
 // Parts of the keys: one while a CTA has few keys or the pairs fill the SMs; else two CTAs per SM
-// with at least 256 keys each.  (96 pairs of 512 keys: in two parts the second launch and the
-// workspace cost the host more than the GPU saves.)
+// with at least 256 keys each.  (96 pairs of 512 keys: 7.5 us in one part, 7.8 in two.)
 int token_splits(int64_t pairs, int kv_tokens) {
   int64_t s = 2LL * device_sm_count() / pairs;
   if (s > kv_tokens / 256) s = kv_tokens / 256;
@@ -240,8 +237,6 @@ cudaError_t launch_cross_token(const CrossArgs& a, cudaStream_t stream) {
   cudaError_t e;
   if (p.rows == 1)
     e = launch_dependent(cross_token_kernel<1>, grid, dim3(THREADS), 0, stream, p);
-  else if (p.rows == 2)
-    e = launch_dependent(cross_token_kernel<2>, grid, dim3(THREADS), 0, stream, p);
   else
     e = launch_dependent(cross_token_kernel<MAX_ROWS>, grid, dim3(THREADS), 0, stream, p);
   if (e != cudaSuccess || p.splits == 1) return e;

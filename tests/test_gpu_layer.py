@@ -215,6 +215,10 @@ CROSS_CASES = {
     "two_tokens_shared": dict(B=2, Sq=2, Sk=131, H=6, Hk=2),
     "token_long": dict(B=1, Sq=1, Sk=20011, H=8, Hk=2),
     "few_long": dict(B=1, Sq=5, Sk=9000, H=4, Hk=4, lens=[8191]),
+    "two_rows": dict(B=3, Sq=2, Sk=700, H=2, Hk=2, lens=[700, 0, 9]),
+    "two_rows_long": dict(B=1, Sq=1, Sk=5000, H=4, Hk=2),
+    "many_parts_64": dict(B=1, Sq=64, Sk=7000, H=2, Hk=2, lens=[6500]),
+    "many_parts_100": dict(B=1, Sq=100, Sk=7000, H=1, Hk=1),
     "few_64": dict(B=2, Sq=64, Sk=1500, H=3, Hk=3, lens=[1500, 1409]),
     "tile": dict(B=1, Sq=128, Sk=128, H=2, Hk=2),
     "tile_plus": dict(B=1, Sq=129, Sk=129, H=2, Hk=2),
