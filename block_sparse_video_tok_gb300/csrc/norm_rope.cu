@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(1024) norm_rope_dweight_kernel(const float* pa
 
 int lanes_per_head(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
 
-// Blocks of the grid's second dimension: one unless the tokens leave SMs without a block.
+// Blocks of the grid's second dimension: one unless the tokens leave SMs without a block (8 tokens
+// of 12 heads: forward 3.0 us, heads not spread 5.5; 256 of 48: 4.5 and 12.0, backward 8.4 and 17.1).
 int head_chunks(int64_t blocks, int heads) {
   const int64_t want = 2LL * device_sm_count();
   if (blocks >= want || heads < 2) return 1;
