@@ -32,13 +32,13 @@
 // computed, a softmax and a P V before the next unit needs it.  TMEM: O x2 [0, 256), S x2 [256, 512).
 //
 // Measured: 131040 queries on 512 keys, 12 heads: 277 us in short bursts (1.49 PFLOP/s, 78 % of the
-// measured burst peak), 307 us in a long run under the power cap (1.34, 78 % of the sustained
+// measured burst peak), 311 us in a long run under the power cap (1.33, 78 % of the sustained
 // peak).  What bounds it: of the 1630 cycles that a kv tile of a group takes, its two products fill
-// 1036 of the tensor core (54 % active by counter, start and end included), its exponentials 512
-// of the special function units; the rest is the way from S through the softmax back to P V, which
-// the other group's products cover in part, and the copies at a unit's start (64 KB of Q, at 34 to
-// 45 bytes a cycle into an SM).  Tried without gain: P handed over in halves, registers moved
-// between the roles, K and V multicast to pairs of CTAs.
+// 1036 of the tensor core, its exponentials 512 of the special function units.  The rest is no
+// single role's: with half of the softmax left out the same run takes 263 us, without the output's
+// stores 265, without exponentials 277.  Tried without gain: P handed over in halves, registers
+// moved between the roles, K and V multicast to pairs of CTAs, a third K tile in place of the
+// output's staging (287), two softmax warps for each 32 rows (323).
 #include "cross_common.cuh"
 
 namespace vsa {
