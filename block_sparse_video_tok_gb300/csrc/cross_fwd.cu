@@ -38,7 +38,8 @@
 // single role's: with half of the softmax left out the same run takes 263 us, without the output's
 // stores 265, without exponentials 277.  Tried without gain: P handed over in halves, registers
 // moved between the roles, K and V multicast to pairs of CTAs, a third K tile in place of the
-// output's staging (287), two softmax warps for each 32 rows (323).
+// output's staging (287), two softmax warps for each 32 rows (323), an issuing warp for each group
+// (336: their products alternate instruction by instruction).
 #include "cross_common.cuh"
 
 namespace vsa {
