@@ -9,11 +9,40 @@ main...vsa_bwd_fix, _backward_sm100a); here the forward does it once and saves t
 the backward starts on its preprocess at once, and a caller whose layers share one selection can
 invert it once for all of them (`k2q=` below).
 
-Argument marshalling only: every step runs in libvsa.so's kernels through `vsa`.
+Argument marshalling only: every step runs in libvsa.so's kernels through `vsa`.  Nothing here can be
+differentiated twice: doing so raises.
 """
+import functools
+
 import torch
 
 from . import layer, vsa
+
+
+class _FirstDerivative(torch.autograd.Function):
+    """compute(), as a function of the tensors it depends on that has no derivative."""
+
+    @staticmethod
+    def forward(ctx, compute, *tensors):
+        return compute()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradients of these operators can be taken once only: their backward "
+                           "kernels have no derivative")
+
+
+def _once(backward):
+    """A backward whose results refuse to be differentiated.  The kernels record nothing, so with
+    create_graph the results would pass for constants.  (torch's once_differentiable refuses only
+    where the incoming gradients require one; the results depend on the saved tensors too, and on
+    them alone where the loss is a sum.)"""
+    @functools.wraps(backward)
+    def wrapper(ctx, *grads):
+        if not torch.is_grad_enabled():              # no create_graph
+            return backward(ctx, *grads)
+        return _FirstDerivative.apply(lambda: backward(ctx, *grads), *grads, *ctx.saved_tensors)
+    return wrapper
 
 
 class BlockSparseAttention(torch.autograd.Function):
@@ -38,6 +67,7 @@ class BlockSparseAttention(torch.autograd.Function):
         return o, lse
 
     @staticmethod
+    @_once
     def backward(ctx, do, _dlse):
         q, k, v, o, lse, k2q_idx, k2q_num, vbs = ctx.saved_tensors
         dq, dk, dv = vsa.vsa_bwd(do.contiguous(), q, k, v, o, lse, k2q_idx, k2q_num, vbs,
@@ -70,6 +100,7 @@ class NormRope(torch.autograd.Function):
         return out
 
     @staticmethod
+    @_once
     def backward(ctx, dq_out, dk_out, dv_out):
         q, k, q_weight, k_weight, cos, sin, dst = ctx.saved_tensors
         grads = []
@@ -95,6 +126,7 @@ class CrossAttention(torch.autograd.Function):
         return o, lse
 
     @staticmethod
+    @_once
     def backward(ctx, do, _dlse):
         q, k, v, o, lse, kv_len = ctx.saved_tensors
         return layer.vsa_cross_bwd(_aligned(do), q, k, v, o, lse, kv_len, ctx.sm_scale) + (None,) * 2
