@@ -133,9 +133,12 @@ class CrossAttention(torch.autograd.Function):
 
 
 def _aligned(g):
-    """g, copied where its strides are not the kernels' (an expanded or transposed gradient)."""
+    """g, copied where its address or strides are not the kernels' (a slice that starts off 16 bytes, an
+    expanded or a transposed gradient)."""
     unit = 16 // g.element_size()
-    if g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and all(s and s % unit == 0 for s in g.stride()[:-1]):
+    if g.data_ptr() % 16:
+        return g.clone(memory_format=torch.contiguous_format)
+    if g.stride(-1) == 1 and all(s and s % unit == 0 for s in g.stride()[:-1]):
         return g
     return g.contiguous()
 

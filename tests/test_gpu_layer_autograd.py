@@ -1,0 +1,54 @@
+"""GPU: the layer operators through autograd, in the surroundings of a user's program."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def layer():
+    assert torch.cuda.is_available(), "the gpu tests need a CUDA device"
+    from block_sparse_video_tok_gb300 import build
+    build.build()
+    from block_sparse_video_tok_gb300 import layer as binding
+    return binding
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(layer):
+    layer.vsa_layer_device_error()
+    yield
+    assert layer.vsa_layer_device_error() == 0
+
+
+def randn(*shape, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed + sum(shape))
+    return torch.randn(shape, generator=g, device="cuda").to(BF16)
+
+
+def behind_a_cat(f, leaves, before):
+    """Gradients of the leaves through torch.cat([.., f(leaves) flattened]), which gives f's outputs
+    gradients that start `before` elements into a buffer."""
+    y = f(*leaves).flatten()
+    head = randn(before).requires_grad_(True)
+    g = torch.cat([randn(before, seed=1), torch.linspace(-1, 1, y.numel(), device="cuda").to(BF16)])
+    return torch.autograd.grad(torch.cat([head, y]), leaves, g)
+
+
+@pytest.mark.parametrize("name", ["norm_rope", "cross_attention"])
+def test_gradient_that_starts_anywhere(layer, name):
+    """An odd number of elements before an output moves its gradient off 16 bytes and changes no bit of
+    what comes back."""
+    from block_sparse_video_tok_gb300 import autograd
+    if name == "norm_rope":
+        f, leaves = lambda x, w: autograd.norm_rope(x, q_weight=w)[0], [randn(2, 37, 4, 128), randn(128)]
+    else:
+        f = autograd.cross_attention
+        leaves = [randn(2, 4, 70, 128), randn(2, 2, 50, 128, seed=1), randn(2, 2, 50, 128, seed=2)]
+    leaves = [x.requires_grad_(True) for x in leaves]
+    want = behind_a_cat(f, leaves, 8)
+    for before in (1, 7, 12):
+        got = behind_a_cat(f, leaves, before)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), before

@@ -80,3 +80,30 @@ def test_a_second_derivative_is_refused(plain, name):
         got = torch.autograd.grad(sum(total(y) for y in f(*leaves)), leaves, create_graph=True)
         with pytest.raises(RuntimeError, match="once"):
             (sum((g * g).sum() for g in got) + sum((x ** 3).sum() for x in leaves)).backward()
+
+
+def sixteen_byte_view(t):
+    return t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and \
+        all(n == 1 or (s and s * t.element_size() % 16 == 0) for n, s in zip(t.shape[:-1], t.stride()))
+
+
+def test_gradients_reach_the_kernels_aligned():
+    """Whatever the memory of an incoming gradient (a slice that starts off 16 bytes, as behind a
+    torch.cat of flattened tensors; broadcast; transposed; odd strides), the kernels get its values with
+    16-byte aligned data and strides; one that has them already is not copied."""
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn(2, 3, 4, 128).to(dtype)
+        flat = torch.zeros(x.numel() + 9, dtype=dtype)
+        for offset in (1, 3, 8, 9):
+            flat[offset:offset + x.numel()] = x.flatten()
+            g = flat[offset:offset + x.numel()].view(x.shape)
+            a = autograd._aligned(g)
+            assert sixteen_byte_view(a) and torch.equal(a, x)
+            assert (a.data_ptr() == g.data_ptr()) == (g.data_ptr() % 16 == 0)
+            one = autograd._aligned(g[:1, :1, :1])               # strides of single entries do not count
+            assert sixteen_byte_view(one) and torch.equal(one, x[:1, :1, :1])
+        for g in (x[:, :1].expand(-1, 3, -1, -1), x.mT.contiguous().mT, torch.cat([x, x[..., :1]], -1)[..., :128],
+                  x[:1, :1, :1, :1].expand(2, 3, 4, 128)):
+            a = autograd._aligned(g)
+            assert sixteen_byte_view(a) and torch.equal(a, g)
+        assert autograd._aligned(x.transpose(1, 2)).data_ptr() == x.data_ptr()
