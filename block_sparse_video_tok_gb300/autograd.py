@@ -70,7 +70,7 @@ class BlockSparseAttention(torch.autograd.Function):
     @_once
     def backward(ctx, do, _dlse):
         q, k, v, o, lse, k2q_idx, k2q_num, vbs = ctx.saved_tensors
-        dq, dk, dv = vsa.vsa_bwd(do.contiguous(), q, k, v, o, lse, k2q_idx, k2q_num, vbs,
+        dq, dk, dv = vsa.vsa_bwd(_aligned(do.contiguous()), q, k, v, o, lse, k2q_idx, k2q_num, vbs,
                                  ctx.sm_scale)
         return dq, dk, dv, None, None, None, None, None, None
 

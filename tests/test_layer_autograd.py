@@ -107,3 +107,25 @@ def test_gradients_reach_the_kernels_aligned():
             a = autograd._aligned(g)
             assert sixteen_byte_view(a) and torch.equal(a, g)
         assert autograd._aligned(x.transpose(1, 2)).data_ptr() == x.data_ptr()
+
+
+def test_block_sparse_gradient_that_starts_anywhere(plain, monkeypatch):
+    """block_sparse_attention's backward takes a contiguous gradient at a 16-byte address, wherever and
+    however the incoming one lies."""
+    seen, bwd = [], vsa.vsa_bwd
+    monkeypatch.setattr(vsa, "vsa_bwd", lambda do, *args: seen.append(do) or bwd(do, *args))
+    one = torch.zeros(1, dtype=torch.int32)
+    leaves = [randn(1, 2, 5, 128, seed=i).requires_grad_(True) for i in range(3)]
+    g = randn(1, 2, 5, 128, seed=7)
+    want = None
+    for before in (2, 1):
+        y = autograd.block_sparse_attention(*leaves, one, one, one)
+        got = torch.autograd.grad(torch.cat([torch.zeros(before, dtype=F64), y.flatten()]), leaves,
+                                  torch.cat([torch.zeros(before, dtype=F64), g.flatten()]))
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y = autograd.block_sparse_attention(*leaves, one, one, one)
+    got = torch.autograd.grad(y.transpose(2, 3), leaves, g.transpose(2, 3).contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for do in seen:
+        assert do.is_contiguous() and do.data_ptr() % 16 == 0 and torch.equal(do, g)
