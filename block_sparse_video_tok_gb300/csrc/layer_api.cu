@@ -9,9 +9,12 @@
 namespace {
 
 constexpr int MAX_DEVICES = 64;
-static __device__ uint32_t g_error_word = 0;
-std::mutex g_word_mutex;
+static __device__ uint32_t g_error_word[2] = {0, 0};  // the word; what the last read took out of it
+std::mutex g_word_mutex, g_read_mutex;
 uint32_t* g_word_addr[MAX_DEVICES] = {nullptr};
+
+// Reads and clears in one step: a bit that another stream raises meanwhile is read now or stays.
+__global__ void take_error_word_kernel(uint32_t* word) { word[1] = atomicExch(word, 0u); }
 
 vsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? VSA_OK : vsa::record_cuda_failure(e); }
 
@@ -299,9 +302,12 @@ vsa_status vsa_layer_device_error(uint32_t* bits, void* stream) {
   uint32_t* word = nullptr;
   const vsa_status st = vsa::layer_error_word(&word);
   if (st != VSA_OK) return st;
-  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) e = cudaMemcpy(bits, word, sizeof(uint32_t), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess) e = cudaMemset(word, 0, sizeof(uint32_t));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_read_mutex);  // readers share word[1]
+  void* args[] = {&word};
+  cudaError_t e = cudaLaunchKernel(take_error_word_kernel, dim3(1), dim3(1), args, 0, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, word + 1, sizeof(uint32_t), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   return cuda_status(e);
 }
 

@@ -52,3 +52,21 @@ def test_gradient_that_starts_anywhere(layer, name):
     for before in (1, 7, 12):
         got = behind_a_cat(f, leaves, before)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), before
+
+
+def test_error_bits_of_another_stream_are_not_lost(layer):
+    """A bit that a call on another stream raises while the word is read and cleared is in that read or in
+    the next.  The call starts after a wait of 0 to 200000 cycles, so that some fall on the read."""
+    q = randn(1, 1, 1, 128)
+    bad = torch.tensor([9], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    lost = 0
+    for i in range(6000):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1000 * (i % 200))
+        layer.vsa_cross_fwd(q, q, q, bad, stream=side)
+        first = layer.vsa_layer_device_error()
+        side.synchronize()
+        lost += (first | layer.vsa_layer_device_error()) != layer.DEVERR_KV_LEN
+    assert lost == 0
