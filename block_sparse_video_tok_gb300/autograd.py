@@ -92,9 +92,13 @@ class NormRope(torch.autograd.Function):
     """vsa_norm_rope of layer.py; gradients flow to q, k, v and the weights."""
 
     @staticmethod
-    def forward(ctx, q, k, v, q_weight, k_weight, cos, sin, src, dst, halves, eps):
-        out = layer.vsa_norm_rope(q, k, v, q_weight, k_weight, cos, sin, src, halves, eps)
-        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, dst)
+    def forward(ctx, q, k, v, q_weight, k_weight, cos, sin, src, dst, halves, eps, recorded):
+        recorded = recorded and any(ctx.needs_input_grad)
+        if recorded and (src is None) != (dst is None):
+            raise ValueError("a gradient needs both of the order's (src, dst)")
+        out = layer.vsa_norm_rope(q, k, v, q_weight, k_weight, cos, sin, src, halves, eps,
+                                  dst=dst if recorded else None)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, src, dst)
         ctx.halves, ctx.eps, ctx.rows = halves, eps, out[0].shape[2]
         ctx.v_heads = None if v is None else v.shape[2]
         return out
@@ -102,7 +106,7 @@ class NormRope(torch.autograd.Function):
     @staticmethod
     @_once
     def backward(ctx, dq_out, dk_out, dv_out):
-        q, k, q_weight, k_weight, cos, sin, dst = ctx.saved_tensors
+        q, k, q_weight, k_weight, cos, sin, src, dst = ctx.saved_tensors
         grads = []
         for g, heads in ((dq_out, q.shape[2]), (dk_out, None if k is None else k.shape[2]),
                          (dv_out, ctx.v_heads)):
@@ -111,7 +115,7 @@ class NormRope(torch.autograd.Function):
             grads.append(g if g is None else _aligned(g))
         need = ctx.needs_input_grad[3] or ctx.needs_input_grad[4]
         return layer.vsa_norm_rope_bwd(*grads, q, k, q_weight, k_weight, cos, sin, dst, ctx.halves,
-                                       ctx.eps, need_dweight=need) + (None,) * 6
+                                       ctx.eps, need_dweight=need, src=src) + (None,) * 7
 
 
 class CrossAttention(torch.autograd.Function):
@@ -147,9 +151,13 @@ def norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin=Non
               halves=False, eps=1e-6):
     """Differentiable layer.vsa_norm_rope: the per-head norm and rotation of q and k in the pass
     that moves q, k and v [B, S, H, D] to [B, H, rows, D].  order: (src, dst) as from
-    layer.video_token_order, or None.  Returns (q, k, v) for block_sparse_attention."""
+    layer.video_token_order, or None.  The two must name each other, dst[src[r]] == r wherever
+    src[r] >= 0 and src[dst[t]] == t wherever dst[t] >= 0, so that no token goes to two rows: the
+    gradients follow dst alone, and where that does not hold, forward and backward raise
+    layer.DEVERR_ORDER in the device's error word.  Returns (q, k, v) for block_sparse_attention."""
     src, dst = order if order is not None else (None, None)
-    return NormRope.apply(q, k, v, q_weight, k_weight, cos, sin, src, dst, bool(halves), float(eps))
+    return NormRope.apply(q, k, v, q_weight, k_weight, cos, sin, src, dst, bool(halves), float(eps),
+                          torch.is_grad_enabled())
 
 
 def cross_attention(q, k, v, kv_len=None, sm_scale=None):

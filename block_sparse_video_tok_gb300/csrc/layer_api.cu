@@ -83,8 +83,9 @@ vsa_status check_norm_rope(const vsa_norm_rope* op) {
     if (!op->cosines || !op->sines || !aligned(op->cosines, 16) || !aligned(op->sines, 16)) return VSA_ERR_INVALID_ARG;
     if (op->table_batch_stride < 0 || op->table_batch_stride % 4 != 0) return VSA_ERR_INVALID_ARG;
   }
-  if (!aligned(op->q_weight, 16) || !aligned(op->k_weight, 16) || !aligned(op->order, 4)) return VSA_ERR_INVALID_ARG;
-  if (!op->order && op->rows != op->tokens) return VSA_ERR_INVALID_ARG;
+  if (!aligned(op->q_weight, 16) || !aligned(op->k_weight, 16) || !aligned(op->order, 4) || !aligned(op->inverse, 4))
+    return VSA_ERR_INVALID_ARG;
+  if (!op->order && (op->rows != op->tokens || op->inverse)) return VSA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(op->batch) * op->tokens > INT_MAX ||
       static_cast<int64_t>(op->batch) * op->rows > INT_MAX)
     return VSA_ERR_UNSUPPORTED;
@@ -98,6 +99,7 @@ void fill_norm_rope(const vsa_norm_rope* op, vsa::NormRopeArgs* a) {
   a->sines = op->sines;
   a->table_batch = op->table_batch_stride;
   a->order = op->order;
+  a->inverse = op->inverse;
   a->batch = op->batch;
   a->tokens = op->tokens;
   a->rows = op->rows;

@@ -27,7 +27,7 @@ struct NormRopeArgs {
   void* dweight[2];
   const float *cosines, *sines;
   int64_t table_batch;
-  const int32_t* order;
+  const int32_t *order, *inverse;
   float* partial;  // backward: one [2][head_dim] fp32 sum per CTA
   uint32_t* err;
   int batch, tokens, rows, head_dim, rot;

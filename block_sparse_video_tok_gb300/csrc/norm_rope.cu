@@ -130,6 +130,18 @@ __device__ __forceinline__ int mapped(const int32_t* order, int i, int n, uint32
   return -1;
 }
 
+// Entries of an order of n entries in [-1, m) that the other direction's order does not name back.  The
+// grid's threads take one entry after another when their activations are done: values kept for it
+// beside them cost up to 9 of 394 us in spilled registers.
+__device__ __forceinline__ void check_inverse(const NormRopeArgs& a, int n, int m) {
+  if (!a.inverse || blockIdx.y > 0) return;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * THREADS) {
+    const int t = a.order[i];
+    if (t >= 0 && t < m && a.inverse[t] != i) atomicOr(a.err, VSA_DEVERR_ORDER);
+  }
+}
+
 // One lane's share of a token's rotation: the angles of its 8 elements and, with HALVES, the lane
 // that holds the other element of each pair.  Lanes past `rot` get the identity.
 template <int LPR, bool HALVES>
@@ -239,6 +251,7 @@ __global__ void __launch_bounds__(THREADS) norm_rope_fwd_kernel(const Params p) 
       }
     }
   }
+  check_inverse(a, a.rows, a.tokens);
 }
 
 template <typename T, typename W, int LPR, bool HALVES>
@@ -315,6 +328,7 @@ __global__ void __launch_bounds__(THREADS, BWD_CTAS) norm_rope_bwd_kernel(const 
       }
     }
   }
+  check_inverse(a, a.tokens, a.rows);
   if (!a.dweight[0] && !a.dweight[1]) return;
   // The groups' sums, added in group order.
   float* part = a.partial + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * a.head_dim;

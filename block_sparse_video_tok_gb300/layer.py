@@ -43,7 +43,8 @@ class VsaNormRope(ctypes.Structure):
                 ("halves", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
                 ("cosines", ctypes.c_void_p), ("sines", ctypes.c_void_p),
-                ("table_batch_stride", ctypes.c_int64), ("order", ctypes.c_void_p)]
+                ("table_batch_stride", ctypes.c_int64), ("order", ctypes.c_void_p),
+                ("inverse", ctypes.c_void_p)]
 
 
 class VsaCross(ctypes.Structure):
@@ -74,7 +75,7 @@ SIGNATURES = {
 # The wrappers below hand structures over as packed bytes: a single call into C builds one, where
 # a ctypes.Structure converts field by field, which would cost more than a small kernel.
 _pack_heads = struct.Struct("@4Pi4x").pack
-_pack_norm = struct.Struct("@8if4PqP").pack
+_pack_norm = struct.Struct("@8if4PqPP").pack
 _pack_cross = struct.Struct("@6ifP").pack
 
 _fns = None
@@ -188,12 +189,12 @@ def _cross_workspace(name, device, *sizes):
 @functools.lru_cache(maxsize=64)
 def _norm_workspace(device, head_dim):
     return _lib().vsa_norm_rope_bwd_workspace_bytes(
-        VsaNormRope(1, 1, 1, head_dim, 0, 0, 0, 0, 0.0, None, None, None, None, 0, None))
+        VsaNormRope(1, 1, 1, head_dim, 0, 0, 0, 0, 0.0, None, None, None, None, 0, None, None))
 
 
 # ------------------------------------------------------------------------------- norm_rope
 
-def _norm_rope_op(x, rows, q_weight, k_weight, cos, sin, order, order_len, halves, eps):
+def _norm_rope_op(x, rows, q_weight, k_weight, cos, sin, order, order_len, inverse, inverse_len, halves, eps):
     """The packed vsa_norm_rope for activations shaped and typed like x [B, S, H, D]."""
     B, S, _, D = x.shape
     dtype = x.dtype
@@ -229,12 +230,15 @@ def _norm_rope_op(x, rows, q_weight, k_weight, cos, sin, order, order_len, halve
         if rot > D or rot % (16 if halves else 8):
             raise ValueError("cos and sin turn %d of %d elements of a head: at most all, in "
                              "multiples of %d" % (rot, D, 16 if halves else 8))
+    if inverse is not None and order is None:
+        raise ValueError("src and dst come together")
     return _pack_norm(B, S, rows, D, code, _DTYPES[wdtype], rot, 1 if halves else 0, eps, wq, wk, cp,
-                      sp, stride, _vector(order, "the order", torch.int32, order_len, x))
+                      sp, stride, _vector(order, "the order", torch.int32, order_len, x),
+                      _vector(inverse, "the other order", torch.int32, inverse_len, x))
 
 
 def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin=None, src=None,
-                  halves=False, eps=1e-6, q_out=None, k_out=None, v_out=None, stream=None):
+                  halves=False, eps=1e-6, q_out=None, k_out=None, v_out=None, stream=None, dst=None):
     """RMS norm of each head of q and k, rotation by the table, and the move from token order to
     attention rows; v is only moved.
 
@@ -243,14 +247,17 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
     cos, sin: fp32 [S, rot / 2] or [B, S, rot / 2] of each token's angles (None: no rotation); the
     first rot elements of a head are turned, in pairs (2i, 2i + 1) or, with halves, (i, i + rot/2).
     src: int32 [rows], the token of each output row, -1 for a row of zeros (None: row t is token
-    t).  Returns (q_out, k_out, v_out), [B, H, rows, D]; None where the input is None."""
+    t).  dst: the order that the backward will be given, if src is to be checked against it: a row
+    whose token it does not send back raises DEVERR_ORDER (a token may go to several rows, but its
+    gradients come from one).  Returns (q_out, k_out, v_out), [B, H, rows, D]; None where the input
+    is None."""
     if stream is not None:
         return _on(stream, vsa_norm_rope, q, k, v, q_weight, k_weight, cos, sin, src, halves, eps,
-                   q_out, k_out, v_out)
+                   q_out, k_out, v_out, dst=dst)
     _cuda(q, "q")
     B, S, _, D = q.shape
     rows = S if src is None else src.numel()
-    op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, src, rows, halves, eps)
+    op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, src, rows, dst, S, halves, eps)
     dtype, where, device = q.dtype, q.device, q.get_device()
     ins, outs, res = [], [], []
     for x, y, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
@@ -277,15 +284,17 @@ def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin
 
 def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight=None, cos=None,
                       sin=None, dst=None, halves=False, eps=1e-6, dq=None, dk=None, dv=None,
-                      need_dweight=True, workspace=None, stream=None):
+                      need_dweight=True, workspace=None, stream=None, src=None):
     """Gradients of vsa_norm_rope: dq_out, dk_out, dv_out [B, H, rows, D] are the gradients of its
     outputs (dk_out with k, dv_out may be None), q and k its inputs.  dst: int32 [S], the row of
-    each token, -1 for a token that no row takes (None: row t).  Returns (dq, dk, dv, dq_weight,
-    dk_weight): dq, dk, dv in token order [B, S, H, D]; weight gradients in the weights' type, None
-    for a weight that is None (or with need_dweight false)."""
+    each token, -1 for a token that no row takes (None: row t).  src: the order that the forward was
+    given, if dst is to be checked against it: a token whose row it does not fill from the token
+    raises DEVERR_ORDER.  Returns (dq, dk, dv, dq_weight, dk_weight): dq, dk, dv in token order
+    [B, S, H, D]; weight gradients in the weights' type, None for a weight that is None (or with
+    need_dweight false)."""
     if stream is not None:
         return _on(stream, vsa_norm_rope_bwd, dq_out, dk_out, dv_out, q, k, q_weight, k_weight, cos,
-                   sin, dst, halves, eps, dq, dk, dv, need_dweight, workspace)
+                   sin, dst, halves, eps, dq, dk, dv, need_dweight, workspace, src=src)
     _cuda(q, "q")
     _cuda(dq_out, "dq_out")
     if (k is None) != (dk_out is None):
@@ -294,7 +303,7 @@ def vsa_norm_rope_bwd(dq_out, dk_out, dv_out, q, k=None, q_weight=None, k_weight
     rows = dq_out.shape[2]
     if dst is None and rows != S:
         raise ValueError("dq_out has %d rows for %d tokens, without dst" % (rows, S))
-    op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, dst, S, halves, eps)
+    op = _norm_rope_op(q, rows, q_weight, k_weight, cos, sin, dst, S, src, rows, halves, eps)
     dtype, where, device = q.dtype, q.device, q.get_device()
     dys, xs, dxs, res, dws = [], [], [], [], []
     for dy, x, dx, w, name in ((dq_out, q, dq, q_weight, "q"), (dk_out, k, dk, k_weight, "k"),

@@ -30,7 +30,8 @@ extern "C" {
 #endif
 
 /* Further bits of the device error word. */
-#define VSA_DEVERR_ORDER 0x40u  /* an order entry outside [-1, n) was read as -1 */
+#define VSA_DEVERR_ORDER 0x40u  /* an order entry outside [-1, n) was read as -1, or `inverse`
+                                 * does not name it back */
 #define VSA_DEVERR_KV_LEN 0x80u /* a kv_len entry outside [0, kv_tokens] was clamped */
 
 typedef enum vsa_dtype { VSA_BF16 = 0, VSA_F16 = 1, VSA_F32 = 2 } vsa_dtype;
@@ -69,8 +70,12 @@ typedef struct vsa_norm_rope {
   int64_t table_batch_stride; /* elements from one batch entry's table to the next; 0: shared */
   /* Forward: [rows], the token each row takes, -1 for a row of zeros.  Backward: [tokens], the
    * row each token went to, -1 for none (its gradients are zero).  NULL: row t is token t, and
-   * rows == tokens. */
+   * rows == tokens.  A forward may take a token for several rows, but a backward follows one row
+   * of each token: its gradients are the forward's only where the two orders name each other. */
   const int32_t* order;
+  /* The order of the other direction, to have that checked, or NULL.  An entry of `order` that it
+   * does not name back raises VSA_DEVERR_ORDER; the outputs are those of `order` all the same. */
+  const int32_t* inverse;
 } vsa_norm_rope;
 
 /*

@@ -70,3 +70,34 @@ def test_error_bits_of_another_stream_are_not_lost(layer):
         side.synchronize()
         lost += (first | layer.vsa_layer_device_error()) != layer.DEVERR_KV_LEN
     assert lost == 0
+
+
+def test_orders_that_do_not_fit(layer):
+    """norm_rope's gradients follow dst alone: a token that goes to two rows, one that no row takes although
+    dst says so and one whose row dst leaves out raise DEVERR_ORDER, in the forward or the backward that
+    meets it.  Orders that fit raise nothing, and a forward without gradients may repeat tokens."""
+    from block_sparse_video_tok_gb300.autograd import norm_rope
+    q = randn(2, 4, 3, 128).requires_grad_(True)
+
+    def bits(src, dst, grad=True):
+        src, dst = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (src, dst))
+        with torch.set_grad_enabled(grad):
+            y = norm_rope(q, order=(src, dst))[0]
+        forward = layer.vsa_layer_device_error()
+        if grad:
+            y.float().sum().backward()
+        return forward, layer.vsa_layer_device_error()
+
+    fits = [([0, 1, 2, 3], [0, 1, 2, 3]), ([3, -1, 0, 2, 1], [2, 4, 3, 0]), ([2, -1, -1], [-1, -1, 0, -1])]
+    for src, dst in fits:
+        assert bits(src, dst) == (0, 0), (src, dst)
+    bad = layer.DEVERR_ORDER
+    assert bits([3, -1, 0, 3, 1], [2, 4, -1, 0]) == (bad, 0)        # token 3 in rows 0 and 3
+    assert bits([3, -1, 0, 2, 1], [2, 4, -1, 0]) == (bad, 0)        # token 2 left out
+    assert bits([3, -1, 0, -1, 1], [2, 4, 3, 0]) == (0, bad)        # row 3 is empty
+    assert bits([1, 0, 2, 3], [0, 1, 2, 3]) == (bad, bad)           # two rows exchanged
+    assert bits([3, -1, 0, 3, 1], [2, 4, -1, 0], grad=False) == (0, 0)
+    for src, dst in ((None, torch.arange(4, dtype=torch.int32, device="cuda")),
+                     (torch.arange(4, dtype=torch.int32, device="cuda"), None)):
+        with pytest.raises(ValueError):
+            norm_rope(q, order=(src, dst))

@@ -129,3 +129,25 @@ def test_block_sparse_gradient_that_starts_anywhere(plain, monkeypatch):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     for do in seen:
         assert do.is_contiguous() and do.data_ptr() % 16 == 0 and torch.equal(do, g)
+
+
+def test_half_an_order_gives_no_gradient(plain):
+    """norm_rope's backward cannot do without the order of the other direction."""
+    x, one = randn(1, 4, 2, 8).requires_grad_(True), torch.arange(4, dtype=torch.int32)
+    for order in ((one, None), (None, one)):
+        with pytest.raises(ValueError, match="order"):
+            autograd.norm_rope(x, order=order)
+    with torch.no_grad():
+        assert autograd.norm_rope(x, order=(one, None))[0].shape == (1, 2, 4, 8)
+    assert autograd.norm_rope(x, order=(one, one))[0].requires_grad
+
+
+def test_an_order_to_check_against_is_refused():
+    from block_sparse_video_tok_gb300 import build
+    build.build()
+    at = 0x100000
+    h = layer.VsaHeads(at, 4 * 10 * 128, 10 * 128, 128, 4)
+    for order, inverse in ((None, at), (at, at + 2)):               # none to check; misaligned
+        op = layer.VsaNormRope(batch=1, tokens=10, rows=10, head_dim=128, eps=1e-6, order=order, inverse=inverse)
+        assert layer._lib().vsa_norm_rope_fwd(op, h, None, None, h, None, None, None) == 1
+        assert layer._lib().vsa_norm_rope_bwd(op, h, None, None, h, None, h, *[None] * 5, 0, None) == 1
