@@ -63,6 +63,13 @@ __device__ __forceinline__ void load32(uint32_t taddr, uint32_t* v) {
   tmem_ld_32x32b_x32(taddr, v);
   tmem_wait_ld();
 }
+// Columns from n on of a thread's 32 become 0.
+__device__ __forceinline__ void keep_columns(uint32_t* v, int n) {
+  if (__builtin_expect(n < 32, 0)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] : 0u;
+  }
+}
 
 // A dkv softmax warp's 32 rows x 32 columns of sums, scaled and rounded, to global memory: through 2
 // KB of shared memory, so that 64 consecutive bytes of a row leave together.  `at`: distance of
@@ -742,6 +749,7 @@ constexpr uint32_t SM_ABORT = SM_TMEM_SLOT + 4;
 constexpr uint32_t SMEM_BYTES = SM_ABORT + 4;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 384;
+constexpr float NO_ROW = -3.0e38f;  // -lse of a row that does not exist: P = 2^(0 - 3e38) = 0
 
 struct Unit {
   int b, kh, j, split, q0, q1, keys;  // kv tile j; query tiles [q0, q1); visible keys of the tile
@@ -824,22 +832,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const float4* lse = reinterpret_cast<const float4*>(smem + SM_LSE) + (x & 1u) * (TILE / 4) + col * 8;
-        ok = warp_wait(bar(LSE_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit) &&
-             warp_wait(bar(S_FULL), x & 1u, abort, limit);
+        ok = warp_wait(bar(LSE_FULL0 + (x & 1u)), (x >> 1) & 1u, abort, limit);
+        if (!ok) break;
+        // Query rows that do not exist are zeros in Q and dO, and times an infinite key or value NaN:
+        // their scores and dP are taken as 0, of which NO_ROW makes P = dS = 0 (1.2 us of 248 at
+        // 32760 x 512).  With one short query tile a unit, half of the warps may have no row at all.
+        const int rows = __popc(__ballot_sync(0xffffffffu, reinterpret_cast<const float*>(lse)[lane] != NO_ROW));
+        ok = warp_wait(bar(S_FULL), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
         uint32_t pk[16];
-        load32(lanes + TM_S, v);
         float pr[32];
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 nl = lse[c / 4];
-          float a0, a1, a2, a3;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c2, f2_pack(nl.x, nl.y)), a0, a1);
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), c2, f2_pack(nl.z, nl.w)), a2, a3);
-          pr[c] = ex2(a0), pr[c + 1] = ex2(a1), pr[c + 2] = ex2(a2), pr[c + 3] = ex2(a3);
-          pk[c >> 1] = pack_bf162(pr[c], pr[c + 1]);
-          pk[(c >> 1) + 1] = pack_bf162(pr[c + 2], pr[c + 3]);
+        for (int c = 0; c < 16; ++c) pk[c] = 0u;
+        if (!FEW || rows > 0) {
+          load32(lanes + TM_S, v);
+          keep_columns(v, rows);
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 nl = lse[c / 4];
+            float a0, a1, a2, a3;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), c2, f2_pack(nl.x, nl.y)), a0, a1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), c2, f2_pack(nl.z, nl.w)), a2, a3);
+            pr[c] = ex2(a0), pr[c + 1] = ex2(a1), pr[c + 2] = ex2(a2), pr[c + 3] = ex2(a3);
+            pk[c >> 1] = pack_bf162(pr[c], pr[c + 1]);
+            pk[(c >> 1) + 1] = pack_bf162(pr[c + 2], pr[c + 3]);
+          }
         }
         tmem_st_32x32b_x16(lanes + TM_S, pk);  // over the warp's own columns
         tmem_wait_st();
@@ -852,18 +870,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = warp_wait(bar(DELTA_FULL), x & 1u, abort, limit) && warp_wait(bar(DP_FULL), x & 1u, abort, limit);
         if (!ok) break;
         tc_fence_after_sync();
-        load32(lanes + TM_DP, v);
-        const float4* delta = reinterpret_cast<const float4*>(smem + SM_DELTA) + col * 8;
+        if (!FEW || rows > 0) {  // (else pk holds the zeros of P)
+          load32(lanes + TM_DP, v);
+          keep_columns(v, rows);
+          const float4* delta = reinterpret_cast<const float4*>(smem + SM_DELTA) + col * 8;
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 nd = delta[c / 4];
-          float a0, a1, a2, a3;
-          f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f2_pack(nd.x, nd.y)),
-                           f2_pack(pr[c], pr[c + 1])), a0, a1);
-          f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), f2_pack(nd.z, nd.w)),
-                           f2_pack(pr[c + 2], pr[c + 3])), a2, a3);
-          pk[c >> 1] = pack_bf162(a0, a1);
-          pk[(c >> 1) + 1] = pack_bf162(a2, a3);
+          for (int c = 0; c < 32; c += 4) {
+            const float4 nd = delta[c / 4];
+            float a0, a1, a2, a3;
+            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f2_pack(nd.x, nd.y)),
+                             f2_pack(pr[c], pr[c + 1])), a0, a1);
+            f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), f2_pack(nd.z, nd.w)),
+                             f2_pack(pr[c + 2], pr[c + 3])), a2, a3);
+            pk[c >> 1] = pack_bf162(a0, a1);
+            pk[(c >> 1) + 1] = pack_bf162(a2, a3);
+          }
         }
         tmem_st_32x32b_x16(lanes + TM_DP, pk);
         tmem_wait_st();
@@ -982,7 +1003,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ -lse and -Delta of the rows
-    // A row that does not exist gets -lse = -inf: its P is 0.
     float* lse = reinterpret_cast<float*>(smem + SM_LSE);
     float* delta = reinterpret_cast<float*>(smem + SM_DELTA);
     int64_t at[4];
@@ -1005,7 +1025,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float nl[4], nd[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          nl[k] = -INFINITY;
+          nl[k] = NO_ROW;
           nd[k] = 0.f;
           if (k * 32 + lane < rows) {
             const float l = p.a.lse[row + at[k]];
