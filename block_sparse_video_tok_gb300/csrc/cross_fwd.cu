@@ -188,9 +188,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int r = quarter * 32 + lane;  // row of the tile == TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_off + TM_S + g * 128u, t_o = tmem + lane_off + TM_O + g * 128u;
-    // S carries the sign of the scale.  Scale 0: 1e-30 keeps 0 * -inf out of the mask, and finite
-    // scores still give s = 0.
-    const float c1 = p.a.sm_scale == 0.f ? 1e-30f : fabsf(p.a.sm_scale) * LOG2E_F;
+    // S carries the sign of the scale.  Scale 0: the least positive value, 2^-149, keeps 0 * -inf
+    // out of the mask, and the largest finite scores give |s| < 2^-21.
+    const float c1 = p.a.sm_scale == 0.f ? __uint_as_float(1u) : fabsf(p.a.sm_scale) * LOG2E_F;
     float2* ml = reinterpret_cast<float2*>(gbase + SM_ML) + g * TILE + r;
     uint32_t sn = 0, on = 0;  // kv tiles and units of this group
     bool ok = true;

@@ -146,6 +146,21 @@ def test_a_key_that_every_score_hides(layer, name):
     assert not dv[:, :, 5].any() and not dk[:, :, 5].any()
 
 
+@pytest.mark.parametrize("name", ["token", "few_parts", "half_tile", "long"])
+def test_scale_zero_on_large_scores(layer, name):
+    """With scale 0 every visible key has the same weight, however large the finite scores are."""
+    do, q, k, v, _ = inputs(name)
+    q = (q.float() * 1e34).to(BF16)
+    lens = torch.full((q.shape[0],), k.shape[2] - 7, dtype=torch.int32, device="cuda")
+    o, lse = layer.vsa_cross_fwd(q, k, v, lens, 0.0)
+    (wo, bo), (wl, bl) = ref.cross_fwd(q, k, v, lens, 0.0)
+    ref.check("o", o, wo, bo)
+    ref.check("lse", lse, wl, bl)
+    got = layer.vsa_cross_bwd(do, q, k, v, o, lse, lens, 0.0)
+    for n, g, (w, b) in zip(("dq", "dk", "dv"), got, ref.cross_bwd(do, q, k, v, o, lse, lens, 0.0)):
+        ref.check(n, g, w, b)
+
+
 # ---------------------------------------------------------------------- long sums
 
 @pytest.mark.parametrize("Sq, Sk, H, Hk", [(40000, 130, 2, 2), (11000, 130, 4, 1), (130, 40000, 2, 1), (3, 60000, 1, 1)])
