@@ -92,7 +92,8 @@ class NormRope(torch.autograd.Function):
     """vsa_norm_rope of layer.py; gradients flow to q, k, v and the weights."""
 
     @staticmethod
-    def forward(ctx, q, k, v, q_weight, k_weight, cos, sin, src, dst, halves, eps, recorded):
+    def forward(ctx, q, k, v, q_weight, k_weight, cos, sin, src, dst, halves, eps,
+                recorded=True):
         recorded = recorded and any(ctx.needs_input_grad)
         if recorded and (src is None) != (dst is None):
             raise ValueError("a gradient needs both of the order's (src, dst)")

@@ -11,8 +11,9 @@ constexpr int TILE = 128;                        // rows of a query tile, keys o
 constexpr uint32_t TILE_BYTES = TILE * 128 * 2;  // one operand tile: two column halves of 16 KB
 
 // Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiply and a shift (the persistent kernels
-// decode their units in every role, and the code of a 32-bit division there counts): with
-// 2^s >= d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, m) + n) >> s.
+// decode their units in every role, and the code of a 32-bit division there counts), after Granlund and
+// Montgomery, "Division by invariant integers using multiplication" (1994): with 2^s >= d and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, m) + n) >> s.
 struct Divisor {
   uint32_t d, m, s;
 #ifdef __CUDACC__

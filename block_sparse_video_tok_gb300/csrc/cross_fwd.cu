@@ -12,8 +12,8 @@
 // its softmax the tensor pipe works for the other.  The groups share every K and V tile.
 //
 // P is rounded to bf16 because kind::f16 takes one type for both operands and V is the caller's
-// bf16; l adds up the unrounded values.  The rounding is of the size of O's own (2^-9 relative,
-// independent per key).
+// bf16; l adds up the unrounded values.  The rounding is of the size of O's own (2^-8 relative at
+// most, independent per key).
 //
 // The last kv tile multiplies only as many columns as have keys (S in steps of 16, P V of 64);
 // scores past the last key are overwritten with -inf, and rows of V past it, which may hold
@@ -21,7 +21,7 @@
 //
 // When there are fewer units than SMs the keys are split: each part leaves its unnormalised O
 // and (m, l) in the workspace, and cross_combine_kernel joins them in part order (2 x 8 heads, 64
-// queries on 8191 keys: 23 us, without parts 89).
+// queries on 8191 keys: 19 to 22 us, without parts 89).
 //
 // Roles (512 threads): warp 0 TMEM owner and TMA producer of Q and K; warp 1 UMMA issuer; warp 2 TMA
 // producer of V; warp 3 idle; warps 4-7 and 8-11 softmax groups; warps 12-15 output (one row of
@@ -32,8 +32,8 @@
 // computed, a softmax and a P V before the next unit needs it.  TMEM: O x2 [0, 256), S x2 [256, 512).
 //
 // Measured: 131040 queries on 512 keys, 12 heads: 277 us in short bursts (1.49 PFLOP/s, 78 % of the
-// measured burst peak), 311 us in a long run under the power cap (1.33, 78 % of the sustained
-// peak).  What bounds it: of the 1630 cycles that a kv tile of a group takes, its two products fill
+// measured burst peak), 311 to 317 us in a long run under the power cap (1.30 to 1.33, 76 to 78 % of
+// the sustained peak).  What bounds it: of the 1630 cycles that a kv tile of a group takes, its two products fill
 // 1036 of the tensor core, its exponentials 512 of the special function units.  The rest is no
 // single role's: with half of the softmax left out the same run takes 263 us, without the output's
 // stores 265, without exponentials 277.  Tried without gain: P handed over in halves, registers
@@ -659,9 +659,11 @@ struct Plan {
   size_t ml_off, total;  // workspace
 };
 
-// Parts of the keys: one when the units fill the SMs; else as many as keep every SM busy with one,
-// down to a kv tile each (parts of at least two: 8 x 12 heads of 4 rows, 512 keys 10.9 instead of
-// 9.9 us; 2 x 8 heads, 64 queries on 8191 keys 22.7 instead of 21.9).
+// Parts of the keys: as many as give every SM at most one, down to a kv tile each (parts of at least
+// two: 8 x 12 heads of 4 rows, 512 keys 10.9 instead of 9.9 us; 2 x 8 heads, 64 queries on 8191 keys
+// 22.7 instead of 21.9).  From 77 units on that is one part, and up to half of the SMs have nothing to
+// do: 2 x 8 heads, 1280 queries on 20000 keys are 80 units of 157 kv tiles and take 229 us, 48 % of the
+// measured rate.  (Parts in several waves, weighed as cross_bwd.cu weighs its own, are not built here.)
 Plan plan_of(int batch, int heads, int kv_heads, int q_tokens, int kv_tokens) {
   Plan p{};
   p.t = q_tiles(heads, kv_heads, q_tokens);

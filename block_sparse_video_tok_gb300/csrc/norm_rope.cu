@@ -22,7 +22,15 @@ namespace {
 // Heads in flight per group of lanes, and what the backward's registers leave room for: 6 heads and
 // four CTAs of 128 threads per SM.  (12 heads of 128, bf16: forward of 131040 tokens 388 us, 99 % of
 // the measured copy rate, with 4 heads 394; backward of 2 x 32760 266 us, 90 %, with 4 heads 287,
-// with 8 heads 340.)
+// with 8 heads 340.  One number for all sizes is a compromise: heads come in sixes, 8 as 6 + 2.  2 x
+// 32760 tokens, as many heads of k and v as of q, us with 6, 4 and 8 in flight:
+//   heads of         forward            backward
+//   8 x 128, bf16    152, 140, 139      214, 198, 205
+//   16 x 128, bf16   273, 273, 269      369, 381, 405
+//   24 x 128, bf16   403, 407, 401      517, 564, 591
+//   8 x 256, bf16    296, 273, 273      442, 386, 405
+//   8 x 64, fp32     138, 137, 136      204, 181, 237
+//   12 x 128, fp32   397, 399, 397      579, 525, 750.)
 constexpr int THREADS = 128, BWD_CTAS = 4;
 constexpr int UNROLL = 6;
 constexpr unsigned FULL = 0xffffffffu;

@@ -239,8 +239,8 @@ def _norm_rope_op(x, rows, q_weight, k_weight, cos, sin, order, order_len, inver
 
 def vsa_norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin=None, src=None,
                   halves=False, eps=1e-6, q_out=None, k_out=None, v_out=None, stream=None, dst=None):
-    """RMS norm of each head of q and k, rotation by the table, and the move from token order to
-    attention rows; v is only moved.
+    """RMS norm of each head of q and k by itself (not over all heads together), rotation by the
+    table, and the move from token order to attention rows; v is only moved.
 
     q, k, v: [B, S, H, D] (bf16, fp16 or fp32; D a multiple of 8 up to 256; k and v may be None or
     have other head counts).  q_weight, k_weight: [D], fp32 or the activations' type (None: ones).

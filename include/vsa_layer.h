@@ -51,7 +51,10 @@ typedef struct vsa_heads {
  * where R_t turns the pairs of the first `rot` elements of a head by the angles of token t:
  *   (a, b) -> (a cos - b sin, b cos + a sin),
  * pair i being elements (2i, 2i + 1), or (i, i + rot/2) with `halves` set.  v is only moved.
- * Arithmetic is in fp32; each output is rounded once.
+ * Every head is normalised by itself, with one weight for all heads of q and one for all of k: a
+ * model that takes the mean over all heads together, with a weight for each of their elements, is
+ * not served.  Arithmetic is in fp32, the sums of the weights' gradients included; each output is
+ * rounded once.
  */
 typedef struct vsa_norm_rope {
   int32_t batch;        /* >= 1; batch * tokens and batch * rows below 2^31 */
@@ -124,6 +127,10 @@ size_t vsa_cross_bwd_workspace_bytes(const vsa_cross* op);
 /*
  * vsa_cross_fwd -- O = softmax(q k^T sm_scale) v, bf16, and lse [batch, heads, q_tokens] fp32
  * contiguous, base 2 in the M form of vsa_fwd.  Without a visible key O = 0 and lse = -inf.
+ * With more than two query rows per key head (heads / kv_heads * q_tokens) the softmax's weights
+ * are rounded to bf16 as an operand of the tensor cores (2^-8 at most; O is off by 0.0023 of its norm
+ * on random inputs, where its own rounding makes 0.0017); up to two rows they stay fp32.  Sums, lse
+ * and the statistics are fp32 everywhere.
  */
 vsa_status vsa_cross_fwd(const vsa_cross* op, const vsa_heads* q, const vsa_heads* k,
                          const vsa_heads* v, const vsa_heads* o, float* lse, void* workspace,
@@ -135,6 +142,7 @@ vsa_status vsa_cross_fwd(const vsa_cross* op, const vsa_heads* q, const vsa_head
  *   dV = P^T dO,   dK = sm_scale dS^T q  (each summed over the query heads that share the key
  *   head),   dQ = sm_scale dS k.
  * o and lse as vsa_cross_fwd wrote them.  Rows at or past kv_len[b] of dK and dV are exact zeros.
+ * P and dS are rounded to bf16 as operands (gradients off by 0.0024 of their norm, likewise).
  */
 vsa_status vsa_cross_bwd(const vsa_cross* op, const vsa_heads* dout, const vsa_heads* q,
                          const vsa_heads* k, const vsa_heads* v, const vsa_heads* o,
