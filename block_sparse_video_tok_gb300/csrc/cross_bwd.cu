@@ -21,7 +21,7 @@
 // heads, 16 queries: 38 us, without parts 94, without packing the heads that share keys 91).
 //
 // Measured: 32760 queries on 512 keys, 12 heads: 249 us in short bursts (1.03 PFLOP/s of the five
-// products that the formulas have, 1.45 of the seven that are done), 270 us in a long run under
+// products that the formulas have, 1.45 of the seven that are done), 267 to 276 us in a long run under
 // the power cap; dQ 132 us, dK and dV 114 us, the join 7 us.
 // What bounds dQ (tensor pipe 49 % active): an SM takes copies in at 34 to 45 bytes a cycle, and a
 // step's 64 KB of K and V with its share of a unit's Q, dO and O are 2000 to 2500 cycles against

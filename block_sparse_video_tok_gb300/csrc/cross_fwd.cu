@@ -32,7 +32,7 @@
 // computed, a softmax and a P V before the next unit needs it.  TMEM: O x2 [0, 256), S x2 [256, 512).
 //
 // Measured: 131040 queries on 512 keys, 12 heads: 277 us in short bursts (1.49 PFLOP/s, 78 % of the
-// measured burst peak), 311 to 317 us in a long run under the power cap (1.30 to 1.33, 76 to 78 % of
+// measured burst peak), 306 to 317 us in a long run under the power cap (1.30 to 1.35, 76 to 79 % of
 // the sustained peak).  What bounds it: of the 1630 cycles that a kv tile of a group takes, its two products fill
 // 1036 of the tensor core, its exponentials 512 of the special function units.  The rest is no
 // single role's: with half of the softmax left out the same run takes 263 us, without the output's
