@@ -14,7 +14,13 @@ The operators around it in a video transformer layer (include/vsa_layer.h):
     from block_sparse_video_tok_gb300.autograd import cross_attention, norm_rope
     q, k, v = norm_rope(q, k, v, q_weight, k_weight, cos, sin, order)   # [B,S,H,D] -> [B,H,S',D]
     o = cross_attention(q, k, v, kv_len)                         # to states of another length
-"""
-from . import autograd, build, layer, vsa, workloads  # noqa: F401
 
-__all__ = ["autograd", "build", "layer", "vsa", "workloads"]
+and those that make a whole block of it (include/vsa_block.h):
+
+    from block_sparse_video_tok_gb300.autograd import gate_norm, linear, mlp
+    x, h = gate_norm(x, y, gate, scale=scale, shift=shift)       # gated sum, norm, modulation
+    y = mlp(h, w1, b1, w2, b2, act="gelu_tanh")                  # products with their epilogues
+"""
+from . import autograd, block, build, layer, vsa, workloads  # noqa: F401
+
+__all__ = ["autograd", "block", "build", "layer", "vsa", "workloads"]

@@ -16,7 +16,7 @@ import functools
 
 import torch
 
-from . import layer, vsa
+from . import block, layer, vsa
 
 
 class _FirstDerivative(torch.autograd.Function):
@@ -137,6 +137,82 @@ class CrossAttention(torch.autograd.Function):
         return layer.vsa_cross_bwd(_aligned(do), q, k, v, o, lse, kv_len, ctx.sm_scale) + (None,) * 2
 
 
+class GateNorm(torch.autograd.Function):
+    """vsa_gate_norm of block.py: (x', h), or h alone without y; gradients flow to x, y and every
+    parameter."""
+
+    @staticmethod
+    def forward(ctx, x, y, gate, post_weight, weight, bias, scale, shift, kind, eps, post_eps, h_dtype):
+        ctx.set_materialize_grads(False)
+        x_out, h = block.vsa_gate_norm(x, y, gate, post_weight, weight, bias, scale, shift, kind, eps,
+                                       post_eps, h_dtype)
+        ctx.save_for_backward(x_out, y, gate, post_weight, weight, bias, scale, shift)
+        ctx.settings, ctx.h_dtype = (kind, eps, post_eps), h.dtype
+        return h if y is None else (x_out, h)
+
+    @staticmethod
+    @_once
+    def backward(ctx, *grads):
+        dx_out, dh = grads if len(grads) == 2 else (None, grads[0])
+        if dx_out is None and dh is None:
+            return (None,) * 12
+        x_out, y, *params = ctx.saved_tensors
+        dh = torch.zeros(x_out.shape, dtype=ctx.h_dtype, device=x_out.device) if dh is None else _aligned(dh)
+        need = any(ctx.needs_input_grad[2:8])
+        return block.vsa_gate_norm_bwd(dh, None if dx_out is None else _aligned(dx_out), x_out, y, *params,
+                                       *ctx.settings, need_dparams=need) + (None,) * 4
+
+
+class Linear(torch.autograd.Function):
+    """vsa_linear of block.py; gradients flow to x, the weight, the bias and the residual."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, act, recorded=True):
+        recorded = recorded and any(ctx.needs_input_grad)
+        out, pre = block.vsa_linear(x, weight, bias, act, residual, need_pre=recorded and act is not None)
+        ctx.save_for_backward(x, weight, bias, pre)
+        ctx.act = act
+        return out
+
+    @staticmethod
+    @_once
+    def backward(ctx, dout):
+        x, weight, bias, pre = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        g = _aligned(dout)
+        dx, dw, db = block.vsa_linear_bwd(g, x, weight, bias if need[2] else None, ctx.act, pre,
+                                          need_dx=need[0], need_dweight=need[1])
+        return dx, dw, db, dout if need[3] else None, None, None
+
+
+class Mlp(torch.autograd.Function):
+    """Two products with an activation between them; the backward of the second goes through the
+    activation in the epilogue of its product."""
+
+    @staticmethod
+    def forward(ctx, x, w1, b1, w2, b2, residual, act, recorded=True):
+        recorded = recorded and any(ctx.needs_input_grad)
+        mid, pre = block.vsa_linear(x, w1, b1, act, need_pre=recorded)
+        out, _ = block.vsa_linear(mid, w2, b2, residual=residual)
+        ctx.save_for_backward(x, w1, b1, w2, b2, mid, pre)
+        ctx.act = act
+        return out
+
+    @staticmethod
+    @_once
+    def backward(ctx, dout):
+        x, w1, b1, w2, b2, mid, pre = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        first = need[0] or need[1] or need[2]
+        dz, dw2, db2 = block.vsa_linear_bwd(_aligned(dout), mid, w2, b2 if need[4] else None, x_act=ctx.act,
+                                            x_pre=pre, need_dx=first, need_dweight=need[3])
+        dx = dw1 = db1 = None
+        if first:
+            dx, dw1, db1 = block.vsa_linear_bwd(dz, x, w1, b1 if need[2] else None, need_dx=need[0],
+                                                need_dweight=need[1])
+        return dx, dw1, db1, dw2, db2, dout if need[5] else None, None, None
+
+
 def _aligned(g):
     """g, copied where its address or strides are not the kernels' (a slice that starts off 16 bytes, an
     expanded or a transposed gradient)."""
@@ -167,3 +243,25 @@ def cross_attention(q, k, v, kv_len=None, sm_scale=None):
     if sm_scale is None:
         sm_scale = q.shape[-1] ** -0.5
     return CrossAttention.apply(q, k, v, kv_len, float(sm_scale))[0]
+
+
+def gate_norm(x, y=None, gate=None, post_weight=None, weight=None, bias=None, scale=None, shift=None,
+              kind="layer", eps=1e-6, post_eps=1e-6, h_dtype=None):
+    """Differentiable block.vsa_gate_norm: (x', h) with x' = x + gate * y (y normalised first with a
+    post_weight) and h = (norm(x') * weight + bias) * (1 + scale) + shift.  Without y, x' is x."""
+    out = GateNorm.apply(x, y, gate, post_weight, weight, bias, scale, shift, kind, float(eps),
+                         float(post_eps), h_dtype)
+    return (x, out) if y is None else out
+
+
+def linear(x, weight, bias=None, act=None, residual=None):
+    """Differentiable block.vsa_linear: act(x weight^T + bias) + residual."""
+    return Linear.apply(x, weight, bias, residual, act, torch.is_grad_enabled())
+
+
+def mlp(x, w1, b1, w2, b2, act="gelu_tanh", residual=None):
+    """act(x w1^T + b1) w2^T + b2 + residual, differentiable in all of them.  The backward keeps both
+    sides of the activation, [..., w1's rows] each."""
+    if act is None:
+        raise ValueError("mlp needs an activation")
+    return Mlp.apply(x, w1, b1, w2, b2, residual, act, torch.is_grad_enabled())

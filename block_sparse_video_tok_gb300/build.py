@@ -18,9 +18,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libvsa.so")
 SOURCES = ["api.cu", "invert.cu", "prepost.cu", "tmap.cu", "bwd_main.cu", "fwd_main.cu",
            "noalloc.cu", "layer_api.cu", "norm_rope.cu", "cross_fwd.cu", "cross_token.cu",
-           "cross_bwd.cu"]
+           "cross_bwd.cu", "block_api.cu", "gate_norm.cu", "linear.cu"]
 HEADERS = ["ptx.cuh", "queue.cuh", "vsa_internal.cuh", "layer_internal.cuh",
-           "cross_common.cuh"]
+           "cross_common.cuh", "block_internal.cuh", "vec8.cuh", "act.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -35,7 +35,7 @@ def _nvcc():
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files += [os.path.join(ROOT, "include", h) for h in ("vsa.h", "vsa_layer.h")]
+    files += [os.path.join(ROOT, "include", h) for h in ("vsa.h", "vsa_layer.h", "vsa_block.h")]
     return files
 
 

@@ -14,6 +14,7 @@
 // leave the last lanes of a group idle.  When the tokens alone do not fill the GPU (single tokens
 // above all), the heads are spread over the grid's second dimension.
 #include "layer_internal.cuh"
+#include "vec8.cuh"
 
 namespace vsa {
 
@@ -33,88 +34,6 @@ namespace {
 //   12 x 128, fp32   397, 399, 397      579, 525, 750.)
 constexpr int THREADS = 128, BWD_CTAS = 4;
 constexpr int UNROLL = 6;
-constexpr unsigned FULL = 0xffffffffu;
-
-// 8 elements as loaded (16 or 32 bytes), widened where they are used: a lane keeps several heads'
-// worth in flight.
-template <typename T>
-struct Raw {
-  uint4 u[sizeof(T) / 2];
-
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
-  }
-  __device__ __forceinline__ void store(T* p) const {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
-  }
-  __device__ __forceinline__ void widen(float* v) const;
-};
-template <>
-__device__ __forceinline__ void Raw<float>::widen(float* v) const {
-  v[0] = __uint_as_float(u[0].x), v[1] = __uint_as_float(u[0].y), v[2] = __uint_as_float(u[0].z);
-  v[3] = __uint_as_float(u[0].w), v[4] = __uint_as_float(u[1].x), v[5] = __uint_as_float(u[1].y);
-  v[6] = __uint_as_float(u[1].z), v[7] = __uint_as_float(u[1].w);
-}
-template <>
-__device__ __forceinline__ void Raw<__nv_bfloat16>::widen(float* v) const {
-  const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-template <>
-__device__ __forceinline__ void Raw<__half>::widen(float* v) const {
-  const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* v) {
-  Raw<T> r;
-  r.load(p);
-  r.widen(v);
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* v);
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <>
-__device__ __forceinline__ void store8<__half>(__half* p, const float* v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 template <int LPR>
 __device__ __forceinline__ float group_sum(float v) {
