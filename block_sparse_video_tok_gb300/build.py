@@ -18,9 +18,11 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libvsa.so")
 SOURCES = ["api.cu", "invert.cu", "prepost.cu", "tmap.cu", "bwd_main.cu", "fwd_main.cu",
            "noalloc.cu", "layer_api.cu", "norm_rope.cu", "cross_fwd.cu", "cross_token.cu",
-           "cross_bwd.cu", "block_api.cu", "gate_norm.cu", "linear.cu"]
+           "cross_bwd.cu", "block_api.cu", "gate_norm.cu", "linear.cu",
+           "gemm.cu"]
 HEADERS = ["ptx.cuh", "queue.cuh", "vsa_internal.cuh", "layer_internal.cuh",
-           "cross_common.cuh", "block_internal.cuh", "vec8.cuh", "act.cuh"]
+           "cross_common.cuh", "block_internal.cuh", "vec8.cuh", "act.cuh",
+           "gemm.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

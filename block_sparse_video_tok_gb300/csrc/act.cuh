@@ -36,22 +36,32 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.f;
 }
 
-// The same with the activation known at run time only.
-__device__ __forceinline__ float act_value(float z, int act) {
-  return act == VSA_ACT_NONE    ? z
-         : act == VSA_GELU      ? act_value<VSA_GELU>(z)
-         : act == VSA_GELU_TANH ? act_value<VSA_GELU_TANH>(z)
-                                : act_value<VSA_SILU>(z);
+// 8 values at once, the activation known at run time only: z = act(z), z *= act'(at).
+__device__ __forceinline__ void act8(int act, float* z) {
+  if (act == VSA_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value<VSA_GELU_TANH>(z[i]);
+  } else if (act == VSA_SILU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value<VSA_SILU>(z[i]);
+  } else if (act == VSA_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value<VSA_GELU>(z[i]);
+  }
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
-  return act == VSA_ACT_NONE    ? 1.f
-         : act == VSA_GELU      ? act_slope<VSA_GELU>(z)
-         : act == VSA_GELU_TANH ? act_slope<VSA_GELU_TANH>(z)
-                                : act_slope<VSA_SILU>(z);
+__device__ __forceinline__ void slope8(int act, const float* at, float* z) {
+  if (act == VSA_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] *= act_slope<VSA_GELU_TANH>(at[i]);
+  } else if (act == VSA_SILU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] *= act_slope<VSA_SILU>(at[i]);
+  } else if (act == VSA_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] *= act_slope<VSA_GELU>(at[i]);
+  }
 }
 
-__device__ __forceinline__ float widen16(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float widen16(__half v) { return __half2float(v); }
 __device__ __forceinline__ void narrow(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void narrow(float v, __half* p) { *p = __float2half_rn(v); }
 

@@ -1,164 +1,154 @@
 // linear.cu -- out = act(x W^T + bias) + residual and its gradients.
 #include "act.cuh"
+#include "gemm.cuh"
 #include "vec8.cuh"
 
 namespace vsa {
 
 namespace {
 
-constexpr int T = 64, KT = 16;  // tile of the result, step of the sum
-
-// C[i][j] = sum_k A(i, k) B(j, k), element (i, k) of A at a[i * ai + k * ak], and what follows it.
-template <typename E>
-struct Product {
-  const E *a, *b;
-  int64_t ai, ak, bj, bk;
-  int m, n, k;
-  const void* bias;
-  bool bias_f32;
-  int act;                 // out = act(z) + residual
-  MatrixView residual, pre, out;
-  MatrixView slope;        // out *= act'(slope)
-  int slope_act;
-};
-
-template <typename E>
-__global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ Product<E> p) {
-  __shared__ float sa[KT][T + 1], sb[KT][T + 1];
-  grid_dependency_wait();
-  const int i0 = blockIdx.y * T, j0 = blockIdx.x * T, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.k; k0 += KT) {
-    for (int x = threadIdx.x; x < T * KT; x += 256) {
-      const int r = p.ak == 1 ? x / KT : x % T, k = p.ak == 1 ? x % KT : x / T;
-      sa[k][r] = i0 + r < p.m && k0 + k < p.k ? widen16(p.a[(i0 + r) * p.ai + (k0 + k) * p.ak]) : 0.f;
-      const int s = p.bk == 1 ? x / KT : x % T, l = p.bk == 1 ? x % KT : x / T;
-      sb[l][s] = j0 + s < p.n && k0 + l < p.k ? widen16(p.b[(j0 + s) * p.bj + (k0 + l) * p.bk]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = i0 + ty * 4 + i, c = j0 + tx * 4 + j;
-      if (r >= p.m || c >= p.n) continue;
-      float z = acc[i][j];
-      if (p.bias) z += p.bias_f32 ? static_cast<const float*>(p.bias)[c] : widen16(static_cast<const E*>(p.bias)[c]);
-      if (p.pre.data) narrow(z, static_cast<E*>(p.pre.data) + r * p.pre.stride + c);
-      z = act_value(z, p.act);
-      if (p.residual.data) z += widen16(static_cast<const E*>(p.residual.data)[r * p.residual.stride + c]);
-      if (p.slope.data) z *= act_slope(widen16(static_cast<const E*>(p.slope.data)[r * p.slope.stride + c]), p.slope_act);
-      narrow(z, static_cast<E*>(p.out.data) + r * p.out.stride + c);
-    }
-}
+// Columns of 8 to a thread, 32 threads of a warp side by side, ROWS warps down the rows.
+constexpr int ROWS = 8;
 
 // dz = dout act'(pre) (not written without an activation) and the sums of its columns over `chunk`
-// rows, to partial [blockIdx.y][n] fp32.
+// rows, to partial [blockIdx.y][n] fp32 (unless null).  Bound by HBM: one read of each input, one write.
 template <typename E>
-__global__ void __launch_bounds__(256) slope_kernel(MatrixView dout, MatrixView pre, E* dz, float* partial, int m, int n,
-                                                    int chunk, int act) {
+__global__ void __launch_bounds__(32 * ROWS) slope_kernel(MatrixView dout, MatrixView pre, E* dz, float* partial, int m, int n,
+                                                          int chunk, int act) {
+  __shared__ float sums[ROWS][257];
   grid_dependency_wait();
-  const int c = blockIdx.x * 256 + threadIdx.x, r1 = min(m, (static_cast<int>(blockIdx.y) + 1) * chunk);
-  if (c >= n) return;
-  float sum = 0.f;
-  for (int r = blockIdx.y * chunk; r < r1; ++r) {
-    float g = widen16(static_cast<const E*>(dout.data)[r * dout.stride + c]);
-    if (act) {
-      g *= act_slope(widen16(static_cast<const E*>(pre.data)[r * pre.stride + c]), act);
-      narrow(g, dz + static_cast<int64_t>(r) * n + c);
+  const int c = (blockIdx.x * 32 + threadIdx.x) * 8, r1 = min(m, (static_cast<int>(blockIdx.y) + 1) * chunk);
+  float sum[8] = {};
+  if (c < n) {
+#pragma unroll 4
+    for (int r = blockIdx.y * chunk + threadIdx.y; r < r1; r += ROWS) {
+      float g[8];
+      load8(static_cast<const E*>(dout.data) + r * dout.stride + c, g);
+      if (act) {
+        float z[8];
+        load8(static_cast<const E*>(pre.data) + r * pre.stride + c, z);
+        slope8(act, z, g);
+        store8(dz + static_cast<int64_t>(r) * n + c, g);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += g[i];
     }
-    sum += g;
   }
-  if (partial) partial[static_cast<int64_t>(blockIdx.y) * n + c] = sum;
+  if (!partial) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[threadIdx.y][threadIdx.x * 8 + i] = sum[i];
+  __syncthreads();
+  const int t = threadIdx.y * 32 + threadIdx.x, to = blockIdx.x * 256 + t;
+  if (to >= n) return;
+  float s = 0.f;
+#pragma unroll
+  for (int y = 0; y < ROWS; ++y) s += sums[y][t];
+  partial[static_cast<int64_t>(blockIdx.y) * n + to] = s;
 }
 
+// dbias: the chunks' sums, 32 columns a block, 32 strided chunks each, joined in their order.
 template <typename E>
-__global__ void __launch_bounds__(256) dbias_kernel(const float* partial, int parts, int n, void* dbias, bool f32) {
+__global__ void __launch_bounds__(1024) dbias_kernel(const float* partial, int parts, int n, void* dbias, bool f32) {
+  __shared__ float sums[32][33];
   grid_dependency_wait();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= n) return;
-  float sum = 0.f;
-  for (int i = 0; i < parts; ++i) sum += partial[static_cast<int64_t>(i) * n + c];
-  if (f32) static_cast<float*>(dbias)[c] = sum;
-  else narrow(sum, static_cast<E*>(dbias) + c);
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.f;
+  if (c < n)
+    for (int i = threadIdx.y; i < parts; i += 32) s += partial[static_cast<int64_t>(i) * n + c];
+  sums[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= n) return;
+  s = 0.f;
+#pragma unroll
+  for (int y = 0; y < 32; ++y) s += sums[y][threadIdx.x];
+  if (f32) static_cast<float*>(dbias)[c] = s;
+  else narrow(s, static_cast<E*>(dbias) + c);
 }
 
-int chunk_rows(int rows) { return rows / 256 > 16 ? rows / 256 : 16; }
-size_t dz_bytes(int rows, int n, int act) {
-  return act ? align_up(static_cast<size_t>(rows) * n * 2, 256) : 0;
+// Rows of a block: about four blocks to an SM, 32 rows at least.
+int chunk_rows(int rows, int n) {
+  const int64_t columns = (n + 255) / 256, blocks = (4 * device_sm_count() + columns - 1) / columns;
+  const int64_t chunk = (rows + blocks - 1) / blocks;
+  return static_cast<int>(chunk < 32 ? 32 : (chunk + ROWS - 1) / ROWS * ROWS);
+}
+
+struct Layout {
+  int chunk, parts;
+  size_t partial, gemm, total;  // dz is at 0
+};
+Layout layout_of(int rows, int in, int out, int act) {
+  Layout l;
+  l.chunk = chunk_rows(rows, out);
+  l.parts = (rows + l.chunk - 1) / l.chunk;
+  l.partial = act ? align_up(static_cast<size_t>(rows) * out * 2, 256) : 0;
+  l.gemm = align_up(l.partial + static_cast<size_t>(l.parts) * out * sizeof(float), 256);
+  const size_t dx = gemm_workspace(rows, in, out), dw = gemm_workspace(out, in, rows);
+  l.total = l.gemm + (dx > dw ? dx : dw);
+  return l;
 }
 
 template <typename E>
-cudaError_t multiply(const Product<E>& p, cudaStream_t stream) {
-  return launch_dependent(product_kernel<E>, dim3((p.n + T - 1) / T, (p.m + T - 1) / T), dim3(256), 0, stream, p);
-}
-
-template <typename E>
-cudaError_t forward(const LinearArgs& a, cudaStream_t stream) {
-  Product<E> p{};
-  p.a = static_cast<const E*>(a.x.data), p.ai = a.x.stride, p.ak = 1;
-  p.b = static_cast<const E*>(a.weight.data), p.bj = a.weight.stride, p.bk = 1;
-  p.m = a.rows, p.n = a.out_features, p.k = a.in;
-  p.bias = a.bias, p.bias_f32 = a.bias_dtype == VSA_F32, p.act = a.act;
-  p.residual = a.residual, p.pre = a.pre, p.out = a.out;
-  return multiply(p, stream);
-}
-
-template <typename E>
-cudaError_t backward(const LinearArgs& a, cudaStream_t stream) {
-  const int m = a.rows, n = a.out_features, chunk = chunk_rows(m), parts = (m + chunk - 1) / chunk;
-  E* dz = reinterpret_cast<E*>(a.workspace);
-  float* partial = reinterpret_cast<float*>(a.workspace + dz_bytes(m, n, a.act));
-  cudaError_t e = cudaSuccess;
-  if (a.act || a.dbias) {
-    e = launch_dependent(slope_kernel<E>, dim3((n + 255) / 256, parts), dim3(256), 0, stream, a.dout, a.pre, dz,
-                         a.dbias ? partial : nullptr, m, n, chunk, a.act);
-    if (e == cudaSuccess && a.dbias)
-      e = launch_dependent(dbias_kernel<E>, dim3((n + 255) / 256), dim3(256), 0, stream, partial, parts, n, a.dbias,
-                           a.bias_dtype == VSA_F32);
-    if (e != cudaSuccess) return e;
-  }
-  const E* g = a.act ? dz : static_cast<const E*>(a.dout.data);
-  const int64_t gs = a.act ? n : a.dout.stride;
-  if (a.dx.data) {
-    Product<E> p{};
-    p.a = g, p.ai = gs, p.ak = 1;
-    p.b = static_cast<const E*>(a.weight.data), p.bj = 1, p.bk = a.weight.stride;
-    p.m = m, p.n = a.in, p.k = n;
-    p.out = a.dx;
-    p.slope = a.x_pre, p.slope_act = a.x_act;
-    if ((e = multiply(p, stream)) != cudaSuccess) return e;
-  }
-  if (a.dweight.data) {
-    Product<E> p{};
-    p.a = g, p.ai = 1, p.ak = gs;
-    p.b = static_cast<const E*>(a.x.data), p.bj = 1, p.bk = a.x.stride;
-    p.m = n, p.n = a.in, p.k = m;
-    p.out = a.dweight;
-    e = multiply(p, stream);
-  }
-  return e;
+cudaError_t slopes(const LinearArgs& a, const Layout& l, cudaStream_t stream) {
+  const int n = a.out_features;
+  float* partial = a.dbias ? reinterpret_cast<float*>(a.workspace + l.partial) : nullptr;
+  cudaError_t e = launch_dependent(slope_kernel<E>, dim3((n + 255) / 256, l.parts), dim3(32, ROWS), 0, stream, a.dout, a.pre,
+                                   reinterpret_cast<E*>(a.workspace), partial, a.rows, n, l.chunk, a.act);
+  if (e != cudaSuccess || !a.dbias) return e;
+  return launch_dependent(dbias_kernel<E>, dim3((n + 31) / 32), dim3(32, 32), 0, stream, partial, l.parts, n, a.dbias,
+                          a.bias_dtype == VSA_F32);
 }
 
 }  // namespace
 
-size_t linear_fwd_workspace(int, int, int) { return 0; }
-size_t linear_bwd_workspace(int rows, int, int out, int act) {
-  const int chunk = chunk_rows(rows);
-  return align_up(dz_bytes(rows, out, act) + static_cast<size_t>((rows + chunk - 1) / chunk) * out * sizeof(float), 256);
-}
+size_t linear_fwd_workspace(int rows, int in, int out) { return gemm_workspace(rows, out, in); }
+size_t linear_bwd_workspace(int rows, int in, int out, int act) { return layout_of(rows, in, out, act).total; }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t stream) {
-  return a.dtype == VSA_F16 ? forward<__half>(a, stream) : forward<__nv_bfloat16>(a, stream);
+  GemmArgs g{};
+  g.a = a.x;
+  g.b = a.weight;
+  g.out = a.out;
+  g.pre = a.pre;
+  g.aux = a.residual;
+  g.bias = a.bias;
+  g.bias_f32 = a.bias_dtype == VSA_F32;
+  g.m = a.rows, g.n = a.out_features, g.k = a.in;
+  g.act = a.act;
+  g.dtype = a.dtype;
+  g.workspace = a.workspace;
+  g.err = a.err;
+  g.wait_ns = a.wait_ns;
+  return launch_gemm(GEMM_FWD, g, stream);
 }
+
 cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t stream) {
-  return a.dtype == VSA_F16 ? backward<__half>(a, stream) : backward<__nv_bfloat16>(a, stream);
+  const Layout l = layout_of(a.rows, a.in, a.out_features, a.act);
+  cudaError_t e = cudaSuccess;
+  if (a.act || a.dbias)
+    e = a.dtype == VSA_F16 ? slopes<__half>(a, l, stream) : slopes<__nv_bfloat16>(a, l, stream);
+  if (e != cudaSuccess) return e;
+  GemmArgs g{};
+  g.a = a.act ? MatrixView{a.workspace, a.out_features} : a.dout;  // dz
+  g.dtype = a.dtype;
+  g.workspace = a.workspace + l.gemm;
+  g.err = a.err;
+  g.wait_ns = a.wait_ns;
+  if (a.dx.data) {
+    g.b = a.weight;
+    g.out = a.dx;
+    g.aux = a.x_pre;
+    g.act = a.x_act;
+    g.m = a.rows, g.n = a.in, g.k = a.out_features;
+    if ((e = launch_gemm(GEMM_DX, g, stream)) != cudaSuccess) return e;
+  }
+  if (a.dweight.data) {
+    g.b = a.x;
+    g.out = a.dweight;
+    g.aux = MatrixView{};
+    g.m = a.out_features, g.n = a.in, g.k = a.rows;
+    e = launch_gemm(GEMM_DW, g, stream);
+  }
+  return e;
 }
 
 }  // namespace vsa
