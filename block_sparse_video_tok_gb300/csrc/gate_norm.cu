@@ -17,7 +17,10 @@
 // row's tokens.  The means are shuffles and one exchange of the warps' sums in shared memory per
 // round; the variance takes a round of its own, around the mean, so that tokens far from zero keep
 // their precision.  The next tokens' loads are issued before the rounds.
+#include <type_traits>
+
 #include "block_internal.cuh"
+#include "cross_common.cuh"
 #include "vec8.cuh"
 
 namespace vsa {
@@ -30,7 +33,7 @@ constexpr int FWD_ROWS = 2;   // tokens in flight per group of warps
 
 // Registers of a thread with NV vectors: the CTAs of an SM follow from them.
 constexpr int fwd_regs(int nv) { return nv == 1 ? 80 : 112; }
-constexpr int bwd_regs(int nv) { return nv == 1 ? 112 : 128; }
+constexpr int bwd_regs(int nv) { return nv == 1 ? 96 : 128; }
 
 // 8 parameters of either type, or `fallback`.
 __device__ __forceinline__ void load_param(const void* p, int64_t at, int dtype, float fallback, float* v) {
@@ -72,7 +75,7 @@ struct Params {
 // The warps that hold a token together: sums over all of its elements, the same for every lane.
 struct Team {
   float (*buf)[4][MAX_WPR];  // [2]: warps' sums of this round and of the one before
-  int wpr, warp, lane, bar, span;
+  int wpr, warp, lane, bar;
   uint32_t round;
 
   __device__ __forceinline__ Team(float (*b)[4][MAX_WPR], const Params& p) {
@@ -82,37 +85,44 @@ struct Team {
     warp = w % wpr;
     lane = threadIdx.x & 31;
     bar = 1 + w / wpr;
-    span = 1;
-    while (span < wpr) span *= 2;
     round = 0;
   }
 
+  // v[i] = its sum, for N = 1, 2 or 4 values at once: the lanes halve the values among them while
+  // they add (4 values: 6 exchanges, where one by one take 20), and the same lanes then add the warps'.
   template <int N>
   __device__ __forceinline__ void sum(float (&v)[N]) {
-    static_assert(N <= 4, "room for the warps' sums");
+    static_assert(N == 1 || N == 2 || N == 4, "values are halved");
+    constexpr int LANES = 32 / N;  // that add one value
+    float k[N];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int i = 0; i < N; ++i) k[i] = v[i];
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(FULL, v[i], o);
-    if (wpr == 1) return;
-    // Two buffers: a warp that writes round k + 2 has passed the barrier of round k + 1, which every
-    // warp reaches after its reads of round k.
-    float (*b)[MAX_WPR] = buf[round & 1u];
-    ++round;
-    if (lane < N) {
-      float mine = v[0];
+    for (int n = N / 2, o = 16; n > 0; n /= 2, o /= 2) {
+      const bool upper = (lane & o) != 0;
 #pragma unroll
-      for (int i = 1; i < N; ++i) mine = lane == i ? v[i] : mine;
-      b[lane][warp] = mine;
+      for (int i = 0; i < n; ++i) {
+        const float give = upper ? k[i] : k[i + n], keep = upper ? k[i + n] : k[i];
+        k[i] = keep + __shfl_xor_sync(FULL, give, o);
+      }
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(wpr * 32) : "memory");
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane < wpr ? b[i][lane & (MAX_WPR - 1)] : 0.f;
-    for (int o = span / 2; o > 0; o >>= 1)
+    for (int o = LANES / 2; o > 0; o /= 2) k[0] += __shfl_xor_sync(FULL, k[0], o);
+    if (wpr > 1) {
+      // Two buffers: a warp that writes round k + 2 has passed the barrier of round k + 1, which every
+      // warp reaches after its reads of round k.
+      float (*b)[MAX_WPR] = buf[round & 1u];
+      ++round;
+      const int value = lane / LANES, w = lane % LANES;
+      if (w == 0) b[value][warp] = k[0];
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(wpr * 32) : "memory");
+      k[0] = w < wpr ? b[value][w & (MAX_WPR - 1)] : 0.f;
+      if (LANES < MAX_WPR && w + LANES < wpr) k[0] += b[value][(w + LANES) & (MAX_WPR - 1)];
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(FULL, v[i], o);
+      for (int o = (LANES < MAX_WPR ? LANES : MAX_WPR) / 2; o > 0; o /= 2) k[0] += __shfl_xor_sync(FULL, k[0], o);
+    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(FULL, v[i], 0);
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(FULL, k[0], i * LANES);
   }
 };
 
@@ -129,6 +139,13 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
   x.t0 = x.g * p.len + min(first, p.len);
   x.t1 = x.g * p.len + min(first + p.chunk, p.len);
   return x;
+}
+
+__device__ __forceinline__ uint64_t pair(const float* v, int i) { return f2_pack(v[2 * i], v[2 * i + 1]); }
+__device__ __forceinline__ float halves(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo + hi;
 }
 
 template <typename T>
@@ -262,9 +279,107 @@ __global__ void __maxnreg__(fwd_regs(NV)) gate_norm_fwd_kernel(const __grid_cons
   }
 }
 
-// SUMS: the unit's S1, S2, S3 go to the workspace.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A lane's own 8 NV elements of `slots` tokens of one tensor in shared memory, written by asynchronous
+// copies and read by the lane that asked for them.
+template <typename T, int NV>
+struct Ring {
+  static constexpr int PIECES = NV * static_cast<int>(sizeof(T) / 2);  // 16 bytes each, a CTA's side by side
+  const T* from;  // null: absent, the ring holds zeros
+  int64_t stride;
+  int span, left;  // elements from one vector to the next; vectors of this lane
+  uint32_t at, step;
+
+  __device__ __forceinline__ static uint32_t bytes(int slots, int threads) { return slots * PIECES * threads * 16u; }
+  __device__ __forceinline__ Ring(uint32_t base, int slots, int vector_step, int vectors) {
+    at = base + threadIdx.x * 16u;
+    step = blockDim.x * 16u;
+    span = vector_step;
+    left = vectors;
+    for (int i = 0; i < slots * PIECES; ++i)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * step), "r"(0) : "memory");
+  }
+  __device__ __forceinline__ void open(const TokensView& v, int b, int e0) {
+    from = v.data ? static_cast<const T*>(v.data) + b * v.batch + e0 : nullptr;
+    stride = v.token;
+  }
+  __device__ __forceinline__ void load(int slot, int t) const {
+    if (!from) return;
+    const T* p = from + t * stride;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (k < left) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+          copy16(at + ((slot * NV + k) * (sizeof(T) / 2) + i) * step, p + k * span + i * (16 / sizeof(T)));
+      }
+  }
+  __device__ __forceinline__ void get(int slot, int k, float* v) const {
+    Raw<T> r;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.u[i].x), "=r"(r.u[i].y), "=r"(r.u[i].z), "=r"(r.u[i].w)
+                   : "r"(at + ((slot * NV + k) * static_cast<uint32_t>(sizeof(T) / 2) + i) * step)
+                   : "memory");
+    r.widen(v);
+  }
+};
+
+// The same without a ring: read where it is used.
+template <typename T, int NV>
+struct NoRing {
+  const T* from;
+  int64_t stride;
+  int span, left;
+
+  __device__ __forceinline__ static uint32_t bytes(int, int) { return 0u; }
+  __device__ __forceinline__ NoRing(uint32_t, int, int vector_step, int vectors) {
+    span = vector_step;
+    left = vectors;
+  }
+  __device__ __forceinline__ void open(const TokensView& v, int b, int e0) {
+    from = v.data ? static_cast<const T*>(v.data) + b * v.batch + e0 : nullptr;
+    stride = v.token;
+  }
+  __device__ __forceinline__ void load(int, int) const {}
+  __device__ __forceinline__ void get(int t, int k, float* v) const {
+    Raw<T> r;
+    r.zero();
+    if (from && k < left) r.load(from + t * stride + k * span);
+    r.widen(v);
+  }
+};
+
+// Tokens of the backward's rings, and their bytes: x', dx_out, dh and y.  Two are the fewest; four fit
+// where a token's lane has 16 bytes of each.  fp32 beyond 4096 channels leaves no room for dx_out's.
+template <typename TX, int NV>
+constexpr int slots_of() { return NV == 1 && sizeof(TX) == 2 ? 4 : 2; }
+template <typename TX, typename TY, int NV>
+constexpr bool o_direct() { return NV == 2 && sizeof(TX) == 4 && sizeof(TY) == 4; }
+template <typename TX, typename TY, int NV>
+constexpr int ring_bytes(int threads) {
+  return slots_of<TX, NV>() * ((o_direct<TX, TY, NV>() ? 1 : 2) * Ring<TX, NV>::PIECES + 2 * Ring<TY, NV>::PIECES) * 16 * threads;
+}
+constexpr int SM_SMEM = 228 * 1024, CTA_SMEM = 227 * 1024, STATIC_SMEM = CTA_WARPS * 2 * 4 * MAX_WPR * 4 + 1024;
+
+// One round of sums a token: those of the token itself around its mean, and the mean of the next one.
+// A post norm takes a second round.  The inputs come SLOTS - 1 tokens ahead through shared memory: in
+// registers beside the three sums there is room for one.  SUMS: the unit's S1, S2, S3 go to the
+// workspace.
 template <typename TX, typename TY, int NV, bool SUMS>
 __global__ void __maxnreg__(bwd_regs(NV)) gate_norm_bwd_kernel(const __grid_constant__ Params p) {
+  constexpr int SLOTS = slots_of<TX, NV>();
+  constexpr bool DIRECT = o_direct<TX, TY, NV>();
+  extern __shared__ uint4 room[];
   __shared__ float sums[CTA_WARPS][2][4][MAX_WPR];
   grid_dependency_wait();
   const GateNormArgs& a = p.a;
@@ -272,147 +387,169 @@ __global__ void __maxnreg__(bwd_regs(NV)) gate_norm_bwd_kernel(const __grid_cons
   Team team(sums[group], p);
   const int e0 = (team.warp * 32 + team.lane) * 8, step = p.wpr * 256;
   const bool branch = a.y.data != nullptr, post = a.post_weight != nullptr, layer = a.kind == VSA_LAYER_NORM;
+  const int vectors = a.channels > e0 ? (a.channels - e0 + step - 1) / step : 0;
+  uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(room));
+  Ring<TX, NV> x(base, SLOTS, step, vectors);
+  base += Ring<TX, NV>::bytes(SLOTS, blockDim.x);
+  using Other = typename std::conditional<DIRECT, NoRing<TX, NV>, Ring<TX, NV>>::type;
+  Other o(base, SLOTS, step, vectors);
+  base += Other::bytes(SLOTS, blockDim.x);
+  Ring<TY, NV> h(base, SLOTS, step, vectors);
+  base += Ring<TY, NV>::bytes(SLOTS, blockDim.x);
+  Ring<TY, NV> y(base, SLOTS, step, vectors);
 
   for (int u = blockIdx.x * p.per_cta + group; u < p.units; u += gridDim.x * p.per_cta) {
     const Unit unit = unit_of(p, u);
-    float ca[NV][8], cg[NV][8], cp[NV][8], acc[SUMS ? NV : 1][3][8];
+    x.open(a.x_out, unit.b, e0);
+    o.open(a.dx_out, unit.b, e0);
+    h.open(a.dh, unit.b, e0);
+    y.open(a.y, unit.b, e0);
+    // Copies go in groups: group i has token i's dh, dx_out and y, and x' of token i + 1.
+    if (unit.t0 < unit.t1) x.load(0, unit.t0);
+    auto ahead = [&](int t) {  // t0 + i: slot i % SLOTS
+      const int slot = (t - unit.t0) & (SLOTS - 1);
+      if (t < unit.t1) {
+        h.load(slot, t);
+        o.load(slot, t);
+        y.load(slot, t);
+      }
+      if (t + 1 < unit.t1) x.load((slot + 1) & (SLOTS - 1), t + 1);
+      copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < SLOTS - 1; ++i) ahead(unit.t0 + i);
+    uint64_t ca[NV][4], cg[NV][4], acc[SUMS ? NV : 1][3][4];  // pairs; cg: gate, times post_weight
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int e = e0 + k * step;
 #pragma unroll
       for (int j = 0; SUMS && j < 3; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[SUMS ? k : 0][j][i] = 0.f;
-      if (e >= a.channels) continue;
-      float s[8];
-      load_param(a.weight, e, a.weight_dtype, 1.f, ca[k]);
+        for (int i = 0; i < 4; ++i) acc[SUMS ? k : 0][j][i] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ca[k][i] = cg[k][i] = 0;
+      if (k >= vectors) continue;
+      float w[8], s[8];
+      load_param(a.weight, e, a.weight_dtype, 1.f, w);
       load_param(a.scale.data, unit.b * a.scale.batch + unit.g * a.scale.group + e, a.mod_dtype, 0.f, s);
-      load_param(a.gate.data, unit.b * a.gate.batch + unit.g * a.gate.group + e, a.mod_dtype, 1.f, cg[k]);
-      if (post) load_param(a.post_weight, e, a.weight_dtype, 1.f, cp[k]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ca[k][i] *= 1.f + s[i];
+      for (int i = 0; i < 4; ++i) ca[k][i] = f2_pack(w[2 * i] * (1.f + s[2 * i]), w[2 * i + 1] * (1.f + s[2 * i + 1]));
+      load_param(a.gate.data, unit.b * a.gate.batch + unit.g * a.gate.group + e, a.mod_dtype, 1.f, w);
+      load_param(a.post_weight, e, a.weight_dtype, 1.f, s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cg[k][i] = f2_pack(w[2 * i] * s[2 * i], w[2 * i + 1] * s[2 * i + 1]);
     }
-    Raw<TX> rx[NV], ro[NV];
-    Raw<TY> rh[NV], ry[NV];
-    auto load = [&](int t) {
+    TX* pdx = static_cast<TX*>(a.dx.data) + unit.b * a.dx.batch + unit.t0 * a.dx.token + e0;
+    TY* pdy = static_cast<TY*>(a.dy.data) + unit.b * a.dy.batch + unit.t0 * a.dy.token + e0;
+    auto total = [&](int slot) {
+      uint64_t s = 0;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int e = e0 + k * step;
-        rx[k].zero();
-        ro[k].zero();
-        rh[k].zero();
-        ry[k].zero();
-        if (t < unit.t1 && e < a.channels) {
-          rx[k].load(at<const TX>(a.x_out, unit.b, t) + e);
-          rh[k].load(at<const TY>(a.dh, unit.b, t) + e);
-          if (a.dx_out.data) ro[k].load(at<const TX>(a.dx_out, unit.b, t) + e);
-          if (branch) ry[k].load(at<const TY>(a.y, unit.b, t) + e);
-        }
+        float v[8];
+        x.get(slot, k, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s = f2_add(s, pair(v, i));
       }
+      return halves(s);
     };
-    load(unit.t0);
-    for (int t = unit.t0; t < unit.t1; ++t) {
-      float v[NV][8], g[NV][8], o[NV][8];
-      Raw<TY> y[NV];
-      float q = 0.f;  // sum of y^2
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        rx[k].widen(v[k]);
-        rh[k].widen(g[k]);
-        ro[k].widen(o[k]);
-        y[k] = ry[k];
-        if (post) {
-          float z[8];
-          y[k].widen(z);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q = fmaf(z[i], z[i], q);
-        }
-      }
-      load(t + 1);
-      if (layer) {
-        float s[2] = {0.f, q};
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] += v[k][i];
-        team.sum(s);
-        q = s[1];
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-          if (e0 + k * step < a.channels) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = fmaf(-s[0], p.inv_dim, v[k][i]);
-          }
-      }
-      float s[4] = {0.f, 0.f, 0.f, q};  // v^2, g v, g, y^2
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (e0 + k * step < a.channels) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float ga = g[k][i] * ca[k][i];
-            s[0] = fmaf(v[k][i], v[k][i], s[0]);
-            s[1] = fmaf(ga, v[k][i], s[1]);
-            s[2] += ga;
-          }
-        }
+    float mean = 0.f;
+    if (layer) {
+      copy_wait<SLOTS - 2>();
+      float s[1] = {total(0)};
       team.sum(s);
-      if (!layer) q = s[3];
-      const float f = rsqrtf(fmaf(s[0], p.inv_dim, a.eps));
-      const float m1 = layer ? s[2] * p.inv_dim : 0.f, m2 = s[1] * f * p.inv_dim;
-      const float fy = post ? rsqrtf(fmaf(q, p.inv_dim, a.post_eps)) : 1.f;
-      float z[1] = {0.f};
+      mean = s[0] * p.inv_dim;
+    }
+    for (int t = unit.t0; t < unit.t1; ++t) {
+      const int slot = (t - unit.t0) & (SLOTS - 1);
+      copy_wait<SLOTS - 2>();
+      uint64_t v[NV][4], s2[3] = {0, 0, 0};
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int e = e0 + k * step;
-        if (e >= a.channels) continue;
-        float ny[8];
-        if (branch) y[k].widen(ny);
+        float w[8], g[8];
+        x.get(slot, k, w);
+        h.get(slot, k, g);
+        const float off = k < vectors ? -mean : 0.f;
+        const uint64_t off2 = f2_pack(off, off);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float n = v[k][i] * f;
-          const float dx = fmaf(f, fmaf(g[k][i], ca[k][i], -m1) - n * m2, o[k][i]);
-          if (SUMS) {
-            acc[SUMS ? k : 0][0][i] += g[k][i];
-            acc[SUMS ? k : 0][1][i] = fmaf(g[k][i], n, acc[SUMS ? k : 0][1][i]);
-          }
-          o[k][i] = dx;
-          if (branch) {
-            ny[i] *= fy;
-            if (SUMS) acc[SUMS ? k : 0][2][i] = fmaf(dx, ny[i], acc[SUMS ? k : 0][2][i]);
-            g[k][i] = dx * cg[k][i];
-            if (post) {
-              g[k][i] *= cp[k][i];
-              z[0] = fmaf(g[k][i], ny[i], z[0]);
-            }
-          }
+        for (int i = 0; i < 4; ++i) {
+          v[k][i] = f2_add(pair(w, i), off2);
+          const uint64_t ga = f2_mul(pair(g, i), ca[k][i]);
+          s2[0] = f2_fma(v[k][i], v[k][i], s2[0]);
+          s2[1] = f2_fma(ga, v[k][i], s2[1]);
+          s2[2] = f2_add(ga, s2[2]);
         }
-        store8(at<TX>(a.dx, unit.b, t) + e, o[k]);
-        if (branch && !post) store8(at<TY>(a.dy, unit.b, t) + e, g[k]);
+      }
+      // v^2, g v, g of this token; x' of the next
+      float s[4] = {halves(s2[0]), halves(s2[1]), halves(s2[2]), 0.f};
+      if (layer) s[3] = total((slot + 1) & (SLOTS - 1));
+      team.sum(s);
+      ahead(t + SLOTS - 1);  // into the slots of token t - 1, and of x' of token t
+      const float f = rsqrtf(fmaf(s[0], p.inv_dim, a.eps));
+      const float m1 = layer ? -s[2] * p.inv_dim : 0.f, m2 = -s[1] * f * p.inv_dim;
+      const uint64_t f2 = f2_pack(f, f), m12 = f2_pack(m1, m1), m22 = f2_pack(m2, m2);
+      mean = s[3] * p.inv_dim;
+      uint64_t z2[2] = {0, 0};  // post norm: q y, y^2
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float g[8], d[8], w[8];
+        h.get(slot, k, g);
+        o.get(DIRECT ? t : slot, k, d);
+        y.get(slot, k, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t n = f2_mul(v[k][i], f2), gi = pair(g, i), yi = pair(w, i);
+          const uint64_t dx = f2_fma(f2, f2_fma(n, m22, f2_fma(gi, ca[k][i], m12)), pair(d, i));
+          if (SUMS) {
+            acc[SUMS ? k : 0][0][i] = f2_add(acc[SUMS ? k : 0][0][i], gi);
+            acc[SUMS ? k : 0][1][i] = f2_fma(gi, n, acc[SUMS ? k : 0][1][i]);
+          }
+          v[k][i] = dx;
+          const uint64_t q = f2_mul(dx, cg[k][i]);
+          if (post) {
+            z2[0] = f2_fma(q, yi, z2[0]);
+            z2[1] = f2_fma(yi, yi, z2[1]);
+          } else if (SUMS) {
+            acc[SUMS ? k : 0][2][i] = f2_fma(dx, yi, acc[SUMS ? k : 0][2][i]);
+          }
+          f2_unpack(dx, d[2 * i], d[2 * i + 1]);
+          f2_unpack(q, g[2 * i], g[2 * i + 1]);
+        }
+        if (k < vectors) {
+          store8(pdx + k * step, d);
+          if (branch && !post) store8(pdy + k * step, g);
+        }
       }
       if (post) {
+        float z[2] = {halves(z2[0]), halves(z2[1])};
         team.sum(z);
-        const float m = z[0] * p.inv_dim;
+        const float fy = rsqrtf(fmaf(z[1], p.inv_dim, a.post_eps)), m = -z[0] * fy * p.inv_dim;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          const int e = e0 + k * step;
-          if (e >= a.channels) continue;
-          float ny[8];
-          y[k].widen(ny);
+          float w[8];
+          y.get(slot, k, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[k][i] = fy * fmaf(-ny[i] * fy, m, g[k][i]);
-          store8(at<TY>(a.dy, unit.b, t) + e, g[k]);
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t ny = f2_mul(pair(w, i), f2_pack(fy, fy));
+            if (SUMS) acc[SUMS ? k : 0][2][i] = f2_fma(v[k][i], ny, acc[SUMS ? k : 0][2][i]);
+            f2_unpack(f2_mul(f2_fma(ny, f2_pack(m, m), f2_mul(v[k][i], cg[k][i])), f2_pack(fy, fy)), w[2 * i], w[2 * i + 1]);
+          }
+          if (k < vectors) store8(pdy + k * step, w);
         }
       }
+      pdx += a.dx.token;
+      pdy += a.dy.token;
     }
     if (SUMS) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int e = e0 + k * step;
-        if (e >= a.channels) continue;
+        if (k >= vectors) continue;
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-          store8(a.workspace + (static_cast<int64_t>(u) * 3 + j) * a.channels + e, acc[SUMS ? k : 0][j]);
+        for (int j = 0; j < 3; ++j) {
+          float w[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f2_unpack(acc[SUMS ? k : 0][j][i], w[2 * i], w[2 * i + 1]);
+          store8(a.workspace + (static_cast<int64_t>(u) * 3 + j) * a.channels + e0 + k * step, w);
+        }
       }
     }
   }
@@ -493,15 +630,21 @@ int vectors(int channels) { return channels <= 256 * MAX_WPR ? 1 : 2; }
 constexpr int FWD_EXTRA = 2, BWD_EXTRA = 4;
 struct Plan {
   int wpr, per_cta, ctas, parts, chunk, units;
+  size_t most;  // units at most, whatever the type
 };
-Plan plan_of(int batch, int tokens, int channels, int groups, bool forward) {
+Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int lane_bytes) {
   const int extra = forward ? FWD_EXTRA : BWD_EXTRA;
   Plan q{};
   const int nv = vectors(channels);
   q.wpr = (channels + 256 * nv - 1) / (256 * nv);
   q.per_cta = q.wpr < CTA_WARPS ? CTA_WARPS / q.wpr : 1;
   const int regs = (forward ? fwd_regs(nv) : bwd_regs(nv)) * 32 * q.wpr * q.per_cta;
-  const int per_sm = 65536 / regs;
+  int per_sm = 65536 / regs;
+  q.most = static_cast<size_t>(device_sm_count()) * per_sm * q.per_cta * 4;
+  if (!forward) {
+    const int room = SM_SMEM / (lane_bytes * 32 * q.wpr * q.per_cta + STATIC_SMEM);
+    per_sm = per_sm < room ? per_sm : room;
+  }
   const int64_t slots = static_cast<int64_t>(device_sm_count()) * per_sm * q.per_cta;
   const int64_t rows = static_cast<int64_t>(batch) * groups;
   const int len = tokens / groups;
@@ -520,6 +663,7 @@ Plan plan_of(int batch, int tokens, int channels, int groups, bool forward) {
     }
   }
   q.units = static_cast<int>(rows * q.parts);
+  if (q.most < static_cast<size_t>(rows)) q.most = static_cast<size_t>(rows);
   const int64_t need = (q.units + q.per_cta - 1) / q.per_cta, most = slots / q.per_cta;
   q.ctas = static_cast<int>(need < most ? need : most);
   return q;
@@ -531,7 +675,7 @@ bool wants_sums(const GateNormArgs& a) {
 
 template <typename TX, typename TY, int NV>
 cudaError_t launch(const GateNormArgs& a, bool forward, cudaStream_t stream) {
-  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, forward);
+  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, forward, ring_bytes<TX, TY, NV>(1));
   Params p;
   p.a = a;
   p.wpr = q.wpr;
@@ -543,8 +687,16 @@ cudaError_t launch(const GateNormArgs& a, bool forward, cudaStream_t stream) {
   p.inv_dim = 1.f / static_cast<float>(a.channels);
   const dim3 grid(q.ctas), block(q.wpr * q.per_cta * 32);
   if (forward) return launch_dependent(gate_norm_fwd_kernel<TX, TY, NV>, grid, block, 0, stream, p);
-  if (!wants_sums(a)) return launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, false>, grid, block, 0, stream, p);
-  cudaError_t e = launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, true>, grid, block, 0, stream, p);
+  const int smem = ring_bytes<TX, TY, NV>(block.x);
+  cudaError_t e;
+  if (!wants_sums(a)) {
+    static std::atomic<uint64_t> smem_set{0};
+    e = ensure_smem_limit(gate_norm_bwd_kernel<TX, TY, NV, false>, CTA_SMEM - STATIC_SMEM, smem_set);
+    return e != cudaSuccess ? e : launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, false>, grid, block, smem, stream, p);
+  }
+  static std::atomic<uint64_t> smem_set{0};
+  if ((e = ensure_smem_limit(gate_norm_bwd_kernel<TX, TY, NV, true>, CTA_SMEM - STATIC_SMEM, smem_set)) != cudaSuccess) return e;
+  e = launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, true>, grid, block, smem, stream, p);
   if (e != cudaSuccess) return e;
   const int rows = a.batch * a.groups, columns = (a.channels + 31) / 32;
   float* share = rows > 1 && (a.dpost || a.dweight || a.dbias)
@@ -575,9 +727,9 @@ cudaError_t launch_typed(const GateNormArgs& a, bool forward, cudaStream_t strea
 }  // namespace
 
 size_t gate_norm_bwd_workspace(int batch, int tokens, int channels, int groups) {
-  const Plan q = plan_of(batch, tokens, channels, groups, false);
+  const Plan q = plan_of(batch, tokens, channels, groups, false, 0);
   const size_t rows = static_cast<size_t>(batch) * groups;
-  return align_up((q.units + rows) * 3 * channels * sizeof(float), 256);
+  return align_up((q.most + rows) * 3 * channels * sizeof(float), 256);
 }
 
 cudaError_t launch_gate_norm_fwd(const GateNormArgs& a, cudaStream_t stream) { return launch_typed(a, true, stream); }
