@@ -29,11 +29,13 @@ namespace {
 
 constexpr int MAX_WPR = 16;   // warps of a token
 constexpr int CTA_WARPS = 8;  // warps of a CTA that holds several tokens
+constexpr int BWD_ONE = 512;  // channels up to which the backward gives a lane one vector
 constexpr int FWD_ROWS = 2;   // tokens in flight per group of warps
 
 // Registers of a thread with NV vectors: the CTAs of an SM follow from them.
 constexpr int fwd_regs(int nv) { return nv == 1 ? 80 : 112; }
-constexpr int bwd_regs(int nv) { return nv == 1 ? 96 : 128; }
+// (Backward, two vectors: more than 128 where a CTA's threads leave room.)
+constexpr int BWD_REGS_1 = 96, BWD_REGS_2 = 168, BWD_REGS_WIDE = 128;
 
 // 8 parameters of either type, or `fallback`.
 __device__ __forceinline__ void load_param(const void* p, int64_t at, int dtype, float fallback, float* v) {
@@ -375,8 +377,8 @@ constexpr int SM_SMEM = 228 * 1024, CTA_SMEM = 227 * 1024, STATIC_SMEM = CTA_WAR
 // A post norm takes a second round.  The inputs come SLOTS - 1 tokens ahead through shared memory: in
 // registers beside the three sums there is room for one.  SUMS: the unit's S1, S2, S3 go to the
 // workspace.
-template <typename TX, typename TY, int NV, bool SUMS>
-__global__ void __maxnreg__(bwd_regs(NV)) gate_norm_bwd_kernel(const __grid_constant__ Params p) {
+template <typename TX, typename TY, int NV, int REGS, bool SUMS>
+__global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ Params p) {
   constexpr int SLOTS = slots_of<TX, NV>();
   constexpr bool DIRECT = o_direct<TX, TY, NV>();
   extern __shared__ uint4 room[];
@@ -482,8 +484,8 @@ __global__ void __maxnreg__(bwd_regs(NV)) gate_norm_bwd_kernel(const __grid_cons
       // v^2, g v, g of this token; x' of the next
       float s[4] = {halves(s2[0]), halves(s2[1]), halves(s2[2]), 0.f};
       if (layer) s[3] = total((slot + 1) & (SLOTS - 1));
-      team.sum(s);
       ahead(t + SLOTS - 1);  // into the slots of token t - 1, and of x' of token t
+      team.sum(s);
       const float f = rsqrtf(fmaf(s[0], p.inv_dim, a.eps));
       const float m1 = layer ? -s[2] * p.inv_dim : 0.f, m2 = -s[1] * f * p.inv_dim;
       const uint64_t f2 = f2_pack(f, f), m12 = f2_pack(m1, m1), m22 = f2_pack(m2, m2);
@@ -623,7 +625,11 @@ __global__ void __launch_bounds__(1024) gate_norm_weights_kernel(const __grid_co
   store_param(j == 0 ? a.dbias : j == 1 ? a.dweight : a.dpost, c, a.weight_dtype, s);
 }
 
-int vectors(int channels) { return channels <= 256 * MAX_WPR ? 1 : 2; }
+int fwd_vectors(int channels) { return channels <= 256 * MAX_WPR ? 1 : 2; }
+int bwd_vectors(int channels) { return channels <= BWD_ONE ? 1 : 2; }
+int bwd_regs(int channels) {
+  return bwd_vectors(channels) == 1 ? BWD_REGS_1 : (channels + 511) / 512 * 32 * BWD_REGS_2 <= 65536 ? BWD_REGS_2 : BWD_REGS_WIDE;
+}
 
 // Units: parts of every modulation row.  The grid takes them in waves of `slots`, each as long as a
 // unit's tokens and what a unit costs besides (`extra` tokens); the least of up to four waves.
@@ -635,17 +641,25 @@ struct Plan {
 Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int lane_bytes) {
   const int extra = forward ? FWD_EXTRA : BWD_EXTRA;
   Plan q{};
-  const int nv = vectors(channels);
+  const int nv = forward ? fwd_vectors(channels) : bwd_vectors(channels);
   q.wpr = (channels + 256 * nv - 1) / (256 * nv);
-  q.per_cta = q.wpr < CTA_WARPS ? CTA_WARPS / q.wpr : 1;
-  const int regs = (forward ? fwd_regs(nv) : bwd_regs(nv)) * 32 * q.wpr * q.per_cta;
-  int per_sm = 65536 / regs;
-  q.most = static_cast<size_t>(device_sm_count()) * per_sm * q.per_cta * 4;
-  if (!forward) {
-    const int room = SM_SMEM / (lane_bytes * 32 * q.wpr * q.per_cta + STATIC_SMEM);
-    per_sm = per_sm < room ? per_sm : room;
+  // Tokens of a CTA: as many on an SM as its registers and shared memory hold, in at most 4 CTAs (a CTA
+  // takes 16 of an SM's 64 barriers).
+  const int warp_regs = (forward ? fwd_regs(nv) : bwd_regs(channels)) * 32;
+  int most = 0, teams = 0;
+  for (int n = 1; n == 1 || n * q.wpr <= CTA_WARPS; ++n) {
+    int ctas = 65536 / (warp_regs * q.wpr * n);
+    ctas = ctas < 4 ? ctas : 4;
+    most = most > ctas * n ? most : ctas * n;
+    const int room = SM_SMEM / (lane_bytes * 32 * q.wpr * n + STATIC_SMEM);
+    ctas = ctas < room ? ctas : room;
+    if (ctas * n > teams) {
+      teams = ctas * n;
+      q.per_cta = n;
+    }
   }
-  const int64_t slots = static_cast<int64_t>(device_sm_count()) * per_sm * q.per_cta;
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * teams;
+  q.most = static_cast<size_t>(device_sm_count()) * most * 4;
   const int64_t rows = static_cast<int64_t>(batch) * groups;
   const int len = tokens / groups;
   int64_t best = INT64_MAX;
@@ -664,8 +678,8 @@ Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int 
   }
   q.units = static_cast<int>(rows * q.parts);
   if (q.most < static_cast<size_t>(rows)) q.most = static_cast<size_t>(rows);
-  const int64_t need = (q.units + q.per_cta - 1) / q.per_cta, most = slots / q.per_cta;
-  q.ctas = static_cast<int>(need < most ? need : most);
+  const int64_t need = (q.units + q.per_cta - 1) / q.per_cta, grid = slots / q.per_cta;
+  q.ctas = static_cast<int>(need < grid ? need : grid);
   return q;
 }
 
@@ -673,9 +687,7 @@ bool wants_sums(const GateNormArgs& a) {
   return a.dgate || a.dscale || a.dshift || a.dpost || a.dweight || a.dbias;
 }
 
-template <typename TX, typename TY, int NV>
-cudaError_t launch(const GateNormArgs& a, bool forward, cudaStream_t stream) {
-  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, forward, ring_bytes<TX, TY, NV>(1));
+Params params_of(const GateNormArgs& a, const Plan& q) {
   Params p;
   p.a = a;
   p.wpr = q.wpr;
@@ -685,18 +697,32 @@ cudaError_t launch(const GateNormArgs& a, bool forward, cudaStream_t stream) {
   p.chunk = q.chunk;
   p.units = q.units;
   p.inv_dim = 1.f / static_cast<float>(a.channels);
-  const dim3 grid(q.ctas), block(q.wpr * q.per_cta * 32);
-  if (forward) return launch_dependent(gate_norm_fwd_kernel<TX, TY, NV>, grid, block, 0, stream, p);
-  const int smem = ring_bytes<TX, TY, NV>(block.x);
-  cudaError_t e;
-  if (!wants_sums(a)) {
-    static std::atomic<uint64_t> smem_set{0};
-    e = ensure_smem_limit(gate_norm_bwd_kernel<TX, TY, NV, false>, CTA_SMEM - STATIC_SMEM, smem_set);
-    return e != cudaSuccess ? e : launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, false>, grid, block, smem, stream, p);
-  }
+  return p;
+}
+
+template <typename TX, typename TY, int NV>
+cudaError_t launch_fwd(const GateNormArgs& a, cudaStream_t stream) {
+  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, true, 0);
+  return launch_dependent(gate_norm_fwd_kernel<TX, TY, NV>, dim3(q.ctas), dim3(q.wpr * q.per_cta * 32), 0, stream,
+                          params_of(a, q));
+}
+
+template <typename TX, typename TY, int NV, int REGS, bool SUMS>
+cudaError_t launch_main(const Params& p, const Plan& q, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  if ((e = ensure_smem_limit(gate_norm_bwd_kernel<TX, TY, NV, true>, CTA_SMEM - STATIC_SMEM, smem_set)) != cudaSuccess) return e;
-  e = launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, true>, grid, block, smem, stream, p);
+  const cudaError_t e = ensure_smem_limit(gate_norm_bwd_kernel<TX, TY, NV, REGS, SUMS>, CTA_SMEM - STATIC_SMEM, smem_set);
+  if (e != cudaSuccess) return e;
+  const int threads = q.wpr * q.per_cta * 32;
+  return launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, REGS, SUMS>, dim3(q.ctas), dim3(threads),
+                          ring_bytes<TX, TY, NV>(threads), stream, p);
+}
+
+template <typename TX, typename TY, int NV, int REGS>
+cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
+  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, false, ring_bytes<TX, TY, NV>(1));
+  const Params p = params_of(a, q);
+  if (!wants_sums(a)) return launch_main<TX, TY, NV, REGS, false>(p, q, stream);
+  cudaError_t e = launch_main<TX, TY, NV, REGS, true>(p, q, stream);
   if (e != cudaSuccess) return e;
   const int rows = a.batch * a.groups, columns = (a.channels + 31) / 32;
   float* share = rows > 1 && (a.dpost || a.dweight || a.dbias)
@@ -710,9 +736,12 @@ cudaError_t launch(const GateNormArgs& a, bool forward, cudaStream_t stream) {
 
 template <typename TX, typename TY>
 cudaError_t launch_width(const GateNormArgs& a, bool forward, cudaStream_t stream) {
-  switch (vectors(a.channels)) {
-    case 1: return launch<TX, TY, 1>(a, forward, stream);
-    default: return launch<TX, TY, 2>(a, forward, stream);
+  if (forward)
+    return fwd_vectors(a.channels) == 1 ? launch_fwd<TX, TY, 1>(a, stream) : launch_fwd<TX, TY, 2>(a, stream);
+  switch (bwd_regs(a.channels)) {
+    case BWD_REGS_1: return launch_bwd<TX, TY, 1, BWD_REGS_1>(a, stream);
+    case BWD_REGS_2: return launch_bwd<TX, TY, 2, BWD_REGS_2>(a, stream);
+    default: return launch_bwd<TX, TY, 2, BWD_REGS_WIDE>(a, stream);
   }
 }
 
