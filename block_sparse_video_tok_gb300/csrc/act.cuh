@@ -1,36 +1,68 @@
-// act.cuh -- the activations of vsa_linear and their slopes, in fp32, and 16-bit conversions.
+// act.cuh -- the activations of vsa_linear and their slopes, in fp32.
 //
-// The logistic function takes one fast exponential and one fast division: together good to about
-// 2^-20 relative where the result is above 2^-20, against the 2^-8 or 2^-11 of the 16-bit results.
-// The normal distribution goes through erfc, whose relative precision holds into the lower tail.
+// The logistic function is one fast exponential and one fast reciprocal.  The normal distribution is
+//   Phi(-a) = exp(-a^2 / 2) t P(t),  t = 1 / (1 + 0.36 a),  a >= 0,
+// with P a polynomial of degree 6 fitted here to exp(a^2 / 2) Phi(-a) / t by least squares reweighted
+// towards the largest relative error (at most 2^-20 for a up to 14, where Phi leaves the range of
+// fp32), so its lower tail keeps the results' precision; its slope's exp(-z^2 / 2) is the same one.  All
+// are good to about 2^-18 relative, exponents of a size x to x 2^-23 more, against the 2^-8 or 2^-11 of the
+// 16-bit results.  (With the library's erfc in its place the product 32760 x 1536 x 6144 took 775 us with
+// gelu, 366 with silu.)
 #pragma once
 
 #include "block_internal.cuh"
+#include "cross_common.cuh"
 
 namespace vsa {
 
 constexpr float GELU_C = 0.7978845608028654f, GELU_D = 0.044715f;  // sqrt(2 / pi)
 
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.7071067811865476f * z); }
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / (1 + 2^-x): the logistic function of x / log2(e).
+__device__ __forceinline__ float logistic2(float x) { return reciprocal(1.f + ex2(-x)); }
+
+// Phi(z), and exp(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf(float z, float* bell) {
+  const float a = fabsf(z), t = reciprocal(fmaf(0.36f, a, 1.f));
+  float q = fmaf(0.047056187f, t, -0.17976487f);
+  q = fmaf(q, t, 0.18095505f);
+  q = fmaf(q, t, 0.026548008f);
+  q = fmaf(q, t, 0.13971997f);
+  q = fmaf(q, t, 0.14177228f);
+  q = fmaf(q, t, 0.14371306f);
+  *bell = ex2(-0.5f * LOG2E_F * z * z);
+  const float tail = *bell * (t * q);
+  return z < 0.f ? tail : 1.f - tail;
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-  if (ACT == VSA_GELU) return z * normal_cdf(z);
-  if (ACT == VSA_GELU_TANH) return z * logistic(2.f * GELU_C * fmaf(GELU_D * z * z, z, z));
-  if (ACT == VSA_SILU) return z * logistic(z);
+  if (ACT == VSA_GELU) {
+    float bell;
+    return z * normal_cdf(z, &bell);
+  }
+  if (ACT == VSA_GELU_TANH) return z * logistic2(z * fmaf(2.f * LOG2E_F * GELU_C * GELU_D, z * z, 2.f * LOG2E_F * GELU_C));
+  if (ACT == VSA_SILU) return z * logistic2(LOG2E_F * z);
   return z;
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-  if (ACT == VSA_GELU) return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), normal_cdf(z));
+  if (ACT == VSA_GELU) {
+    float bell;
+    const float cdf = normal_cdf(z, &bell);
+    return fmaf(z * 0.3989422804014327f, bell, cdf);
+  }
   if (ACT == VSA_GELU_TANH) {
-    const float zz = z * z, s = logistic(2.f * GELU_C * fmaf(GELU_D * zz, z, z));
-    return fmaf(2.f * GELU_C * z * fmaf(3.f * GELU_D, zz, 1.f), s * (1.f - s), s);
+    const float zz = z * z, s = logistic2(z * fmaf(2.f * LOG2E_F * GELU_C * GELU_D, zz, 2.f * LOG2E_F * GELU_C));
+    return fmaf(z * fmaf(6.f * GELU_C * GELU_D, zz, 2.f * GELU_C), s * (1.f - s), s);
   }
   if (ACT == VSA_SILU) {
-    const float s = logistic(z);
+    const float s = logistic2(LOG2E_F * z);
     return s * fmaf(z, 1.f - s, 1.f);
   }
   return 1.f;

@@ -14,8 +14,8 @@
 // parts leave fp32 sums in the workspace, which gemm_join_kernel adds in part order and finishes.
 // The same rule splits small problems, all of whose tiles are such a rest.
 //
-// Roles (256 threads): warp 0 TMA producer; warp 1 UMMA issuer (first CTA of the pair); warp 2 tensor
-// memory; warps 4-7 epilogue, a row per thread: bias, activation, residual or slope in fp32, rounded
+// Roles (384 threads): warp 0 TMA producer; warp 1 UMMA issuer (first CTA of the pair); warp 2 tensor
+// memory; warps 4-11 epilogue, half a row of the tile per thread: bias, activation, residual or slope in fp32, rounded
 // once, through swizzled shared memory to TMA stores, which clip at the matrix's edges.
 #include <type_traits>
 
@@ -30,30 +30,28 @@ namespace {
 
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair
 constexpr int GROUP_M = 8;
-constexpr int NUM_THREADS = 256;
-constexpr int TMA_WARP = 0, MMA_WARP = 1, TMEM_WARP = 2, EPI_WARP = 4, EPI_WARPS = 4;
+constexpr int NUM_THREADS = 384;
+constexpr int TMA_WARP = 0, MMA_WARP = 1, TMEM_WARP = 2, EPI_WARP = 4, EPI_WARPS = 8;
 constexpr uint32_t OPERAND_BYTES = 128 * BK * 2;  // a CTA's A or B of a stage
 constexpr uint32_t STAGE_BYTES = 2 * OPERAND_BYTES;
 constexpr uint32_t OUT_BYTES = 32 * 128;  // 32 rows x 64 results of an epilogue warp
 
-// With an operand of the epilogue to load, a warp has 4 output buffers to load ahead into.
-constexpr int stages_of(bool aux) { return aux ? 5 : 6; }
-constexpr int buffers_of(bool aux) { return aux ? 4 : 2; }
+constexpr int STAGES = 5;
+constexpr int BUFFERS = 2;  // of an epilogue warp: 64 results each of its 32 rows x 128 columns
 
-constexpr uint32_t MAX_STAGES = 6, MAX_BUFFERS = 4;
 enum Bar : uint32_t {
   FULL0 = 0,                        // first CTA: both CTAs' copies of a stage have landed
-  EMPTY0 = FULL0 + MAX_STAGES,      // each CTA: a stage's products are done
-  ACC_FULL0 = EMPTY0 + MAX_STAGES,  // each CTA: a tile's products are done
+  EMPTY0 = FULL0 + STAGES,          // each CTA: a stage's products are done
+  ACC_FULL0 = EMPTY0 + STAGES,      // each CTA: a tile's products are done
   ACC_EMPTY0 = ACC_FULL0 + 2,       // first CTA: both CTAs' epilogues have read a tile
   AUX0 = ACC_EMPTY0 + 2,            // per epilogue warp and buffer
-  DRAIN = AUX0 + EPI_WARPS * MAX_BUFFERS,
+  DRAIN = AUX0 + EPI_WARPS * BUFFERS,
   NUM_BARS
 };
-constexpr uint32_t sm_out(bool aux) { return stages_of(aux) * STAGE_BYTES; }
-constexpr uint32_t sm_bar(bool aux) { return sm_out(aux) + EPI_WARPS * buffers_of(aux) * OUT_BYTES; }
-constexpr uint32_t smem_bytes(bool aux) { return sm_bar(aux) + NUM_BARS * 8 + 8 + 1024; }
-static_assert(smem_bytes(false) <= 232448 && smem_bytes(true) <= 232448, "shared memory budget");
+constexpr uint32_t SM_OUT = STAGES * STAGE_BYTES;
+constexpr uint32_t SM_BAR = SM_OUT + EPI_WARPS * BUFFERS * OUT_BYTES;
+constexpr uint32_t SMEM_BYTES = SM_BAR + NUM_BARS * 8 + 8 + 1024;  // + alignment slack
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 struct Maps {
   CUtensorMap a, b, out, pre, aux;
@@ -206,14 +204,13 @@ __device__ __noinline__ void linger(uint64_t ns) {
 template <typename E, int OP, bool AUX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-  constexpr int STAGES = stages_of(AUX), BUFFERS = buffers_of(AUX);
   constexpr bool A_MN = OP == GEMM_DW, B_MN = OP != GEMM_FWD;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  volatile int* abort = reinterpret_cast<volatile int*>(gbase + sm_bar(AUX) + NUM_BARS * 8 + 4);
-  auto bar = [&](uint32_t b) { return base + sm_bar(AUX) + 8u * b; };
+  volatile int* abort = reinterpret_cast<volatile int*>(gbase + SM_BAR + NUM_BARS * 8 + 4);
+  auto bar = [&](uint32_t b) { return base + SM_BAR + 8u * b; };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = uniform(static_cast<int>(cluster_rank()));
   const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -316,15 +313,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp >= EPI_WARP) {
     // ------------------------------------------------------------------ epilogue
-    const int w = warp - EPI_WARP;
-    const uint32_t t_row = static_cast<uint32_t>(w * 32) << 16;
-    const uint32_t room = base + sm_out(AUX) + w * BUFFERS * OUT_BYTES;
+    // A warp reads the quarter of tensor memory's rows that its number gives; two share it, 128 columns
+    // each.
+    const int e = warp - EPI_WARP, row0 = (warp & 3) * 32, col0 = (e >> 2) * 128;
+    const uint32_t t_row = (static_cast<uint32_t>(row0) << 16) + col0;
+    const uint32_t room = base + SM_OUT + e * BUFFERS * OUT_BYTES, aux_bar = bar(AUX0 + e * BUFFERS);
     const uint32_t acc_empty = in_first_cta(bar(ACC_EMPTY0));
     uint32_t done = 0, loads = 0;  // tiles; tiles whose operand has been sent for
     bool ok = true, pending = false;
     for (int u = first; u < p.units && ok; u += pairs) {
       const Unit x = unit_of(p, u);
-      const int m0 = x.m0 + rank * 128 + w * 32;
+      const int m0 = x.m0 + rank * 128 + row0;
       const uint32_t acc = done & 1u;
       if (AUX && x.part < 0) {
         // The epilogue's operand comes while the products run, each 64 columns into the buffer that
@@ -332,9 +331,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0) {
           bulk_wait_read_all();
 #pragma unroll 1
-          for (int c = 0; c < BN / 64; ++c) {
-            mbar_arrive_expect_tx(bar(AUX0 + w * MAX_BUFFERS + c), OUT_BYTES);
-            tma_load_2d(room + c * OUT_BYTES, &maps.aux, bar(AUX0 + w * MAX_BUFFERS + c), x.n0 + c * 64, m0);
+          for (int c = 0; c < 2; ++c) {
+            mbar_arrive_expect_tx(aux_bar + 8u * c, OUT_BYTES);
+            tma_load_2d(room + c * OUT_BYTES, &maps.aux, aux_bar + 8u * c, x.n0 + col0 + c * 64, m0);
           }
         }
         __syncwarp();
@@ -346,9 +345,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after_sync();
       const uint32_t t_acc = tmem + t_row + acc * BN;
       if (x.part >= 0) {
-        float* to = p.parts + ((static_cast<int64_t>(x.part) * 2 + rank) * BN) * 128 + w * 32 + lane;
+        float* to = p.parts + ((static_cast<int64_t>(x.part) * 2 + rank) * BN + col0) * 128 + row0 + lane;
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
+        for (int c = 0; c < 128; c += 32) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(t_acc + c, v);
           tmem_wait_ld();
@@ -357,14 +356,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < BN / 64; ++c) {
-          const int n0 = x.n0 + c * 64;
-          // Buffers: with AUX one for each 64 columns; else two in turn, or one for pre and one for
-          // the result.
+        for (int c = 0; c < 2; ++c) {
+          const int n0 = x.n0 + col0 + c * 64;
+          // Buffers: one for each 64 columns, or one for pre and one for the result.
           const bool pre_room = OP == GEMM_FWD && !AUX && p.has_pre;
-          const uint32_t out = room + (AUX ? c : pre_room ? 1 : c & 1) * OUT_BYTES;
+          const uint32_t out = room + (pre_room ? 1 : c) * OUT_BYTES;
           if (AUX) {
-            ok = warp_wait(bar(AUX0 + w * MAX_BUFFERS + c), (loads - 1) & 1u, abort, limit);
+            ok = warp_wait(aux_bar + 8u * c, (loads - 1) & 1u, abort, limit);
             if (!ok) break;
           } else {
             if (lane == 0) {
@@ -377,7 +375,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           for (int h = 0; h < 2; ++h) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(t_acc + c * 64 + h * 32, v);
-            tmem_wait_ld();
+            // 32 biases, alike for all lanes, on their way at the same time.
+            const int col = n0 + h * 32;
+            const bool bias = OP == GEMM_FWD && p.bias;
+            Raw<E> b16[4];
+            Raw<float> b32[4];
+            if (bias) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (col + j * 8 < p.n) {
+                  if (p.bias_f32) b32[j].load(static_cast<const float*>(p.bias) + col + j * 8);
+                  else b16[j].load(static_cast<const E*>(p.bias) + col + j * 8);
+                }
+            }
+            tmem_wait_ld_regs(v);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float z[8];
@@ -385,14 +396,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
               for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(v[8 * j + i]);
               const uint32_t spot = swizzled(lane, h * 4 + j);
               if (OP == GEMM_FWD) {
-                const int col = n0 + h * 32 + j * 8;
-                if (p.bias && col < p.n) add_bias<E>(p.bias, p.bias_f32, col, z);
+                if (bias) {
+                  float b[8];
+                  if (p.bias_f32) b32[j].widen(b);
+                  else b16[j].widen(b);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) z[i] += b[i];
+                }
                 if (pre_room) {
                   const uint4 t = pack8<E>(z);
                   st_shared16(room + spot, t.x, t.y, t.z, t.w);
-                } else if (AUX && p.has_pre && col < p.n && m0 + lane < p.m) {
-                  // No room for a fifth buffer: straight from the registers.
-                  store8(static_cast<E*>(p.pre.data) + (m0 + lane) * p.pre.stride + col, z);
+                } else if (AUX && p.has_pre && col + j * 8 < p.n && m0 + lane < p.m) {
+                  // No room for a buffer of its own: straight from the registers.
+                  store8(static_cast<E*>(p.pre.data) + (m0 + lane) * p.pre.stride + col + j * 8, z);
                 }
                 act8(p.act, z);
               }
@@ -433,8 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     if (!ok && lane == 0) {
       raise_abort(abort, p.err);
       volatile int never = 0;
-      for (int c = 0; c < BN / 64 && pending; ++c)
-        mbar_wait_bounded(bar(AUX0 + w * MAX_BUFFERS + c), (loads - 1) & 1u, &never, DRAIN_LIMIT_NS);
+      for (int c = 0; c < 2 && pending; ++c)
+        mbar_wait_bounded(aux_bar + 8u * c, (loads - 1) & 1u, &never, DRAIN_LIMIT_NS);
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -536,9 +552,9 @@ Plan plan_of(int m, int n, int k) {
 template <typename E, int OP, bool AUX>
 cudaError_t launch_kernel(const Maps& maps, const Params& p, int pairs, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = ensure_smem_limit(gemm_kernel<E, OP, AUX>, static_cast<int>(smem_bytes(AUX)), smem_set);
+  cudaError_t e = ensure_smem_limit(gemm_kernel<E, OP, AUX>, static_cast<int>(SMEM_BYTES), smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(gemm_kernel<E, OP, AUX>, dim3(2 * pairs), dim3(NUM_THREADS), smem_bytes(AUX), stream, maps, p);
+  e = launch_dependent(gemm_kernel<E, OP, AUX>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, stream, maps, p);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_dependent(gemm_join_kernel<E, OP>, dim3(32, p.tail), dim3(256), 0, stream, p);
 }
