@@ -94,6 +94,8 @@ __device__ __forceinline__ void slope8(int act, const float* at, float* z) {
   }
 }
 
+__device__ __forceinline__ float widen16(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float widen16(__half v) { return __half2float(v); }
 __device__ __forceinline__ void narrow(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void narrow(float v, __half* p) { *p = __float2half_rn(v); }
 

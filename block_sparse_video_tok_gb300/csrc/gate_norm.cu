@@ -557,11 +557,12 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
   }
 }
 
-// The units' sums of a modulation row, joined in unit order: 32 columns a block, 32 strided units
+// The units' sums of a modulation row, joined in unit order: 32 columns a block, Y strided units
 // each, joined in their order.  Writes the row's gradients and, for the weights' gradients, its
 // share of them: the result itself if there is one row, else to `share` [row][3][channels].
-__global__ void __launch_bounds__(1024) gate_norm_sums_kernel(const __grid_constant__ Params p, float* share) {
-  __shared__ float sums[3][32][33];
+template <int Y>
+__global__ void __launch_bounds__(32 * Y) gate_norm_sums_kernel(const __grid_constant__ Params p, float* share) {
+  __shared__ float sums[3][Y][33];
   grid_dependency_wait();
   const GateNormArgs& a = p.a;
   const int c = blockIdx.x * 32 + threadIdx.x;
@@ -569,7 +570,8 @@ __global__ void __launch_bounds__(1024) gate_norm_sums_kernel(const __grid_const
   for (int bg = blockIdx.y; bg < rows; bg += gridDim.y) {
     float s[3] = {0.f, 0.f, 0.f};
     if (c < a.channels)
-      for (int i = threadIdx.y; i < p.parts; i += 32) {
+#pragma unroll 4
+      for (int i = threadIdx.y; i < p.parts; i += Y) {
         const float* from = a.workspace + (static_cast<int64_t>(bg) * p.parts + i) * 3 * a.channels + c;
 #pragma unroll
         for (int j = 0; j < 3; ++j) s[j] += from[static_cast<int64_t>(j) * a.channels];
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(1024) gate_norm_sums_kernel(const __grid_const
     for (int j = 0; j < 3; ++j) {
       s[j] = 0.f;
 #pragma unroll
-      for (int y = 0; y < 32; ++y) s[j] += sums[j][y][threadIdx.x];
+      for (int y = 0; y < Y; ++y) s[j] += sums[j][y][threadIdx.x];
     }
     const int b = bg / a.groups, g = bg - b * a.groups;
     const float w = param(a.weight, c, a.weight_dtype, 1.f), bias = param(a.bias, c, a.weight_dtype, 0.f);
@@ -728,7 +730,9 @@ cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
   float* share = rows > 1 && (a.dpost || a.dweight || a.dbias)
                      ? a.workspace + static_cast<int64_t>(q.units) * 3 * a.channels
                      : nullptr;
-  e = launch_dependent(gate_norm_sums_kernel, dim3(columns, rows < 65535 ? rows : 65535), dim3(32, 32), 0, stream, p, share);
+  const dim3 sums_grid(columns, rows < 65535 ? rows : 65535);
+  e = q.parts > 64 ? launch_dependent(gate_norm_sums_kernel<32>, sums_grid, dim3(32, 32), 0, stream, p, share)
+                   : launch_dependent(gate_norm_sums_kernel<8>, sums_grid, dim3(32, 8), 0, stream, p, share);
   if (e != cudaSuccess || !share) return e;
   return launch_dependent(gate_norm_weights_kernel, dim3(columns, 3), dim3(32, 32), 0, stream, p,
                           static_cast<const float*>(share));

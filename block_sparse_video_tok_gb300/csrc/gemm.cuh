@@ -27,6 +27,10 @@ struct GemmArgs {
 cudaError_t launch_gemm(GemmOp op, const GemmArgs& a, cudaStream_t stream);
 size_t gemm_workspace(int m, int n, int k);
 
+// The forward for a few rows, and whether it is the one to use.
+cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);
+bool use_linear_rows(int rows, int out);
+
 // 2-D tensor map of a 16-bit matrix of `columns` x `rows`, box 64 columns x box_rows, 128-byte swizzle.
 cudaError_t make_tmap_matrix(CUtensorMap* map, const MatrixView& x, int columns, int rows, int box_rows, bool bf16);
 

@@ -8,7 +8,7 @@ namespace vsa {
 namespace {
 
 // Columns of 8 to a thread, 32 threads of a warp side by side, ROWS warps down the rows.
-constexpr int ROWS = 8;
+constexpr int ROWS = 8, AHEAD = 2;  // AHEAD rows of a thread in flight
 
 // dz = dout act'(pre) (not written without an activation) and the sums of its columns over `chunk`
 // rows, to partial [blockIdx.y][n] fp32 (unless null).  Bound by HBM: one read of each input, one write.
@@ -20,18 +20,32 @@ __global__ void __launch_bounds__(32 * ROWS) slope_kernel(MatrixView dout, Matri
   const int c = (blockIdx.x * 32 + threadIdx.x) * 8, r1 = min(m, (static_cast<int>(blockIdx.y) + 1) * chunk);
   float sum[8] = {};
   if (c < n) {
-#pragma unroll 4
-    for (int r = blockIdx.y * chunk + threadIdx.y; r < r1; r += ROWS) {
-      float g[8];
-      load8(static_cast<const E*>(dout.data) + r * dout.stride + c, g);
-      if (act) {
-        float z[8];
-        load8(static_cast<const E*>(pre.data) + r * pre.stride + c, z);
-        slope8(act, z, g);
-        store8(dz + static_cast<int64_t>(r) * n + c, g);
+    for (int r0 = blockIdx.y * chunk + threadIdx.y; r0 < r1; r0 += AHEAD * ROWS) {
+      Raw<E> rg[AHEAD], rz[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int r = r0 + i * ROWS;
+        rg[i].zero();
+        rz[i].zero();
+        if (r >= r1) continue;
+        rg[i].load(static_cast<const E*>(dout.data) + r * dout.stride + c);
+        if (act) rz[i].load(static_cast<const E*>(pre.data) + r * pre.stride + c);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += g[i];
+      for (int i = 0; i < AHEAD; ++i) {
+        const int r = r0 + i * ROWS;
+        float g[8];
+        rg[i].widen(g);
+        if (r >= r1) continue;
+        if (act) {
+          float z[8];
+          rz[i].widen(z);
+          slope8(act, z, g);
+          store8(dz + static_cast<int64_t>(r) * n + c, g);
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sum[x] += g[x];
+      }
     }
   }
   if (!partial) return;
@@ -100,10 +114,13 @@ cudaError_t slopes(const LinearArgs& a, const Layout& l, cudaStream_t stream) {
 
 }  // namespace
 
-size_t linear_fwd_workspace(int rows, int in, int out) { return gemm_workspace(rows, out, in); }
+size_t linear_fwd_workspace(int rows, int in, int out) {
+  return use_linear_rows(rows, out) ? 0 : gemm_workspace(rows, out, in);
+}
 size_t linear_bwd_workspace(int rows, int in, int out, int act) { return layout_of(rows, in, out, act).total; }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t stream) {
+  if (use_linear_rows(a.rows, a.out_features)) return launch_linear_rows(a, stream);
   GemmArgs g{};
   g.a = a.x;
   g.b = a.weight;
