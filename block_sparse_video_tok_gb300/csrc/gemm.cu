@@ -15,7 +15,7 @@
 // The same rule splits small problems, all of whose tiles are such a rest.
 //
 // Roles (384 threads): warp 0 TMA producer; warp 1 UMMA issuer (first CTA of the pair); warp 2 tensor
-// memory; warps 4-11 epilogue, half a row of the tile per thread: bias, activation, residual or slope in fp32, rounded
+// memory; warp 3 biases; warps 4-11 epilogue, half a row of the tile per thread: bias, activation, residual or slope in fp32, rounded
 // once, through swizzled shared memory to TMA stores, which clip at the matrix's edges.
 #include <type_traits>
 
@@ -31,7 +31,7 @@ namespace {
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair
 constexpr int GROUP_M = 8;
 constexpr int NUM_THREADS = 384;
-constexpr int TMA_WARP = 0, MMA_WARP = 1, TMEM_WARP = 2, EPI_WARP = 4, EPI_WARPS = 8;
+constexpr int TMA_WARP = 0, MMA_WARP = 1, TMEM_WARP = 2, BIAS_WARP = 3, EPI_WARP = 4, EPI_WARPS = 8;
 constexpr uint32_t OPERAND_BYTES = 128 * BK * 2;  // a CTA's A or B of a stage
 constexpr uint32_t STAGE_BYTES = 2 * OPERAND_BYTES;
 constexpr uint32_t OUT_BYTES = 32 * 128;  // 32 rows x 64 results of an epilogue warp
@@ -46,10 +46,13 @@ enum Bar : uint32_t {
   ACC_EMPTY0 = ACC_FULL0 + 2,       // first CTA: both CTAs' epilogues have read a tile
   AUX0 = ACC_EMPTY0 + 2,            // per epilogue warp and buffer
   DRAIN = AUX0 + EPI_WARPS * BUFFERS,
+  BIAS_FULL,                        // a tile's biases are in shared memory
+  BIAS_EMPTY,                       // the epilogue warps have read them
   NUM_BARS
 };
 constexpr uint32_t SM_OUT = STAGES * STAGE_BYTES;
-constexpr uint32_t SM_BAR = SM_OUT + EPI_WARPS * BUFFERS * OUT_BYTES;
+constexpr uint32_t SM_BIAS = SM_OUT + EPI_WARPS * BUFFERS * OUT_BYTES;  // 256 floats
+constexpr uint32_t SM_BAR = SM_BIAS + BN * 4;
 constexpr uint32_t SMEM_BYTES = SM_BAR + NUM_BARS * 8 + 8 + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
@@ -216,9 +219,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const uint64_t limit = p.wait_ns;
 
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
+    tma_prefetch_desc(&maps.out);
+    if (AUX) tma_prefetch_desc(&maps.aux);
+  }
   if (threadIdx.x == 0) {
     *abort = 0;
-    for (uint32_t b = 0; b < NUM_BARS; ++b) mbar_init(bar(b), b >= ACC_EMPTY0 && b < AUX0 ? 2 * EPI_WARPS : 1);
+    for (uint32_t b = 0; b < NUM_BARS; ++b)
+      mbar_init(bar(b), b >= ACC_EMPTY0 && b < AUX0 ? 2 * EPI_WARPS : b == BIAS_EMPTY ? EPI_WARPS : 1);
     fence_barrier_init();
   }
   if (warp == TMEM_WARP) {
@@ -311,6 +321,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) mbar_wait_bounded(bar(DRAIN), 0, &never, DRAIN_LIMIT_NS);
       __syncwarp();
     }
+  } else if (warp == BIAS_WARP && OP == GEMM_FWD && p.bias) {
+    // ------------------------------------------------------------------ biases
+    // 8 a lane, widened: loaded by the epilogue where it needs them they cost it a wait for every
+    // 32 columns (32 rows, 256 -> 1536 features: 3 of 8.8 us).
+    uint32_t done = 0;
+    bool ok = true;
+    for (int u = first; u < p.units && ok; u += pairs) {
+      const Unit x = unit_of(p, u);
+      if (x.part >= 0) continue;
+      float b[8] = {};
+      if (x.n0 + lane * 8 < p.n) {
+        if (p.bias_f32) load8(static_cast<const float*>(p.bias) + x.n0 + lane * 8, b);
+        else load8(static_cast<const E*>(p.bias) + x.n0 + lane * 8, b);
+      }
+      ok = warp_wait(bar(BIAS_EMPTY), (done & 1u) ^ 1u, abort, limit);
+      if (!ok) break;
+      float4* to = reinterpret_cast<float4*>(gbase + SM_BIAS) + lane * 2;
+      to[0] = make_float4(b[0], b[1], b[2], b[3]);
+      to[1] = make_float4(b[4], b[5], b[6], b[7]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BIAS_FULL));
+      ++done;
+    }
+    if (!ok && lane == 0) raise_abort(abort, p.err);
+    __syncwarp();
   } else if (warp >= EPI_WARP) {
     // ------------------------------------------------------------------ epilogue
     // A warp reads the quarter of tensor memory's rows that its number gives; two share it, 128 columns
@@ -319,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const uint32_t t_row = (static_cast<uint32_t>(row0) << 16) + col0;
     const uint32_t room = base + SM_OUT + e * BUFFERS * OUT_BYTES, aux_bar = bar(AUX0 + e * BUFFERS);
     const uint32_t acc_empty = in_first_cta(bar(ACC_EMPTY0));
-    uint32_t done = 0, loads = 0;  // tiles; tiles whose operand has been sent for
+    uint32_t done = 0, whole = 0;  // tiles; those that are not parts
     bool ok = true, pending = false;
     for (int u = first; u < p.units && ok; u += pairs) {
       const Unit x = unit_of(p, u);
@@ -337,10 +372,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           }
         }
         __syncwarp();
-        ++loads;
         pending = true;
       }
       ok = warp_wait(bar(ACC_FULL0 + acc), (done >> 1) & 1u, abort, limit);
+      const bool bias = OP == GEMM_FWD && p.bias && x.part < 0;
+      if (ok && bias) ok = warp_wait(bar(BIAS_FULL), whole & 1u, abort, limit);
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t t_acc = tmem + t_row + acc * BN;
@@ -362,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           const bool pre_room = OP == GEMM_FWD && !AUX && p.has_pre;
           const uint32_t out = room + (pre_room ? 1 : c) * OUT_BYTES;
           if (AUX) {
-            ok = warp_wait(aux_bar + 8u * c, (loads - 1) & 1u, abort, limit);
+            ok = warp_wait(aux_bar + 8u * c, whole & 1u, abort, limit);
             if (!ok) break;
           } else {
             if (lane == 0) {
@@ -375,37 +411,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           for (int h = 0; h < 2; ++h) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(t_acc + c * 64 + h * 32, v);
-            // 32 biases, alike for all lanes, on their way at the same time.
             const int col = n0 + h * 32;
-            const bool bias = OP == GEMM_FWD && p.bias;
-            Raw<E> b16[4];
-            Raw<float> b32[4];
+            // The other operands are on their way before the wait for tensor memory: the stores below
+            // keep what follows them in order.
+            float4 b4[8];
             if (bias) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (col + j * 8 < p.n) {
-                  if (p.bias_f32) b32[j].load(static_cast<const float*>(p.bias) + col + j * 8);
-                  else b16[j].load(static_cast<const E*>(p.bias) + col + j * 8);
-                }
+              for (int j = 0; j < 8; ++j)
+                b4[j] = reinterpret_cast<const float4*>(gbase + SM_BIAS)[(col0 + c * 64 + h * 32) / 4 + j];
+            }
+            Raw<E> r[4];
+            if (AUX) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) r[j].u[0] = ld_shared16(out + swizzled(lane, h * 4 + j));
             }
             tmem_wait_ld_regs(v);
+            uint4 t[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float z[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(v[8 * j + i]);
-              const uint32_t spot = swizzled(lane, h * 4 + j);
               if (OP == GEMM_FWD) {
                 if (bias) {
-                  float b[8];
-                  if (p.bias_f32) b32[j].widen(b);
-                  else b16[j].widen(b);
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) z[i] += b[i];
+                  z[0] += b4[2 * j].x, z[1] += b4[2 * j].y, z[2] += b4[2 * j].z, z[3] += b4[2 * j].w;
+                  z[4] += b4[2 * j + 1].x, z[5] += b4[2 * j + 1].y, z[6] += b4[2 * j + 1].z, z[7] += b4[2 * j + 1].w;
                 }
                 if (pre_room) {
-                  const uint4 t = pack8<E>(z);
-                  st_shared16(room + spot, t.x, t.y, t.z, t.w);
+                  const uint4 y = pack8<E>(z);
+                  st_shared16(room + swizzled(lane, h * 4 + j), y.x, y.y, y.z, y.w);
                 } else if (AUX && p.has_pre && col + j * 8 < p.n && m0 + lane < p.m) {
                   // No room for a buffer of its own: straight from the registers.
                   store8(static_cast<E*>(p.pre.data) + (m0 + lane) * p.pre.stride + col + j * 8, z);
@@ -413,10 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 act8(p.act, z);
               }
               if (AUX) {
-                Raw<E> r;
-                r.u[0] = ld_shared16(out + spot);
                 float a[8];
-                r.widen(a);
+                r[j].widen(a);
                 if (OP == GEMM_FWD) {
 #pragma unroll
                   for (int i = 0; i < 8; ++i) z[i] += a[i];
@@ -424,9 +456,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                   slope8(p.act, a, z);
                 }
               }
-              const uint4 t = pack8<E>(z);
-              st_shared16(out + spot, t.x, t.y, t.z, t.w);
+              t[j] = pack8<E>(z);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) st_shared16(out + swizzled(lane, h * 4 + j), t[j].x, t[j].y, t[j].z, t[j].w);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -440,6 +473,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
         if (!ok) break;
         pending = false;
+        ++whole;
+        if (bias) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(BIAS_EMPTY));
+        }
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -450,9 +488,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       raise_abort(abort, p.err);
       volatile int never = 0;
       for (int c = 0; c < 2 && pending; ++c)
-        mbar_wait_bounded(aux_bar + 8u * c, (loads - 1) & 1u, &never, DRAIN_LIMIT_NS);
+        mbar_wait_bounded(aux_bar + 8u * c, whole & 1u, &never, DRAIN_LIMIT_NS);
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_read_all();  // (the end of the grid waits for the writes)
     __syncwarp();
   }
 
