@@ -19,7 +19,7 @@ LIB = os.path.join(BUILD, "libvsa.so")
 SOURCES = ["api.cu", "invert.cu", "prepost.cu", "tmap.cu", "bwd_main.cu", "fwd_main.cu",
            "noalloc.cu", "layer_api.cu", "norm_rope.cu", "cross_fwd.cu", "cross_token.cu",
            "cross_bwd.cu", "block_api.cu", "gate_norm.cu", "linear.cu",
-           "gemm.cu", "linear_rows.cu"]
+           "gemm.cu", "gemm_small.cu", "linear_rows.cu"]
 HEADERS = ["ptx.cuh", "queue.cuh", "vsa_internal.cuh", "layer_internal.cuh",
            "cross_common.cuh", "block_internal.cuh", "vec8.cuh", "act.cuh",
            "gemm.cuh"]

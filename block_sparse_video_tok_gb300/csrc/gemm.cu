@@ -614,9 +614,10 @@ cudaError_t launch_typed(GemmOp op, const Maps& maps, const Params& p, int pairs
 
 }  // namespace
 
-size_t gemm_workspace(int m, int n, int k) { return align_up(plan_of(m, n, k).bytes, 256); }
+size_t gemm_workspace(int m, int n, int k) { return use_gemm_small(m, n, k) ? 0 : align_up(plan_of(m, n, k).bytes, 256); }
 
 cudaError_t launch_gemm(GemmOp op, const GemmArgs& a, cudaStream_t stream) {
+  if (use_gemm_small(a.m, a.n, a.k)) return launch_gemm_small(op, a, stream);
   const Plan q = plan_of(a.m, a.n, a.k);
   Params p{};
   p.m = a.m;

@@ -1,0 +1,351 @@
+// gemm_small.cu -- the products of vsa_linear where a tile of 256 x 256 results is too coarse: a CTA has
+// 128 x 64 results of one tile, and a cluster shares the tile along k.
+//
+// Such calls are bound by what comes before and after the products: a pair of CTAs of gemm.cu takes 6.7 us
+// for a tile with 256 elements of k, of which its products are 0.4 (two cluster barriers, the epilogue
+// of 256 columns, TMA stores), and its tiles in parts a second kernel that adds them.  Here nothing is
+// persistent: two warps copy and multiply, then all eight write the results; the CTAs of a cluster leave
+// their sums in shared memory, and each adds a share of the tile's results over all of them, in rank
+// order, through distributed shared memory.
+//
+// The 128 results of a tile's one side are those of m or of n, whichever fits better (SWAP: of n): few
+// rows of x meet 128 features.  Either operand comes K-major or MN-major, as in gemm.cu.
+#include <type_traits>
+
+#include "act.cuh"
+#include "cross_common.cuh"
+#include "gemm.cuh"
+#include "vec8.cuh"
+
+namespace vsa {
+
+namespace {
+
+constexpr int TA = 128, TB = 64, BK = 64;  // results of a tile; elements of k of a stage
+constexpr int STAGES = 4, WARPS = 8, THREADS = WARPS * 32;
+constexpr int MAX_SHARE = 8;  // CTAs of a cluster
+constexpr int TMA_WARP = 0, MMA_WARP = 1;
+constexpr uint32_t A_BYTES = TA * BK * 2, B_BYTES = TB * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr uint32_t TMEM_COLUMNS = 64;
+
+enum Bar : uint32_t { FULL0 = 0, EMPTY0 = FULL0 + STAGES, DONE = EMPTY0 + STAGES, NUM_BARS };
+constexpr uint32_t SM_BAR = STAGES * STAGE_BYTES;
+constexpr uint32_t SMEM_BYTES = SM_BAR + NUM_BARS * 8 + 8 + 1024;  // + alignment slack
+constexpr int PITCH = TA + 4;  // of the sums, [64][128 + pad] fp32 where the stages were, theirs and the cluster's
+static_assert(2 * TB * PITCH * 4 <= STAGES * STAGE_BYTES, "room for the sums");
+
+struct Params {
+  int m, n, steps;       // steps of BK along k
+  int share;             // CTAs of a cluster
+  const void* bias;
+  bool bias_f32;
+  int op, act;
+  MatrixView out, pre, aux;
+  uint32_t* err;
+  uint64_t wait_ns;
+};
+
+template <int AS, int BS>
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, c, t;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 c, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, c;\n\t"
+      "add.u64 a, %1, %5;\n\tadd.u64 b, %2, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, a, %5;\n\tadd.u64 b, b, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, a, %5;\n\tadd.u64 b, b, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(AS), "n"(BS)
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void load4_cluster(uint32_t addr, float* v) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr));
+}
+template <typename E, bool A_MN, bool B_MN, bool SWAP>
+__global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_constant__ CUtensorMap tm_a,
+                                                             const __grid_constant__ CUtensorMap tm_b,
+                                                             const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  volatile int* abort = reinterpret_cast<volatile int*>(gbase + SM_BAR + NUM_BARS * 8 + 4);
+  auto bar = [&](uint32_t b) { return base + SM_BAR + 8u * b; };
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = blockIdx.x;
+  const int k0 = rank * p.steps / p.share, k1 = (rank + 1) * p.steps / p.share;
+  const int a0 = (SWAP ? blockIdx.z : blockIdx.y) * TA, b0 = (SWAP ? blockIdx.y : blockIdx.z) * TB;
+  const uint64_t limit = p.wait_ns;
+
+  if (warp == TMA_WARP && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    *abort = 0;
+    for (uint32_t b = 0; b < NUM_BARS; ++b) mbar_init(bar(b), 1);
+    fence_barrier_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(bar(NUM_BARS), TMEM_COLUMNS);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  // 8 results of a row a thread, at a time: a tile has 1024 such, the CTAs of the cluster write those of
+  // equal shares of its 64 (SWAP: rows m of 16 such; else columns n, 128 rows of 1 to 8).  A thread's
+  // columns stay the same.
+  const int wide = SWAP ? TA / 8 : TB / 8 / p.share;  // such, side by side
+  const int n_first = SWAP ? a0 + threadIdx.x % wide * 8 : b0 + (rank * wide + threadIdx.x % wide) * 8;
+  float bias[8] = {};
+  if (p.bias && n_first < p.n) {
+    if (p.bias_f32) load8(static_cast<const float*>(p.bias) + n_first, bias);
+    else load8(static_cast<const E*>(p.bias) + n_first, bias);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + SM_BAR + NUM_BARS * 8);
+
+  bool ok = true;
+  if (warp == TMA_WARP) {
+    // ------------------------------------------------------------------ TMA producer
+    uint32_t it = 0;
+    for (int k = k0; k < k1; ++k, ++it) {
+      const uint32_t s = it % STAGES, to = base + s * STAGE_BYTES, full = bar(FULL0 + s);
+      ok = warp_wait(bar(EMPTY0 + s), ((it / STAGES) & 1u) ^ 1u, abort, limit);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full, STAGE_BYTES);
+        if (A_MN) {
+          tma_load_2d(to, &tm_a, full, a0, k * BK);
+          tma_load_2d(to + A_BYTES / 2, &tm_a, full, a0 + 64, k * BK);
+        } else {
+          tma_load_2d(to, &tm_a, full, k * BK, a0);
+        }
+        if (B_MN) tma_load_2d(to + A_BYTES, &tm_b, full, b0, k * BK);
+        else tma_load_2d(to + A_BYTES, &tm_b, full, k * BK, b0);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) {
+      raise_abort(abort, p.err);
+      drain_copies(bar(FULL0), STAGES, it);
+    }
+    __syncwarp();
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------------ UMMA issuer
+    constexpr uint32_t IDESC = idesc_f16_f32acc(TA, TB, A_MN, B_MN, std::is_same<E, __nv_bfloat16>::value);
+    const uint64_t a_desc = sdesc_sw128(base, A_MN ? A_BYTES / 2 : 16, 1024);
+    const uint64_t b_desc = sdesc_sw128(base + A_BYTES, B_MN ? B_BYTES : 16, 1024);
+    uint32_t it = 0;
+    for (int k = k0; k < k1; ++k, ++it) {
+      const uint32_t s = it % STAGES;
+      ok = warp_wait(bar(FULL0 + s), (it / STAGES) & 1u, abort, limit);
+      if (!ok) break;
+      tc_fence_after_sync();
+      product<A_MN ? 128 : 2, B_MN ? 128 : 2>(tmem, sdesc_advance(a_desc, s * STAGE_BYTES), sdesc_advance(b_desc, s * STAGE_BYTES),
+                                              IDESC, k > k0 ? 1u : 0u);
+      umma_commit_elect(bar(EMPTY0 + s));
+    }
+    if (!ok && lane == 0) raise_abort(abort, p.err);
+    umma_commit_elect(bar(DONE));
+  }
+  // Every product is done, and every stage has been read.  (After an abort the sums are not used: the
+  // wait only keeps tensor memory until they are there.)
+  ok = warp_wait(bar(DONE), 0, abort, limit) && ok;
+  if (!ok) {
+    if (lane == 0) {
+      raise_abort(abort, p.err);
+      volatile int never = 0;
+      mbar_wait_bounded(bar(DONE), 0, &never, DRAIN_LIMIT_NS);
+    }
+    __syncwarp();
+  }
+  // ------------------------------------------------------------------ results
+  tc_fence_after_sync();
+  float* sums = reinterpret_cast<float*>(gbase);
+  __syncthreads();  // both readers of the stages are past them, whichever way they ended
+  {
+    const int r = (warp & 3) * 32 + lane, c = (warp >> 2) * 32;
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sums[(c + i) * PITCH + r] = __uint_as_float(v[i]);
+  }
+  tc_fence_before_sync();
+  const int mine = TB / p.share, first = rank * mine;  // of the tile's 64
+  if (p.share > 1) {
+    // Whole rows of 128 sums, 16 bytes a lane: other patterns are several times slower over the
+    // cluster.  All CTAs' loads of a row are on their way before the first is added.
+    cluster_sync();
+    const uint32_t at = smem_u32(sums) + lane * 16;
+    float* total = sums + TB * PITCH;
+    for (int c = first + warp; c < first + mine; c += WARPS) {
+      float from[MAX_SHARE][4], z[4] = {};
+#pragma unroll
+      for (int r = 0; r < MAX_SHARE; ++r)
+        if (r < p.share) load4_cluster(in_cta(at + c * PITCH * 4, r), from[r]);
+#pragma unroll
+      for (int r = 0; r < MAX_SHARE; ++r)
+        if (r < p.share) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] += from[r][i];
+        }
+      *reinterpret_cast<float4*>(total + c * PITCH + lane * 4) = make_float4(z[0], z[1], z[2], z[3]);
+    }
+    sums = total;
+    // The sums of a CTA stay until they have been read.
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  __syncthreads();
+  constexpr int MOST = TA * TB / 8 / THREADS;
+  Raw<E> aux[MOST];
+  auto here = [&](int i) { return ok && static_cast<int>(threadIdx.x) + i * THREADS < mine * (TA / 8) && n_first < p.n; };
+  auto place = [&](int i, int* m) {  // of the thread's result i: its row, and where its sums are
+    const int row = (threadIdx.x + i * THREADS) / wide;
+    *m = SWAP ? b0 + first + row : a0 + row;
+    return SWAP ? (first + row) * PITCH + threadIdx.x % wide * 8 : (first + threadIdx.x % wide * 8) * PITCH + row;
+  };
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    int m;
+    place(i, &m);
+    if (here(i) && p.aux.data && m < p.m)
+      aux[i].load(static_cast<const E*>(p.aux.data) + m * p.aux.stride + n_first);
+  }
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    int m;
+    const int at = place(i, &m);
+    if (!here(i) || m >= p.m) continue;
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = sums[at + (SWAP ? j : j * PITCH)];
+    if (p.op == GEMM_FWD) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] += bias[j];
+      if (p.pre.data) store8(static_cast<E*>(p.pre.data) + m * p.pre.stride + n_first, z);
+      act8(p.act, z);
+    }
+    if (p.aux.data) {
+      float a[8];
+      aux[i].widen(a);
+      if (p.op == GEMM_FWD) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += a[j];
+      } else {
+        slope8(p.act, a, z);
+      }
+    }
+    store8(static_cast<E*>(p.out.data) + m * p.out.stride + n_first, z);
+  }
+  if (p.share > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  tc_fence_after_sync();
+  if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM_COLUMNS);
+}
+
+template <typename E, bool A_MN, bool B_MN, bool SWAP>
+cudaError_t launch_kernel(const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, dim3 grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> smem_set{0};
+  const cudaError_t e = ensure_smem_limit(gemm_small_kernel<E, A_MN, B_MN, SWAP>, static_cast<int>(SMEM_BYTES), smem_set);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = grid.x;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm_small_kernel<E, A_MN, B_MN, SWAP>, ta, tb, p);
+}
+
+// How a product is cut: tiles of 128 along n and 64 along m or the other way round, whichever are
+// fewer; a cluster of up to 8 while the CTAs do not fill two to an SM and each keeps two steps.
+struct Plan {
+  bool swap;
+  int64_t tiles;
+  int steps, share, per;
+};
+Plan plan_of(int m, int n, int k) {
+  Plan q;
+  auto count = [](int x, int t) { return static_cast<int64_t>((x + t - 1) / t); };
+  const int64_t swapped = count(n, TA) * count(m, TB), straight = count(m, TA) * count(n, TB);
+  q.swap = swapped <= straight;
+  q.tiles = q.swap ? swapped : straight;
+  q.steps = (k + BK - 1) / BK;
+  q.share = 1;
+  while (q.share < MAX_SHARE && q.tiles * q.share * 2 <= 2 * device_sm_count() && q.steps >= q.share * 2 * 2) q.share *= 2;
+  q.per = (q.steps + q.share - 1) / q.share;
+  return q;
+}
+
+template <typename E>
+cudaError_t launch_typed(GemmOp op, bool swap, const CUtensorMap& tm, const CUtensorMap& tn, const Params& p, dim3 grid,
+                         cudaStream_t stream) {
+  switch (op) {
+    case GEMM_FWD:
+      return swap ? launch_kernel<E, false, false, true>(tn, tm, p, grid, stream)
+                  : launch_kernel<E, false, false, false>(tm, tn, p, grid, stream);
+    case GEMM_DX:
+      return swap ? launch_kernel<E, true, false, true>(tn, tm, p, grid, stream)
+                  : launch_kernel<E, false, true, false>(tm, tn, p, grid, stream);
+    default:
+      return swap ? launch_kernel<E, true, true, true>(tn, tm, p, grid, stream)
+                  : launch_kernel<E, true, true, false>(tm, tn, p, grid, stream);
+  }
+}
+
+}  // namespace
+
+bool use_gemm_small(int m, int n, int k) {
+  const Plan q = plan_of(m, n, k);
+  return q.tiles * q.share <= 2 * device_sm_count() && q.per <= 24;
+}
+
+cudaError_t launch_gemm_small(GemmOp op, const GemmArgs& a, cudaStream_t stream) {
+  const Plan q = plan_of(a.m, a.n, a.k);
+  Params p{};
+  p.m = a.m;
+  p.n = a.n;
+  p.steps = q.steps;
+  p.share = q.share;
+  p.bias = a.bias;
+  p.bias_f32 = a.bias_f32;
+  p.op = op;
+  p.act = a.act;
+  p.out = a.out;
+  p.pre = a.pre;
+  p.aux = a.aux;
+  p.err = a.err;
+  p.wait_ns = a.wait_ns;
+  const bool bf16 = a.dtype == VSA_BF16;
+  const int box_m = q.swap ? TB : TA, box_n = q.swap ? TA : TB;
+  CUtensorMap tm, tn;
+  cudaError_t e = op == GEMM_DW ? make_tmap_matrix(&tm, a.a, a.m, a.k, BK, bf16) : make_tmap_matrix(&tm, a.a, a.k, a.m, box_m, bf16);
+  if (e != cudaSuccess) return e;
+  e = op == GEMM_FWD ? make_tmap_matrix(&tn, a.b, a.k, a.n, box_n, bf16) : make_tmap_matrix(&tn, a.b, a.n, a.k, BK, bf16);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(q.share, static_cast<unsigned>((a.m + box_m - 1) / box_m), static_cast<unsigned>((a.n + box_n - 1) / box_n));
+  return bf16 ? launch_typed<__nv_bfloat16>(op, q.swap, tm, tn, p, grid, stream)
+              : launch_typed<__half>(op, q.swap, tm, tn, p, grid, stream);
+}
+
+}  // namespace vsa
