@@ -9,6 +9,7 @@ namespace {
 
 constexpr int64_t MAX_TOKENS = 1 << 30;
 constexpr int MAX_FEATURES = 1 << 24;
+constexpr int64_t MAX_ELEMENTS = 1ll << 44;  // tiles are counted in 32 bits
 
 vsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? VSA_OK : vsa::record_cuda_failure(e); }
 
@@ -132,6 +133,8 @@ vsa_status check_linear(const vsa_linear* op) {
   if (op->in_features < 8 || op->in_features % 8 != 0 || op->in_features > MAX_FEATURES ||
       op->out_features < 8 || op->out_features % 8 != 0 || op->out_features > MAX_FEATURES || op->rows > MAX_TOKENS)
     return VSA_ERR_UNSUPPORTED;
+  const int64_t m = op->rows, k = op->in_features, n = op->out_features;
+  if (m * k > MAX_ELEMENTS || m * n > MAX_ELEMENTS || n * k > MAX_ELEMENTS) return VSA_ERR_UNSUPPORTED;
   if (op->dtype != VSA_BF16 && op->dtype != VSA_F16) return VSA_ERR_UNSUPPORTED;
   if (op->bias_dtype != VSA_F32 && op->bias_dtype != op->dtype) return VSA_ERR_UNSUPPORTED;
   if (!is_act(op->act)) return VSA_ERR_UNSUPPORTED;

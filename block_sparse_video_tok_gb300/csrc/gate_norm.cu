@@ -71,8 +71,15 @@ struct Params {
   int len;           // tokens of a modulation row
   int parts, chunk;  // units of a modulation row, tokens of a unit
   int units;
-  float inv_dim;
+  float dim, inv_dim;  // channels
 };
+
+// sum / channels: the product with the rounded 1 / channels, corrected once, so that a constant token is its
+// own mean.  (The backward does without: its registers are full, 216 us instead of 201 for 2 x 32760 x 1536.)
+__device__ __forceinline__ float mean_of(const Params& p, float sum) {
+  const float m = sum * p.inv_dim;
+  return fmaf(fmaf(-m, p.dim, sum), p.inv_dim, m);
+}
 
 // The warps that hold a token together: sums over all of its elements, the same for every lane.
 struct Team {
@@ -247,13 +254,15 @@ __global__ void __maxnreg__(fwd_regs(NV)) gate_norm_fwd_kernel(const __grid_cons
       if (layer) {
         team.sum(s);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r) {
+          const float mean = mean_of(p, s[r]);
 #pragma unroll
           for (int k = 0; k < NV; ++k)
             if (e0 + k * step < a.channels) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[r][k][i] = fmaf(-s[r], p.inv_dim, v[r][k][i]);
+              for (int i = 0; i < 8; ++i) v[r][k][i] -= mean;
             }
+        }
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -698,7 +707,8 @@ Params params_of(const GateNormArgs& a, const Plan& q) {
   p.parts = q.parts;
   p.chunk = q.chunk;
   p.units = q.units;
-  p.inv_dim = 1.f / static_cast<float>(a.channels);
+  p.dim = static_cast<float>(a.channels);
+  p.inv_dim = 1.f / p.dim;
   return p;
 }
 

@@ -561,7 +561,7 @@ Plan plan_of(int m, int n, int k) {
   q.tiles_m = (m + BM - 1) / BM;
   q.tiles_n = (n + BN - 1) / BN;
   q.steps = (k + BK - 1) / BK;
-  q.pairs = device_sm_count() / 2;
+  q.pairs = device_sm_count() > 1 ? device_sm_count() / 2 : 1;
   const int64_t tiles = static_cast<int64_t>(q.tiles_m) * q.tiles_n;
   q.full = static_cast<int>(tiles / q.pairs * q.pairs);
   q.tail = static_cast<int>(tiles - q.full);
@@ -613,6 +613,13 @@ cudaError_t launch_typed(GemmOp op, const Maps& maps, const Params& p, int pairs
 }
 
 }  // namespace
+
+double gemm_microseconds(int m, int n, int k) {
+  const Plan q = plan_of(m, n, k);
+  const int rounds = (q.tail * q.splits + q.pairs - 1) / q.pairs;
+  return 7.5 + 0.27 * (static_cast<double>(q.full / q.pairs) * q.steps + static_cast<double>(rounds) * q.per) +
+         (q.splits > 1 ? 3.5 : 0.0);
+}
 
 size_t gemm_workspace(int m, int n, int k) { return use_gemm_small(m, n, k) ? 0 : align_up(plan_of(m, n, k).bytes, 256); }
 

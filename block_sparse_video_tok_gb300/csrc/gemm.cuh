@@ -30,6 +30,8 @@ size_t gemm_workspace(int m, int n, int k);
 // The same for small products (no workspace), and whether it is the one to use.
 cudaError_t launch_gemm_small(GemmOp op, const GemmArgs& a, cudaStream_t stream);
 bool use_gemm_small(int m, int n, int k);
+// About what gemm.cu's own kernels take.
+double gemm_microseconds(int m, int n, int k);
 
 // The forward for a few rows, and whether it is the one to use.
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);

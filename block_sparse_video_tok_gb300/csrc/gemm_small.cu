@@ -138,8 +138,9 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
       }
       __syncwarp();
     }
-    if (!ok && lane == 0) {
-      raise_abort(abort, p.err);
+    // No copy is in flight when the CTA ends, also after the issuer has given up.
+    if (lane == 0) {
+      if (!ok) raise_abort(abort, p.err);
       drain_copies(bar(FULL0), STAGES, it);
     }
     __syncwarp();
@@ -278,7 +279,8 @@ cudaError_t launch_kernel(const CUtensorMap& ta, const CUtensorMap& tb, const Pa
 }
 
 // How a product is cut: tiles of 128 along n and 64 along m or the other way round, whichever are
-// fewer; a cluster of up to 8 while the CTAs do not fill two to an SM and each keeps two steps.
+// fewer; a cluster of up to 8 while the CTAs do not fill two to an SM and each keeps four steps (with eight
+// kept, 32 x 1536 -> 1536 features take 7.3 us instead of 5.8, with two 256 -> 1536 take 5.2 instead of 3.8).
 struct Plan {
   bool swap;
   int64_t tiles;
@@ -292,7 +294,7 @@ Plan plan_of(int m, int n, int k) {
   q.tiles = q.swap ? swapped : straight;
   q.steps = (k + BK - 1) / BK;
   q.share = 1;
-  while (q.share < MAX_SHARE && q.tiles * q.share * 2 <= 2 * device_sm_count() && q.steps >= q.share * 2 * 2) q.share *= 2;
+  while (q.share < MAX_SHARE && q.tiles * q.share * 2 <= 2 * device_sm_count() && q.steps >= q.share * 2 * 4) q.share *= 2;
   q.per = (q.steps + q.share - 1) / q.share;
   return q;
 }
@@ -315,9 +317,18 @@ cudaError_t launch_typed(GemmOp op, bool swap, const CUtensorMap& tm, const CUte
 
 }  // namespace
 
+// Where its CTAs fit on the GPU at once and its estimated time is the shorter.  Measured, us, here and
+// with gemm.cu's tiles (forward, rows x in -> out features):
+//   512 x 1536 -> 1536    9.0 and 11.5      512 x 4096 -> 1536   13.7 and 13.9
+//   1024 x 1536 -> 1536   9.6 and 13.0      512 x 6144 -> 1536   18.0 and 15.7
+//   256 x 1536 -> 9216   11.2 and 13.1      384 x 1536 -> 9216   18.2 and 13.8
+// The estimate: 3 us for a call, 1.5 for a cluster, and for a step of 64 elements of k 0.2 where an SM has one
+// CTA and 0.28 where it has two.
 bool use_gemm_small(int m, int n, int k) {
   const Plan q = plan_of(m, n, k);
-  return q.tiles * q.share <= 2 * device_sm_count() && q.per <= 24;
+  const int64_t ctas = q.tiles * q.share;
+  if (ctas > 2 * device_sm_count()) return false;
+  return 3.0 + (q.share > 1 ? 1.5 : 0.0) + q.per * (ctas > device_sm_count() ? 0.28 : 0.2) <= gemm_microseconds(m, n, k);
 }
 
 cudaError_t launch_gemm_small(GemmOp op, const GemmArgs& a, cudaStream_t stream) {

@@ -109,7 +109,7 @@ typedef enum vsa_act {
 /* One product: z = x weight^T + bias, out = act(z) + residual.  Products are of 16-bit operands with
  * fp32 sums; the epilogue is in fp32 and each output is rounded once. */
 typedef struct vsa_linear {
-  int32_t rows;         /* of x and out, 1 .. 2^30 */
+  int32_t rows;         /* of x and out, 1 .. 2^30; each matrix of 2^44 elements at most */
   int32_t in_features;  /* a multiple of 8, 8 .. 2^24 */
   int32_t out_features; /* a multiple of 8, 8 .. 2^24 */
   int32_t dtype;        /* of every matrix: VSA_BF16 or VSA_F16 */

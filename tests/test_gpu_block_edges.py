@@ -1,0 +1,173 @@
+"""GPU: the block operators where sizes, values and surroundings are unusual: sums of tens of thousands
+of terms, offsets past 2^31 elements, norms of nothing but zeros, values that are not finite, two
+streams at once."""
+import pytest
+import torch
+
+from tests import block_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def block():
+    assert torch.cuda.is_available(), "the gpu tests need a CUDA device"
+    from block_sparse_video_tok_gb300 import build
+    build.build()
+    from block_sparse_video_tok_gb300 import block as binding
+    return binding
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(block):
+    from block_sparse_video_tok_gb300 import layer
+    layer.vsa_layer_device_error()
+    yield
+    assert layer.vsa_layer_device_error() == 0
+    torch.cuda.empty_cache()
+
+
+def randn(*shape, dtype=BF16, seed=0, scale=1.0):
+    g = torch.Generator("cuda").manual_seed(seed + sum(shape))
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def same_bits(a, b):
+    return all(torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)) for x, y in zip(a, b))
+
+
+def test_long_sums_of_parameters(block):
+    """A token gradient of one sign, 70000 tokens: the sums keep fp32's precision.  A unit adds at most 512
+    terms in a row (2^-15 of their magnitudes), the parts as many again."""
+    B, S, C = 2, 35000, 64
+    x, y = randn(B, S, C), randn(B, S, C, seed=1)
+    dh = randn(B, S, C, seed=2).abs() + 1
+    mods = [randn(B, C, dtype=FP32, seed=3 + i) for i in range(3)]
+    w, b = randn(C, dtype=FP32, seed=6), randn(C, dtype=FP32, seed=7)
+    args = (dh, None, x, y, mods[0], None, w, b, mods[1], mods[2])
+    for g, r in zip(block.vsa_gate_norm_bwd(*args), ref.gate_norm_bwd(*args, "layer", 1e-6, 1e-6)):
+        if g is not None:
+            ref.check("grad", g, r[0], 2 * r[1])
+
+
+def test_long_sums_of_products(block):
+    """Products of one sign over 70000 rows (dweight, dbias) and over 65536 features (out): all operands 1,
+    so that every partial sum is whole and results are exact up to their rounding."""
+    M, K, N = 70000, 64, 72
+    x, w = torch.ones(M, K, dtype=BF16, device="cuda"), torch.ones(N, K, dtype=BF16, device="cuda")
+    dout = torch.ones(M, N, dtype=BF16, device="cuda")
+    _, dw, db = block.vsa_linear_bwd(dout, x, w, torch.zeros(N, device="cuda"), need_dx=False)
+    assert bool((db == 70000).all()) and bool((dw == torch.tensor(70000.0).to(BF16)).all())
+    for M in (1, 16, 100, 300):
+        x, w = (torch.ones(n, 1 << 16, dtype=FP16, device="cuda") * 0.5 for n in (M, 264))
+        out, _ = block.vsa_linear(x, w)
+        assert bool((out == 16384).all()), M
+
+
+def test_gate_norm_past_2_31_elements(block):
+    """The last tokens of tensors of more than 2^31 elements are those of the same tokens by themselves."""
+    S, C = (1 << 31) // 2048 + 40, 2048
+    x = torch.zeros(1, S, C, dtype=BF16, device="cuda")
+    y = torch.zeros(1, S, C, dtype=BF16, device="cuda")
+    tail = slice(S - 64, S)
+    x[:, tail], y[:, tail] = randn(1, 64, C), randn(1, 64, C, seed=1)
+    gate, scale, shift = (randn(1, C, seed=2 + i) for i in range(3))
+    xo, h = block.vsa_gate_norm(x, y, gate, scale=scale, shift=shift, x_out=x)
+    got = xo[:, tail].clone(), h[:, tail].clone()
+    torch.cuda.synchronize()
+    small = [randn(1, 64, C), randn(1, 64, C, seed=1)]
+    assert same_bits(block.vsa_gate_norm(*small, gate, scale=scale, shift=shift), got)
+    h.zero_()
+    h[:, tail] = randn(1, 64, C, seed=7)
+    out = block.vsa_gate_norm_bwd(h, None, xo, y, gate, scale=scale, shift=shift, need_dparams=False, dx=xo)
+    want = block.vsa_gate_norm_bwd(randn(1, 64, C, seed=7), None, got[0], small[1], gate, scale=scale, shift=shift,
+                                   need_dparams=False)
+    assert same_bits((out[0][:, tail], out[1][:, tail]), want[:2])
+
+
+def test_linear_past_2_31_elements(block):
+    M, K, N = (1 << 31) // 512 + 300, 64, 512
+    x = torch.zeros(M, K, dtype=BF16, device="cuda")
+    x[-600:] = randn(600, K)
+    w, b = randn(N, K, seed=1), randn(N, seed=2)
+    out, _ = block.vsa_linear(x, w, b, "silu")
+    want, _ = block.vsa_linear(x[-600:], w, b, "silu")
+    bound = ref.linear(x[-600:], w, b, "silu", None)[0]
+    ref.check("out", out[-600:], *bound)
+    ref.check("want", want, *bound)
+    assert bool((out[:8] == block.vsa_linear(x[:8], w, b, "silu")[0]).all())
+    out.zero_()
+    out[-600:] = randn(600, N, seed=3)
+    dx, dw, db = block.vsa_linear_bwd(out, x, w, b)
+    (rx, bx), (rw, bw), (rb, bb) = ref.linear_bwd(out[-600:], x[-600:], w, b, None, None, None, None)
+    ref.check("dx", dx[-600:], rx, bx)
+    ref.check("dw", dw, rw, bw)
+    ref.check("db", db, rb, bb)
+    assert not dx[:-600].any()
+
+
+def test_tokens_of_zeros(block):
+    """Zeros with an eps are zeros, without one undefined in their token alone; a constant token is a zero
+    of the layer norm."""
+    x, dh = randn(1, 6, 264), randn(1, 6, 264, seed=1)
+    x[0, 2] = 0
+    for kind in ("layer", "rms"):
+        _, h = block.vsa_gate_norm(x, kind=kind)
+        assert not h[0, 2].any() and torch.isfinite(h.float()).all()
+        dx = block.vsa_gate_norm_bwd(dh, None, x, kind=kind)[0]
+        assert torch.isfinite(dx.float()).all()
+        _, h0 = block.vsa_gate_norm(x, kind=kind, eps=0.0)
+        rest = [0, 1, 3, 4, 5]
+        assert torch.isfinite(h0[0, rest].float()).all()
+    x[0, 3] = 5
+    assert not block.vsa_gate_norm(x)[1][0, 3].any()
+
+
+def test_values_that_are_not_finite_stay_in_their_token(block):
+    B, S, C = 2, 40, 520
+    x, y, dh, g = (randn(B, S, C, seed=i) for i in range(4))
+    gate = randn(B, C, seed=5)
+    base = block.vsa_gate_norm(x, y, gate)
+    base_b = block.vsa_gate_norm_bwd(dh, g, x, y, gate, need_dparams=False)
+    bad = x.clone()
+    bad[0, 7, 3], bad[1, 39, 519], bad[1, 0, 0] = float("inf"), float("nan"), -float("inf")
+    keep = torch.ones(B, S, dtype=torch.bool, device="cuda")
+    keep[0, 7] = keep[1, 39] = keep[1, 0] = False
+    for got, want in ((block.vsa_gate_norm(bad, y, gate), base),
+                      (block.vsa_gate_norm_bwd(dh, g, bad, y, gate, need_dparams=False)[:2], base_b[:2])):
+        assert same_bits([t[keep] for t in got], [t[keep] for t in want])
+        assert torch.isnan(got[1][~keep].float()).any(-1).all()
+
+
+def test_two_streams_at_once(block):
+    """Calls on two streams, each with its own workspaces, do not meet."""
+    cases = []
+    for i in range(2):
+        x, w = randn(300, 4096, seed=i), randn(1536, 4096, seed=2 + i, scale=1 / 64)
+        cases.append((x, w, randn(300, 1536, seed=4 + i), randn(1, 300, 1536, seed=6 + i)))
+
+    def all_of(x, w, dout, t):
+        out, _ = block.vsa_linear(x, w)
+        return [out, *block.vsa_linear_bwd(dout, x, w)[:2], *block.vsa_gate_norm_bwd(t, None, t, weight=t[0, 0])[::4]]
+
+    want = [all_of(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = all_of(*cases[i])
+        torch.cuda.synchronize()
+        assert all(same_bits(g, w) for g, w in zip(got, want))
+
+
+def test_the_current_device_is_the_tensors(block):
+    """A tensor of a device that is not the current one is refused (with one GPU: nothing to refuse)."""
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one GPU")
+    x = torch.zeros(1, 4, 64, dtype=BF16, device="cuda:1")
+    with pytest.raises(ValueError):
+        block.vsa_gate_norm(x)
