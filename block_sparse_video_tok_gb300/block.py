@@ -81,6 +81,8 @@ _pack_grads = struct.Struct("@6P").pack
 _pack_matrix = struct.Struct("@Pq").pack
 _pack_linear = struct.Struct("@6iPqP").pack
 
+_Tensor, _empty, _empty_like = torch.Tensor, torch.empty, torch.empty_like
+
 _fns = None
 _calls = None
 
@@ -153,17 +155,34 @@ def _strides3(t, name):
 
 
 def _tokens(t, name, shape, dtype, device):
-    _like(t, name, shape, dtype, device)
-    return _pack_tokens(*_strides3(t, name))
+    """The [B, S, C] tensor t as a packed vsa_tokens, after checking it."""
+    if not isinstance(t, _Tensor) or t.get_device() != device or t.dtype is not dtype or t.shape != shape:
+        _like(t, name, shape, dtype, device)
+    s0, s1, s2 = t.stride()
+    ptr = t.data_ptr()
+    if s1 != shape[2] or s0 != shape[1] * s1 or s2 != 1 or ptr & 15:      # not the usual case
+        return _pack_tokens(*_strides3(t, name))
+    return _pack_tokens(ptr, s0, s1)
+
+
+def _new_tokens(like, shape, dtype):
+    """A tensor for an output shaped like `like`, contiguous, and its packed vsa_tokens."""
+    # (empty_like takes three quarters of empty's time.)
+    if like.dtype is dtype and like.is_contiguous():
+        t = _empty_like(like)
+    else:
+        t = _empty(shape, dtype=dtype, device=like.device)
+    return t, _pack_tokens(t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
 def _vector(t, name, dtype, n, device):
     """The address of a contiguous 1-D tensor, or 0 for None."""
     if t is None:
         return 0
-    _like(t, name, (n,), dtype, device)
+    if not isinstance(t, _Tensor) or t.get_device() != device or t.dtype is not dtype or t.shape != (n,):
+        _like(t, name, (n,), dtype, device)
     ptr = t.data_ptr()
-    if not t.is_contiguous() or ptr & 15:
+    if ptr & 15 or not t.is_contiguous():
         raise ValueError("%s must be contiguous and 16-byte aligned" % name)
     return ptr
 
@@ -172,28 +191,32 @@ def _param_dtype(tensors, branch, what):
     """The one type of the parameters that are given: fp32 or the branch's."""
     dtype = None
     for t in tensors:
-        if t is None:
-            continue
-        d = getattr(t, "dtype", None)
-        if dtype is None:
-            dtype = d
-        if d is not dtype or (d is not branch and d is not torch.float32):
-            raise TypeError("%s must all be fp32 or all %s" % (what, branch))
+        if t is not None:
+            d = getattr(t, "dtype", None)
+            if d is not dtype:
+                if dtype is not None or (d is not branch and d is not torch.float32):
+                    raise TypeError("%s must all be fp32 or all %s" % (what, branch))
+                dtype = d
     return branch if dtype is None else dtype
 
 
 # ------------------------------------------------------------------------------- gate_norm
 
+_NO_MODULATION = (0, 0, 0, None)
+
+
 def _modulation(m, name, B, S, C, dtype, device):
     """(address, batch stride, group stride, groups) of a [B, C] or [B, G, C] modulation."""
     if m is None:
-        return 0, 0, 0, None
-    if not isinstance(m, torch.Tensor) or m.dim() not in (2, 3):
+        return _NO_MODULATION
+    if not isinstance(m, _Tensor) or m.dim() not in (2, 3):
         raise TypeError("%s must be a [B, C] or [B, groups, C] tensor" % name)
     if m.dim() == 2:
         m = m.unsqueeze(1)
-    G = m.shape[1]
-    _like(m, name, (B, G, C), dtype, device)
+    shape = m.shape
+    G = shape[1]
+    if m.get_device() != device or m.dtype is not dtype or shape[0] != B or shape[2] != C:
+        _like(m, name, (B, G, C), dtype, device)
     if G < 1 or S % G:
         raise ValueError("%s: %d tokens do not share %d groups evenly" % (name, S, G))
     return (*_strides3(m, name), G)
@@ -218,10 +241,13 @@ def _gate_norm_op(x, branch, y, gate, post_weight, weight, bias, scale, shift, k
     wdtype = _param_dtype((post_weight, weight, bias), branch, "the weights and the bias")
     mods = [_modulation(m, n, B, S, C, mdtype, device)
             for m, n in ((gate, "gate"), (scale, "scale"), (shift, "shift"))]
-    groups = {m[3] for m in mods if m[3] is not None} or {1}
-    if len(groups) > 1:
-        raise ValueError("gate, scale and shift must have the same groups, got %s" % sorted(groups))
-    G = groups.pop()
+    G = None
+    for m in mods:
+        if m[3] is not None and m[3] != G:
+            if G is not None:
+                raise ValueError("gate, scale and shift must have the same groups, got %d and %d" % (G, m[3]))
+            G = m[3]
+    G = G or 1
     op = _pack_norm(B, S, C, G, KINDS[kind], _DTYPES[dtype], _DTYPES[branch], _DTYPES[mdtype],
                     _DTYPES[wdtype], eps, post_eps, *mods[0][:3], *mods[1][:3], *mods[2][:3],
                     _vector(post_weight, "post_weight", wdtype, C, device),
@@ -261,8 +287,7 @@ def vsa_gate_norm(x, y=None, gate=None, post_weight=None, weight=None, bias=None
     shape, dtype, device = x.shape, x.dtype, x.get_device()
     xs = _tokens(x, "x", shape, dtype, device)
     if h is None:
-        h = torch.empty(shape, dtype=branch, device=x.device)
-        hs = _pack_tokens(h.data_ptr(), S * C, C)
+        h, hs = _new_tokens(x if y is None else y, shape, branch)
     else:
         hs = _tokens(h, "h", shape, branch, device)
     if y is None:
@@ -272,8 +297,7 @@ def vsa_gate_norm(x, y=None, gate=None, post_weight=None, weight=None, bias=None
         return x, h
     ys = _tokens(y, "y", shape, branch, device)
     if x_out is None:
-        x_out = torch.empty(shape, dtype=dtype, device=x.device)
-        os = _pack_tokens(x_out.data_ptr(), S * C, C)
+        x_out, os = _new_tokens(x, shape, dtype)
     else:
         os = _tokens(x_out, "x_out", shape, dtype, device)
     _call("vsa_gate_norm_fwd", op, xs, ys, os, hs, _current(device))
@@ -301,8 +325,8 @@ def vsa_gate_norm_bwd(dh, dx_out, x_out, y=None, gate=None, post_weight=None, we
            _tokens(x_out, "x_out", shape, dtype, device),
            None if y is None else _tokens(y, "y", shape, branch, device)]
     if dx is None:
-        dx = torch.empty(shape, dtype=dtype, device=where)
-        ins.append(_pack_tokens(dx.data_ptr(), S * C, C))
+        dx, packed = _new_tokens(x_out, shape, dtype)
+        ins.append(packed)
     else:
         ins.append(_tokens(dx, "dx", shape, dtype, device))
     if y is None:
@@ -310,12 +334,12 @@ def vsa_gate_norm_bwd(dh, dx_out, x_out, y=None, gate=None, post_weight=None, we
             raise ValueError("dy is given without y")
         ins.append(None)
     elif dy is None:
-        dy = torch.empty(shape, dtype=branch, device=where)
-        ins.append(_pack_tokens(dy.data_ptr(), S * C, C))
+        dy, packed = _new_tokens(y, shape, branch)
+        ins.append(packed)
     else:
         ins.append(_tokens(dy, "dy", shape, branch, device))
-    grads = [torch.empty(p.shape, dtype=p.dtype, device=where) if p is not None and need_dparams else None
-             for p in (gate, post_weight, weight, bias, scale, shift)]
+    grads = [None if p is None or not need_dparams else _empty_like(p) if p.is_contiguous() else
+             _empty(p.shape, dtype=p.dtype, device=where) for p in (gate, post_weight, weight, bias, scale, shift)]
     dgate, dpost, dweight, dbias, dscale, dshift = grads
     need = 0 if all(g is None for g in grads) else _norm_workspace(device, *sizes)
     keep, wp, wn = _workspace(workspace, need, x_out)
@@ -329,7 +353,7 @@ def vsa_gate_norm_bwd(dh, dx_out, x_out, y=None, gate=None, post_weight=None, we
 
 def _matrix(t, name, rows, columns, dtype, device):
     """A tensor [..., columns] of `rows` rows at one stride, as a packed vsa_matrix."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+    if not isinstance(t, _Tensor) or t.get_device() != device:
         raise TypeError("%s must be a tensor on cuda:%d" % (name, device))
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
