@@ -37,7 +37,12 @@ constexpr uint32_t STAGE_BYTES = 2 * OPERAND_BYTES;
 constexpr uint32_t OUT_BYTES = 32 * 128;  // 32 rows x 64 results of an epilogue warp
 
 constexpr int STAGES = 5;
-constexpr int BUFFERS = 2;  // of an epilogue warp: 64 results each of its 32 rows x 128 columns
+// Buffers of an epilogue warp: 64 results each of its 32 rows x 128 columns.  With pre (and no operand to load)
+// they are four of 32 results, two for pre and two for out, so that a store has the time of 32 columns'
+// work to leave its buffer: one of 64 for each of the two waited for its last store every time (32760 x
+// 1536 x 6144, gelu_tanh and pre: 400 us, now 366, 320 without pre: the
+// rest is the traffic between L2 and the SMs, which the operands alone take to about 18 TB/s).
+constexpr int BUFFERS = 2;
 
 enum Bar : uint32_t {
   FULL0 = 0,                        // first CTA: both CTAs' copies of a stage have landed
@@ -68,7 +73,7 @@ struct Params {
   int units;
   float* parts;                // [split][tail tile][CTA][256 columns][128 rows]
   const void* bias;
-  bool bias_f32, has_pre;
+  bool bias_f32, has_pre;  // has_pre: in a kernel with PRE, or from the registers
   int act;
   MatrixView out, pre, aux;    // of the join
   uint32_t* err;
@@ -145,6 +150,9 @@ __device__ __forceinline__ void product_pair(uint32_t d, uint64_t a, uint64_t b,
       : "memory");
 }
 
+// Byte offset of 16-byte chunk c of row r of 64 bytes, 64-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled64(uint32_t r, uint32_t c) { return r * 64u + ((c ^ ((r >> 1) & 3u)) << 4); }
+
 // ------------------------------------------------------------------------------ units
 
 struct Unit {
@@ -204,7 +212,7 @@ __device__ __noinline__ void linger(uint64_t ns) {
   }
 }
 
-template <typename E, int OP, bool AUX>
+template <typename E, int OP, bool AUX, bool PRE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   constexpr bool A_MN = OP == GEMM_DW, B_MN = OP != GEMM_FWD;
@@ -223,6 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b);
     tma_prefetch_desc(&maps.out);
+    if (PRE) tma_prefetch_desc(&maps.pre);
     if (AUX) tma_prefetch_desc(&maps.aux);
   }
   if (threadIdx.x == 0) {
@@ -394,17 +403,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           const int n0 = x.n0 + col0 + c * 64;
-          // Buffers: one for each 64 columns, or one for pre and one for the result.
-          const bool pre_room = OP == GEMM_FWD && !AUX && p.has_pre;
-          const uint32_t out = room + (pre_room ? 1 : c) * OUT_BYTES;
+          const uint32_t out = room + c * OUT_BYTES;
           if (AUX) {
             ok = warp_wait(aux_bar + 8u * c, whole & 1u, abort, limit);
             if (!ok) break;
-          } else {
-            if (lane == 0) {
-              if (pre_room) bulk_wait_read_all();
-              else bulk_wait_read<1>();
-            }
+          } else if (!PRE) {
+            if (lane == 0) bulk_wait_read<1>();  // all but the last 64 columns' stores
             __syncwarp();
           }
 #pragma unroll 1
@@ -426,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
               for (int j = 0; j < 4; ++j) r[j].u[0] = ld_shared16(out + swizzled(lane, h * 4 + j));
             }
             tmem_wait_ld_regs(v);
-            uint4 t[4];
+            uint4 t[4], before[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float z[8];
@@ -437,9 +441,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                   z[0] += b4[2 * j].x, z[1] += b4[2 * j].y, z[2] += b4[2 * j].z, z[3] += b4[2 * j].w;
                   z[4] += b4[2 * j + 1].x, z[5] += b4[2 * j + 1].y, z[6] += b4[2 * j + 1].z, z[7] += b4[2 * j + 1].w;
                 }
-                if (pre_room) {
-                  const uint4 y = pack8<E>(z);
-                  st_shared16(room + swizzled(lane, h * 4 + j), y.x, y.y, y.z, y.w);
+                if (PRE) {
+                  before[j] = pack8<E>(z);
                 } else if (AUX && p.has_pre && col + j * 8 < p.n && m0 + lane < p.m) {
                   // No room for a buffer of its own: straight from the registers.
                   store8(static_cast<E*>(p.pre.data) + (m0 + lane) * p.pre.stride + col + j * 8, z);
@@ -458,16 +461,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
               }
               t[j] = pack8<E>(z);
             }
+            if (PRE) {
+              if (lane == 0) bulk_wait_read<1>();  // all but the last 32 columns' stores
+              __syncwarp();
+              const uint32_t here = room + h * OUT_BYTES;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) st_shared16(out + swizzled(lane, h * 4 + j), t[j].x, t[j].y, t[j].z, t[j].w);
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t spot = here + swizzled64(lane, j);
+                st_shared16(spot, before[j].x, before[j].y, before[j].z, before[j].w);
+                st_shared16(spot + OUT_BYTES / 2, t[j].x, t[j].y, t[j].z, t[j].w);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (col < p.n && m0 < p.m) {
+                  tma_store_2d(&maps.pre, here, col, m0);
+                  tma_store_2d(&maps.out, here + OUT_BYTES / 2, col, m0);
+                }
+                bulk_commit_group();
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) st_shared16(out + swizzled(lane, h * 4 + j), t[j].x, t[j].y, t[j].z, t[j].w);
+            }
           }
+          if (PRE) continue;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (n0 < p.n && m0 < p.m) {
-              if (pre_room) tma_store_2d(&maps.pre, room, n0, m0);
-              tma_store_2d(&maps.out, out, n0, m0);
-            }
+            if (n0 < p.n && m0 < p.m) tma_store_2d(&maps.out, out, n0, m0);
             bulk_commit_group();
           }
         }
@@ -587,12 +609,12 @@ Plan plan_of(int m, int n, int k) {
   return q;
 }
 
-template <typename E, int OP, bool AUX>
+template <typename E, int OP, bool AUX, bool PRE>
 cudaError_t launch_kernel(const Maps& maps, const Params& p, int pairs, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = ensure_smem_limit(gemm_kernel<E, OP, AUX>, static_cast<int>(SMEM_BYTES), smem_set);
+  cudaError_t e = ensure_smem_limit(gemm_kernel<E, OP, AUX, PRE>, static_cast<int>(SMEM_BYTES), smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(gemm_kernel<E, OP, AUX>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, stream, maps, p);
+  e = launch_dependent(gemm_kernel<E, OP, AUX, PRE>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, stream, maps, p);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_dependent(gemm_join_kernel<E, OP>, dim3(32, p.tail), dim3(256), 0, stream, p);
 }
@@ -602,13 +624,14 @@ cudaError_t launch_typed(GemmOp op, const Maps& maps, const Params& p, int pairs
   const bool aux = p.aux.data != nullptr;
   switch (op) {
     case GEMM_FWD:
-      return aux ? launch_kernel<E, GEMM_FWD, true>(maps, p, pairs, stream)
-                 : launch_kernel<E, GEMM_FWD, false>(maps, p, pairs, stream);
+      if (!aux && p.has_pre) return launch_kernel<E, GEMM_FWD, false, true>(maps, p, pairs, stream);
+      return aux ? launch_kernel<E, GEMM_FWD, true, false>(maps, p, pairs, stream)
+                 : launch_kernel<E, GEMM_FWD, false, false>(maps, p, pairs, stream);
     case GEMM_DX:
-      return aux ? launch_kernel<E, GEMM_DX, true>(maps, p, pairs, stream)
-                 : launch_kernel<E, GEMM_DX, false>(maps, p, pairs, stream);
+      return aux ? launch_kernel<E, GEMM_DX, true, false>(maps, p, pairs, stream)
+                 : launch_kernel<E, GEMM_DX, false, false>(maps, p, pairs, stream);
     default:
-      return launch_kernel<E, GEMM_DW, false>(maps, p, pairs, stream);
+      return launch_kernel<E, GEMM_DW, false, false>(maps, p, pairs, stream);
   }
 }
 
@@ -655,8 +678,9 @@ cudaError_t launch_gemm(GemmOp op, const GemmArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = op == GEMM_FWD ? make_tmap_matrix(&maps.b, a.b, a.k, a.n, 128, bf16) : make_tmap_matrix(&maps.b, a.b, a.n, a.k, BK, bf16);
   if (e != cudaSuccess) return e;
-  if ((e = make_tmap_matrix(&maps.out, a.out, a.n, a.m, 32, bf16)) != cudaSuccess) return e;
-  if (a.pre.data && (e = make_tmap_matrix(&maps.pre, a.pre, a.n, a.m, 32, bf16)) != cudaSuccess) return e;
+  const bool narrow = op == GEMM_FWD && a.pre.data && !a.aux.data;  // PRE: boxes of 32 columns
+  if ((e = make_tmap_matrix(&maps.out, a.out, a.n, a.m, 32, bf16, narrow)) != cudaSuccess) return e;
+  if (narrow && (e = make_tmap_matrix(&maps.pre, a.pre, a.n, a.m, 32, bf16, true)) != cudaSuccess) return e;
   if (a.aux.data && (e = make_tmap_matrix(&maps.aux, a.aux, a.n, a.m, 32, bf16)) != cudaSuccess) return e;
   return bf16 ? launch_typed<__nv_bfloat16>(op, maps, p, q.pairs, stream) : launch_typed<__half>(op, maps, p, q.pairs, stream);
 }

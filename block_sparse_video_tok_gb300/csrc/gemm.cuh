@@ -37,7 +37,9 @@ double gemm_microseconds(int m, int n, int k);
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);
 bool use_linear_rows(int rows, int out);
 
-// 2-D tensor map of a 16-bit matrix of `columns` x `rows`, box 64 columns x box_rows, 128-byte swizzle.
-cudaError_t make_tmap_matrix(CUtensorMap* map, const MatrixView& x, int columns, int rows, int box_rows, bool bf16);
+// 2-D tensor map of a 16-bit matrix of `columns` x `rows`, box 64 columns x box_rows, 128-byte swizzle; narrow: 32
+// columns, 64-byte swizzle.
+cudaError_t make_tmap_matrix(CUtensorMap* map, const MatrixView& x, int columns, int rows, int box_rows, bool bf16,
+                             bool narrow = false);
 
 }  // namespace vsa

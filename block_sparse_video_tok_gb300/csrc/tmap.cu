@@ -108,15 +108,16 @@ cudaError_t make_tmap_heads(CUtensorMap* map, const HeadsView& x, int tokens, in
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tmap_matrix(CUtensorMap* map, const MatrixView& x, int columns, int rows, int box_rows, bool bf16) {
+cudaError_t make_tmap_matrix(CUtensorMap* map, const MatrixView& x, int columns, int rows, int box_rows, bool bf16,
+                             bool narrow) {
   auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t gdim[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)};
   const cuuint64_t gstride[1] = {static_cast<cuuint64_t>(x.stride) * 2};
-  const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[2] = {narrow ? 32u : 64u, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estride[2] = {1u, 1u};
   CUresult r = encode(map, two_byte_type(bf16), 2, x.data, gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                      narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
