@@ -83,6 +83,11 @@ _pack_linear = struct.Struct("@6iPqP").pack
 
 _Tensor, _empty, _empty_like = torch.Tensor, torch.empty, torch.empty_like
 
+
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
 _fns = None
 _calls = None
 
@@ -118,15 +123,18 @@ def _call(name, *args):
 # ------------------------------------------------------------------------------- arguments
 
 def _first(t, name, dims):
-    """Checks the tensor that names the call's device."""
+    """The index of the current device, after checking that the tensor is on it."""
+    if isinstance(t, _Tensor):
+        device = t.get_device()
+        if device >= 0 and device == _current_device() and dims[0] <= t.dim() <= dims[1] and t.numel():
+            return device
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dim() < dims[0] or t.dim() > dims[1]:
         raise ValueError("%s has %d dimensions" % (name, t.dim()))
     if t.numel() == 0:
         raise ValueError("%s is empty: %s" % (name, tuple(t.shape)))
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError("%s is on %s, which is not the current device" % (name, t.device))
+    raise ValueError("%s is on %s, which is not the current device" % (name, t.device))
 
 
 def _like(t, name, shape, dtype, device):
@@ -213,13 +221,16 @@ def _modulation(m, name, B, S, C, dtype, device):
         raise TypeError("%s must be a [B, C] or [B, groups, C] tensor" % name)
     if m.dim() == 2:
         m = m.unsqueeze(1)
-    shape = m.shape
-    G = shape[1]
-    if m.get_device() != device or m.dtype is not dtype or shape[0] != B or shape[2] != C:
+    n0, G, n2 = m.shape
+    if m.get_device() != device or m.dtype is not dtype or n0 != B or n2 != C:
         _like(m, name, (B, G, C), dtype, device)
     if G < 1 or S % G:
         raise ValueError("%s: %d tokens do not share %d groups evenly" % (name, S, G))
-    return (*_strides3(m, name), G)
+    s0, s1, s2 = m.stride()
+    ptr = m.data_ptr()
+    if s2 != 1 or ptr & 15 or (s0 | s1) & 7:                                # not the usual case
+        ptr, s0, s1 = _strides3(m, name)
+    return ptr, s0, s1, G
 
 
 def _gate_norm_op(x, branch, y, gate, post_weight, weight, bias, scale, shift, kind, eps, post_eps):
@@ -239,17 +250,15 @@ def _gate_norm_op(x, branch, y, gate, post_weight, weight, bias, scale, shift, k
         raise ValueError("gate and post_weight need y")
     mdtype = _param_dtype((gate, scale, shift), branch, "gate, scale and shift")
     wdtype = _param_dtype((post_weight, weight, bias), branch, "the weights and the bias")
-    mods = [_modulation(m, n, B, S, C, mdtype, device)
-            for m, n in ((gate, "gate"), (scale, "scale"), (shift, "shift"))]
-    G = None
-    for m in mods:
-        if m[3] is not None and m[3] != G:
-            if G is not None:
-                raise ValueError("gate, scale and shift must have the same groups, got %d and %d" % (G, m[3]))
-            G = m[3]
-    G = G or 1
+    gp, gs0, gs1, G = _modulation(gate, "gate", B, S, C, mdtype, device)
+    cp, cs0, cs1, G1 = _modulation(scale, "scale", B, S, C, mdtype, device)
+    tp, ts0, ts1, G2 = _modulation(shift, "shift", B, S, C, mdtype, device)
+    G = G or G1 or G2 or 1
+    if (G1 or G) != G or (G2 or G) != G:
+        raise ValueError("gate, scale and shift must have the same groups, got %s" %
+                         sorted({n for n in (G, G1, G2) if n}))
     op = _pack_norm(B, S, C, G, KINDS[kind], _DTYPES[dtype], _DTYPES[branch], _DTYPES[mdtype],
-                    _DTYPES[wdtype], eps, post_eps, *mods[0][:3], *mods[1][:3], *mods[2][:3],
+                    _DTYPES[wdtype], eps, post_eps, gp, gs0, gs1, cp, cs0, cs1, tp, ts0, ts1,
                     _vector(post_weight, "post_weight", wdtype, C, device),
                     _vector(weight, "weight", wdtype, C, device), _vector(bias, "bias", wdtype, C, device))
     return op, (B, S, C, G)
@@ -278,13 +287,13 @@ def vsa_gate_norm(x, y=None, gate=None, post_weight=None, weight=None, bias=None
     if stream is not None:
         return _on(stream, vsa_gate_norm, x, y, gate, post_weight, weight, bias, scale, shift, kind, eps,
                    post_eps, h_dtype, x_out, h)
-    _first(x, "x", (3, 3))
+    device = _first(x, "x", (3, 3))
     branch = getattr(y, "dtype", None) if y is not None else x.dtype if h_dtype is None else h_dtype
     if h_dtype is not None and h_dtype is not branch:
         raise TypeError("h has y's type, %s" % branch)
     op, (B, S, C, _) = _gate_norm_op(x, branch, y, gate, post_weight, weight, bias, scale, shift, kind,
                                      eps, post_eps)
-    shape, dtype, device = x.shape, x.dtype, x.get_device()
+    shape, dtype = x.shape, x.dtype
     xs = _tokens(x, "x", shape, dtype, device)
     if h is None:
         h, hs = _new_tokens(x if y is None else y, shape, branch)
@@ -314,12 +323,12 @@ def vsa_gate_norm_bwd(dh, dx_out, x_out, y=None, gate=None, post_weight=None, we
     if stream is not None:
         return _on(stream, vsa_gate_norm_bwd, dh, dx_out, x_out, y, gate, post_weight, weight, bias, scale,
                    shift, kind, eps, post_eps, need_dparams, dx, dy, workspace)
-    _first(x_out, "x_out", (3, 3))
+    device = _first(x_out, "x_out", (3, 3))
     branch = getattr(dh if y is None else y, "dtype", None)
     op, sizes = _gate_norm_op(x_out, branch, y, gate, post_weight, weight, bias, scale, shift, kind, eps,
                               post_eps)
     B, S, C, _ = sizes
-    shape, dtype, device, where = x_out.shape, x_out.dtype, x_out.get_device(), x_out.device
+    shape, dtype, where = x_out.shape, x_out.dtype, x_out.device
     ins = [_tokens(dh, "dh", shape, branch, device),
            None if dx_out is None else _tokens(dx_out, "dx_out", shape, dtype, device),
            _tokens(x_out, "x_out", shape, dtype, device),
@@ -427,9 +436,9 @@ def vsa_linear(x, weight, bias=None, act=None, residual=None, need_pre=False, ou
     an activation takes (None unless need_pre or a place for it is given)."""
     if stream is not None:
         return _on(stream, vsa_linear, x, weight, bias, act, residual, need_pre, out, pre, workspace)
-    _first(x, "x", (1, 64))
+    device = _first(x, "x", (1, 64))
     make, N, K = _linear_op(x, weight, bias, act)
-    dtype, device = x.dtype, x.get_device()
+    dtype = x.dtype
     rows = x.numel() // x.shape[-1]
     op = make(rows)
     xs = _matrix(x, "x", rows, K, dtype, device)
@@ -438,7 +447,7 @@ def vsa_linear(x, weight, bias=None, act=None, residual=None, need_pre=False, ou
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
     if pre is None and need_pre:
-        pre = torch.empty(shape, dtype=dtype, device=x.device)
+        pre = _empty_like(out) if out.is_contiguous() else _empty(shape, dtype=dtype, device=x.device)
     keep, wp, wn = _workspace(workspace, _linear_workspace("vsa_linear_fwd_workspace_bytes", device, rows, K, N,
                                                            ACTS[act]), x)
     _call("vsa_linear_fwd", op, xs, rs, _matrix(out, "out", rows, N, dtype, device),
@@ -455,24 +464,24 @@ def vsa_linear_bwd(dout, x, weight, bias=None, act=None, pre=None, x_act=None, x
     if stream is not None:
         return _on(stream, vsa_linear_bwd, dout, x, weight, bias, act, pre, x_act, x_pre, need_dx,
                    need_dweight, dx, dweight, dbias, workspace)
-    _first(x, "x", (1, 64))
+    device = _first(x, "x", (1, 64))
     make, N, K = _linear_op(x, weight, bias, act)
     if x_act not in ACTS:
         raise ValueError("x_act must be None, 'gelu', 'gelu_tanh' or 'silu', got %r" % (x_act,))
     if (act is None) != (pre is None) or (x_act is None) != (x_pre is None):
         raise ValueError("an activation and what went into it come together")
-    dtype, device, where = x.dtype, x.get_device(), x.device
+    dtype, where = x.dtype, x.device
     rows = x.numel() // x.shape[-1]
     op = make(rows)
     if dx is None and need_dx:
-        dx = torch.empty(x.shape, dtype=dtype, device=where)
+        dx = _empty_like(x) if x.is_contiguous() else _empty(x.shape, dtype=dtype, device=where)
     if dweight is None and need_dweight:
-        dweight = torch.empty((N, K), dtype=dtype, device=where)
+        dweight = _empty_like(weight) if weight.is_contiguous() else _empty((N, K), dtype=dtype, device=where)
     if bias is None:
         if dbias is not None:
             raise ValueError("dbias is given without bias")
     elif dbias is None:
-        dbias = torch.empty(N, dtype=bias.dtype, device=where)
+        dbias = _empty_like(bias)
     if dx is None and dweight is None and dbias is None:
         return None, None, None
 

@@ -1,5 +1,6 @@
 // block_api.cu -- the extern "C" entry points declared in include/vsa_block.h: argument checks and
 // the stream-ordered launches of each operator.
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -13,13 +14,19 @@ constexpr int64_t MAX_ELEMENTS = 1ll << 44;  // tiles are counted in 32 bits
 
 vsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? VSA_OK : vsa::record_cuda_failure(e); }
 
+// The current device's capability, looked up once for each.
 vsa_status check_device() {
+  static std::atomic<uint64_t> known{0};
   int dev = 0, major = 0, minor = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (e == cudaSuccess && (known.load(std::memory_order_relaxed) & bit) != 0) return VSA_OK;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (e != cudaSuccess) return vsa::record_cuda_failure(e);
-  return major == 10 && minor == 3 ? VSA_OK : VSA_ERR_UNSUPPORTED;
+  if (major != 10 || minor != 3) return VSA_ERR_UNSUPPORTED;
+  known.fetch_or(bit, std::memory_order_relaxed);
+  return VSA_OK;
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }

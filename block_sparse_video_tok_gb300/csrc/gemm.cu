@@ -591,9 +591,12 @@ Plan plan_of(int m, int n, int k) {
   q.per = q.steps;
   if (q.tail > 0) {
     double best = q.steps + 5.0;
-    for (int s = 2; s <= q.steps && static_cast<int64_t>(s) * q.tail <= 2 * q.pairs; ++s) {
+    // The parts that lengths of a part give (about 2 sqrt(steps) of them): s, then the next with shorter
+    // ones.
+    for (int s = 2; s <= q.steps && static_cast<int64_t>(s) * q.tail <= 2 * q.pairs;) {
       const int per = (q.steps + s - 1) / s;
-      if ((q.steps + per - 1) / per != s) continue;  // no part without a step
+      s = (q.steps + per - 1) / per;  // no part without a step
+      if (static_cast<int64_t>(s) * q.tail > 2 * q.pairs) break;
       const int rounds = (s * q.tail + q.pairs - 1) / q.pairs;
       const double cost = rounds * (per + 5.0) + 9.0 + 0.1 * s * q.tail;
       if (cost < best) {
@@ -601,6 +604,8 @@ Plan plan_of(int m, int n, int k) {
         q.splits = s;
         q.per = per;
       }
+      if (per == 1) break;
+      s = (q.steps + per - 2) / (per - 1);
     }
   }
   q.units = q.full + q.tail * q.splits;
