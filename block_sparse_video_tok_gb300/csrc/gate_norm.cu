@@ -17,6 +17,16 @@
 // row's tokens.  The means are shuffles and one exchange of the warps' sums in shared memory per
 // round; the variance takes a round of its own, around the mean, so that tokens far from zero keep
 // their precision.  The next tokens' loads are issued before the rounds.
+//
+// Measured, one GB300: forward of 131040 x 1536 bf16 with gate, scale and shift 246 us, 96 % of the copy
+// rate.  Backward of 2 x 32760 x 1536 202 us, 88 %: its warps' instructions take 58 % of the issue slots, and
+// a token's round of sums is a chain of shuffles and a barrier that 4 x 3 warps an SM do not quite
+// hide.  What made it fast, from 514 us: one round of sums a token instead of two, 9 instructions of
+// exchange instead of some 40, inputs through shared memory instead of registers, and packed pairs of fp32
+// (247, then 227); two vectors to a lane, so that half as many warps take part in a round (213); the
+// copies asked for before the round instead of after it (202).  Tried without gain: two tokens a round (289
+// where one took 227), five or six tokens ahead (267, 279 where four took 251), 80 registers and a fourth
+// CTA (332).
 #include <type_traits>
 
 #include "block_internal.cuh"
@@ -29,12 +39,12 @@ namespace {
 
 constexpr int MAX_WPR = 16;   // warps of a token
 constexpr int CTA_WARPS = 8;  // warps of a CTA that holds several tokens
-constexpr int BWD_ONE = 512;  // channels up to which the backward gives a lane one vector
 constexpr int FWD_ROWS = 2;   // tokens in flight per group of warps
 
-// Registers of a thread with NV vectors: the CTAs of an SM follow from them.
+// Registers of a thread with NV vectors: the CTAs of an SM follow from them.  Backward, two vectors: 168 where a
+// CTA's threads leave room for them; more than 6144 channels do not, and there 128 spill (8192 channels run at
+// a third of the copy rate).
 constexpr int fwd_regs(int nv) { return nv == 1 ? 80 : 112; }
-// (Backward, two vectors: more than 128 where a CTA's threads leave room.)
 constexpr int BWD_REGS_1 = 96, BWD_REGS_2 = 168, BWD_REGS_WIDE = 128;
 
 // 8 parameters of either type, or `fallback`.
@@ -636,8 +646,14 @@ __global__ void __launch_bounds__(1024) gate_norm_weights_kernel(const __grid_co
   store_param(j == 0 ? a.dbias : j == 1 ? a.dweight : a.dpost, c, a.weight_dtype, s);
 }
 
+// Vectors of a lane.  Forward: as few as 16 warps allow.  Backward: two where they fill four fifths of the lanes
+// (2 x 32760 tokens of 512 channels 75 us, one vector 80; 1024: 138 and 148; 768, three quarters: 121 and
+// 113).
 int fwd_vectors(int channels) { return channels <= 256 * MAX_WPR ? 1 : 2; }
-int bwd_vectors(int channels) { return channels <= BWD_ONE ? 1 : 2; }
+int bwd_vectors(int channels) {
+  const int full = (channels + 511) / 512 * 512;
+  return channels * 5 < full * 4 && channels <= 256 * MAX_WPR ? 1 : 2;
+}
 int bwd_regs(int channels) {
   return bwd_vectors(channels) == 1 ? BWD_REGS_1 : (channels + 511) / 512 * 32 * BWD_REGS_2 <= 65536 ? BWD_REGS_2 : BWD_REGS_WIDE;
 }

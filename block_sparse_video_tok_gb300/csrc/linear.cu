@@ -1,4 +1,10 @@
-// linear.cu -- out = act(x W^T + bias) + residual and its gradients.
+// linear.cu -- out = act(x W^T + bias) + residual and its gradients: which kernels a call takes.
+//
+// Forward: one product with its epilogue (linear_rows.cu up to 16 rows, gemm_small.cu for small products,
+// gemm.cu).  Backward: dz = dout act'(pre) and the columns' sums in a pass of their own, then dx = dz W and
+// dweight = dz^T x.  The pass is left out where there is neither an activation nor a bias; and a chain of two
+// products does not pay for it twice, as the second's dx goes on through the activation in its
+// epilogue (x_act).
 #include "act.cuh"
 #include "gemm.cuh"
 #include "vec8.cuh"
@@ -7,8 +13,10 @@ namespace vsa {
 
 namespace {
 
-// Columns of 8 to a thread, 32 threads of a warp side by side, ROWS warps down the rows.
-constexpr int ROWS = 8, AHEAD = 2;  // AHEAD rows of a thread in flight
+// Columns of 8 to a thread, 32 threads of a warp side by side, ROWS warps down the rows, AHEAD rows of a thread in
+// flight (32760 x 6144 with gelu_tanh: 188 us, 95 % of the copy rate; 4 in flight 204, 1 214; sums alone 60, 84,
+// 63).
+constexpr int ROWS = 8, AHEAD = 2;
 
 // dz = dout act'(pre) (not written without an activation) and the sums of its columns over `chunk`
 // rows, to partial [blockIdx.y][n] fp32 (unless null).  Bound by HBM: one read of each input, one write.

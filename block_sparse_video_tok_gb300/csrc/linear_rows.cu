@@ -11,6 +11,9 @@
 // A CTA has 16 features; its 8 warps share k, 32 elements at a time in turn, all of a warp's loads in
 // flight together.  Where there are fewer features than fill the GPU, the CTAs of a cluster share k
 // too.  The warps' and CTAs' sums are added in their order, through shared memory.
+//
+// Measured: 8 x 1536 -> 9216 with silu 5.0 us, 84 % of the copy rate (weights 28 MB); 8 x 6144 -> 1536 5.0; 16 rows
+// 6.0 and 6.6, where gemm_small.cu's tiles take 8 to 9.
 #include "act.cuh"
 #include "gemm.cuh"
 #include "vec8.cuh"
