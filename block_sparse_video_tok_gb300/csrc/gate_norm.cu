@@ -45,7 +45,7 @@ constexpr int FWD_ROWS = 2;   // tokens in flight per group of warps
 // CTA's threads leave room for them; more than 6144 channels do not, and there 128 spill (8192 channels run at
 // a third of the copy rate).
 constexpr int fwd_regs(int nv) { return nv == 1 ? 80 : 112; }
-constexpr int BWD_REGS_1 = 96, BWD_REGS_2 = 168, BWD_REGS_WIDE = 128;
+constexpr int BWD_REGS_1 = 96, BWD_REGS_2 = 168, BWD_REGS_4 = 255;
 
 // 8 parameters of either type, or `fallback`.
 __device__ __forceinline__ void load_param(const void* p, int64_t at, int dtype, float fallback, float* v) {
@@ -385,7 +385,7 @@ struct NoRing {
 template <typename TX, int NV>
 constexpr int slots_of() { return NV == 1 && sizeof(TX) == 2 ? 4 : 2; }
 template <typename TX, typename TY, int NV>
-constexpr bool o_direct() { return NV == 2 && sizeof(TX) == 4 && sizeof(TY) == 4; }
+constexpr bool o_direct() { return NV > 1 && sizeof(TX) == 4 && sizeof(TY) == 4; }
 template <typename TX, typename TY, int NV>
 constexpr int ring_bytes(int threads) {
   return slots_of<TX, NV>() * ((o_direct<TX, TY, NV>() ? 1 : 2) * Ring<TX, NV>::PIECES + 2 * Ring<TY, NV>::PIECES) * 16 * threads;
@@ -651,11 +651,13 @@ __global__ void __launch_bounds__(1024) gate_norm_weights_kernel(const __grid_co
 // 113).
 int fwd_vectors(int channels) { return channels <= 256 * MAX_WPR ? 1 : 2; }
 int bwd_vectors(int channels) {
+  if ((channels + 511) / 512 * 32 * BWD_REGS_2 > 65536) return 4;
   const int full = (channels + 511) / 512 * 512;
   return channels * 5 < full * 4 && channels <= 256 * MAX_WPR ? 1 : 2;
 }
 int bwd_regs(int channels) {
-  return bwd_vectors(channels) == 1 ? BWD_REGS_1 : (channels + 511) / 512 * 32 * BWD_REGS_2 <= 65536 ? BWD_REGS_2 : BWD_REGS_WIDE;
+  const int nv = bwd_vectors(channels);
+  return nv == 1 ? BWD_REGS_1 : nv == 2 ? BWD_REGS_2 : BWD_REGS_4;
 }
 
 // Units: parts of every modulation row.  The grid takes them in waves of `slots`, each as long as a
@@ -771,7 +773,7 @@ cudaError_t launch_width(const GateNormArgs& a, bool forward, cudaStream_t strea
   switch (bwd_regs(a.channels)) {
     case BWD_REGS_1: return launch_bwd<TX, TY, 1, BWD_REGS_1>(a, stream);
     case BWD_REGS_2: return launch_bwd<TX, TY, 2, BWD_REGS_2>(a, stream);
-    default: return launch_bwd<TX, TY, 2, BWD_REGS_WIDE>(a, stream);
+    default: return launch_bwd<TX, TY, 4, BWD_REGS_4>(a, stream);
   }
 }
 
