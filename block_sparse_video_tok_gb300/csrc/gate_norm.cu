@@ -91,10 +91,16 @@ __device__ __forceinline__ float mean_of(const Params& p, float sum) {
   return fmaf(fmaf(-m, p.dim, sum), p.inv_dim, m);
 }
 
-// The warps that hold a token together: sums over all of its elements, the same for every lane.
+// Lanes that hold a token of few channels: a part of a warp.
+constexpr int NARROW_CHANNELS = 128;
+__host__ __device__ constexpr int narrow_lanes(int channels) { return channels <= 64 ? 8 : 16; }
+
+// The warps (NARROW: lanes) that hold a token together: sums over all of its elements, the same for every
+// lane.
+template <bool NARROW>
 struct Team {
   float (*buf)[4][MAX_WPR];  // [2]: warps' sums of this round and of the one before
-  int wpr, warp, lane, bar;
+  int wpr, warp, lane, bar, width;
   uint32_t round;
 
   __device__ __forceinline__ Team(float (*b)[4][MAX_WPR], const Params& p) {
@@ -104,6 +110,7 @@ struct Team {
     warp = w % wpr;
     lane = threadIdx.x & 31;
     bar = 1 + w / wpr;
+    width = NARROW ? narrow_lanes(p.a.channels) : 32;
     round = 0;
   }
 
@@ -112,6 +119,16 @@ struct Team {
   template <int N>
   __device__ __forceinline__ void sum(float (&v)[N]) {
     static_assert(N == 1 || N == 2 || N == 4, "values are halved");
+    if (NARROW) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int o = 4; o > 0; o /= 2) v[i] += __shfl_xor_sync(FULL, v[i], o);
+        const float other = __shfl_xor_sync(FULL, v[i], 8);
+        if (width == 16) v[i] += other;
+      }
+      return;
+    }
     constexpr int LANES = 32 / N;  // that add one value
     float k[N];
 #pragma unroll
@@ -172,19 +189,23 @@ __device__ __forceinline__ T* at(const TokensView& v, int b, int t) {
   return static_cast<T*>(v.data) + b * v.batch + t * v.token;
 }
 
-template <typename TX, typename TY, int NV>
+// NARROW: a warp has the tokens of several units, and every lane of it takes part in each round of sums.
+template <typename TX, typename TY, int NV, bool NARROW>
 __global__ void __maxnreg__(fwd_regs(NV)) gate_norm_fwd_kernel(const __grid_constant__ Params p) {
   constexpr int R = NV == 1 ? FWD_ROWS : 1;
   __shared__ float sums[CTA_WARPS][2][4][MAX_WPR];
   grid_dependency_wait();
   const GateNormArgs& a = p.a;
   const int group = (threadIdx.x >> 5) / p.wpr;
-  Team team(sums[group], p);
-  const int e0 = (team.warp * 32 + team.lane) * 8, step = p.wpr * 256;  // vectors e0, e0 + step, ..
+  Team<NARROW> team(sums[group], p);
+  const int e0 = (team.warp * 32 + (team.lane & (team.width - 1))) * 8, step = p.wpr * 256;  // vectors e0, e0 + step, ..
   const bool branch = a.y.data != nullptr, post = a.post_weight != nullptr, layer = a.kind == VSA_LAYER_NORM;
 
-  for (int u = blockIdx.x * p.per_cta + group; u < p.units; u += gridDim.x * p.per_cta) {
-    const Unit unit = unit_of(p, u);
+  for (int u0 = blockIdx.x * p.per_cta + (NARROW ? group * (32 / team.width) : group); u0 < p.units;
+       u0 += gridDim.x * p.per_cta) {
+    const int u = NARROW ? u0 + team.lane / team.width : u0;
+    Unit unit = unit_of(p, NARROW ? min(u, p.units - 1) : u);
+    if (NARROW && u >= p.units) unit.t1 = unit.t0;
     float ca[NV][8], cc[NV][8], cg[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -221,7 +242,7 @@ __global__ void __maxnreg__(fwd_regs(NV)) gate_norm_fwd_kernel(const __grid_cons
         }
     };
     load(unit.t0);
-    for (int t = unit.t0; t < unit.t1; t += R) {
+    for (int t = unit.t0, i = 0; NARROW ? i < p.chunk : t < unit.t1; t += R, i += R) {
       float v[R][NV][8], s[R];
       float inv[R];
 #pragma unroll
@@ -396,7 +417,7 @@ constexpr int SM_SMEM = 228 * 1024, CTA_SMEM = 227 * 1024, STATIC_SMEM = CTA_WAR
 // A post norm takes a second round.  The inputs come SLOTS - 1 tokens ahead through shared memory: in
 // registers beside the three sums there is room for one.  SUMS: the unit's S1, S2, S3 go to the
 // workspace.
-template <typename TX, typename TY, int NV, int REGS, bool SUMS>
+template <typename TX, typename TY, int NV, int REGS, bool NARROW, bool SUMS>
 __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ Params p) {
   constexpr int SLOTS = slots_of<TX, NV>();
   constexpr bool DIRECT = o_direct<TX, TY, NV>();
@@ -405,8 +426,8 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
   grid_dependency_wait();
   const GateNormArgs& a = p.a;
   const int group = (threadIdx.x >> 5) / p.wpr;
-  Team team(sums[group], p);
-  const int e0 = (team.warp * 32 + team.lane) * 8, step = p.wpr * 256;
+  Team<NARROW> team(sums[group], p);
+  const int e0 = (team.warp * 32 + (team.lane & (team.width - 1))) * 8, step = p.wpr * 256;
   const bool branch = a.y.data != nullptr, post = a.post_weight != nullptr, layer = a.kind == VSA_LAYER_NORM;
   const int vectors = a.channels > e0 ? (a.channels - e0 + step - 1) / step : 0;
   uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(room));
@@ -419,8 +440,11 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
   base += Ring<TY, NV>::bytes(SLOTS, blockDim.x);
   Ring<TY, NV> y(base, SLOTS, step, vectors);
 
-  for (int u = blockIdx.x * p.per_cta + group; u < p.units; u += gridDim.x * p.per_cta) {
-    const Unit unit = unit_of(p, u);
+  for (int u0 = blockIdx.x * p.per_cta + (NARROW ? group * (32 / team.width) : group); u0 < p.units;
+       u0 += gridDim.x * p.per_cta) {
+    const int u = NARROW ? u0 + team.lane / team.width : u0;
+    Unit unit = unit_of(p, NARROW ? min(u, p.units - 1) : u);
+    if (NARROW && u >= p.units) unit.t1 = unit.t0;
     x.open(a.x_out, unit.b, e0);
     o.open(a.dx_out, unit.b, e0);
     h.open(a.dh, unit.b, e0);
@@ -480,7 +504,8 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
       team.sum(s);
       mean = s[0] * p.inv_dim;
     }
-    for (int t = unit.t0; t < unit.t1; ++t) {
+    for (int t = unit.t0, i = 0; NARROW ? i < p.chunk : t < unit.t1; ++t, ++i) {
+      const bool here = !NARROW || t < unit.t1;
       const int slot = (t - unit.t0) & (SLOTS - 1);
       copy_wait<SLOTS - 2>();
       uint64_t v[NV][4], s2[3] = {0, 0, 0};
@@ -520,7 +545,7 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
         for (int i = 0; i < 4; ++i) {
           const uint64_t n = f2_mul(v[k][i], f2), gi = pair(g, i), yi = pair(w, i);
           const uint64_t dx = f2_fma(f2, f2_fma(n, m22, f2_fma(gi, ca[k][i], m12)), pair(d, i));
-          if (SUMS) {
+          if (SUMS && here) {
             acc[SUMS ? k : 0][0][i] = f2_add(acc[SUMS ? k : 0][0][i], gi);
             acc[SUMS ? k : 0][1][i] = f2_fma(gi, n, acc[SUMS ? k : 0][1][i]);
           }
@@ -529,13 +554,13 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
           if (post) {
             z2[0] = f2_fma(q, yi, z2[0]);
             z2[1] = f2_fma(yi, yi, z2[1]);
-          } else if (SUMS) {
+          } else if (SUMS && here) {
             acc[SUMS ? k : 0][2][i] = f2_fma(dx, yi, acc[SUMS ? k : 0][2][i]);
           }
           f2_unpack(dx, d[2 * i], d[2 * i + 1]);
           f2_unpack(q, g[2 * i], g[2 * i + 1]);
         }
-        if (k < vectors) {
+        if (k < vectors && here) {
           store8(pdx + k * step, d);
           if (branch && !post) store8(pdy + k * step, g);
         }
@@ -551,10 +576,10 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint64_t ny = f2_mul(pair(w, i), f2_pack(fy, fy));
-            if (SUMS) acc[SUMS ? k : 0][2][i] = f2_fma(v[k][i], ny, acc[SUMS ? k : 0][2][i]);
+            if (SUMS && here) acc[SUMS ? k : 0][2][i] = f2_fma(v[k][i], ny, acc[SUMS ? k : 0][2][i]);
             f2_unpack(f2_mul(f2_fma(ny, f2_pack(m, m), f2_mul(v[k][i], cg[k][i])), f2_pack(fy, fy)), w[2 * i], w[2 * i + 1]);
           }
-          if (k < vectors) store8(pdy + k * step, w);
+          if (k < vectors && here) store8(pdy + k * step, w);
         }
       }
       pdx += a.dx.token;
@@ -563,7 +588,7 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
     if (SUMS) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (k >= vectors) continue;
+        if (k >= vectors || (NARROW && u >= p.units)) continue;
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
           float w[8];
@@ -648,12 +673,14 @@ __global__ void __launch_bounds__(1024) gate_norm_weights_kernel(const __grid_co
 
 // Vectors of a lane.  Forward: as few as 16 warps allow.  Backward: two where they fill four fifths of the lanes
 // (2 x 32760 tokens of 512 channels 75 us, one vector 80; 1024: 138 and 148; 768, three quarters: 121 and
-// 113).
+// 113); from 2056 to 4096 channels one, as two leave an SM 8 or 10 warps (2304: 321 and 338; 4096: 568 and 611);
+// beyond, two and four.
 int fwd_vectors(int channels) { return channels <= 256 * MAX_WPR ? 1 : 2; }
 int bwd_vectors(int channels) {
   if ((channels + 511) / 512 * 32 * BWD_REGS_2 > 65536) return 4;
+  if (channels > 256 * MAX_WPR) return 2;
   const int full = (channels + 511) / 512 * 512;
-  return channels * 5 < full * 4 && channels <= 256 * MAX_WPR ? 1 : 2;
+  return channels > 2048 || channels * 5 < full * 4 ? 1 : 2;
 }
 int bwd_regs(int channels) {
   const int nv = bwd_vectors(channels);
@@ -664,7 +691,7 @@ int bwd_regs(int channels) {
 // unit's tokens and what a unit costs besides (`extra` tokens); the least of up to four waves.
 constexpr int FWD_EXTRA = 2, BWD_EXTRA = 4;
 struct Plan {
-  int wpr, per_cta, ctas, parts, chunk, units;
+  int wpr, warps, per_cta, ctas, parts, chunk, units;  // warps of a token, of a CTA; units of a CTA
   size_t most;  // units at most, whatever the type
 };
 Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int lane_bytes) {
@@ -675,6 +702,7 @@ Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int 
   // Tokens of a CTA: as many on an SM as its registers and shared memory hold, in at most 4 CTAs (a CTA
   // takes 16 of an SM's 64 barriers).
   const int warp_regs = (forward ? fwd_regs(nv) : bwd_regs(channels)) * 32;
+  const int narrow = channels <= NARROW_CHANNELS ? 32 / narrow_lanes(channels) : 1;  // tokens of a warp
   int most = 0, teams = 0;
   for (int n = 1; n == 1 || n * q.wpr <= CTA_WARPS; ++n) {
     int ctas = 65536 / (warp_regs * q.wpr * n);
@@ -684,9 +712,12 @@ Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int 
     ctas = ctas < room ? ctas : room;
     if (ctas * n > teams) {
       teams = ctas * n;
-      q.per_cta = n;
+      q.warps = n * q.wpr;
+      q.per_cta = n * narrow;
     }
   }
+  teams *= narrow;
+  most *= narrow;
   const int64_t slots = static_cast<int64_t>(device_sm_count()) * teams;
   q.most = static_cast<size_t>(device_sm_count()) * most * 4;
   const int64_t rows = static_cast<int64_t>(batch) * groups;
@@ -730,29 +761,29 @@ Params params_of(const GateNormArgs& a, const Plan& q) {
   return p;
 }
 
-template <typename TX, typename TY, int NV>
+template <typename TX, typename TY, int NV, bool NARROW>
 cudaError_t launch_fwd(const GateNormArgs& a, cudaStream_t stream) {
   const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, true, 0);
-  return launch_dependent(gate_norm_fwd_kernel<TX, TY, NV>, dim3(q.ctas), dim3(q.wpr * q.per_cta * 32), 0, stream,
+  return launch_dependent(gate_norm_fwd_kernel<TX, TY, NV, NARROW>, dim3(q.ctas), dim3(q.warps * 32), 0, stream,
                           params_of(a, q));
 }
 
-template <typename TX, typename TY, int NV, int REGS, bool SUMS>
+template <typename TX, typename TY, int NV, int REGS, bool NARROW, bool SUMS>
 cudaError_t launch_main(const Params& p, const Plan& q, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = ensure_smem_limit(gate_norm_bwd_kernel<TX, TY, NV, REGS, SUMS>, CTA_SMEM - STATIC_SMEM, smem_set);
+  const cudaError_t e = ensure_smem_limit(gate_norm_bwd_kernel<TX, TY, NV, REGS, NARROW, SUMS>, CTA_SMEM - STATIC_SMEM, smem_set);
   if (e != cudaSuccess) return e;
-  const int threads = q.wpr * q.per_cta * 32;
-  return launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, REGS, SUMS>, dim3(q.ctas), dim3(threads),
+  const int threads = q.warps * 32;
+  return launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, REGS, NARROW, SUMS>, dim3(q.ctas), dim3(threads),
                           ring_bytes<TX, TY, NV>(threads), stream, p);
 }
 
-template <typename TX, typename TY, int NV, int REGS>
+template <typename TX, typename TY, int NV, int REGS, bool NARROW>
 cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
   const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, false, ring_bytes<TX, TY, NV>(1));
   const Params p = params_of(a, q);
-  if (!wants_sums(a)) return launch_main<TX, TY, NV, REGS, false>(p, q, stream);
-  cudaError_t e = launch_main<TX, TY, NV, REGS, true>(p, q, stream);
+  if (!wants_sums(a)) return launch_main<TX, TY, NV, REGS, NARROW, false>(p, q, stream);
+  cudaError_t e = launch_main<TX, TY, NV, REGS, NARROW, true>(p, q, stream);
   if (e != cudaSuccess) return e;
   const int rows = a.batch * a.groups, columns = (a.channels + 31) / 32;
   float* share = rows > 1 && (a.dpost || a.dweight || a.dbias)
@@ -768,12 +799,14 @@ cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
 
 template <typename TX, typename TY>
 cudaError_t launch_width(const GateNormArgs& a, bool forward, cudaStream_t stream) {
+  if (a.channels <= NARROW_CHANNELS)
+    return forward ? launch_fwd<TX, TY, 1, true>(a, stream) : launch_bwd<TX, TY, 1, BWD_REGS_1, true>(a, stream);
   if (forward)
-    return fwd_vectors(a.channels) == 1 ? launch_fwd<TX, TY, 1>(a, stream) : launch_fwd<TX, TY, 2>(a, stream);
+    return fwd_vectors(a.channels) == 1 ? launch_fwd<TX, TY, 1, false>(a, stream) : launch_fwd<TX, TY, 2, false>(a, stream);
   switch (bwd_regs(a.channels)) {
-    case BWD_REGS_1: return launch_bwd<TX, TY, 1, BWD_REGS_1>(a, stream);
-    case BWD_REGS_2: return launch_bwd<TX, TY, 2, BWD_REGS_2>(a, stream);
-    default: return launch_bwd<TX, TY, 4, BWD_REGS_4>(a, stream);
+    case BWD_REGS_1: return launch_bwd<TX, TY, 1, BWD_REGS_1, false>(a, stream);
+    case BWD_REGS_2: return launch_bwd<TX, TY, 2, BWD_REGS_2, false>(a, stream);
+    default: return launch_bwd<TX, TY, 4, BWD_REGS_4, false>(a, stream);
   }
 }
 
