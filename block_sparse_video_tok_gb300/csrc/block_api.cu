@@ -187,7 +187,7 @@ vsa_status vsa_gate_norm_fwd(const vsa_gate_norm* op, const vsa_tokens* x, const
 
 size_t vsa_gate_norm_bwd_workspace_bytes(const vsa_gate_norm* op) {
   return check_gate_norm(op) == VSA_OK
-             ? vsa::gate_norm_bwd_workspace(op->batch, op->tokens, op->channels, op->groups)
+             ? vsa::gate_norm_bwd_workspace(op->batch, op->channels, op->groups)
              : 0;
 }
 

@@ -33,7 +33,7 @@ struct GateNormArgs {
 
 cudaError_t launch_gate_norm_fwd(const GateNormArgs& a, cudaStream_t stream);
 cudaError_t launch_gate_norm_bwd(const GateNormArgs& a, cudaStream_t stream);
-size_t gate_norm_bwd_workspace(int batch, int tokens, int channels, int groups);
+size_t gate_norm_bwd_workspace(int batch, int channels, int groups);
 
 // ---------------------------------------------------------------------------- linear
 

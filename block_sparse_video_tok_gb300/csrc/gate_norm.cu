@@ -77,9 +77,10 @@ __device__ __forceinline__ void store_param(void* p, int64_t at, int dtype, floa
 
 struct Params {
   GateNormArgs a;
-  int wpr, per_cta;  // warps of a token, groups of them in a CTA
+  int wpr, per_cta;  // warps of a token, teams of a CTA
   int len;           // tokens of a modulation row
   int parts, chunk;  // units of a modulation row, tokens of a unit
+  int share;         // NARROW, backward: a unit is a CTA's; tokens of each of its teams
   int units;
   float dim, inv_dim;  // channels
 };
@@ -411,12 +412,14 @@ template <typename TX, typename TY, int NV>
 constexpr int ring_bytes(int threads) {
   return slots_of<TX, NV>() * ((o_direct<TX, TY, NV>() ? 1 : 2) * Ring<TX, NV>::PIECES + 2 * Ring<TY, NV>::PIECES) * 16 * threads;
 }
+constexpr int SPARE_BYTES = 32;  // of a lane, NARROW: one of the three sums at a time
 constexpr int SM_SMEM = 228 * 1024, CTA_SMEM = 227 * 1024, STATIC_SMEM = CTA_WARPS * 2 * 4 * MAX_WPR * 4 + 1024;
 
 // One round of sums a token: those of the token itself around its mean, and the mean of the next one.
 // A post norm takes a second round.  The inputs come SLOTS - 1 tokens ahead through shared memory: in
 // registers beside the three sums there is room for one.  SUMS: the unit's S1, S2, S3 go to the
-// workspace.
+// workspace.  NARROW: a unit is a CTA's and shared out to its many teams, whose sums are added before they
+// leave (65520 x 64: 19 us, a unit to a team 46; with more channels 1 to 2 % slower).
 template <typename TX, typename TY, int NV, int REGS, bool NARROW, bool SUMS>
 __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ Params p) {
   constexpr int SLOTS = slots_of<TX, NV>();
@@ -440,11 +443,13 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
   base += Ring<TY, NV>::bytes(SLOTS, blockDim.x);
   Ring<TY, NV> y(base, SLOTS, step, vectors);
 
-  for (int u0 = blockIdx.x * p.per_cta + (NARROW ? group * (32 / team.width) : group); u0 < p.units;
-       u0 += gridDim.x * p.per_cta) {
-    const int u = NARROW ? u0 + team.lane / team.width : u0;
-    Unit unit = unit_of(p, NARROW ? min(u, p.units - 1) : u);
-    if (NARROW && u >= p.units) unit.t1 = unit.t0;
+  const int mine = group * (32 / team.width) + team.lane / team.width;  // NARROW: team of the CTA
+  for (int u = NARROW ? blockIdx.x : blockIdx.x * p.per_cta + group; u < p.units; u += gridDim.x * (NARROW ? 1 : p.per_cta)) {
+    Unit unit = unit_of(p, u);
+    if (NARROW) {
+      unit.t0 = min(unit.t0 + mine * p.share, unit.t1);
+      unit.t1 = min(unit.t0 + p.share, unit.t1);
+    }
     x.open(a.x_out, unit.b, e0);
     o.open(a.dx_out, unit.b, e0);
     h.open(a.dh, unit.b, e0);
@@ -504,7 +509,7 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
       team.sum(s);
       mean = s[0] * p.inv_dim;
     }
-    for (int t = unit.t0, i = 0; NARROW ? i < p.chunk : t < unit.t1; ++t, ++i) {
+    for (int t = unit.t0, i = 0; NARROW ? i < p.share : t < unit.t1; ++t, ++i) {
       const bool here = !NARROW || t < unit.t1;
       const int slot = (t - unit.t0) & (SLOTS - 1);
       copy_wait<SLOTS - 2>();
@@ -586,19 +591,58 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
       pdy += a.dy.token;
     }
     if (SUMS) {
+      if (!NARROW) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        if (k >= vectors || (NARROW && u >= p.units)) continue;
+        for (int k = 0; k < NV; ++k) {
+          if (k >= vectors) continue;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
+          for (int j = 0; j < 3; ++j) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_unpack(acc[SUMS ? k : 0][j][i], w[2 * i], w[2 * i + 1]);
+            store8(a.workspace + (static_cast<int64_t>(u) * 3 + j) * a.channels + e0 + k * step, w);
+          }
+        }
+      } else {
+        // The teams' sums, added in their order.
+        float* to = a.workspace + static_cast<int64_t>(u) * 3 * a.channels;
+        float* spare = reinterpret_cast<float*>(room) + ring_bytes<TX, TY, NV>(blockDim.x) / 4;
+#pragma unroll
+        for (int j = 0; j < 3; ++j, to += a.channels) {
           float w[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f2_unpack(acc[SUMS ? k : 0][j][i], w[2 * i], w[2 * i + 1]);
-          store8(a.workspace + (static_cast<int64_t>(u) * 3 + j) * a.channels + e0 + k * step, w);
+          for (int i = 0; i < 4; ++i) f2_unpack(acc[0][j][i], w[2 * i], w[2 * i + 1]);
+          if (vectors) store8(spare + mine * a.channels + e0, w);
+          __syncthreads();
+          for (int c = threadIdx.x; c < a.channels; c += blockDim.x) {
+            float sum = 0.f;
+            for (int m = 0; m < p.per_cta; ++m) sum += spare[m * a.channels + c];
+            to[c] = sum;
+          }
+          __syncthreads();
         }
       }
     }
   }
+}
+
+// What a modulation row's sums s give its gradients at column c; and its share of the weights' gradients.
+__device__ __forceinline__ void finish_row(const GateNormArgs& a, int bg, int c, float* s) {
+  const int b = bg / a.groups, g = bg - b * a.groups;
+  const float w = param(a.weight, c, a.weight_dtype, 1.f), bias = param(a.bias, c, a.weight_dtype, 0.f);
+  const int64_t to = static_cast<int64_t>(bg) * a.channels + c;
+  store_param(a.dshift, to, a.mod_dtype, s[0]);
+  store_param(a.dscale, to, a.mod_dtype, fmaf(w, s[1], bias * s[0]));
+  store_param(a.dgate, to, a.mod_dtype, param(a.post_weight, c, a.weight_dtype, 1.f) * s[2]);
+  const float one = 1.f + param(a.scale.data, b * a.scale.batch + g * a.scale.group + c, a.mod_dtype, 0.f);
+  s[0] *= one;
+  s[1] *= one;
+  s[2] *= param(a.gate.data, b * a.gate.batch + g * a.gate.group + c, a.mod_dtype, 1.f);
+}
+__device__ __forceinline__ void finish_weights(const GateNormArgs& a, int c, const float* s) {
+  store_param(a.dbias, c, a.weight_dtype, s[0]);
+  store_param(a.dweight, c, a.weight_dtype, s[1]);
+  store_param(a.dpost, c, a.weight_dtype, s[2]);
 }
 
 // The units' sums of a modulation row, joined in unit order: 32 columns a block, Y strided units
@@ -609,59 +653,74 @@ __global__ void __launch_bounds__(32 * Y) gate_norm_sums_kernel(const __grid_con
   __shared__ float sums[3][Y][33];
   grid_dependency_wait();
   const GateNormArgs& a = p.a;
-  const int c = blockIdx.x * 32 + threadIdx.x;
-  const int rows = a.batch * a.groups;
-  for (int bg = blockIdx.y; bg < rows; bg += gridDim.y) {
-    float s[3] = {0.f, 0.f, 0.f};
-    if (c < a.channels)
+  const int c = blockIdx.x * 32 + threadIdx.x, bg = blockIdx.y;
+  float s[3] = {0.f, 0.f, 0.f};
+  if (c < a.channels) {
 #pragma unroll 4
-      for (int i = threadIdx.y; i < p.parts; i += Y) {
-        const float* from = a.workspace + (static_cast<int64_t>(bg) * p.parts + i) * 3 * a.channels + c;
+    for (int i = threadIdx.y; i < p.parts; i += Y) {
+      const float* from = a.workspace + (static_cast<int64_t>(bg) * p.parts + i) * 3 * a.channels + c;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) s[j] += from[static_cast<int64_t>(j) * a.channels];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 3; ++j) sums[j][threadIdx.y][threadIdx.x] = s[j];
-    __syncthreads();
-    if (threadIdx.y != 0 || c >= a.channels) continue;
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      s[j] = 0.f;
-#pragma unroll
-      for (int y = 0; y < Y; ++y) s[j] += sums[j][y][threadIdx.x];
+      for (int j = 0; j < 3; ++j) s[j] += from[static_cast<int64_t>(j) * a.channels];
     }
-    const int b = bg / a.groups, g = bg - b * a.groups;
-    const float w = param(a.weight, c, a.weight_dtype, 1.f), bias = param(a.bias, c, a.weight_dtype, 0.f);
-    const float post = param(a.post_weight, c, a.weight_dtype, 1.f);
-    const int64_t to = static_cast<int64_t>(bg) * a.channels + c;
-    store_param(a.dshift, to, a.mod_dtype, s[0]);
-    store_param(a.dscale, to, a.mod_dtype, fmaf(w, s[1], bias * s[0]));
-    store_param(a.dgate, to, a.mod_dtype, post * s[2]);
-    const float one = 1.f + param(a.scale.data, b * a.scale.batch + g * a.scale.group + c, a.mod_dtype, 0.f);
-    const float gate = param(a.gate.data, b * a.gate.batch + g * a.gate.group + c, a.mod_dtype, 1.f);
-    if (rows == 1) {
-      store_param(a.dbias, c, a.weight_dtype, one * s[0]);
-      store_param(a.dweight, c, a.weight_dtype, one * s[1]);
-      store_param(a.dpost, c, a.weight_dtype, gate * s[2]);
-    } else if (share) {
-      float* at = share + static_cast<int64_t>(bg) * 3 * a.channels + c;
-      at[0] = one * s[0];
-      at[a.channels] = one * s[1];
-      at[2 * static_cast<int64_t>(a.channels)] = gate * s[2];
-    }
+  }
+#pragma unroll
+  for (int j = 0; j < 3; ++j) sums[j][threadIdx.y][threadIdx.x] = s[j];
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= a.channels) return;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    s[j] = 0.f;
+#pragma unroll
+    for (int y = 0; y < Y; ++y) s[j] += sums[j][y][threadIdx.x];
+  }
+  finish_row(a, bg, c, s);
+  if (a.batch * a.groups == 1) {
+    finish_weights(a, c, s);
+  } else if (share) {
+    float* to = share + static_cast<int64_t>(bg) * 3 * a.channels + c;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) to[static_cast<int64_t>(j) * a.channels] = s[j];
   }
 }
 
-// dbias, dweight, dpost_weight: the modulation rows' shares, likewise.
-__global__ void __launch_bounds__(1024) gate_norm_weights_kernel(const __grid_constant__ Params p, const float* share) {
+// The same for many rows of few units: a thread has a column of FEW_ROWS rows, and leaves one share for them.
+// (A row of 32 columns to a block as above, one unit each: 4082 rows of 1000 channels took 600 us.)
+constexpr int FEW_UNITS = 8, FEW_ROWS = 16;
+__global__ void __launch_bounds__(256) gate_norm_few_kernel(const __grid_constant__ Params p, float* share) {
+  grid_dependency_wait();
+  const GateNormArgs& a = p.a;
+  const int c = blockIdx.y * 256 + threadIdx.x, rows = a.batch * a.groups;
+  if (c >= a.channels) return;
+  float total[3] = {0.f, 0.f, 0.f};
+  const int first = blockIdx.x * FEW_ROWS;
+  for (int bg = first; bg < rows && bg < first + FEW_ROWS; ++bg) {
+    float s[3] = {0.f, 0.f, 0.f};
+    for (int i = 0; i < p.parts; ++i) {
+      const float* from = a.workspace + (static_cast<int64_t>(bg) * p.parts + i) * 3 * a.channels + c;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) s[j] += from[static_cast<int64_t>(j) * a.channels];
+    }
+    finish_row(a, bg, c, s);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) total[j] += s[j];
+  }
+  if (!share) return;
+  float* to = share + static_cast<int64_t>(blockIdx.x) * 3 * a.channels + c;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) to[static_cast<int64_t>(j) * a.channels] = total[j];
+}
+
+// dbias, dweight, dpost_weight: the sums of the shares, likewise.
+__global__ void __launch_bounds__(1024) gate_norm_weights_kernel(const __grid_constant__ Params p, const float* share, int shares) {
   __shared__ float sums[32][33];
   grid_dependency_wait();
   const GateNormArgs& a = p.a;
-  const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y, rows = a.batch * a.groups;
+  const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y;
   float s = 0.f;
-  if (c < a.channels)
-    for (int i = threadIdx.y; i < rows; i += 32) s += share[(static_cast<int64_t>(i) * 3 + j) * a.channels + c];
+  if (c < a.channels) {
+#pragma unroll 4
+    for (int i = threadIdx.y; i < shares; i += 32) s += share[(static_cast<int64_t>(i) * 3 + j) * a.channels + c];
+  }
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || c >= a.channels) return;
@@ -691,37 +750,37 @@ int bwd_regs(int channels) {
 // unit's tokens and what a unit costs besides (`extra` tokens); the least of up to four waves.
 constexpr int FWD_EXTRA = 2, BWD_EXTRA = 4;
 struct Plan {
-  int wpr, warps, per_cta, ctas, parts, chunk, units;  // warps of a token, of a CTA; units of a CTA
-  size_t most;  // units at most, whatever the type
+  int wpr, warps, per_cta;  // warps of a token, of a CTA; teams of a CTA
+  int ctas, parts, chunk, share, units;
 };
 Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int lane_bytes) {
   const int extra = forward ? FWD_EXTRA : BWD_EXTRA;
   Plan q{};
   const int nv = forward ? fwd_vectors(channels) : bwd_vectors(channels);
   q.wpr = (channels + 256 * nv - 1) / (256 * nv);
-  // Tokens of a CTA: as many on an SM as its registers and shared memory hold, in at most 4 CTAs (a CTA
-  // takes 16 of an SM's 64 barriers).
+  const int64_t rows = static_cast<int64_t>(batch) * groups;
+  const int len = tokens / groups;
+  // Teams of a CTA: as many on an SM as its registers and shared memory hold, in at most 4 CTAs (a CTA
+  // takes 16 of an SM's 64 barriers); where a unit is a CTA's, no more than a modulation row's tokens.
   const int warp_regs = (forward ? fwd_regs(nv) : bwd_regs(channels)) * 32;
-  const int narrow = channels <= NARROW_CHANNELS ? 32 / narrow_lanes(channels) : 1;  // tokens of a warp
-  int most = 0, teams = 0;
-  for (int n = 1; n == 1 || n * q.wpr <= CTA_WARPS; ++n) {
+  const int narrow = channels <= NARROW_CHANNELS ? 32 / narrow_lanes(channels) : 1;  // teams of a warp
+  const bool shared = !forward && narrow > 1;                                        // a unit is a CTA's
+  int teams = 0, sm_ctas = 0;
+  for (int n = 1; n == 1 || (n * q.wpr <= CTA_WARPS && (!shared || n * narrow <= len)); ++n) {
     int ctas = 65536 / (warp_regs * q.wpr * n);
     ctas = ctas < 4 ? ctas : 4;
-    most = most > ctas * n ? most : ctas * n;
-    const int room = SM_SMEM / (lane_bytes * 32 * q.wpr * n + STATIC_SMEM);
+    const int bytes = lane_bytes + (shared ? SPARE_BYTES : 0);
+    const int room = SM_SMEM / (bytes * 32 * q.wpr * n + STATIC_SMEM);
     ctas = ctas < room ? ctas : room;
     if (ctas * n > teams) {
       teams = ctas * n;
+      sm_ctas = ctas;
       q.warps = n * q.wpr;
       q.per_cta = n * narrow;
     }
   }
-  teams *= narrow;
-  most *= narrow;
-  const int64_t slots = static_cast<int64_t>(device_sm_count()) * teams;
-  q.most = static_cast<size_t>(device_sm_count()) * most * 4;
-  const int64_t rows = static_cast<int64_t>(batch) * groups;
-  const int len = tokens / groups;
+  // Units that run at once.
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * (shared ? sm_ctas : teams * narrow);
   int64_t best = INT64_MAX;
   for (int w = 1; w <= 4; ++w) {
     int64_t parts = w * slots / rows;
@@ -729,18 +788,27 @@ Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int 
     if (parts > len) parts = len;
     const int64_t chunk = (len + parts - 1) / parts;
     parts = (len + chunk - 1) / chunk;
-    const int64_t waves = (rows * parts + slots - 1) / slots, cost = waves * (chunk + extra);
+    const int64_t share = shared ? (chunk + q.per_cta - 1) / q.per_cta : chunk;
+    const int64_t waves = (rows * parts + slots - 1) / slots, cost = waves * (share + extra);
     if (cost < best) {
       best = cost;
       q.parts = static_cast<int>(parts);
       q.chunk = static_cast<int>(chunk);
+      q.share = static_cast<int>(share);
     }
   }
   q.units = static_cast<int>(rows * q.parts);
-  if (q.most < static_cast<size_t>(rows)) q.most = static_cast<size_t>(rows);
-  const int64_t need = (q.units + q.per_cta - 1) / q.per_cta, grid = slots / q.per_cta;
+  const int64_t per = shared ? 1 : q.per_cta, need = (q.units + per - 1) / per, grid = slots / per;
   q.ctas = static_cast<int>(need < grid ? need : grid);
   return q;
+}
+
+// Units of a backward at most, whatever its types: four waves of what runs at once (four CTAs of at most 8
+// teams to an SM, or of one unit), or a unit to a row.
+size_t most_units(int64_t rows, int channels) {
+  const int wpr = (channels + 256 * bwd_vectors(channels) - 1) / (256 * bwd_vectors(channels));
+  const int64_t at_once = 4LL * device_sm_count() * (channels <= NARROW_CHANNELS || wpr > CTA_WARPS ? 1 : CTA_WARPS / wpr);
+  return static_cast<size_t>(4 * at_once > rows ? 4 * at_once : rows);
 }
 
 bool wants_sums(const GateNormArgs& a) {
@@ -756,6 +824,7 @@ Params params_of(const GateNormArgs& a, const Plan& q) {
   p.parts = q.parts;
   p.chunk = q.chunk;
   p.units = q.units;
+  p.share = q.share;
   p.dim = static_cast<float>(a.channels);
   p.inv_dim = 1.f / p.dim;
   return p;
@@ -775,13 +844,14 @@ cudaError_t launch_main(const Params& p, const Plan& q, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int threads = q.warps * 32;
   return launch_dependent(gate_norm_bwd_kernel<TX, TY, NV, REGS, NARROW, SUMS>, dim3(q.ctas), dim3(threads),
-                          ring_bytes<TX, TY, NV>(threads), stream, p);
+                          ring_bytes<TX, TY, NV>(threads) + (NARROW ? SPARE_BYTES * threads : 0), stream, p);
 }
 
 template <typename TX, typename TY, int NV, int REGS, bool NARROW>
 cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
   const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, false, ring_bytes<TX, TY, NV>(1));
   const Params p = params_of(a, q);
+  if (static_cast<size_t>(q.units) > most_units(static_cast<int64_t>(a.batch) * a.groups, a.channels)) return cudaErrorInvalidValue;
   if (!wants_sums(a)) return launch_main<TX, TY, NV, REGS, NARROW, false>(p, q, stream);
   cudaError_t e = launch_main<TX, TY, NV, REGS, NARROW, true>(p, q, stream);
   if (e != cudaSuccess) return e;
@@ -789,12 +859,17 @@ cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
   float* share = rows > 1 && (a.dpost || a.dweight || a.dbias)
                      ? a.workspace + static_cast<int64_t>(q.units) * 3 * a.channels
                      : nullptr;
-  const dim3 sums_grid(columns, rows < 65535 ? rows : 65535);
-  e = q.parts > 64 ? launch_dependent(gate_norm_sums_kernel<32>, sums_grid, dim3(32, 32), 0, stream, p, share)
-                   : launch_dependent(gate_norm_sums_kernel<8>, sums_grid, dim3(32, 8), 0, stream, p, share);
+  const bool few = rows > 64 && q.parts <= FEW_UNITS;
+  const int shares = few ? (rows + FEW_ROWS - 1) / FEW_ROWS : rows;
+  if (few)  // (more than 65535 rows are of one unit each)
+    e = launch_dependent(gate_norm_few_kernel, dim3(shares, (a.channels + 255) / 256), dim3(256), 0, stream, p, share);
+  else if (q.parts > 64)
+    e = launch_dependent(gate_norm_sums_kernel<32>, dim3(columns, rows), dim3(32, 32), 0, stream, p, share);
+  else
+    e = launch_dependent(gate_norm_sums_kernel<8>, dim3(columns, rows), dim3(32, 8), 0, stream, p, share);
   if (e != cudaSuccess || !share) return e;
   return launch_dependent(gate_norm_weights_kernel, dim3(columns, 3), dim3(32, 32), 0, stream, p,
-                          static_cast<const float*>(share));
+                          static_cast<const float*>(share), shares);
 }
 
 template <typename TX, typename TY>
@@ -820,10 +895,9 @@ cudaError_t launch_typed(const GateNormArgs& a, bool forward, cudaStream_t strea
 
 }  // namespace
 
-size_t gate_norm_bwd_workspace(int batch, int tokens, int channels, int groups) {
-  const Plan q = plan_of(batch, tokens, channels, groups, false, 0);
+size_t gate_norm_bwd_workspace(int batch, int channels, int groups) {
   const size_t rows = static_cast<size_t>(batch) * groups;
-  return align_up((q.most + rows) * 3 * channels * sizeof(float), 256);
+  return align_up((most_units(static_cast<int64_t>(rows), channels) + rows) * 3 * channels * sizeof(float), 256);
 }
 
 cudaError_t launch_gate_norm_fwd(const GateNormArgs& a, cudaStream_t stream) { return launch_typed(a, true, stream); }
