@@ -179,7 +179,7 @@ class Linear(torch.autograd.Function):
     def backward(ctx, dout):
         x, weight, bias, pre = ctx.saved_tensors
         need = ctx.needs_input_grad
-        g = _aligned(dout)
+        g = _flat(dout)
         dx, dw, db = block.vsa_linear_bwd(g, x, weight, bias if need[2] else None, ctx.act, pre,
                                           need_dx=need[0], need_dweight=need[1])
         return dx, dw, db, dout if need[3] else None, None, None
@@ -204,7 +204,7 @@ class Mlp(torch.autograd.Function):
         x, w1, b1, w2, b2, mid, pre = ctx.saved_tensors
         need = ctx.needs_input_grad
         first = need[0] or need[1] or need[2]
-        dz, dw2, db2 = block.vsa_linear_bwd(_aligned(dout), mid, w2, b2 if need[4] else None, x_act=ctx.act,
+        dz, dw2, db2 = block.vsa_linear_bwd(_flat(dout), mid, w2, b2 if need[4] else None, x_act=ctx.act,
                                             x_pre=pre, need_dx=first, need_dweight=need[3])
         dx = dw1 = db1 = None
         if first:
@@ -222,6 +222,18 @@ def _aligned(g):
     if g.stride(-1) == 1 and all(s and s % unit == 0 for s in g.stride()[:-1]):
         return g
     return g.contiguous()
+
+
+def _flat(g):
+    """_aligned, and copied where its rows do not lie at one stride (a gradient with its leading dimensions
+    permuted)."""
+    g = _aligned(g)
+    if not g.is_contiguous():
+        try:
+            g.view(-1, g.shape[-1])
+        except RuntimeError:
+            return g.contiguous()
+    return g
 
 
 def norm_rope(q, k=None, v=None, q_weight=None, k_weight=None, cos=None, sin=None, order=None,

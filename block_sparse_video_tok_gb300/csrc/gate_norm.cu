@@ -811,6 +811,18 @@ size_t most_units(int64_t rows, int channels) {
   return static_cast<size_t>(4 * at_once > rows ? 4 * at_once : rows);
 }
 
+// How the units' sums are joined: by rows (gate_norm_few_kernel) or a row to a block, and the shares of the
+// weights' gradients that leaves.
+bool few_units(int64_t rows, int parts) { return rows > 64 && parts <= FEW_UNITS; }
+int64_t shares_of(int64_t rows, bool few) { return few ? (rows + FEW_ROWS - 1) / FEW_ROWS : rows; }
+// At most: a row to a block are up to 64 rows, or as many as have more than FEW_UNITS units each.
+size_t most_shares(int64_t rows, int channels) {
+  if (rows <= 64) return static_cast<size_t>(rows);
+  const int64_t many = static_cast<int64_t>(most_units(rows, channels)) / FEW_UNITS, blocks = rows < many ? rows : many;
+  const int64_t few = shares_of(rows, true);
+  return static_cast<size_t>(few > blocks ? few : blocks);
+}
+
 bool wants_sums(const GateNormArgs& a) {
   return a.dgate || a.dscale || a.dshift || a.dpost || a.dweight || a.dbias;
 }
@@ -859,8 +871,8 @@ cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
   float* share = rows > 1 && (a.dpost || a.dweight || a.dbias)
                      ? a.workspace + static_cast<int64_t>(q.units) * 3 * a.channels
                      : nullptr;
-  const bool few = rows > 64 && q.parts <= FEW_UNITS;
-  const int shares = few ? (rows + FEW_ROWS - 1) / FEW_ROWS : rows;
+  const bool few = few_units(rows, q.parts);
+  const int shares = static_cast<int>(shares_of(rows, few));
   if (few)  // (more than 65535 rows are of one unit each)
     e = launch_dependent(gate_norm_few_kernel, dim3(shares, (a.channels + 255) / 256), dim3(256), 0, stream, p, share);
   else if (q.parts > 64)
@@ -896,8 +908,8 @@ cudaError_t launch_typed(const GateNormArgs& a, bool forward, cudaStream_t strea
 }  // namespace
 
 size_t gate_norm_bwd_workspace(int batch, int channels, int groups) {
-  const size_t rows = static_cast<size_t>(batch) * groups;
-  return align_up((most_units(static_cast<int64_t>(rows), channels) + rows) * 3 * channels * sizeof(float), 256);
+  const int64_t rows = static_cast<int64_t>(batch) * groups;
+  return align_up((most_units(rows, channels) + most_shares(rows, channels)) * 3 * channels * sizeof(float), 256);
 }
 
 cudaError_t launch_gate_norm_fwd(const GateNormArgs& a, cudaStream_t stream) { return launch_typed(a, true, stream); }

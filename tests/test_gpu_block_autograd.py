@@ -142,7 +142,11 @@ def test_gradient_that_starts_anywhere(autograd, name):
         room = torch.zeros(before + g.numel(), dtype=BF16, device="cuda")
         room[before:] = g.flatten()
         assert same(torch.autograd.grad(f(*ts), ts, room[before:].view(2, 30, 64)), want), before
-    assert same(torch.autograd.grad(f(*ts), ts, g.transpose(1, 2).contiguous().transpose(1, 2)), want)
+    for a, b in ((1, 2), (0, 1)):
+        assert same(torch.autograd.grad(f(*ts), ts, g.transpose(a, b).contiguous().transpose(a, b)), want), (a, b)
+    wide = torch.zeros(2, 30, 72, dtype=BF16, device="cuda")
+    wide[..., 8:] = g
+    assert same(torch.autograd.grad(f(*ts), ts, wide[..., 8:]), want)
     row = randn(64, seed=4)
     assert same(torch.autograd.grad(f(*ts), ts, row.expand(2, 30, 64)),
                 torch.autograd.grad(f(*ts), ts, row.expand(2, 30, 64).contiguous()))
