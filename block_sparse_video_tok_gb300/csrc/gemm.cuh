@@ -30,6 +30,9 @@ size_t gemm_workspace(int m, int n, int k);
 // The same for small products (no workspace), and whether it is the one to use.
 cudaError_t launch_gemm_small(GemmOp op, const GemmArgs& a, cudaStream_t stream);
 bool use_gemm_small(int m, int n, int k);
+// Two of them in one launch, of one type and independent of each other, and whether that is offered.
+cudaError_t launch_gemm_small_pair(GemmOp op_a, const GemmArgs& a, GemmOp op_b, const GemmArgs& b, cudaStream_t stream);
+bool use_gemm_small_pair(const GemmArgs& a, const GemmArgs& b);
 // About what gemm.cu's own kernels take.
 double gemm_microseconds(int m, int n, int k);
 

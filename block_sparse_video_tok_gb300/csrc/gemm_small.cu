@@ -8,8 +8,12 @@
 // their sums in shared memory, and each adds a share of the tile's results over all of them, in rank
 // order, through distributed shared memory.
 //
-// The 128 results of a tile's one side are those of m or of n, whichever fits better (SWAP: of n): few
+// The 128 results of a tile's one side are those of m or of n, whichever fits better (swap: of n): few
 // rows of x meet 128 features.  Either operand comes K-major or MN-major, as in gemm.cu.
+//
+// One launch takes the two products of a backward, dx and dweight, which do not depend on each other: a cluster
+// has tiles of one of them, several where that one's tiles are shared by fewer CTAs.  How a tile is shared
+// does not depend on the company, so neither do its bits.
 #include <type_traits>
 
 #include "act.cuh"
@@ -34,17 +38,26 @@ constexpr uint32_t SMEM_BYTES = SM_BAR + NUM_BARS * 8 + 8 + 1024;  // + alignmen
 constexpr int PITCH = TA + 4;  // of the sums, [64][128 + pad] fp32 where the stages were, theirs and the cluster's
 static_assert(2 * TB * PITCH * 4 <= STAGES * STAGE_BYTES, "room for the sums");
 
-struct Params {
-  int m, n, steps;       // steps of BK along k
-  int share;             // CTAs of a cluster
+struct Job {
+  CUtensorMap map_a, map_b;
+  bool a_mn, b_mn, swap;
+  int m, n, steps;  // steps of BK along k
+  int tiles_m, tiles;
+  int share;        // CTAs of a tile
   const void* bias;
   bool bias_f32;
   int op, act;
   MatrixView out, pre, aux;
+};
+template <int JOBS>
+struct Params {
+  Job job[JOBS];
+  int first;  // clusters of job 0
   uint32_t* err;
   uint64_t wait_ns;
 };
 
+// The four UMMAs of a stage; AS, BS: descriptor steps of 16 elements of k.
 template <int AS, int BS>
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -74,10 +87,11 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void load4_cluster(uint32_t addr, float* v) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr));
 }
-template <typename E, bool A_MN, bool B_MN, bool SWAP>
-__global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_constant__ CUtensorMap tm_a,
-                                                             const __grid_constant__ CUtensorMap tm_b,
-                                                             const __grid_constant__ Params p) {
+// FORM of a lone product: A_MN + 2 B_MN + 4 swap, and its tiles are (y, z).  A pair reads these from its jobs, which
+// costs a lone product up to 1.4 us (64 x 256 -> 256: 5.6 instead of 4.2).
+constexpr int PAIR = 8;
+template <typename E, int FORM>
+__global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_constant__ Params<FORM == PAIR ? 2 : 1> params) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -85,14 +99,29 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + SM_BAR + NUM_BARS * 8 + 4);
   auto bar = [&](uint32_t b) { return base + SM_BAR + 8u * b; };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int rank = blockIdx.x;
-  const int k0 = rank * p.steps / p.share, k1 = (rank + 1) * p.steps / p.share;
-  const int a0 = (SWAP ? blockIdx.z : blockIdx.y) * TA, b0 = (SWAP ? blockIdx.y : blockIdx.z) * TB;
-  const uint64_t limit = p.wait_ns;
+  // Of the cluster's CTAs, `share` in a row have a tile.
+  constexpr bool pair = FORM == PAIR;
+  const int y = blockIdx.y;
+  const bool second = pair && y >= params.first;
+  const Job& p = params.job[second ? 1 : 0];
+  const bool a_mn = pair ? p.a_mn : FORM & 1, b_mn = pair ? p.b_mn : FORM & 2, swap = pair ? p.swap : FORM & 4;
+  const int cluster = pair ? static_cast<int>(gridDim.x) : p.share;
+  const int peer0 = pair ? static_cast<int>(blockIdx.x) / p.share * p.share : 0, rank = static_cast<int>(blockIdx.x) - peer0;
+  int tm = y, tn = blockIdx.z;
+  bool has = true;
+  if (pair) {
+    const int tile = ((second ? y - params.first : y) * cluster + peer0) / p.share;
+    has = tile < p.tiles;
+    tn = tile / p.tiles_m;
+    tm = tile - tn * p.tiles_m;
+  }
+  const int k0 = has ? rank * p.steps / p.share : 0, k1 = has ? (rank + 1) * p.steps / p.share : 0;
+  const int a0 = (swap ? tn : tm) * TA, b0 = (swap ? tm : tn) * TB;
+  const uint64_t limit = params.wait_ns;
 
   if (warp == TMA_WARP && lane == 0) {
-    tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&p.map_a);
+    tma_prefetch_desc(&p.map_b);
     *abort = 0;
     for (uint32_t b = 0; b < NUM_BARS; ++b) mbar_init(bar(b), 1);
     fence_barrier_init();
@@ -103,10 +132,10 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
   }
   grid_dependency_wait();
   // 8 results of a row a thread, at a time: a tile has 1024 such, the CTAs of the cluster write those of
-  // equal shares of its 64 (SWAP: rows m of 16 such; else columns n, 128 rows of 1 to 8).  A thread's
+  // equal shares of its 64 (swap: rows m of 16 such; else columns n, 128 rows of 1 to 8).  A thread's
   // columns stay the same.
-  const int wide = SWAP ? TA / 8 : TB / 8 / p.share;  // such, side by side
-  const int n_first = SWAP ? a0 + threadIdx.x % wide * 8 : b0 + (rank * wide + threadIdx.x % wide) * 8;
+  const int wide = swap ? TA / 8 : TB / 8 / p.share;  // such, side by side
+  const int n_first = !has ? p.n : swap ? a0 + threadIdx.x % wide * 8 : b0 + (rank * wide + threadIdx.x % wide) * 8;
   float bias[8] = {};
   if (p.bias && n_first < p.n) {
     if (p.bias_f32) load8(static_cast<const float*>(p.bias) + n_first, bias);
@@ -127,39 +156,44 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(full, STAGE_BYTES);
-        if (A_MN) {
-          tma_load_2d(to, &tm_a, full, a0, k * BK);
-          tma_load_2d(to + A_BYTES / 2, &tm_a, full, a0 + 64, k * BK);
+        if (a_mn) {
+          tma_load_2d(to, &p.map_a, full, a0, k * BK);
+          tma_load_2d(to + A_BYTES / 2, &p.map_a, full, a0 + 64, k * BK);
         } else {
-          tma_load_2d(to, &tm_a, full, k * BK, a0);
+          tma_load_2d(to, &p.map_a, full, k * BK, a0);
         }
-        if (B_MN) tma_load_2d(to + A_BYTES, &tm_b, full, b0, k * BK);
-        else tma_load_2d(to + A_BYTES, &tm_b, full, k * BK, b0);
+        if (b_mn) tma_load_2d(to + A_BYTES, &p.map_b, full, b0, k * BK);
+        else tma_load_2d(to + A_BYTES, &p.map_b, full, k * BK, b0);
       }
       __syncwarp();
     }
     // No copy is in flight when the CTA ends, also after the issuer has given up.
     if (lane == 0) {
-      if (!ok) raise_abort(abort, p.err);
+      if (!ok) raise_abort(abort, params.err);
       drain_copies(bar(FULL0), STAGES, it);
     }
     __syncwarp();
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------------ UMMA issuer
-    constexpr uint32_t IDESC = idesc_f16_f32acc(TA, TB, A_MN, B_MN, std::is_same<E, __nv_bfloat16>::value);
-    const uint64_t a_desc = sdesc_sw128(base, A_MN ? A_BYTES / 2 : 16, 1024);
-    const uint64_t b_desc = sdesc_sw128(base + A_BYTES, B_MN ? B_BYTES : 16, 1024);
+    const uint32_t idesc = idesc_f16_f32acc(TA, TB, a_mn, b_mn, std::is_same<E, __nv_bfloat16>::value);
+    const uint64_t a_desc = sdesc_sw128(base, a_mn ? A_BYTES / 2 : 16, 1024);
+    const uint64_t b_desc = sdesc_sw128(base + A_BYTES, b_mn ? B_BYTES : 16, 1024);
+    auto stage = [&](uint64_t a, uint64_t b, uint32_t accumulate) {
+      if (a_mn && b_mn) product<128, 128>(tmem, a, b, idesc, accumulate);
+      else if (a_mn) product<128, 2>(tmem, a, b, idesc, accumulate);
+      else if (b_mn) product<2, 128>(tmem, a, b, idesc, accumulate);
+      else product<2, 2>(tmem, a, b, idesc, accumulate);
+    };
     uint32_t it = 0;
     for (int k = k0; k < k1; ++k, ++it) {
       const uint32_t s = it % STAGES;
       ok = warp_wait(bar(FULL0 + s), (it / STAGES) & 1u, abort, limit);
       if (!ok) break;
       tc_fence_after_sync();
-      product<A_MN ? 128 : 2, B_MN ? 128 : 2>(tmem, sdesc_advance(a_desc, s * STAGE_BYTES), sdesc_advance(b_desc, s * STAGE_BYTES),
-                                              IDESC, k > k0 ? 1u : 0u);
+      stage(sdesc_advance(a_desc, s * STAGE_BYTES), sdesc_advance(b_desc, s * STAGE_BYTES), k > k0 ? 1u : 0u);
       umma_commit_elect(bar(EMPTY0 + s));
     }
-    if (!ok && lane == 0) raise_abort(abort, p.err);
+    if (!ok && lane == 0) raise_abort(abort, params.err);
     umma_commit_elect(bar(DONE));
   }
   // Every product is done, and every stage has been read.  (After an abort the sums are not used: the
@@ -167,7 +201,7 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
   ok = warp_wait(bar(DONE), 0, abort, limit) && ok;
   if (!ok) {
     if (lane == 0) {
-      raise_abort(abort, p.err);
+      raise_abort(abort, params.err);
       volatile int never = 0;
       mbar_wait_bounded(bar(DONE), 0, &never, DRAIN_LIMIT_NS);
     }
@@ -187,17 +221,17 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
   }
   tc_fence_before_sync();
   const int mine = TB / p.share, first = rank * mine;  // of the tile's 64
+  if (cluster > 1) cluster_sync();
   if (p.share > 1) {
     // Whole rows of 128 sums, 16 bytes a lane: other patterns are several times slower over the
     // cluster.  All CTAs' loads of a row are on their way before the first is added.
-    cluster_sync();
     const uint32_t at = smem_u32(sums) + lane * 16;
     float* total = sums + TB * PITCH;
     for (int c = first + warp; c < first + mine; c += WARPS) {
       float from[MAX_SHARE][4], z[4] = {};
 #pragma unroll
       for (int r = 0; r < MAX_SHARE; ++r)
-        if (r < p.share) load4_cluster(in_cta(at + c * PITCH * 4, r), from[r]);
+        if (r < p.share) load4_cluster(in_cta(at + c * PITCH * 4, peer0 + r), from[r]);
 #pragma unroll
       for (int r = 0; r < MAX_SHARE; ++r)
         if (r < p.share) {
@@ -207,17 +241,17 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
       *reinterpret_cast<float4*>(total + c * PITCH + lane * 4) = make_float4(z[0], z[1], z[2], z[3]);
     }
     sums = total;
-    // The sums of a CTA stay until they have been read.
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
+  // The sums of a CTA stay until they have been read.
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   __syncthreads();
   constexpr int MOST = TA * TB / 8 / THREADS;
   Raw<E> aux[MOST];
   auto here = [&](int i) { return ok && static_cast<int>(threadIdx.x) + i * THREADS < mine * (TA / 8) && n_first < p.n; };
   auto place = [&](int i, int* m) {  // of the thread's result i: its row, and where its sums are
     const int row = (threadIdx.x + i * THREADS) / wide;
-    *m = SWAP ? b0 + first + row : a0 + row;
-    return SWAP ? (first + row) * PITCH + threadIdx.x % wide * 8 : (first + threadIdx.x % wide * 8) * PITCH + row;
+    *m = swap ? b0 + first + row : a0 + row;
+    return swap ? (first + row) * PITCH + threadIdx.x % wide * 8 : (first + threadIdx.x % wide * 8) * PITCH + row;
   };
 #pragma unroll
   for (int i = 0; i < MOST; ++i) {
@@ -233,7 +267,7 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
     if (!here(i) || m >= p.m) continue;
     float z[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = sums[at + (SWAP ? j : j * PITCH)];
+    for (int j = 0; j < 8; ++j) z[j] = sums[at + (swap ? j : j * PITCH)];
     if (p.op == GEMM_FWD) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[j] += bias[j];
@@ -252,15 +286,15 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
     }
     store8(static_cast<E*>(p.out.data) + m * p.out.stride + n_first, z);
   }
-  if (p.share > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after_sync();
   if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM_COLUMNS);
 }
 
-template <typename E, bool A_MN, bool B_MN, bool SWAP>
-cudaError_t launch_kernel(const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, dim3 grid, cudaStream_t stream) {
+template <typename E, int FORM>
+cudaError_t launch_form(const Params<FORM == PAIR ? 2 : 1>& p, dim3 grid, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = ensure_smem_limit(gemm_small_kernel<E, A_MN, B_MN, SWAP>, static_cast<int>(SMEM_BYTES), smem_set);
+  const cudaError_t e = ensure_smem_limit(gemm_small_kernel<E, FORM>, static_cast<int>(SMEM_BYTES), smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -275,7 +309,19 @@ cudaError_t launch_kernel(const CUtensorMap& ta, const CUtensorMap& tb, const Pa
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_small_kernel<E, A_MN, B_MN, SWAP>, ta, tb, p);
+  return cudaLaunchKernelEx(&cfg, gemm_small_kernel<E, FORM>, p);
+}
+template <typename E>
+cudaError_t launch_typed(const Params<1>& p, dim3 grid, cudaStream_t stream) {
+  const Job& j = p.job[0];
+  switch (j.a_mn + 2 * j.b_mn + 4 * j.swap) {  // forward 0, 4; dx 2, 5; dweight 3, 7
+    case 0: return launch_form<E, 0>(p, grid, stream);
+    case 2: return launch_form<E, 2>(p, grid, stream);
+    case 3: return launch_form<E, 3>(p, grid, stream);
+    case 4: return launch_form<E, 4>(p, grid, stream);
+    case 5: return launch_form<E, 5>(p, grid, stream);
+    default: return launch_form<E, 7>(p, grid, stream);
+  }
 }
 
 // How a product is cut: tiles of 128 along n and 64 along m or the other way round, whichever are
@@ -299,20 +345,31 @@ Plan plan_of(int m, int n, int k) {
   return q;
 }
 
-template <typename E>
-cudaError_t launch_typed(GemmOp op, bool swap, const CUtensorMap& tm, const CUtensorMap& tn, const Params& p, dim3 grid,
-                         cudaStream_t stream) {
-  switch (op) {
-    case GEMM_FWD:
-      return swap ? launch_kernel<E, false, false, true>(tn, tm, p, grid, stream)
-                  : launch_kernel<E, false, false, false>(tm, tn, p, grid, stream);
-    case GEMM_DX:
-      return swap ? launch_kernel<E, true, false, true>(tn, tm, p, grid, stream)
-                  : launch_kernel<E, false, true, false>(tm, tn, p, grid, stream);
-    default:
-      return swap ? launch_kernel<E, true, true, true>(tn, tm, p, grid, stream)
-                  : launch_kernel<E, true, true, false>(tm, tn, p, grid, stream);
-  }
+cudaError_t fill(Job* j, GemmOp op, const GemmArgs& a, const Plan& q) {
+  const bool bf16 = a.dtype == VSA_BF16, m_mn = op == GEMM_DW, n_mn = op != GEMM_FWD;  // operands as stored
+  const int box_m = q.swap ? TB : TA, box_n = q.swap ? TA : TB;
+  CUtensorMap* map_m = q.swap ? &j->map_b : &j->map_a;
+  CUtensorMap* map_n = q.swap ? &j->map_a : &j->map_b;
+  cudaError_t e = m_mn ? make_tmap_matrix(map_m, a.a, a.m, a.k, BK, bf16) : make_tmap_matrix(map_m, a.a, a.k, a.m, box_m, bf16);
+  if (e != cudaSuccess) return e;
+  e = n_mn ? make_tmap_matrix(map_n, a.b, a.n, a.k, BK, bf16) : make_tmap_matrix(map_n, a.b, a.k, a.n, box_n, bf16);
+  j->a_mn = q.swap ? n_mn : m_mn;
+  j->b_mn = q.swap ? m_mn : n_mn;
+  j->swap = q.swap;
+  j->m = a.m;
+  j->n = a.n;
+  j->steps = q.steps;
+  j->tiles_m = (a.m + box_m - 1) / box_m;
+  j->tiles = static_cast<int>(q.tiles);
+  j->share = q.share;
+  j->bias = a.bias;
+  j->bias_f32 = a.bias_f32;
+  j->op = op;
+  j->act = a.act;
+  j->out = a.out;
+  j->pre = a.pre;
+  j->aux = a.aux;
+  return e;
 }
 
 }  // namespace
@@ -333,30 +390,36 @@ bool use_gemm_small(int m, int n, int k) {
 
 cudaError_t launch_gemm_small(GemmOp op, const GemmArgs& a, cudaStream_t stream) {
   const Plan q = plan_of(a.m, a.n, a.k);
-  Params p{};
-  p.m = a.m;
-  p.n = a.n;
-  p.steps = q.steps;
-  p.share = q.share;
-  p.bias = a.bias;
-  p.bias_f32 = a.bias_f32;
-  p.op = op;
-  p.act = a.act;
-  p.out = a.out;
-  p.pre = a.pre;
-  p.aux = a.aux;
+  Params<1> p{};
+  const cudaError_t e = fill(&p.job[0], op, a, q);
+  if (e != cudaSuccess) return e;
+  p.first = static_cast<int>(q.tiles);
   p.err = a.err;
   p.wait_ns = a.wait_ns;
-  const bool bf16 = a.dtype == VSA_BF16;
-  const int box_m = q.swap ? TB : TA, box_n = q.swap ? TA : TB;
-  CUtensorMap tm, tn;
-  cudaError_t e = op == GEMM_DW ? make_tmap_matrix(&tm, a.a, a.m, a.k, BK, bf16) : make_tmap_matrix(&tm, a.a, a.k, a.m, box_m, bf16);
+  const dim3 grid(q.share, p.job[0].tiles_m, p.job[0].tiles / p.job[0].tiles_m);
+  return a.dtype == VSA_BF16 ? launch_typed<__nv_bfloat16>(p, grid, stream) : launch_typed<__half>(p, grid, stream);
+}
+
+// Where the CTAs of both fit on the GPU at once (us on the GPU, in one launch and in two: 64 x 256 -> 256 5.0 and 6.9,
+// 512 x 512 -> 512 6.7 and 11.1, 1021 x 1000 -> 264 9.2 and 12.5; with 480 CTAs, 256 x 1536 -> 1536, 13.6 and 12.5).
+bool use_gemm_small_pair(const GemmArgs& a, const GemmArgs& b) {
+  if (!use_gemm_small(a.m, a.n, a.k) || !use_gemm_small(b.m, b.n, b.k)) return false;
+  const Plan q = plan_of(a.m, a.n, a.k), r = plan_of(b.m, b.n, b.k);
+  return q.tiles * q.share + r.tiles * r.share <= 2 * device_sm_count();
+}
+
+cudaError_t launch_gemm_small_pair(GemmOp op_a, const GemmArgs& a, GemmOp op_b, const GemmArgs& b, cudaStream_t stream) {
+  const Plan q = plan_of(a.m, a.n, a.k), r = plan_of(b.m, b.n, b.k);
+  Params<2> p{};
+  cudaError_t e = fill(&p.job[0], op_a, a, q);
+  if (e == cudaSuccess) e = fill(&p.job[1], op_b, b, r);
   if (e != cudaSuccess) return e;
-  e = op == GEMM_FWD ? make_tmap_matrix(&tn, a.b, a.k, a.n, box_n, bf16) : make_tmap_matrix(&tn, a.b, a.n, a.k, BK, bf16);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(q.share, static_cast<unsigned>((a.m + box_m - 1) / box_m), static_cast<unsigned>((a.n + box_n - 1) / box_n));
-  return bf16 ? launch_typed<__nv_bfloat16>(op, q.swap, tm, tn, p, grid, stream)
-              : launch_typed<__half>(op, q.swap, tm, tn, p, grid, stream);
+  const int cluster = q.share > r.share ? q.share : r.share;
+  p.first = static_cast<int>((q.tiles * q.share + cluster - 1) / cluster);
+  p.err = a.err;
+  p.wait_ns = a.wait_ns;
+  const dim3 grid(cluster, static_cast<unsigned>(p.first + (r.tiles * r.share + cluster - 1) / cluster));
+  return a.dtype == VSA_BF16 ? launch_form<__nv_bfloat16, PAIR>(p, grid, stream) : launch_form<__half, PAIR>(p, grid, stream);
 }
 
 }  // namespace vsa

@@ -158,22 +158,22 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t stream) {
   g.workspace = a.workspace + l.gemm;
   g.err = a.err;
   g.wait_ns = a.wait_ns;
+  GemmArgs w = g;
   if (a.dx.data) {
     g.b = a.weight;
     g.out = a.dx;
     g.aux = a.x_pre;
     g.act = a.x_act;
     g.m = a.rows, g.n = a.in, g.k = a.out_features;
-    if ((e = launch_gemm(GEMM_DX, g, stream)) != cudaSuccess) return e;
   }
   if (a.dweight.data) {
-    g.b = a.x;
-    g.out = a.dweight;
-    g.aux = MatrixView{};
-    g.m = a.out_features, g.n = a.in, g.k = a.rows;
-    e = launch_gemm(GEMM_DW, g, stream);
+    w.b = a.x;
+    w.out = a.dweight;
+    w.m = a.out_features, w.n = a.in, w.k = a.rows;
   }
-  return e;
+  if (a.dx.data && a.dweight.data && use_gemm_small_pair(g, w)) return launch_gemm_small_pair(GEMM_DX, g, GEMM_DW, w, stream);
+  if (a.dx.data && (e = launch_gemm(GEMM_DX, g, stream)) != cudaSuccess) return e;
+  return a.dweight.data ? launch_gemm(GEMM_DW, w, stream) : cudaSuccess;
 }
 
 }  // namespace vsa

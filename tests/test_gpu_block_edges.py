@@ -171,3 +171,25 @@ def test_the_current_device_is_the_tensors(block):
     x = torch.zeros(1, 4, 64, dtype=BF16, device="cuda:1")
     with pytest.raises(ValueError):
         block.vsa_gate_norm(x)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("size", [(1, 8, 8), (64, 64, 64), (40, 256, 256), (17, 1000, 264), (300, 1000, 264),
+                                  (1021, 1000, 264), (2000, 64, 136), (20, 64, 2048), (20, 2048, 64), (512, 1024, 512),
+                                  (4096, 64, 64), (256, 1536, 1536)], ids=str)
+def test_linear_bwd_alone_and_together(block, size, dtype):
+    # Both gradients may come from one launch whose tiles are shared by different numbers of CTAs: the bits
+    # are those of each gradient asked for alone.
+    M, K, N = size
+    dout, x, w = randn(M, N, dtype=dtype, seed=1), randn(M, K, dtype=dtype, seed=2), randn(N, K, dtype=dtype, seed=3, scale=K ** -0.5)
+    x_pre = randn(M, K, dtype=dtype, seed=4)
+    for more in ({}, {"x_act": "silu", "x_pre": x_pre}):
+        dx, dw, _ = block.vsa_linear_bwd(dout, x, w, **more)
+        alone_x = block.vsa_linear_bwd(dout, x, w, need_dweight=False, **more)[0]
+        alone_w = block.vsa_linear_bwd(dout, x, w, need_dx=False)[1]
+        assert same_bits((dx, dw), (alone_x, alone_w))
+        want = dout.double().t() @ x.double()
+        err = (dw.double() - want).abs().max() / want.abs().max().clamp(min=1e-6)
+        # One rounding, and M sums in fp32 of products that are exact there, relative to the largest of them all.
+        big = (dout.double().abs().t() @ x.double().abs()).max() / want.abs().max().clamp(min=1e-6)
+        assert err <= torch.finfo(dtype).eps / 2 + big * M * 2.0 ** -24
