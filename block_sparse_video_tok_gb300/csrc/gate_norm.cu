@@ -683,17 +683,66 @@ __global__ void __launch_bounds__(32 * Y) gate_norm_sums_kernel(const __grid_con
   }
 }
 
-// The same for many rows of few units: a thread has a column of FEW_ROWS rows, and leaves one share for them.
-// (A row of 32 columns to a block as above, one unit each: 4082 rows of 1000 channels took 600 us.)
-constexpr int FEW_UNITS = 8, FEW_ROWS = 16;
-__global__ void __launch_bounds__(256) gate_norm_few_kernel(const __grid_constant__ Params p, float* share) {
+// Both in one launch, of few rows: a block has X columns of all rows, the units of a row are strided over its
+// equal part of the block's 1024 / X slots.  X: as many as make up to 256 blocks (8 columns are a sector of
+// each unit's sums; 2 x 1000 tokens of 8192 channels 75 us with 8, 60 with 32, 68 in two launches).  Taken
+// where the weights' gradients are wanted (a backward of 64 x 128 tokens of 1536 37 us, in two launches 42;
+// 2 x 13 frames of 157 tokens of 1000 18.2 and 17.6, called 59 and 62), and without them where a row to a
+// block makes more than ten blocks to an SM (64 x 128 of 1536 36 and 39, but 26 rows of 1000 17.4 and 15.4).
+template <int X>
+__global__ void __launch_bounds__(1024) gate_norm_join_kernel(const __grid_constant__ Params p) {
+  constexpr int SLOTS = 1024 / X;
+  __shared__ float sums[3][SLOTS][X];
+  __shared__ float shares[3][SLOTS][X];
+  grid_dependency_wait();
+  const GateNormArgs& a = p.a;
+  const int rows = a.batch * a.groups, each = SLOTS / rows;  // slots of a row
+  const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * X + x, bg = y / each;
+  float s[3] = {0.f, 0.f, 0.f};
+  if (bg < rows && c < a.channels) {
+#pragma unroll 4
+    for (int i = y - bg * each; i < p.parts; i += each) {
+      const float* from = a.workspace + (static_cast<int64_t>(bg) * p.parts + i) * 3 * a.channels + c;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) s[j] += from[static_cast<int64_t>(j) * a.channels];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 3; ++j) sums[j][y][x] = s[j];
+  __syncthreads();
+  if (y < rows && c < a.channels) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      s[j] = 0.f;
+      for (int i = 0; i < each; ++i) s[j] += sums[j][y * each + i][x];
+    }
+    finish_row(a, y, c, s);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) shares[j][y][x] = s[j];
+  }
+  __syncthreads();
+  if (y != 0 || c >= a.channels) return;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    s[j] = 0.f;
+    for (int i = 0; i < rows; ++i) s[j] += shares[j][i][x];
+  }
+  finish_weights(a, c, s);
+}
+
+// The same for many rows of few units: a thread has a column of few_rows rows, as many as let all threads run
+// at once, and leaves one share for them.  (A row of 32 columns to a block as above, one unit each: 4082 rows
+// of 1000 channels took 600 us.  16 rows a thread, whatever their number: 150 rows of 40 tokens of 1536 55 us,
+// now 27; 600 of 16 65, now 46.)
+constexpr int FEW_UNITS = 8, FEW_ROWS = 16;  // at most
+__global__ void __launch_bounds__(256) gate_norm_few_kernel(const __grid_constant__ Params p, float* share, int few_rows) {
   grid_dependency_wait();
   const GateNormArgs& a = p.a;
   const int c = blockIdx.y * 256 + threadIdx.x, rows = a.batch * a.groups;
   if (c >= a.channels) return;
   float total[3] = {0.f, 0.f, 0.f};
-  const int first = blockIdx.x * FEW_ROWS;
-  for (int bg = first; bg < rows && bg < first + FEW_ROWS; ++bg) {
+  const int first = blockIdx.x * few_rows;
+  for (int bg = first; bg < rows && bg < first + few_rows; ++bg) {
     float s[3] = {0.f, 0.f, 0.f};
     for (int i = 0; i < p.parts; ++i) {
       const float* from = a.workspace + (static_cast<int64_t>(bg) * p.parts + i) * 3 * a.channels + c;
@@ -814,12 +863,19 @@ size_t most_units(int64_t rows, int channels) {
 // How the units' sums are joined: by rows (gate_norm_few_kernel) or a row to a block, and the shares of the
 // weights' gradients that leaves.
 bool few_units(int64_t rows, int parts) { return rows > 64 && parts <= FEW_UNITS; }
-int64_t shares_of(int64_t rows, bool few) { return few ? (rows + FEW_ROWS - 1) / FEW_ROWS : rows; }
+int few_rows(int64_t rows, int channels) {
+  const int64_t at_once = 2048LL * device_sm_count(), fill = (rows * channels + at_once - 1) / at_once;
+  return static_cast<int>(fill < 1 ? 1 : fill < FEW_ROWS ? fill : FEW_ROWS);
+}
+int64_t shares_of(int64_t rows, int channels, bool few) {
+  const int each = few ? few_rows(rows, channels) : 1;
+  return (rows + each - 1) / each;
+}
 // At most: a row to a block are up to 64 rows, or as many as have more than FEW_UNITS units each.
 size_t most_shares(int64_t rows, int channels) {
   if (rows <= 64) return static_cast<size_t>(rows);
   const int64_t many = static_cast<int64_t>(most_units(rows, channels)) / FEW_UNITS, blocks = rows < many ? rows : many;
-  const int64_t few = shares_of(rows, true);
+  const int64_t few = shares_of(rows, channels, true);
   return static_cast<size_t>(few > blocks ? few : blocks);
 }
 
@@ -859,6 +915,11 @@ cudaError_t launch_main(const Params& p, const Plan& q, cudaStream_t stream) {
                           ring_bytes<TX, TY, NV>(threads) + (NARROW ? SPARE_BYTES * threads : 0), stream, p);
 }
 
+template <int X>
+cudaError_t launch_join(const Params& p, cudaStream_t stream) {
+  return launch_dependent(gate_norm_join_kernel<X>, dim3((p.a.channels + X - 1) / X), dim3(X, 1024 / X), 0, stream, p);
+}
+
 template <typename TX, typename TY, int NV, int REGS, bool NARROW>
 cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
   const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, false, ring_bytes<TX, TY, NV>(1));
@@ -871,10 +932,15 @@ cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
   float* share = rows > 1 && (a.dpost || a.dweight || a.dbias)
                      ? a.workspace + static_cast<int64_t>(q.units) * 3 * a.channels
                      : nullptr;
+  if (share || static_cast<int64_t>(rows) * columns > 10 * device_sm_count()) {
+    const int x = a.channels <= 8 * 256 ? 8 : a.channels <= 16 * 256 ? 16 : 32;
+    if (rows <= 1024 / x) return x == 8 ? launch_join<8>(p, stream) : x == 16 ? launch_join<16>(p, stream) : launch_join<32>(p, stream);
+  }
   const bool few = few_units(rows, q.parts);
-  const int shares = static_cast<int>(shares_of(rows, few));
+  const int shares = static_cast<int>(shares_of(rows, a.channels, few));
   if (few)  // (more than 65535 rows are of one unit each)
-    e = launch_dependent(gate_norm_few_kernel, dim3(shares, (a.channels + 255) / 256), dim3(256), 0, stream, p, share);
+    e = launch_dependent(gate_norm_few_kernel, dim3(shares, (a.channels + 255) / 256), dim3(256), 0, stream, p, share,
+                         few_rows(rows, a.channels));
   else if (q.parts > 64)
     e = launch_dependent(gate_norm_sums_kernel<32>, dim3(columns, rows), dim3(32, 32), 0, stream, p, share);
   else

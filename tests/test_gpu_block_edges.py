@@ -193,3 +193,24 @@ def test_linear_bwd_alone_and_together(block, size, dtype):
         # One rounding, and M sums in fp32 of products that are exact there, relative to the largest of them all.
         big = (dout.double().abs().t() @ x.double().abs()).max() / want.abs().max().clamp(min=1e-6)
         assert err <= torch.finfo(dtype).eps / 2 + big * M * 2.0 ** -24
+
+
+@pytest.mark.parametrize("weights", [True, False])
+@pytest.mark.parametrize("case", [(2, 1, 1000, 400), (1, 2, 8, 64), (32, 1, 4104, 9), (33, 1, 4104, 9), (8, 8, 2056, 32),
+                                  (65, 1, 2056, 5), (64, 2, 264, 34), (3, 43, 264, 86), (43, 1, 64, 3000), (7, 23, 1536, 69),
+                                  (300, 1, 1536, 20), (1100, 1, 128, 3), (129, 1, 256, 130)], ids=str)
+def test_gate_norm_bwd_rows(block, case, weights):
+    # The joins of the units' sums are chosen by the number of modulation rows, of channels and of units.
+    B, G, C, S = case
+    x, y, dh = (randn(B, S, C, seed=i) for i in range(3))
+    mods = [randn(*((B, C) if G == 1 else (B, G, C)), seed=10 + i, scale=0.4) for i in range(3)]
+    w, b = (randn(C, dtype=FP32, seed=20), randn(C, dtype=FP32, seed=21)) if weights else (None, None)
+    args = (y, mods[0], None, w, b, mods[1], mods[2])
+    got = block.vsa_gate_norm_bwd(dh, None, x, *args)
+    want = ref.gate_norm_bwd(dh, None, x, *args, "layer", 1e-6, 1e-6)
+    for n, g, v in zip(("dx", "dy", "dgate", "dpost_weight", "dweight", "dbias", "dscale", "dshift"), got, want):
+        assert (g is None) == (v is None), n
+        if g is not None:
+            ref.check(n, g, *v)
+    again = block.vsa_gate_norm_bwd(dh, None, x, *args)
+    assert same_bits([g for g in got if g is not None], [g for g in again if g is not None])
