@@ -47,18 +47,35 @@ constexpr int FWD_ROWS = 2;   // tokens in flight per group of warps
 constexpr int fwd_regs(int nv) { return nv == 1 ? 80 : 112; }
 constexpr int BWD_REGS_1 = 96, BWD_REGS_2 = 168, BWD_REGS_4 = 255;
 
-// 8 parameters of either type, or `fallback`.
-__device__ __forceinline__ void load_param(const void* p, int64_t at, int dtype, float fallback, float* v) {
-  if (!p) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fallback;
-  } else if (dtype == VSA_F32) {
-    load8(static_cast<const float*>(p) + at, v);
-  } else if (dtype == VSA_BF16) {
-    load8(static_cast<const __nv_bfloat16*>(p) + at, v);
-  } else {
-    load8(static_cast<const __half*>(p) + at, v);
+// 8 parameters of either type, or `fallback`.  In two steps, so that both modulations' loads of the backward are
+// under way before the first is used (a modulation of every token, above: 139 us, one after the other 160).  The
+// forward has no registers for that (16384 tokens of 1024 channels: 27 us instead of 24.5).
+struct Param8 {
+  Raw<float> r;
+
+  __device__ __forceinline__ void load(const void* p, int64_t at, int dtype) {
+    r.zero();
+    if (!p) return;
+    if (dtype == VSA_F32) r.load(static_cast<const float*>(p) + at);
+    else r.u[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
   }
+  __device__ __forceinline__ void widen(const void* p, int dtype, float fallback, float* v) const {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fallback;
+    } else if (dtype == VSA_F32) {
+      r.widen(v);
+    } else if (dtype == VSA_BF16) {
+      Raw<__nv_bfloat16>{r.u[0]}.widen(v);
+    } else {
+      Raw<__half>{r.u[0]}.widen(v);
+    }
+  }
+};
+__device__ __forceinline__ void load_param(const void* p, int64_t at, int dtype, float fallback, float* v) {
+  Param8 x;
+  x.load(p, at, dtype);
+  x.widen(p, dtype, fallback, v);
 }
 
 __device__ __forceinline__ float param(const void* p, int64_t at, int dtype, float fallback) {
@@ -73,6 +90,13 @@ __device__ __forceinline__ void store_param(void* p, int64_t at, int dtype, floa
   if (dtype == VSA_F32) static_cast<float*>(p)[at] = v;
   else if (dtype == VSA_BF16) static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
   else static_cast<__half*>(p)[at] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ void store_params(void* p, int64_t at, int dtype, const float* v) {
+  if (!p) return;
+  if (dtype == VSA_F32) store8(static_cast<float*>(p) + at, v);
+  else if (dtype == VSA_BF16) store8(static_cast<__nv_bfloat16*>(p) + at, v);
+  else store8(static_cast<__half*>(p) + at, v);
 }
 
 struct Params {
@@ -194,6 +218,9 @@ __device__ __forceinline__ T* at(const TokensView& v, int b, int t) {
 template <typename TX, typename TY, int NV, bool NARROW>
 __global__ void __maxnreg__(fwd_regs(NV)) gate_norm_fwd_kernel(const __grid_constant__ Params p) {
   constexpr int R = NV == 1 ? FWD_ROWS : 1;
+  // A unit's first tokens before its parameters (a modulation of each of 16384 tokens of 1536 channels: 110 us,
+  // after them 120); an fp32 stream has no registers for that (777 tokens of 1024: 5.1 us, after them 4.7).
+  constexpr bool EARLY = sizeof(TX) == 2;
   __shared__ float sums[CTA_WARPS][2][4][MAX_WPR];
   grid_dependency_wait();
   const GateNormArgs& a = p.a;
@@ -207,6 +234,23 @@ __global__ void __maxnreg__(fwd_regs(NV)) gate_norm_fwd_kernel(const __grid_cons
     const int u = NARROW ? u0 + team.lane / team.width : u0;
     Unit unit = unit_of(p, NARROW ? min(u, p.units - 1) : u);
     if (NARROW && u >= p.units) unit.t1 = unit.t0;
+    Raw<TX> rx[R][NV];
+    Raw<TY> ry[R][NV];
+    auto load = [&](int t) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const int e = e0 + k * step;
+          rx[r][k].zero();
+          ry[r][k].zero();
+          if (t + r < unit.t1 && e < a.channels) {
+            rx[r][k].load(at<const TX>(a.x, unit.b, t + r) + e);
+            if (branch) ry[r][k].load(at<const TY>(a.y, unit.b, t + r) + e);
+          }
+        }
+    };
+    if (EARLY) load(unit.t0);
     float ca[NV][8], cc[NV][8], cg[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -226,23 +270,7 @@ __global__ void __maxnreg__(fwd_regs(NV)) gate_norm_fwd_kernel(const __grid_cons
         cg[k][i] *= w[i];
       }
     }
-    Raw<TX> rx[R][NV];
-    Raw<TY> ry[R][NV];
-    auto load = [&](int t) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-          const int e = e0 + k * step;
-          rx[r][k].zero();
-          ry[r][k].zero();
-          if (t + r < unit.t1 && e < a.channels) {
-            rx[r][k].load(at<const TX>(a.x, unit.b, t + r) + e);
-            if (branch) ry[r][k].load(at<const TY>(a.y, unit.b, t + r) + e);
-          }
-        }
-    };
-    load(unit.t0);
+    if (!EARLY) load(unit.t0);
     for (int t = unit.t0, i = 0; NARROW ? i < p.chunk : t < unit.t1; t += R, i += R) {
       float v[R][NV][8], s[R];
       float inv[R];
@@ -417,10 +445,13 @@ constexpr int SM_SMEM = 228 * 1024, CTA_SMEM = 227 * 1024, STATIC_SMEM = CTA_WAR
 
 // One round of sums a token: those of the token itself around its mean, and the mean of the next one.
 // A post norm takes a second round.  The inputs come SLOTS - 1 tokens ahead through shared memory: in
-// registers beside the three sums there is room for one.  SUMS: the unit's S1, S2, S3 go to the
-// workspace.  NARROW: a unit is a CTA's and shared out to its many teams, whose sums are added before they
-// leave (65520 x 64: 19 us, a unit to a team 46; with more channels 1 to 2 % slower).
-template <typename TX, typename TY, int NV, int REGS, bool NARROW, bool SUMS>
+// registers beside the three sums there is room for one.  SUMS: the unit's S1, S2, S3 go to the workspace,
+// or, where it is the whole of a modulation row, to the row's gradients (a modulation of each of 16384
+// tokens of 1536 channels: 139 us, through the workspace 361; both ways in one kernel cost the others 4 %).
+// NARROW: a unit is a CTA's and shared out to its many teams, whose sums are added before they leave (65520 x 64:
+// 19 us, a unit to a team 46; with more channels 1 to 2 % slower).
+enum Sums { NO_SUMS, WORKSPACE, FINISH };
+template <typename TX, typename TY, int NV, int REGS, bool NARROW, Sums SUMS>
 __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ Params p) {
   constexpr int SLOTS = slots_of<TX, NV>();
   constexpr bool DIRECT = o_direct<TX, TY, NV>();
@@ -479,12 +510,15 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
 #pragma unroll
       for (int i = 0; i < 4; ++i) ca[k][i] = cg[k][i] = 0;
       if (k >= vectors) continue;
+      Param8 scale, gate;
+      scale.load(a.scale.data, unit.b * a.scale.batch + unit.g * a.scale.group + e, a.mod_dtype);
+      gate.load(a.gate.data, unit.b * a.gate.batch + unit.g * a.gate.group + e, a.mod_dtype);
       float w[8], s[8];
       load_param(a.weight, e, a.weight_dtype, 1.f, w);
-      load_param(a.scale.data, unit.b * a.scale.batch + unit.g * a.scale.group + e, a.mod_dtype, 0.f, s);
+      scale.widen(a.scale.data, a.mod_dtype, 0.f, s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) ca[k][i] = f2_pack(w[2 * i] * (1.f + s[2 * i]), w[2 * i + 1] * (1.f + s[2 * i + 1]));
-      load_param(a.gate.data, unit.b * a.gate.batch + unit.g * a.gate.group + e, a.mod_dtype, 1.f, w);
+      gate.widen(a.gate.data, a.mod_dtype, 1.f, w);
       load_param(a.post_weight, e, a.weight_dtype, 1.f, s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) cg[k][i] = f2_pack(w[2 * i] * s[2 * i], w[2 * i + 1] * s[2 * i + 1]);
@@ -595,6 +629,30 @@ __global__ void __maxnreg__(REGS) gate_norm_bwd_kernel(const __grid_constant__ P
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           if (k >= vectors) continue;
+          if (SUMS == FINISH) {  // as finish_row
+            const int e = e0 + k * step;
+            const int64_t to = static_cast<int64_t>(unit.bg) * a.channels + e;
+            float v[8], s[8], c[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_unpack(acc[SUMS ? k : 0][0][i], s[2 * i], s[2 * i + 1]);
+            store_params(a.dshift, to, a.mod_dtype, s);
+            load_param(a.bias, e, a.weight_dtype, 0.f, c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] *= c[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_unpack(acc[SUMS ? k : 0][1][i], v[2 * i], v[2 * i + 1]);
+            load_param(a.weight, e, a.weight_dtype, 1.f, c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = fmaf(c[i], v[i], s[i]);
+            store_params(a.dscale, to, a.mod_dtype, s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_unpack(acc[SUMS ? k : 0][2][i], v[2 * i], v[2 * i + 1]);
+            load_param(a.post_weight, e, a.weight_dtype, 1.f, c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= c[i];
+            store_params(a.dgate, to, a.mod_dtype, v);
+            continue;
+          }
 #pragma unroll
           for (int j = 0; j < 3; ++j) {
             float w[8];
@@ -802,7 +860,7 @@ struct Plan {
   int wpr, warps, per_cta;  // warps of a token, of a CTA; teams of a CTA
   int ctas, parts, chunk, share, units;
 };
-Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int lane_bytes) {
+Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int lane_bytes, bool narrowed) {
   const int extra = forward ? FWD_EXTRA : BWD_EXTRA;
   Plan q{};
   const int nv = forward ? fwd_vectors(channels) : bwd_vectors(channels);
@@ -812,7 +870,7 @@ Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int 
   // Teams of a CTA: as many on an SM as its registers and shared memory hold, in at most 4 CTAs (a CTA
   // takes 16 of an SM's 64 barriers); where a unit is a CTA's, no more than a modulation row's tokens.
   const int warp_regs = (forward ? fwd_regs(nv) : bwd_regs(channels)) * 32;
-  const int narrow = channels <= NARROW_CHANNELS ? 32 / narrow_lanes(channels) : 1;  // teams of a warp
+  const int narrow = narrowed ? 32 / narrow_lanes(channels) : 1;  // teams of a warp
   const bool shared = !forward && narrow > 1;                                        // a unit is a CTA's
   int teams = 0, sm_ctas = 0;
   for (int n = 1; n == 1 || (n * q.wpr <= CTA_WARPS && (!shared || n * narrow <= len)); ++n) {
@@ -835,6 +893,7 @@ Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int 
     int64_t parts = w * slots / rows;
     if (parts < 1) parts = 1;
     if (parts > len) parts = len;
+    if (channels <= NARROW_CHANNELS && !narrowed) parts = 1;
     const int64_t chunk = (len + parts - 1) / parts;
     parts = (len + chunk - 1) / chunk;
     const int64_t share = shared ? (chunk + q.per_cta - 1) / q.per_cta : chunk;
@@ -900,12 +959,12 @@ Params params_of(const GateNormArgs& a, const Plan& q) {
 
 template <typename TX, typename TY, int NV, bool NARROW>
 cudaError_t launch_fwd(const GateNormArgs& a, cudaStream_t stream) {
-  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, true, 0);
+  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, true, 0, NARROW);
   return launch_dependent(gate_norm_fwd_kernel<TX, TY, NV, NARROW>, dim3(q.ctas), dim3(q.warps * 32), 0, stream,
                           params_of(a, q));
 }
 
-template <typename TX, typename TY, int NV, int REGS, bool NARROW, bool SUMS>
+template <typename TX, typename TY, int NV, int REGS, bool NARROW, Sums SUMS>
 cudaError_t launch_main(const Params& p, const Plan& q, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
   const cudaError_t e = ensure_smem_limit(gate_norm_bwd_kernel<TX, TY, NV, REGS, NARROW, SUMS>, CTA_SMEM - STATIC_SMEM, smem_set);
@@ -922,19 +981,26 @@ cudaError_t launch_join(const Params& p, cudaStream_t stream) {
 
 template <typename TX, typename TY, int NV, int REGS, bool NARROW>
 cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
-  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, false, ring_bytes<TX, TY, NV>(1));
+  const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, false, ring_bytes<TX, TY, NV>(1), NARROW);
   const Params p = params_of(a, q);
+  const bool weights = a.dpost || a.dweight || a.dbias;
   if (static_cast<size_t>(q.units) > most_units(static_cast<int64_t>(a.batch) * a.groups, a.channels)) return cudaErrorInvalidValue;
-  if (!wants_sums(a)) return launch_main<TX, TY, NV, REGS, NARROW, false>(p, q, stream);
-  cudaError_t e = launch_main<TX, TY, NV, REGS, NARROW, true>(p, q, stream);
+  if (!wants_sums(a)) return launch_main<TX, TY, NV, REGS, NARROW, NO_SUMS>(p, q, stream);
+  const auto ends = reinterpret_cast<uintptr_t>(a.dgate) | reinterpret_cast<uintptr_t>(a.dscale) |
+                    reinterpret_cast<uintptr_t>(a.dshift);
+  if constexpr (!NARROW)
+    if (q.parts == 1 && !weights && !(ends & 15))
+      return launch_main<TX, TY, NV, REGS, NARROW, FINISH>(p, q, stream);
+  cudaError_t e = launch_main<TX, TY, NV, REGS, NARROW, WORKSPACE>(p, q, stream);
   if (e != cudaSuccess) return e;
   const int rows = a.batch * a.groups, columns = (a.channels + 31) / 32;
-  float* share = rows > 1 && (a.dpost || a.dweight || a.dbias)
+  float* share = rows > 1 && weights
                      ? a.workspace + static_cast<int64_t>(q.units) * 3 * a.channels
                      : nullptr;
   if (share || static_cast<int64_t>(rows) * columns > 10 * device_sm_count()) {
     const int x = a.channels <= 8 * 256 ? 8 : a.channels <= 16 * 256 ? 16 : 32;
-    if (rows <= 1024 / x) return x == 8 ? launch_join<8>(p, stream) : x == 16 ? launch_join<16>(p, stream) : launch_join<32>(p, stream);
+    if (rows <= 1024 / x)
+      return x == 8 ? launch_join<8>(p, stream) : x == 16 ? launch_join<16>(p, stream) : launch_join<32>(p, stream);
   }
   const bool few = few_units(rows, q.parts);
   const int shares = static_cast<int>(shares_of(rows, a.channels, few));
@@ -950,9 +1016,13 @@ cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
                           static_cast<const float*>(share), shares);
 }
 
+// Up to 128 channels, rows too short for the teams of a CTA: the backward has a warp to a token and a unit to a row
+// (128 channels, 20000 rows of one token 140 us, now 35; 5000 of 4 33 and 17; 2500 of 8 19.5 either way).
+bool short_rows(const GateNormArgs& a) { return a.tokens / a.groups < 8; }
+
 template <typename TX, typename TY>
 cudaError_t launch_width(const GateNormArgs& a, bool forward, cudaStream_t stream) {
-  if (a.channels <= NARROW_CHANNELS)
+  if (a.channels <= NARROW_CHANNELS && (forward || !short_rows(a)))
     return forward ? launch_fwd<TX, TY, 1, true>(a, stream) : launch_bwd<TX, TY, 1, BWD_REGS_1, true>(a, stream);
   if (forward)
     return fwd_vectors(a.channels) == 1 ? launch_fwd<TX, TY, 1, false>(a, stream) : launch_fwd<TX, TY, 2, false>(a, stream);

@@ -214,3 +214,28 @@ def test_gate_norm_bwd_rows(block, case, weights):
             ref.check(n, g, *v)
     again = block.vsa_gate_norm_bwd(dh, None, x, *args)
     assert same_bits([g for g in got if g is not None], [g for g in again if g is not None])
+
+
+@pytest.mark.parametrize("mod", [BF16, FP32])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("case", [(1, 500, 1536, 500), (2, 700, 4104, 700), (1, 1300, 1024, 2600), (1, 3000, 64, 3000),
+                                  (2, 900, 128, 6300), (1, 600, 128, 4800), (3, 1, 8, 1), (1, 1001, 6152, 1001),
+                                  (1, 400, 2056, 800)], ids=str)
+def test_gate_norm_modulations_of_few_tokens(block, case, kind, mod):
+    # A modulation row that one unit covers: its sums become its gradients without the workspace.
+    B, G, C, S = case
+    x, y, dh = (randn(B, S, C, seed=i) for i in range(3))
+    mods = [randn(B, G, C, dtype=mod, seed=10 + i, scale=0.4) for i in range(3)]
+    args = (y, mods[0], None, None, None, mods[1], mods[2])
+    x2, h = block.vsa_gate_norm(x, *args, kind=kind)
+    want_x, want_h = ref.gate_norm(x, *args, kind, 1e-6, 1e-6, BF16)
+    ref.check("x", x2, *want_x)
+    ref.check("h", h, *want_h)
+    got = block.vsa_gate_norm_bwd(dh, None, x, *args, kind=kind)
+    want = ref.gate_norm_bwd(dh, None, x, *args, kind, 1e-6, 1e-6)
+    for n, g, v in zip(("dx", "dy", "dgate", "dpost_weight", "dweight", "dbias", "dscale", "dshift"), got, want):
+        assert (g is None) == (v is None), n
+        if g is not None:
+            ref.check(n, g, *v)
+    again = block.vsa_gate_norm_bwd(dh, None, x, *args, kind=kind)
+    assert same_bits([g for g in got if g is not None], [g for g in again if g is not None])
