@@ -398,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (x.part >= 0) {
         float* to = p.parts + ((static_cast<int64_t>(x.part) * 2 + rank) * BN + col0) * 128 + row0 + lane;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 128 && x.n0 + col0 + c < p.n && m0 < p.m; c += 32) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(t_acc + c, v);
           tmem_wait_ld();
@@ -416,6 +416,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           } else if (!PRE) {
             if (lane == 0) bulk_wait_read<1>();  // all but the last 64 columns' stores
             __syncwarp();
+          }
+          if (n0 >= p.n || m0 >= p.m) {
+            // Nothing of these 64 columns (131040 x 64 -> 64: 22.4 us, now 18.7): groups of no store, which are
+            // counted all the same.
+            if (lane == 0) {
+              bulk_commit_group();
+              if (PRE) bulk_commit_group();
+            }
+            continue;
           }
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -530,34 +539,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// The tiles in parts: a CTA has 32 rows x 64 columns of one, a warp 8 columns of every part (128-byte
-// loads of 32 rows), added in part order; then 8 columns of a row a thread.
-template <typename E, int OP>
+// The tiles in parts, added in part order; then 8 columns of a row a thread.  GROUPS 1: a CTA has 32 rows x 64
+// columns of a tile, a warp 8 columns of every part (128-byte loads of 32 rows).  GROUPS 8, many parts: 8
+// columns, a warp every eighth part, and their sums in warp order (dweight of 32760 rows, 128 x 128 in
+// 76 parts: 34.3 us, now 11.7; 131040 rows, 64 x 64: 44.8 and 16.6).
+template <typename E, int OP, int GROUPS>
 __global__ void __launch_bounds__(256) gemm_join_kernel(const __grid_constant__ Params p) {
-  __shared__ float sums[32][65];
+  constexpr int COLUMNS = 64 / GROUPS;
+  __shared__ float sums[GROUPS][32][COLUMNS + 1];
   grid_dependency_wait();
-  const int t = blockIdx.y, sub = blockIdx.x, rank = sub >> 4, r0 = (sub & 3) * 32, c0 = ((sub >> 2) & 3) * 64;
+  const int t = blockIdx.y, sub = blockIdx.x, rank = sub / (16 * GROUPS), r0 = (sub & 3) * 32;
+  const int c0 = (sub >> 2) % (4 * GROUPS) * COLUMNS;
   int m0, n0;
   tile_origin(p, p.full + t, &m0, &n0);
   m0 += rank * 128 + r0;
   n0 += c0;
   if (m0 >= p.m || n0 >= p.n) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const float* from = p.parts + ((static_cast<int64_t>(t) * 2 + rank) * BN + c0 + w * 8) * 128 + r0 + lane;
+  const int group = GROUPS == 1 ? 0 : w, column = GROUPS == 1 ? w * 8 : 0;
+  const float* from = p.parts + ((static_cast<int64_t>(t) * 2 + rank) * BN + c0 + column) * 128 + r0 + lane;
   const int64_t step = static_cast<int64_t>(p.tail) * 2 * BN * 128;
   float s[8] = {};
 #pragma unroll 4
-  for (int i = 0; i < p.splits; ++i) {
+  for (int i = group; i < p.splits; i += GROUPS) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] += from[i * step + j * 128];
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sums[lane][w * 8 + j] = s[j];
+  for (int j = 0; j < 8; ++j) sums[group][lane][column + j] = s[j];
   __syncthreads();
-  const int r = m0 + (threadIdx.x >> 3), c = n0 + (threadIdx.x & 7) * 8;
-  if (r >= p.m || c >= p.n) return;
+  const int r = m0 + threadIdx.x * 8 / COLUMNS, c = n0 + threadIdx.x * 8 % COLUMNS;
+  if (threadIdx.x * 8 >= 32 * COLUMNS || r >= p.m || c >= p.n) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = sums[threadIdx.x >> 3][(threadIdx.x & 7) * 8 + j];
+  for (int j = 0; j < 8; ++j) {
+    s[j] = 0.f;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) s[j] += sums[g][threadIdx.x * 8 / COLUMNS][threadIdx.x * 8 % COLUMNS + j];
+  }
   if (OP == GEMM_FWD) {
     if (p.bias) add_bias<E>(p.bias, p.bias_f32, c, s);
     if (p.pre.data) store8(static_cast<E*>(p.pre.data) + r * p.pre.stride + c, s);
@@ -627,7 +645,8 @@ cudaError_t launch_kernel(const Maps& maps, const Params& p, int pairs, cudaStre
   if (e != cudaSuccess) return e;
   e = launch_dependent(gemm_kernel<E, OP, AUX, PRE>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, stream, maps, p);
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_dependent(gemm_join_kernel<E, OP>, dim3(32, p.tail), dim3(256), 0, stream, p);
+  if (p.splits >= 8) return launch_dependent(gemm_join_kernel<E, OP, 8>, dim3(256, p.tail), dim3(256), 0, stream, p);
+  return launch_dependent(gemm_join_kernel<E, OP, 1>, dim3(32, p.tail), dim3(256), 0, stream, p);
 }
 
 template <typename E>
