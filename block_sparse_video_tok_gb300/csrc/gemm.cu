@@ -14,10 +14,11 @@
 // parts leave fp32 sums in the workspace, which gemm_join_kernel adds in part order and finishes.
 // The same rule splits small problems, all of whose tiles are such a rest.
 //
-// Roles (384 threads): warp 0 TMA producer; warp 1 UMMA issuer (first CTA of the pair); warp 2 tensor
-// memory; warp 3 biases; warps 4-11 epilogue, half a row of the tile per thread: bias, activation,
-// residual or slope in fp32, rounded once, through swizzled shared memory to TMA stores, which clip at
-// the matrix's edges.
+// Roles (384 or 640 threads): warp 0 TMA producer; warp 1 UMMA issuer (first CTA of the pair); warp 2 tensor
+// memory; warp 3 biases; warps from 4 on epilogue, a half or a quarter of a row of the tile per thread: bias,
+// activation, residual or slope in fp32, rounded once, through swizzled shared memory to TMA stores, which clip
+// at the matrix's edges.  ACT: an activation (or its slope).  Without one it has kernels of its own: a branch
+// around it in the epilogue took 32760 x 512 -> 1536 from 42 us to 47, with a residual from 58 to 65.
 //
 // Bound by the tensor cores (91 % of their cycles): 32760 x 1536 x 6144 with bias and gelu_tanh 324 us in
 // bursts (1908 TFLOP/s, the measured burst rate; a plain library product 304), 131040 rows 1267; dx 328, dweight
@@ -37,18 +38,18 @@ namespace {
 
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair
 constexpr int GROUP_M = 8;
-constexpr int NUM_THREADS = 384;
-constexpr int TMA_WARP = 0, MMA_WARP = 1, TMEM_WARP = 2, BIAS_WARP = 3, EPI_WARP = 4, EPI_WARPS = 8;
+constexpr int TMA_WARP = 0, MMA_WARP = 1, TMEM_WARP = 2, BIAS_WARP = 3, EPI_WARP = 4;
+constexpr int EPI_COLUMNS = 1024;  // of all epilogue warps together, a quarter of the rows each
 constexpr uint32_t OPERAND_BYTES = 128 * BK * 2;  // a CTA's A or B of a stage
 constexpr uint32_t STAGE_BYTES = 2 * OPERAND_BYTES;
 constexpr uint32_t OUT_BYTES = 32 * 128;  // 32 rows x 64 results of an epilogue warp
 
 constexpr int STAGES = 5;
-// Buffers of an epilogue warp: 64 results each of its 32 rows x 128 columns.  With pre (and no operand to load)
-// they are four of 32 results, two for pre and two for out, so that a store has the time of 32 columns'
-// work to leave its buffer: one of 64 for each of the two waited for its last store every time (32760 x
-// 1536 x 6144, pre and gelu_tanh 373 us, now 366; gelu 384 and 371).
-constexpr int BUFFERS = 2;
+// Buffers of the epilogue warps, one for each 64 results of their 32 rows.  With pre (and no operand to load) a
+// warp of 128 columns has four of 32 results, two for pre and two for out, so that a store has the time of 32
+// columns' work to leave its buffer: one of 64 for each of the two waited for its last store every time (32760 x
+// 1536 x 6144, pre and gelu_tanh 373 us, now 366; gelu 384 and 371).  A warp of 64 columns has two of 32 and waits.
+constexpr int BUFFERS = 16;
 
 enum Bar : uint32_t {
   FULL0 = 0,                        // first CTA: both CTAs' copies of a stage have landed
@@ -56,13 +57,13 @@ enum Bar : uint32_t {
   ACC_FULL0 = EMPTY0 + STAGES,      // each CTA: a tile's products are done
   ACC_EMPTY0 = ACC_FULL0 + 2,       // first CTA: both CTAs' epilogues have read a tile
   AUX0 = ACC_EMPTY0 + 2,            // per epilogue warp and buffer
-  DRAIN = AUX0 + EPI_WARPS * BUFFERS,
+  DRAIN = AUX0 + BUFFERS,
   BIAS_FULL,                        // a tile's biases are in shared memory
   BIAS_EMPTY,                       // the epilogue warps have read them
   NUM_BARS
 };
 constexpr uint32_t SM_OUT = STAGES * STAGE_BYTES;
-constexpr uint32_t SM_BIAS = SM_OUT + EPI_WARPS * BUFFERS * OUT_BYTES;  // 256 floats
+constexpr uint32_t SM_BIAS = SM_OUT + BUFFERS * OUT_BYTES;  // 256 floats
 constexpr uint32_t SM_BAR = SM_BIAS + BN * 4;
 constexpr uint32_t SMEM_BYTES = SM_BAR + NUM_BARS * 8 + 8 + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -218,9 +219,10 @@ __device__ __noinline__ void linger(uint64_t ns) {
   }
 }
 
-template <typename E, int OP, bool AUX, bool PRE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+template <typename E, int OP, bool AUX, bool PRE, bool ACT, int EPI_WARPS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128 + EPI_WARPS * 32, 1)
     gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  constexpr int COLUMNS = EPI_COLUMNS / EPI_WARPS, CHUNKS = COLUMNS / 64;  // of an epilogue warp; a buffer to each 64
   constexpr bool A_MN = OP == GEMM_DW, B_MN = OP != GEMM_FWD;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -365,9 +367,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------------ epilogue
     // A warp reads the quarter of tensor memory's rows that its number gives; two share it, 128 columns
     // each.
-    const int e = warp - EPI_WARP, row0 = (warp & 3) * 32, col0 = (e >> 2) * 128;
+    const int e = warp - EPI_WARP, row0 = (warp & 3) * 32, col0 = (e >> 2) * COLUMNS;
     const uint32_t t_row = (static_cast<uint32_t>(row0) << 16) + col0;
-    const uint32_t room = base + SM_OUT + e * BUFFERS * OUT_BYTES, aux_bar = bar(AUX0 + e * BUFFERS);
+    const uint32_t room = base + SM_OUT + e * CHUNKS * OUT_BYTES, aux_bar = bar(AUX0 + e * CHUNKS);
     const uint32_t acc_empty = in_first_cta(bar(ACC_EMPTY0));
     uint32_t done = 0, whole = 0;  // tiles; those that are not parts
     bool ok = true, pending = false;
@@ -381,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0) {
           bulk_wait_read_all();
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < CHUNKS; ++c) {
             mbar_arrive_expect_tx(aux_bar + 8u * c, OUT_BYTES);
             tma_load_2d(room + c * OUT_BYTES, &maps.aux, aux_bar + 8u * c, x.n0 + col0 + c * 64, m0);
           }
@@ -398,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (x.part >= 0) {
         float* to = p.parts + ((static_cast<int64_t>(x.part) * 2 + rank) * BN + col0) * 128 + row0 + lane;
 #pragma unroll 1
-        for (int c = 0; c < 128 && x.n0 + col0 + c < p.n && m0 < p.m; c += 32) {
+        for (int c = 0; c < COLUMNS && x.n0 + col0 + c < p.n && m0 < p.m; c += 32) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(t_acc + c, v);
           tmem_wait_ld();
@@ -407,14 +409,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < CHUNKS; ++c) {
           const int n0 = x.n0 + col0 + c * 64;
           const uint32_t out = room + c * OUT_BYTES;
           if (AUX) {
             ok = warp_wait(aux_bar + 8u * c, whole & 1u, abort, limit);
             if (!ok) break;
           } else if (!PRE) {
-            if (lane == 0) bulk_wait_read<1>();  // all but the last 64 columns' stores
+            if (lane == 0) bulk_wait_read<CHUNKS - 1>();  // all but the last 64 columns' stores
             __syncwarp();
           }
           if (n0 >= p.n || m0 >= p.m) {
@@ -462,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                   // No room for a buffer of its own: straight from the registers.
                   store8(static_cast<E*>(p.pre.data) + (m0 + lane) * p.pre.stride + col + j * 8, z);
                 }
-                act8(p.act, z);
+                if (ACT) act8(p.act, z);
               }
               if (AUX) {
                 float a[8];
@@ -477,9 +479,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
               t[j] = pack8<E>(z);
             }
             if (PRE) {
-              if (lane == 0) bulk_wait_read<1>();  // all but the last 32 columns' stores
+              if (lane == 0) bulk_wait_read<CHUNKS - 1>();  // all but the last 32 columns' stores
               __syncwarp();
-              const uint32_t here = room + h * OUT_BYTES;
+              const uint32_t here = room + h % CHUNKS * OUT_BYTES;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint32_t spot = here + swizzled64(lane, j);
@@ -524,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     if (!ok && lane == 0) {
       raise_abort(abort, p.err);
       volatile int never = 0;
-      for (int c = 0; c < 2 && pending; ++c)
+      for (int c = 0; c < CHUNKS && pending; ++c)
         mbar_wait_bounded(aux_bar + 8u * c, whole & 1u, &never, DRAIN_LIMIT_NS);
     }
     if (lane == 0) bulk_wait_read_all();  // (the end of the grid waits for the writes)
@@ -638,12 +640,28 @@ Plan plan_of(int m, int n, int k) {
   return q;
 }
 
-template <typename E, int OP, bool AUX, bool PRE>
-cudaError_t launch_kernel(const Maps& maps, const Params& p, int pairs, cudaStream_t stream) {
+template <typename E, int OP, bool AUX, bool PRE, bool ACT, int EPI_WARPS>
+cudaError_t launch_main(const Maps& maps, const Params& p, int pairs, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = ensure_smem_limit(gemm_kernel<E, OP, AUX, PRE>, static_cast<int>(SMEM_BYTES), smem_set);
+  const auto kernel = gemm_kernel<E, OP, AUX, PRE, ACT, EPI_WARPS>;
+  const cudaError_t e = ensure_smem_limit(kernel, static_cast<int>(SMEM_BYTES), smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(gemm_kernel<E, OP, AUX, PRE>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, stream, maps, p);
+  return launch_dependent(kernel, dim3(2 * pairs), dim3(128 + EPI_WARPS * 32), SMEM_BYTES, stream, maps, p);
+}
+
+// Twice the epilogue warps where activations or slopes would take longer than a tile's products.  Us with 8 and 16
+// of them, 32760 rows -> 1536 features, by elements of k:
+//   gelu_tanh            128: 54 and 44   512: 58 and 52   768: 63 and 59   1024: 69 and 71   1536: 94 and 97
+//   the same + residual  128: 74 and 63   512: 77 and 68   768: 81 and 73   1024: 85 and 79   1536: 101 and 103
+// Without an activation 16 win nothing (512: 40 and 42, with a residual 57 and 58).
+template <typename E, int OP, bool AUX, bool PRE, bool ACT>
+cudaError_t launch_kernel(const Maps& maps, const Params& p, int pairs, cudaStream_t stream) {
+  cudaError_t e;
+  if constexpr (ACT)
+    e = p.steps <= (AUX ? 16 : 12) ? launch_main<E, OP, AUX, PRE, ACT, 16>(maps, p, pairs, stream)
+                                   : launch_main<E, OP, AUX, PRE, ACT, 8>(maps, p, pairs, stream);
+  else
+    e = launch_main<E, OP, AUX, PRE, ACT, 8>(maps, p, pairs, stream);
   if (e != cudaSuccess || p.splits == 1) return e;
   if (p.splits >= 8) return launch_dependent(gemm_join_kernel<E, OP, 8>, dim3(256, p.tail), dim3(256), 0, stream, p);
   return launch_dependent(gemm_join_kernel<E, OP, 1>, dim3(32, p.tail), dim3(256), 0, stream, p);
@@ -654,14 +672,17 @@ cudaError_t launch_typed(GemmOp op, const Maps& maps, const Params& p, int pairs
   const bool aux = p.aux.data != nullptr;
   switch (op) {
     case GEMM_FWD:
-      if (!aux && p.has_pre) return launch_kernel<E, GEMM_FWD, false, true>(maps, p, pairs, stream);
-      return aux ? launch_kernel<E, GEMM_FWD, true, false>(maps, p, pairs, stream)
-                 : launch_kernel<E, GEMM_FWD, false, false>(maps, p, pairs, stream);
+      if (!aux && p.has_pre) return launch_kernel<E, GEMM_FWD, false, true, true>(maps, p, pairs, stream);
+      if (!p.act)
+        return aux ? launch_kernel<E, GEMM_FWD, true, false, false>(maps, p, pairs, stream)
+                   : launch_kernel<E, GEMM_FWD, false, false, false>(maps, p, pairs, stream);
+      return aux ? launch_kernel<E, GEMM_FWD, true, false, true>(maps, p, pairs, stream)
+                 : launch_kernel<E, GEMM_FWD, false, false, true>(maps, p, pairs, stream);
     case GEMM_DX:
-      return aux ? launch_kernel<E, GEMM_DX, true, false>(maps, p, pairs, stream)
-                 : launch_kernel<E, GEMM_DX, false, false>(maps, p, pairs, stream);
+      return aux ? launch_kernel<E, GEMM_DX, true, false, true>(maps, p, pairs, stream)
+                 : launch_kernel<E, GEMM_DX, false, false, false>(maps, p, pairs, stream);
     default:
-      return launch_kernel<E, GEMM_DW, false, false>(maps, p, pairs, stream);
+      return launch_kernel<E, GEMM_DW, false, false, false>(maps, p, pairs, stream);
   }
 }
 

@@ -239,3 +239,28 @@ def test_gate_norm_modulations_of_few_tokens(block, case, kind, mod):
             ref.check(n, g, *v)
     again = block.vsa_gate_norm_bwd(dh, None, x, *args, kind=kind)
     assert same_bits([g for g in got if g is not None], [g for g in again if g is not None])
+
+
+@pytest.mark.parametrize("size", [(20000, 8, 264), (9001, 64, 1528), (5003, 520, 2056), (6000, 768, 1536), (6000, 776, 1032),
+                                  (5000, 1024, 2000), (5000, 1032, 2000), (40000, 64, 40), (30000, 40, 72)], ids=str)
+def test_linear_epilogues(block, size):
+    # Many rows of few features: the epilogue's warps and what it leaves out are chosen by the features.
+    M, K, N = size
+    x, w, r = randn(M, K, seed=1), randn(N, K, seed=2, scale=K ** -0.5), randn(M, N, seed=3)
+    b = randn(N, dtype=FP32, seed=4)
+    for act, residual, bias in ((None, None, None), (None, None, b), (None, r, b), ("gelu_tanh", None, b), ("silu", r, None),
+                                ("gelu", None, None)):
+        out, pre = block.vsa_linear(x, w, bias, act, residual, need_pre=True)
+        want, want_pre = ref.linear(x, w, bias, act, residual)
+        ref.check("out", out, *want)
+        ref.check("pre", pre, *want_pre)
+        assert same_bits((block.vsa_linear(x, w, bias, act, residual)[0],), (out,))
+    # dx of K features from N, with and without a slope; dweight over the many rows.
+    dout, x_pre = randn(M, K, seed=5), r
+    for act in (None, "gelu_tanh"):
+        args = (dout, r if act is None else ref.act(r.double(), act).to(BF16), randn(K, N, seed=6, scale=K ** -0.5), None,
+                None, None, act, None if act is None else x_pre)
+        got, want = block.vsa_linear_bwd(*args), ref.linear_bwd(*args)
+        ref.check("dx", got[0], *want[0])
+        ref.check("dweight", got[1], *want[1])
+        assert same_bits(block.vsa_linear_bwd(*args)[:2], got[:2])
