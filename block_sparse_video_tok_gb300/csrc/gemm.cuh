@@ -38,7 +38,7 @@ double gemm_microseconds(int m, int n, int k);
 
 // The forward for a few rows, and whether it is the one to use.
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream);
-bool use_linear_rows(int rows, int out);
+bool use_linear_rows(int rows, int in, int out);
 
 // 2-D tensor map of a 16-bit matrix of `columns` x `rows`, box 64 columns x box_rows, 128-byte swizzle; narrow: 32
 // columns, 64-byte swizzle.

@@ -1,6 +1,6 @@
 // linear.cu -- out = act(x W^T + bias) + residual and its gradients: which kernels a call takes.
 //
-// Forward: one product with its epilogue (linear_rows.cu up to 16 rows, gemm_small.cu for small products,
+// Forward: one product with its epilogue (linear_rows.cu up to 8 to 24 rows, gemm_small.cu for small products,
 // gemm.cu).  Backward: dz = dout act'(pre) and the columns' sums in a pass of their own, then dx = dz W and
 // dweight = dz^T x.  The pass is left out where there is neither an activation nor a bias; and a chain of two
 // products does not pay for it twice, as the second's dx goes on through the activation in its
@@ -123,12 +123,12 @@ cudaError_t slopes(const LinearArgs& a, const Layout& l, cudaStream_t stream) {
 }  // namespace
 
 size_t linear_fwd_workspace(int rows, int in, int out) {
-  return use_linear_rows(rows, out) ? 0 : gemm_workspace(rows, out, in);
+  return use_linear_rows(rows, in, out) ? 0 : gemm_workspace(rows, out, in);
 }
 size_t linear_bwd_workspace(int rows, int in, int out, int act) { return layout_of(rows, in, out, act).total; }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t stream) {
-  if (use_linear_rows(a.rows, a.out_features)) return launch_linear_rows(a, stream);
+  if (use_linear_rows(a.rows, a.in, a.out_features)) return launch_linear_rows(a, stream);
   GemmArgs g{};
   g.a = a.x;
   g.b = a.weight;

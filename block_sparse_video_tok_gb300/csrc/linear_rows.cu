@@ -13,7 +13,7 @@
 // too.  The warps' and CTAs' sums are added in their order, through shared memory.
 //
 // Measured: 8 x 1536 -> 9216 with silu 5.0 us, 84 % of the copy rate (weights 28 MB); 8 x 6144 -> 1536 5.0; 16 rows
-// 6.0 and 6.6, where gemm_small.cu's tiles take 8 to 9.
+// 6.0 and 6.6, where gemm_small.cu's tiles take 8 to 9; 24 rows, 1536 -> 6144 6.2 and 8.8.
 #include "act.cuh"
 #include "gemm.cuh"
 #include "vec8.cuh"
@@ -22,7 +22,7 @@ namespace vsa {
 
 namespace {
 
-constexpr int WARPS = 8, FEATURES = 16, STEP = 32, UNROLL = 6;
+constexpr int WARPS = 8, FEATURES = 16, STEP = 32;
 
 struct Params {
   LinearArgs a;
@@ -54,7 +54,7 @@ __device__ __forceinline__ float load_cluster(uint32_t addr, uint32_t rank) {
 // TILES: of 8 rows of x.
 template <typename E, int TILES>
 __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const __grid_constant__ Params p) {
-  constexpr int ROWS = 8 * TILES;
+  constexpr int ROWS = 8 * TILES, UNROLL = TILES < 3 ? 6 : 3;  // as the registers allow
   __shared__ float sums[WARPS][FEATURES][ROWS + 1];
   __shared__ float total[FEATURES * ROWS];
   grid_dependency_wait();
@@ -157,12 +157,23 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
 
 template <typename E>
 cudaError_t launch_rows(const LinearArgs& a, cudaStream_t stream) {
-  return a.rows <= 8 ? launch<E, 1>(a, stream) : launch<E, 2>(a, stream);
+  return a.rows <= 8 ? launch<E, 1>(a, stream) : a.rows <= 16 ? launch<E, 2>(a, stream) : launch<E, 3>(a, stream);
 }
 
 }  // namespace
 
-bool use_linear_rows(int rows, int out) { return rows <= 16 && out <= FEATURES * 65535; }
+// Every CTA reads all of x, 1/2 to 3/2 of its weights' bytes: the more rows, the fewer weights.  Us here and with
+// gemm_small.cu's tiles:
+//   rows   1536 -> 1536   1536 -> 6144   1536 -> 9216   4096 -> 4096   6144 -> 6144   8192 -> 8192
+//    8                     4.1 and  8.9   4.8 and 10.4   6.8 and 12.0   13 and 12      29 and 26
+//   16     4.9 and 6.0     5.5 and  8.1   6.2 and 10.2   8.8 and  9.6   17 and 12      45 and 26
+//   24     5.2 and 6.0     6.3 and  8.9  10.7 and  9.8  15.2 and  9.7
+//   32     6.4 and 6.0     8.3 and  8.8   9.5 and  9.3  12.5 and  9.7
+bool use_linear_rows(int rows, int in, int out) {
+  const int64_t weights = static_cast<int64_t>(in) * out;
+  return out <= FEATURES * 65535 &&
+         (rows <= 8 || (rows <= 16 && weights <= 25000000) || (rows <= 24 && weights <= 10000000));
+}
 
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream) {
   return a.dtype == VSA_F16 ? launch_rows<__half>(a, stream) : launch_rows<__nv_bfloat16>(a, stream);

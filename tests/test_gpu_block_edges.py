@@ -264,3 +264,18 @@ def test_linear_epilogues(block, size):
         ref.check("dx", got[0], *want[0])
         ref.check("dweight", got[1], *want[1])
         assert same_bits(block.vsa_linear_bwd(*args)[:2], got[:2])
+
+
+@pytest.mark.parametrize("size", [(8, 8192, 5000), (9, 8192, 3040), (16, 8192, 3048), (16, 8192, 3056), (17, 1000, 1000), (17, 8192, 1224),
+                                  (23, 5000, 2000), (24, 24, 16), (24, 5000, 2008), (25, 1536, 1536)], ids=str)
+def test_linear_few_rows(block, size):
+    # On both sides of where a few rows stop having a kernel of their own.
+    M, K, N = size
+    x, w, r = randn(M, K, seed=1), randn(N, K, seed=2, scale=K ** -0.5), randn(M, N, seed=3)
+    b = randn(N, dtype=FP32, seed=4)
+    for act, residual, bias in ((None, None, None), ("gelu_tanh", r, b), ("silu", None, b)):
+        out, pre = block.vsa_linear(x, w, bias, act, residual, need_pre=True)
+        want, want_pre = ref.linear(x, w, bias, act, residual)
+        ref.check("out", out, *want)
+        ref.check("pre", pre, *want_pre)
+        assert same_bits((block.vsa_linear(x, w, bias, act, residual)[0],), (out,))
