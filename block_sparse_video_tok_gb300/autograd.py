@@ -11,6 +11,10 @@ invert it once for all of them (`k2q=` below).
 
 Argument marshalling only: every step runs in libvsa.so's kernels through `vsa`.  Nothing here can be
 differentiated twice: doing so raises.
+
+A backward is captured into a CUDA graph together with its forward, after warm-up on a side stream, and
+while no autograd graph of the same leaves that was made outside the capture is alive: torch accumulates a
+leaf's gradient on the stream its graph was made on, which a capture cannot join.
 """
 import functools
 
