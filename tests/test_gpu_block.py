@@ -360,3 +360,58 @@ def test_other_stream(block):
     got = block.vsa_linear(x, c["weight"], c["bias"], "silu", need_pre=True, stream=s)
     s.synchronize()
     assert same_bits(got, want)
+
+
+def every_value(dtype):
+    """All values of a 16-bit type but NaNs, [.., 8]."""
+    z = torch.arange(1 << 16, device="cuda").to(torch.int16).view(dtype)
+    z = z[~z.isnan()]
+    return torch.cat([z, z.new_zeros(-z.numel() % 8)]).view(-1, 8)
+
+
+def wanted_slope(z, act):
+    """The slope in 64 bits, its limits at the infinities, and its bound: as a sum of terms of its own size
+    and of 2^-6, each good to 2^-14."""
+    want = torch.where(z.isinf(), (z > 0).double(), ref.slope(z.double().nan_to_num(0.0, 0.0, 0.0), act))
+    return want, ref.half_step(z.dtype) * want.abs() + 2.0 ** -14 * (want.abs() + 2.0 ** -6) + ref.tiny(z.dtype)
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_linear_slopes_of_every_value(block, act, dtype):
+    """Also where z^2 leaves the range of fp32, and at the infinities that a pre rounded to 16 bits may be."""
+    z = every_value(dtype)
+    eye = torch.eye(8, device="cuda", dtype=dtype)
+    one = torch.ones_like(z)
+    want = wanted_slope(z, act)
+    # The slopes' own pass, then those of the products' epilogues: small tiles, and pairs of CTAs.
+    dz, _, db = block.vsa_linear_bwd(one, one, eye, torch.zeros(8, device="cuda"), act, z, need_dweight=False)
+    ref.check(act + "' before the products", dz, *want)
+    assert torch.isfinite(db).all()
+    few = z[-2000:]
+    dz = block.vsa_linear_bwd(one[:2000], one[:2000], eye, None, None, None, act, few, need_dweight=False)[0]
+    ref.check(act + "' in small tiles", dz, *(t[-2000:] for t in want))
+    wide = torch.zeros(8 * z.shape[0], 64, device="cuda", dtype=dtype)
+    for i in range(8):
+        wide.view(8, -1, 64)[i, :, 8 * i:8 * i + 8] = z
+    one = torch.ones_like(wide)
+    dz = block.vsa_linear_bwd(one, one, torch.eye(64, device="cuda", dtype=dtype), None, None, None, act, wide,
+                              need_dweight=False)[0]
+    ref.check(act + "' in pairs", dz, *wanted_slope(wide, act))
+    # An undefined value stays undefined, in its element.
+    few = few.clone()
+    few[3, 5] = float("nan")
+    got = block.vsa_linear_bwd(one[:2000, :8].contiguous(), few, eye, None, None, None, act, few, need_dweight=False)[0]
+    assert got[3, 5].isnan() and int(got.isnan().sum()) == 1
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_linear_activations_of_every_finite_value(block, act, dtype):
+    z = every_value(dtype)
+    z = torch.where(z.isinf(), 0, z)
+    out, pre = block.vsa_linear(z, torch.eye(8, device="cuda", dtype=dtype), None, act, need_pre=True)
+    assert torch.equal(pre, z)
+    want = ref.act(z.double(), act)
+    # Relative as in the test of their range; a logistic function below 2^-126, of a z up to 104, is zero.
+    ref.check(act, out, want, (ref.half_step(dtype) + 2.0 ** -14) * want.abs() + ref.tiny(dtype) + 104 * 2.0 ** -126)
