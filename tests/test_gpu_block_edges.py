@@ -279,3 +279,32 @@ def test_linear_few_rows(block, size):
         ref.check("out", out, *want)
         ref.check("pre", pre, *want_pre)
         assert same_bits((block.vsa_linear(x, w, bias, act, residual)[0],), (out,))
+
+
+@pytest.mark.parametrize("C", [8, 56, 120, 224, 488, 656, 1000, 1272, 1536, 2024, 4080, 6080, 8160])
+@pytest.mark.parametrize("dtype,branch", [(FP32, FP32), (FP32, BF16), (FP16, FP16), (BF16, BF16)], ids=str)
+def test_constant_tokens_are_zeros_of_the_layer_norm(block, C, dtype, branch):
+    """Tokens of one whole number, whose sums are exact in fp32: n is zero in the backward as it is in the
+    forward, so nothing of it reaches dscale or dweight, and dx = (g - mean(g)) / sqrt(eps)."""
+    top = (1 << 24) // C
+    values = [v for v in (5, 120, 1000, 15000, 12345, top) if v <= top and (dtype == FP32 or v <= 60000)]
+    x = torch.tensor(values, device="cuda", dtype=torch.float64)
+    x = x[x.to(dtype).double() == x]
+    S = x.numel()
+    x = x.to(dtype).view(1, S, 1).expand(1, S, C).contiguous()
+    dh = randn(1, S, C, dtype=branch, seed=1, scale=0.25)
+    scale, w = randn(1, S, C, dtype=FP32, seed=2, scale=0.4), randn(C, dtype=FP32, seed=3)
+    _, h = block.vsa_gate_norm(x, scale=scale, h_dtype=branch)
+    assert not h.any()
+    one, g1 = 1 + scale.double(), dh.double()
+    for weight in (None, w):
+        dx, _, _, _, dweight, _, dscale, _ = block.vsa_gate_norm_bwd(dh, None, x, weight=weight, scale=scale)
+        assert not dscale.any() and (dweight is None or not dweight.any())
+        g = g1 * one * (1 if weight is None else weight.double())
+        want = 1000 * (g - g.mean(-1, keepdim=True))
+        bound = 1000 * ref.F32 * (g.abs() + g.abs().mean(-1, keepdim=True)) + ref.half_step(dtype) * want.abs()
+        ref.check("dx", dx, want, bound)
+    # The sums of many tokens' units likewise.
+    x = x[:, -1:].expand(1, 700, C).contiguous()
+    _, _, _, _, dweight, _, _, _ = block.vsa_gate_norm_bwd(randn(1, 700, C, dtype=branch, seed=4), None, x, weight=w)
+    assert not dweight.any()
