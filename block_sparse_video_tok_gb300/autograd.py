@@ -175,7 +175,7 @@ class Linear(torch.autograd.Function):
         recorded = recorded and any(ctx.needs_input_grad)
         out, pre = block.vsa_linear(x, weight, bias, act, residual, need_pre=recorded and act is not None)
         ctx.save_for_backward(x, weight, bias, pre)
-        ctx.act = act
+        ctx.act, ctx.residual = act, _shape(residual)
         return out
 
     @staticmethod
@@ -186,7 +186,7 @@ class Linear(torch.autograd.Function):
         g = _flat(dout)
         dx, dw, db = block.vsa_linear_bwd(g, x, weight, bias if need[2] else None, ctx.act, pre,
                                           need_dx=need[0], need_dweight=need[1])
-        return dx, dw, db, dout if need[3] else None, None, None
+        return dx, dw, db, dout.reshape(ctx.residual) if need[3] else None, None, None
 
 
 class Mlp(torch.autograd.Function):
@@ -199,7 +199,7 @@ class Mlp(torch.autograd.Function):
         mid, pre = block.vsa_linear(x, w1, b1, act, need_pre=recorded)
         out, _ = block.vsa_linear(mid, w2, b2, residual=residual)
         ctx.save_for_backward(x, w1, b1, w2, b2, mid, pre)
-        ctx.act = act
+        ctx.act, ctx.residual = act, _shape(residual)
         return out
 
     @staticmethod
@@ -214,7 +214,11 @@ class Mlp(torch.autograd.Function):
         if first:
             dx, dw1, db1 = block.vsa_linear_bwd(dz, x, w1, b1 if need[2] else None, need_dx=need[0],
                                                 need_dweight=need[1])
-        return dx, dw1, db1, dw2, db2, dout if need[5] else None, None, None
+        return dx, dw1, db1, dw2, db2, dout.reshape(ctx.residual) if need[5] else None, None, None
+
+
+def _shape(t):
+    return None if t is None else t.shape
 
 
 def _aligned(g):
@@ -271,7 +275,8 @@ def gate_norm(x, y=None, gate=None, post_weight=None, weight=None, bias=None, sc
 
 
 def linear(x, weight, bias=None, act=None, residual=None):
-    """Differentiable block.vsa_linear: act(x weight^T + bias) + residual."""
+    """Differentiable block.vsa_linear: act(x weight^T + bias) + residual.  The residual has the output's rows,
+    in any leading dimensions, and so has its gradient."""
     return Linear.apply(x, weight, bias, residual, act, torch.is_grad_enabled())
 
 

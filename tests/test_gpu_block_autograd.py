@@ -219,3 +219,21 @@ def test_backward_in_a_graph(autograd):
         graph.replay()
         torch.cuda.synchronize()
         assert same(grads, step())
+
+
+def test_residual_of_other_leading_dimensions(autograd):
+    """A residual of as many rows as the output: its gradient has its own shape."""
+    ts = leaves(randn(2, 30, 64), randn(64, 64, seed=1, scale=0.1), randn(64, 64, seed=2, scale=0.1))
+    x, w1, w2 = ts
+    dout = randn(2, 30, 64, seed=3)
+    wide = torch.zeros(2, 30, 72, dtype=BF16, device="cuda")
+    wide[..., 8:] = dout
+    for f in (lambda r: autograd.linear(x, w1, None, None, r), lambda r: autograd.linear(x, w1, None, "silu", r),
+              lambda r: autograd.mlp(x, w1, None, w2, None, "silu", r)):
+        for shape in ((60, 64), (1, 60, 64), (6, 10, 64), (2, 30, 1, 64)):
+            (r,) = leaves(randn(60, 64, seed=4).view(shape))
+            (same_r,) = leaves(r.detach().view(2, 30, 64))
+            want = torch.autograd.grad(f(same_r), (x, w1, same_r), dout)
+            for g in (dout, wide[..., 8:]):
+                got = torch.autograd.grad(f(r), (x, w1, r), g)
+                assert got[2].shape == shape and same(got[:2], want[:2]) and torch.equal(got[2].view_as(dout), want[2])
