@@ -162,9 +162,8 @@ class GateNorm(torch.autograd.Function):
             return (None,) * 12
         x_out, y, *params = ctx.saved_tensors
         dh = torch.zeros(x_out.shape, dtype=ctx.h_dtype, device=x_out.device) if dh is None else _aligned(dh)
-        need = any(ctx.needs_input_grad[2:8])
         return block.vsa_gate_norm_bwd(dh, None if dx_out is None else _aligned(dx_out), x_out, y, *params,
-                                       *ctx.settings, need_dparams=need) + (None,) * 4
+                                       *ctx.settings, need_dparams=ctx.needs_input_grad[2:8]) + (None,) * 4
 
 
 class Linear(torch.autograd.Function):

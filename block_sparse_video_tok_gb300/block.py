@@ -265,11 +265,13 @@ def _gate_norm_op(x, branch, y, gate, post_weight, weight, bias, scale, shift, k
 
 
 @functools.lru_cache(maxsize=256)
-def _norm_workspace(device, B, S, C, G):
-    """Workspace bytes of a backward of these sizes (a pure function of them)."""
-    some = VsaModulation(16, 0, 0)
+def _norm_workspace(device, B, S, C, G, dtype, branch, weights):
+    """Workspace bytes of a backward of these sizes and types (a pure function of them), with the gradients of
+    weights or without."""
+    some, dtype, branch = VsaModulation(16, 0, 0), _DTYPES[dtype], _DTYPES[branch]
     return _lib().vsa_gate_norm_bwd_workspace_bytes(
-        VsaGateNorm(B, S, C, G, 0, 0, 0, 0, 0, 0.0, 0.0, some, some, some, None, None, None))
+        VsaGateNorm(B, S, C, G, 0, dtype, branch, branch, branch, 0.0, 0.0, some, some, some, 16 if weights else None,
+                    None, None))
 
 
 def vsa_gate_norm(x, y=None, gate=None, post_weight=None, weight=None, bias=None, scale=None,
@@ -318,8 +320,9 @@ def vsa_gate_norm_bwd(dh, dx_out, x_out, y=None, gate=None, post_weight=None, we
                       dx=None, dy=None, workspace=None, stream=None):
     """Gradients of vsa_gate_norm from those of its outputs (dx_out None: zero), the x' that it
     returned and its other inputs.  Returns (dx, dy, dgate, dpost_weight, dweight, dbias, dscale,
-    dshift), None for what is None (the parameters' with need_dparams false); the parameters'
-    gradients have their types.  dx may be dx_out."""
+    dshift), None for what is None; the parameters' gradients have their types.  need_dparams: whether
+    those are wanted, or six of it, for gate, post_weight, weight, bias, scale and shift.  dx may be
+    dx_out."""
     if stream is not None:
         return _on(stream, vsa_gate_norm_bwd, dh, dx_out, x_out, y, gate, post_weight, weight, bias, scale,
                    shift, kind, eps, post_eps, need_dparams, dx, dy, workspace)
@@ -347,10 +350,17 @@ def vsa_gate_norm_bwd(dh, dx_out, x_out, y=None, gate=None, post_weight=None, we
         ins.append(packed)
     else:
         ins.append(_tokens(dy, "dy", shape, branch, device))
-    grads = [None if p is None or not need_dparams else _empty_like(p) if p.is_contiguous() else
-             _empty(p.shape, dtype=p.dtype, device=where) for p in (gate, post_weight, weight, bias, scale, shift)]
+    wanted = need_dparams if isinstance(need_dparams, (tuple, list)) else (need_dparams,) * 6
+    if len(wanted) != 6:
+        raise ValueError("need_dparams must be one or six truth values, got %d" % len(wanted))
+    grads = [None if p is None or not n else _empty_like(p) if p.is_contiguous() else
+             _empty(p.shape, dtype=p.dtype, device=where)
+             for p, n in zip((gate, post_weight, weight, bias, scale, shift), wanted)]
     dgate, dpost, dweight, dbias, dscale, dshift = grads
-    need = 0 if all(g is None for g in grads) else _norm_workspace(device, *sizes)
+    weights = dpost is not None or dweight is not None or dbias is not None
+    need = 0
+    if weights or dgate is not None or dscale is not None or dshift is not None:
+        need = _norm_workspace(device, *sizes, dtype, branch, weights)
     keep, wp, wn = _workspace(workspace, need, x_out)
     places = _pack_grads(*(0 if g is None else g.data_ptr()
                            for g in (dgate, dscale, dshift, dpost, dweight, dbias)))

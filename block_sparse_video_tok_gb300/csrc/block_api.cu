@@ -186,9 +186,17 @@ vsa_status vsa_gate_norm_fwd(const vsa_gate_norm* op, const vsa_tokens* x, const
 }
 
 size_t vsa_gate_norm_bwd_workspace_bytes(const vsa_gate_norm* op) {
-  return check_gate_norm(op) == VSA_OK
-             ? vsa::gate_norm_bwd_workspace(op->batch, op->channels, op->groups)
-             : 0;
+  if (check_gate_norm(op) != VSA_OK) return 0;
+  vsa::GateNormArgs a{};
+  fill_gate_norm(op, &a);
+  // (Only which gradients there are counts.)
+  a.dgate = const_cast<void*>(op->gate.data);
+  a.dscale = const_cast<void*>(op->scale.data);
+  a.dshift = const_cast<void*>(op->shift.data);
+  a.dpost = const_cast<void*>(op->post_weight);
+  a.dweight = const_cast<void*>(op->weight);
+  a.dbias = const_cast<void*>(op->bias);
+  return vsa::gate_norm_bwd_workspace(a);
 }
 
 vsa_status vsa_gate_norm_bwd(const vsa_gate_norm* op, const vsa_tokens* dh,
@@ -219,14 +227,12 @@ vsa_status vsa_gate_norm_bwd(const vsa_gate_norm* op, const vsa_tokens* dh,
     } g[] = {{grads->gate, op->gate.data, &a.dgate},          {grads->scale, op->scale.data, &a.dscale},
              {grads->shift, op->shift.data, &a.dshift},       {grads->post_weight, op->post_weight, &a.dpost},
              {grads->weight, op->weight, &a.dweight},         {grads->bias, op->bias, &a.dbias}};
-    size_t need = 0;
     for (auto& x : g) {
       if (!x.grad) continue;
       if (!x.of || !aligned(x.grad, 16)) return VSA_ERR_INVALID_ARG;
       *x.to = x.grad;
-      need = vsa_gate_norm_bwd_workspace_bytes(op);
     }
-    if ((st = check_workspace(workspace, workspace_bytes, need)) != VSA_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, vsa::gate_norm_bwd_workspace(a))) != VSA_OK) return st;
     a.workspace = static_cast<float*>(workspace);
   }
   if ((st = check_device()) != VSA_OK) return st;

@@ -33,7 +33,8 @@ struct GateNormArgs {
 
 cudaError_t launch_gate_norm_fwd(const GateNormArgs& a, cudaStream_t stream);
 cudaError_t launch_gate_norm_bwd(const GateNormArgs& a, cudaStream_t stream);
-size_t gate_norm_bwd_workspace(int batch, int channels, int groups);
+// Of the gradients that a has places for.
+size_t gate_norm_bwd_workspace(const GateNormArgs& a);
 
 // ---------------------------------------------------------------------------- linear
 

@@ -916,14 +916,6 @@ Plan plan_of(int batch, int tokens, int channels, int groups, bool forward, int 
   return q;
 }
 
-// Units of a backward at most, whatever its types: four waves of what runs at once (four CTAs of at most 8
-// teams to an SM, or of one unit), or a unit to a row.
-size_t most_units(int64_t rows, int channels) {
-  const int wpr = (channels + 256 * bwd_vectors(channels) - 1) / (256 * bwd_vectors(channels));
-  const int64_t at_once = 4LL * device_sm_count() * (channels <= NARROW_CHANNELS || wpr > CTA_WARPS ? 1 : CTA_WARPS / wpr);
-  return static_cast<size_t>(4 * at_once > rows ? 4 * at_once : rows);
-}
-
 // How the units' sums are joined: by rows (gate_norm_few_kernel) or a row to a block, and the shares of the
 // weights' gradients that leaves.
 bool few_units(int64_t rows, int parts) { return rows > 64 && parts <= FEW_UNITS; }
@@ -935,17 +927,11 @@ int64_t shares_of(int64_t rows, int channels, bool few) {
   const int each = few ? few_rows(rows, channels) : 1;
   return (rows + each - 1) / each;
 }
-// At most: a row to a block are up to 64 rows, or as many as have more than FEW_UNITS units each.
-size_t most_shares(int64_t rows, int channels) {
-  if (rows <= 64) return static_cast<size_t>(rows);
-  const int64_t many = static_cast<int64_t>(most_units(rows, channels)) / FEW_UNITS, blocks = rows < many ? rows : many;
-  const int64_t few = shares_of(rows, channels, true);
-  return static_cast<size_t>(few > blocks ? few : blocks);
-}
-
 bool wants_sums(const GateNormArgs& a) {
   return a.dgate || a.dscale || a.dshift || a.dpost || a.dweight || a.dbias;
 }
+
+bool wants_weights(const GateNormArgs& a) { return a.dpost || a.dweight || a.dbias; }
 
 Params params_of(const GateNormArgs& a, const Plan& q) {
   Params p;
@@ -984,18 +970,31 @@ cudaError_t launch_join(const Params& p, cudaStream_t stream) {
   return launch_dependent(gate_norm_join_kernel<X>, dim3((p.a.channels + X - 1) / X), dim3(X, 1024 / X), 0, stream, p);
 }
 
+// Whether the units' sums become their rows' gradients at once, without the workspace.
+bool finishes(const Plan& q, bool narrow, bool weights) { return !narrow && q.parts == 1 && !weights; }
+
+// Bytes of the units' sums and of the weights' shares (these also where no weight's gradient is wanted, so that one
+// size serves every choice of gradients but the one that needs none).
+size_t workspace_of(const GateNormArgs& a, const Plan& q, bool narrow) {
+  if (!wants_sums(a) || finishes(q, narrow, wants_weights(a))) return 0;
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.groups;
+  const int64_t shares = shares_of(rows, a.channels, few_units(rows, q.parts));
+  return align_up(static_cast<size_t>(q.units + shares) * 3 * a.channels * sizeof(float), 256);
+}
+
+// The backward's launches, or, with `bytes`, the workspace that they need.
 template <typename TX, typename TY, int NV, int REGS, bool NARROW>
-cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
+cudaError_t launch_bwd(const GateNormArgs& a, size_t* bytes, cudaStream_t stream) {
   const Plan q = plan_of(a.batch, a.tokens, a.channels, a.groups, false, ring_bytes<TX, TY, NV>(1), NARROW);
+  if (bytes) {
+    *bytes = workspace_of(a, q, NARROW);
+    return cudaSuccess;
+  }
   const Params p = params_of(a, q);
-  const bool weights = a.dpost || a.dweight || a.dbias;
-  if (static_cast<size_t>(q.units) > most_units(static_cast<int64_t>(a.batch) * a.groups, a.channels)) return cudaErrorInvalidValue;
+  const bool weights = wants_weights(a);
   if (!wants_sums(a)) return launch_main<TX, TY, NV, REGS, NARROW, NO_SUMS>(p, q, stream);
-  const auto ends = reinterpret_cast<uintptr_t>(a.dgate) | reinterpret_cast<uintptr_t>(a.dscale) |
-                    reinterpret_cast<uintptr_t>(a.dshift);
   if constexpr (!NARROW)
-    if (q.parts == 1 && !weights && !(ends & 15))
-      return launch_main<TX, TY, NV, REGS, NARROW, FINISH>(p, q, stream);
+    if (finishes(q, NARROW, weights)) return launch_main<TX, TY, NV, REGS, NARROW, FINISH>(p, q, stream);
   cudaError_t e = launch_main<TX, TY, NV, REGS, NARROW, WORKSPACE>(p, q, stream);
   if (e != cudaSuccess) return e;
   const int rows = a.batch * a.groups, columns = (a.channels + 31) / 32;
@@ -1026,34 +1025,43 @@ cudaError_t launch_bwd(const GateNormArgs& a, cudaStream_t stream) {
 bool short_rows(const GateNormArgs& a) { return a.tokens / a.groups < 8; }
 
 template <typename TX, typename TY>
-cudaError_t launch_width(const GateNormArgs& a, bool forward, cudaStream_t stream) {
-  if (a.channels <= NARROW_CHANNELS && (forward || !short_rows(a)))
-    return forward ? launch_fwd<TX, TY, 1, true>(a, stream) : launch_bwd<TX, TY, 1, BWD_REGS_1, true>(a, stream);
-  if (forward)
-    return fwd_vectors(a.channels) == 1 ? launch_fwd<TX, TY, 1, false>(a, stream) : launch_fwd<TX, TY, 2, false>(a, stream);
+cudaError_t launch_width_fwd(const GateNormArgs& a, cudaStream_t stream) {
+  if (a.channels <= NARROW_CHANNELS) return launch_fwd<TX, TY, 1, true>(a, stream);
+  return fwd_vectors(a.channels) == 1 ? launch_fwd<TX, TY, 1, false>(a, stream) : launch_fwd<TX, TY, 2, false>(a, stream);
+}
+template <typename TX, typename TY>
+cudaError_t launch_width_bwd(const GateNormArgs& a, size_t* bytes, cudaStream_t stream) {
+  if (a.channels <= NARROW_CHANNELS && !short_rows(a)) return launch_bwd<TX, TY, 1, BWD_REGS_1, true>(a, bytes, stream);
   switch (bwd_regs(a.channels)) {
-    case BWD_REGS_1: return launch_bwd<TX, TY, 1, BWD_REGS_1, false>(a, stream);
-    case BWD_REGS_2: return launch_bwd<TX, TY, 2, BWD_REGS_2, false>(a, stream);
-    default: return launch_bwd<TX, TY, 4, BWD_REGS_4, false>(a, stream);
+    case BWD_REGS_1: return launch_bwd<TX, TY, 1, BWD_REGS_1, false>(a, bytes, stream);
+    case BWD_REGS_2: return launch_bwd<TX, TY, 2, BWD_REGS_2, false>(a, bytes, stream);
+    default: return launch_bwd<TX, TY, 4, BWD_REGS_4, false>(a, bytes, stream);
   }
 }
 
-cudaError_t launch_typed(const GateNormArgs& a, bool forward, cudaStream_t stream) {
-  if (a.dtype == VSA_BF16) return launch_width<__nv_bfloat16, __nv_bfloat16>(a, forward, stream);
-  if (a.dtype == VSA_F16) return launch_width<__half, __half>(a, forward, stream);
-  if (a.branch_dtype == VSA_BF16) return launch_width<float, __nv_bfloat16>(a, forward, stream);
-  if (a.branch_dtype == VSA_F16) return launch_width<float, __half>(a, forward, stream);
-  return launch_width<float, float>(a, forward, stream);
+cudaError_t bwd_typed(const GateNormArgs& a, size_t* bytes, cudaStream_t stream) {
+  if (a.dtype == VSA_BF16) return launch_width_bwd<__nv_bfloat16, __nv_bfloat16>(a, bytes, stream);
+  if (a.dtype == VSA_F16) return launch_width_bwd<__half, __half>(a, bytes, stream);
+  if (a.branch_dtype == VSA_BF16) return launch_width_bwd<float, __nv_bfloat16>(a, bytes, stream);
+  if (a.branch_dtype == VSA_F16) return launch_width_bwd<float, __half>(a, bytes, stream);
+  return launch_width_bwd<float, float>(a, bytes, stream);
 }
 
 }  // namespace
 
-size_t gate_norm_bwd_workspace(int batch, int channels, int groups) {
-  const int64_t rows = static_cast<int64_t>(batch) * groups;
-  return align_up((most_units(rows, channels) + most_shares(rows, channels)) * 3 * channels * sizeof(float), 256);
+size_t gate_norm_bwd_workspace(const GateNormArgs& a) {
+  size_t bytes = 0;
+  bwd_typed(a, &bytes, nullptr);
+  return bytes;
 }
 
-cudaError_t launch_gate_norm_fwd(const GateNormArgs& a, cudaStream_t stream) { return launch_typed(a, true, stream); }
-cudaError_t launch_gate_norm_bwd(const GateNormArgs& a, cudaStream_t stream) { return launch_typed(a, false, stream); }
+cudaError_t launch_gate_norm_fwd(const GateNormArgs& a, cudaStream_t stream) {
+  if (a.dtype == VSA_BF16) return launch_width_fwd<__nv_bfloat16, __nv_bfloat16>(a, stream);
+  if (a.dtype == VSA_F16) return launch_width_fwd<__half, __half>(a, stream);
+  if (a.branch_dtype == VSA_BF16) return launch_width_fwd<float, __nv_bfloat16>(a, stream);
+  if (a.branch_dtype == VSA_F16) return launch_width_fwd<float, __half>(a, stream);
+  return launch_width_fwd<float, float>(a, stream);
+}
+cudaError_t launch_gate_norm_bwd(const GateNormArgs& a, cudaStream_t stream) { return bwd_typed(a, nullptr, stream); }
 
 }  // namespace vsa

@@ -75,8 +75,9 @@ typedef struct vsa_gate_norm_grads {
   void *gate, *scale, *shift, *post_weight, *weight, *bias;
 } vsa_gate_norm_grads;
 
-/* Bytes of device workspace vsa_gate_norm_bwd needs where a parameter's gradient is wanted (0 for
- * invalid arguments). */
+/* Bytes of device workspace vsa_gate_norm_bwd needs where gradients of op's parameters are wanted (0: none is
+ * needed, or invalid arguments).  Where those of the modulations alone are wanted it may need none, as it
+ * says of an op without weights and bias: for modulation rows of few tokens it is large with, 0 without. */
 size_t vsa_gate_norm_bwd_workspace_bytes(const vsa_gate_norm* op);
 
 /*

@@ -219,3 +219,27 @@ def test_mlp_needs_an_activation(block):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         mlp(x, x, None, x, None, act=None)
+
+
+def test_gate_norm_bwd_workspace_is_what_is_used(block):
+    """A modulation for every token: its gradients need none, the weights' do; a long row's need some either way."""
+    lib = block._lib()
+    none = dict(post_weight=None, weight=None, bias=None)
+    for dtype, branch in ((0, 0), (1, 1), (2, 0), (2, 2)):
+        f = dict(dtype=dtype, branch_dtype=branch, mod_dtype=branch, weight_dtype=branch, batch=1, tokens=131040,
+                 channels=1536)
+        token, row = norm_op(block, groups=131040, **f, **none), norm_op(block, groups=1, **f, **none)
+        assert lib.vsa_gate_norm_bwd_workspace_bytes(token) == 0
+        assert lib.vsa_gate_norm_bwd_workspace_bytes(row) > 0
+        for name in none:
+            need = lib.vsa_gate_norm_bwd_workspace_bytes(norm_op(block, groups=131040, **f, **{**none, name: PTR}))
+            assert 131040 * 1536 * 12 < need <= 131040 * 1536 * 12 * 17 // 16 + 1536 * 12 * 1024
+    bare = block.VsaModulation(None, 0, 0)
+    assert lib.vsa_gate_norm_bwd_workspace_bytes(norm_op(block, gate=bare, scale=bare, shift=bare, **none)) == 0
+    # The weights are there but only a modulation's gradient is wanted: the size says so without them, and the
+    # call asks for it where it is not zero.
+    t = tokens(block, token_stride=1536, batch_stride=0)
+    op = norm_op(block, batch=1, tokens=5000, channels=1536, groups=1)
+    need = lib.vsa_gate_norm_bwd_workspace_bytes(op)
+    grads = block.VsaGateNormGrads(gate=PTR)
+    assert need > 0 and lib.vsa_gate_norm_bwd(op, t, t, t, t, t, t, grads, ctypes.c_void_p(PTR), need - 1, None) == 3

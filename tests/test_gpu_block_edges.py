@@ -308,3 +308,45 @@ def test_constant_tokens_are_zeros_of_the_layer_norm(block, C, dtype, branch):
     x = x[:, -1:].expand(1, 700, C).contiguous()
     _, _, _, _, dweight, _, _, _ = block.vsa_gate_norm_bwd(randn(1, 700, C, dtype=branch, seed=4), None, x, weight=w)
     assert not dweight.any()
+
+
+def test_gate_norm_bwd_without_a_workspace(block):
+    """Modulations of single tokens: their gradients come with a null workspace, with weights whose own are not
+    wanted too, and are those of all gradients asked for together."""
+    import ctypes
+    B, S, C = 2, 3000, 1536
+    x, y, dh = (randn(B, S, C, seed=i) for i in range(3))
+    mods = [randn(B, S, C, seed=10 + i, scale=0.4) for i in range(3)]
+    w, b = randn(C, seed=20), randn(C, seed=21)
+    want = block.vsa_gate_norm_bwd(dh, None, x, y, mods[0], None, w, b, *mods[1:])
+    outs = [torch.empty_like(x) for _ in range(5)]
+    op = block.VsaGateNorm(B, S, C, S, 0, 0, 0, 0, 0, 1e-6, 1e-6, *(block.VsaModulation(m.data_ptr(), S * C, C) for m in mods),
+                           None, w.data_ptr(), b.data_ptr())
+    view = [block.VsaTokens(t.data_ptr(), S * C, C) for t in (dh, x, y, *outs[:2])]
+    grads = block.VsaGateNormGrads(*(t.data_ptr() for t in outs[2:]))
+    status = block._lib().vsa_gate_norm_bwd(op, view[0], None, *view[1:], grads, None, 0,
+                                            ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert status == 0
+    for got, ref_ in zip(outs, (want[0], want[1], want[2], want[6], want[7])):
+        ref.check("alone", got, ref_.double(), 2 * ref.half_step(BF16) * ref_.double().abs() + 2.0 ** -20)
+    one = block.vsa_gate_norm_bwd(dh, None, x, y, mods[0], None, w, b, *mods[1:],
+                                  need_dparams=(True, False, False, False, True, True))
+    assert one[3] is one[4] is one[5] is None and same_bits((one[0], one[1], one[2], one[6], one[7]), outs)
+    with pytest.raises(ValueError):
+        block.vsa_gate_norm_bwd(dh, None, x, y, need_dparams=(True, False))
+
+
+def test_gate_norm_bwd_memory_of_frozen_weights(block):
+    """Through autograd: a modulation that is trained beside weights that are not takes no workspace."""
+    from block_sparse_video_tok_gb300 import autograd
+    B, S, C = 1, 8192, 1536
+    x, dh, w, shift = randn(B, S, C), randn(B, S, C, seed=1), randn(C, seed=2), randn(B, S, C, seed=4)
+    scale = randn(B, S, C, seed=3, scale=0.4).requires_grad_(True)
+    _, h = autograd.gate_norm(x, weight=w, scale=scale, shift=shift)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    (got,) = torch.autograd.grad(h, scale, dh)
+    assert torch.cuda.max_memory_allocated() - before <= 2 * got.numel() * got.element_size() + (1 << 20)
+    want = ref.gate_norm_bwd(dh, None, x, None, None, None, w, None, scale.detach(), shift, "layer", 1e-6, 1e-6)[6]
+    ref.check("dscale", got, *want)
