@@ -87,6 +87,21 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void load4_cluster(uint32_t addr, float* v) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr));
 }
+
+// warp_wait, which also keeps a limit that is shorter than the time for which the hardware suspends a probe (some
+// microseconds, the whole of such a product): barriers are then looked at without suspending.
+constexpr uint64_t SUSPENDED_NS = 20000;
+static __device__ __noinline__ bool poll_without_suspending(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!__all_sync(FULL, mbar_test_wait(bar, parity)))
+    if (__any_sync(FULL, *abort != 0 || globaltimer_ns() - t0 > limit_ns)) return false;
+  return true;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (limit_ns < SUSPENDED_NS) return __all_sync(FULL, poll_without_suspending(bar, parity, abort, limit_ns));
+  return warp_wait(bar, parity, abort, limit_ns);
+}
+
 // FORM of a lone product: A_MN + 2 B_MN + 4 swap, and its tiles are (y, z).  A pair reads these from its jobs, which
 // costs a lone product up to 1.4 us (64 x 256 -> 256: 5.6 instead of 4.2).
 constexpr int PAIR = 8;
@@ -152,7 +167,7 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
     uint32_t it = 0;
     for (int k = k0; k < k1; ++k, ++it) {
       const uint32_t s = it % STAGES, to = base + s * STAGE_BYTES, full = bar(FULL0 + s);
-      ok = warp_wait(bar(EMPTY0 + s), ((it / STAGES) & 1u) ^ 1u, abort, limit);
+      ok = wait(bar(EMPTY0 + s), ((it / STAGES) & 1u) ^ 1u, abort, limit);
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(full, STAGE_BYTES);
@@ -187,7 +202,7 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
     uint32_t it = 0;
     for (int k = k0; k < k1; ++k, ++it) {
       const uint32_t s = it % STAGES;
-      ok = warp_wait(bar(FULL0 + s), (it / STAGES) & 1u, abort, limit);
+      ok = wait(bar(FULL0 + s), (it / STAGES) & 1u, abort, limit);
       if (!ok) break;
       tc_fence_after_sync();
       stage(sdesc_advance(a_desc, s * STAGE_BYTES), sdesc_advance(b_desc, s * STAGE_BYTES), k > k0 ? 1u : 0u);
@@ -196,9 +211,10 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
     if (!ok && lane == 0) raise_abort(abort, params.err);
     umma_commit_elect(bar(DONE));
   }
-  // Every product is done, and every stage has been read.  (After an abort the sums are not used: the
-  // wait only keeps tensor memory until they are there.)
-  ok = warp_wait(bar(DONE), 0, abort, limit) && ok;
+  // Every product is done, and every stage has been read.  (After an abort this CTA's sums do not leave it but
+  // for the others of its cluster, whose results the error word declares invalid: the wait only keeps tensor
+  // memory until they are there.)
+  ok = wait(bar(DONE), 0, abort, limit) && ok;
   if (!ok) {
     if (lane == 0) {
       raise_abort(abort, params.err);
@@ -211,6 +227,7 @@ __global__ void __launch_bounds__(THREADS) gemm_small_kernel(const __grid_consta
   tc_fence_after_sync();
   float* sums = reinterpret_cast<float*>(gbase);
   __syncthreads();  // both readers of the stages are past them, whichever way they ended
+  ok = ok && *abort == 0;  // (the issuer commits DONE also where it has given up)
   {
     const int r = (warp & 3) * 32 + lane, c = (warp >> 2) * 32;
     uint32_t v[32];

@@ -92,3 +92,34 @@ def test_short_wait_limit_reports_timeout_then_recovers(block, size, long):
     torch.cuda.synchronize()
     assert layer.vsa_layer_device_error() == 0
     assert same_bits(got, want)
+
+
+@pytest.mark.parametrize("size", [(64, 256, 256), (128, 1000, 264), (512, 512, 512), (300, 4096, 64), (1021, 1000, 264)], ids=str)
+def test_short_wait_limit_stops_small_products(block, size):
+    """Products in small tiles, alone, in clusters and two to a launch: a limit below the time of one copy runs out
+    in each, is reported, and the calls after it are right."""
+    from block_sparse_video_tok_gb300 import layer, vsa
+    layer.vsa_layer_device_error()
+    c = case(*size, seed=7)
+    want = every(block, c)
+    torch.cuda.synchronize()
+    assert layer.vsa_layer_device_error() == 0
+    calls = [lambda: block.vsa_linear(c["x"], c["w"], c["b"], "silu", need_pre=True),
+             lambda: block.vsa_linear(c["x"], c["w"], c["b"], None, c["r"]),
+             lambda: block.vsa_linear_bwd(c["dout"], c["x"], c["w"], need_dweight=False),
+             lambda: block.vsa_linear_bwd(c["dout"], c["x"], c["w"], need_dx=False),
+             lambda: block.vsa_linear_bwd(c["dout"], c["x"], c["w"])]
+    for _ in range(3):
+        prev = vsa.vsa_set_wait_limit_ns(SHORT_NS)
+        bits = []
+        try:
+            for call in calls:
+                call()
+                bits.append(layer.vsa_layer_device_error())
+        finally:
+            vsa.vsa_set_wait_limit_ns(prev)
+        assert bits == [vsa.DEVERR_TIMEOUT] * len(calls)
+        got = every(block, c)
+        torch.cuda.synchronize()
+        assert layer.vsa_layer_device_error() == 0
+        assert same_bits(got, want)
