@@ -12,8 +12,8 @@
 // flight together.  Where there are fewer features than fill the GPU, the CTAs of a cluster share k
 // too.  The warps' and CTAs' sums are added in their order, through shared memory.
 //
-// Measured: 8 x 1536 -> 9216 with silu 5.0 us, 84 % of the copy rate (weights 28 MB); 8 x 6144 -> 1536 5.0; 16 rows
-// 6.0 and 6.6, where gemm_small.cu's tiles take 8 to 9; 24 rows, 1536 -> 6144 6.2 and 8.8.
+// Measured: 8 x 1536 -> 9216 with silu 4.8 us where the call before left the weights (28 MB) in L2, 7.2 from HBM (58 %
+// of the copy rate; 4096 -> 32768 85 %); 8 x 6144 -> 1536 5.0 and 7.9.  Where it stops: use_linear_rows.
 #include "act.cuh"
 #include "gemm.cuh"
 #include "vec8.cuh"
@@ -131,15 +131,20 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const __grid_co
   if (p.share > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// CTAs of an SM: the registers of three tiles leave room for three.
+constexpr int sm_ctas(int tiles) { return tiles < 3 ? 4 : 3; }
+
 template <typename E, int TILES>
 cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
   Params p;
   p.a = a;
   p.blocks = (a.in + STEP - 1) / STEP;
   const int features = (a.out_features + FEATURES - 1) / FEATURES;
-  // CTAs of a cluster: while there are less than four CTAs to an SM and a warp has two blocks or more.
+  // CTAs of a cluster: while there are no more CTAs than run at once, up to four to an SM, and a warp has two blocks
+  // or more.  (24 rows, 2048 -> 4096 with four instead of three to an SM: 13.8 us instead of 8.9.)
   p.share = 1;
-  while (p.share < 8 && features * p.share * 2 <= 4 * device_sm_count() && p.blocks >= p.share * 2 * WARPS * 2) p.share *= 2;
+  while (p.share < 8 && features * p.share * 2 <= sm_ctas(TILES) * device_sm_count() && p.blocks >= p.share * 2 * WARPS * 2)
+    p.share *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.share, features);
   cfg.blockDim = dim3(WARPS * 32);
@@ -163,16 +168,29 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // Every CTA reads all of x, 1/2 to 3/2 of its weights' bytes: the more rows, the fewer weights.  Us here and with
-// gemm_small.cu's tiles:
-//   rows   1536 -> 1536   1536 -> 6144   1536 -> 9216   4096 -> 4096   6144 -> 6144   8192 -> 8192
-//    8                     4.1 and  8.9   4.8 and 10.4   6.8 and 12.0   13 and 12      29 and 26
-//   16     4.9 and 6.0     5.5 and  8.1   6.2 and 10.2   8.8 and  9.6   17 and 12      45 and 26
-//   24     5.2 and 6.0     6.3 and  8.9  10.7 and  9.8  15.2 and  9.7
-//   32     6.4 and 6.0     8.3 and  8.8   9.5 and  9.3  12.5 and  9.7
+// tiles (gemm_small.cu, or gemm.cu where those are too many), weights from HBM:
+//   in -> out, million weights   8 rows            16 rows           24 rows
+//    2048 ->  4096    8           6.8 and 10.0      8.4 and  9.6      8.9 and  9.6
+//    8192 ->  1024    8                             8.7 and  9.9     10.6 and  9.9
+//    1024 ->  8192    8                             6.8 and  8.9     10.9 and  8.9
+//    1536 ->  7168   11                             8.2 and 10.0      8.0 and 10.0
+//    1536 ->  9216   14           7.2 and 11.1      9.0 and 11.0     13.5 and 10.5
+//    4096 ->  4096   17          10.3 and 12.3     12.5 and 11.8     19.9 and 11.8
+//    4096 ->  5120   21          13.5 and 12.5     16.3 and 12.7     15.4 and 12.8
+//    4096 ->  8192   34          15.3 and 15.5     18.8 and 15.5     29.7 and 15.5
+//    6144 ->  6144   38          19.8 and 19.2     26.1 and 17.4     22.6 and 17.2
+//    1536 -> 32768   50          20.7 and 20.7     26.5 and 20.9     34.8 and 20.6
+//    8192 ->  8192   67          29.1 and 25.6     44.6 and 25.8     56.2 and 25.9
+//   16384 ->  6144  101          50.3 and 35.8     79.9 and 35.7     62.9 and 35.9
+//    4096 -> 32768  134          46.6 and 54.0     64.0 and 42.8     76.3 and 43.2
+//   28672 ->  8192  235          92.1 and 72.5    146   and 72.8    199   and 72.6
+// (1 and 4 rows take what 8 do here, and with tiles as much or more.)  Between 17 and 24 rows a second wave of CTAs
+// costs more than it can win: there the features' CTAs are at most what runs at once (7168, not 8192).
 bool use_linear_rows(int rows, int in, int out) {
   const int64_t weights = static_cast<int64_t>(in) * out;
-  return out <= FEATURES * 65535 &&
-         (rows <= 8 || (rows <= 16 && weights <= 25000000) || (rows <= 24 && weights <= 10000000));
+  if (rows <= 8) return out <= FEATURES * 65535 && (weights <= 35000000 || in < 6144);
+  if (rows <= 16) return weights <= 17000000;
+  return rows <= 24 && weights <= 12000000 && (out + FEATURES - 1) / FEATURES <= sm_ctas(3) * device_sm_count();
 }
 
 cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t stream) {

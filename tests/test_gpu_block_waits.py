@@ -123,3 +123,27 @@ def test_short_wait_limit_stops_small_products(block, size):
         torch.cuda.synchronize()
         assert layer.vsa_layer_device_error() == 0
         assert same_bits(got, want)
+
+
+@pytest.mark.parametrize("size, own", [
+    ((8, 4096, 8192), True), ((8, 8192, 8192), False), ((1, 8192, 8192), False), ((8, 1536, 32768), True), ((8, 16384, 6144), False),
+    ((16, 1536, 9216), True), ((16, 4096, 5120), False), ((24, 2048, 4096), True), ((17, 1536, 7168), True), ((24, 1024, 8192), False),
+    ((24, 4096, 4096), False), ((25, 256, 256), False)], ids=str)
+def test_which_few_rows_have_a_kernel_of_their_own(block, size, own):
+    """That kernel waits for nothing, the tiles' kernels do: a limit that no wait keeps tells which of them ran."""
+    from block_sparse_video_tok_gb300 import layer, vsa
+    layer.vsa_layer_device_error()
+    M, K, N = size
+    x, w = randn(M, K, seed=1), randn(N, K, seed=2)
+    prev = vsa.vsa_set_wait_limit_ns(SHORT_NS)
+    try:
+        block.vsa_linear(x, w)
+        bits = layer.vsa_layer_device_error()
+    finally:
+        vsa.vsa_set_wait_limit_ns(prev)
+    assert bits == (0 if own else vsa.DEVERR_TIMEOUT)
+    out, want = block.vsa_linear(x, w)[0].double(), x.double() @ w.double().T
+    mag = x.double().abs() @ w.double().abs().T
+    # One rounding, and sums of K terms in fp32.
+    assert bool(((out - want).abs() <= 2.0 ** -8 * want.abs() + K * 2.0 ** -24 * mag).all())
+    assert layer.vsa_layer_device_error() == 0
