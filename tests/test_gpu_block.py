@@ -415,3 +415,63 @@ def test_linear_activations_of_every_finite_value(block, act, dtype):
     want = ref.act(z.double(), act)
     # Relative as in the test of their range; a logistic function below 2^-126, of a z up to 104, is zero.
     ref.check(act, out, want, (ref.half_step(dtype) + 2.0 ** -14) * want.abs() + ref.tiny(dtype) + 104 * 2.0 ** -126)
+
+
+def off(got, want):
+    """Norm of the difference over the norm."""
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+@pytest.mark.parametrize("size", [s for s in LINEAR_SIZES if s[0] > 1] + [(9000, 256, 520)], ids=str)
+@pytest.mark.parametrize("act,x_act,dtype", [("gelu_tanh", None, BF16), ("silu", "gelu", FP16), (None, "silu", BF16)], ids=str)
+def test_linear_in_the_norm(block, size, act, x_act, dtype):
+    """Where single elements may be off by all roundings at once, whole results may not: each rounding is off by at
+    most half a step relative to its value, so results are by half a step of their norm, and dz's roundings, which
+    have no sign of their own, come out of the products as large beside dx and dweight as they were beside dz.
+    2^-10 of the norm more covers fp32 sums (2^-15 of magnitudes up to 2^5 times the result's)."""
+    M, K, N = size
+    step = ref.half_step(dtype)
+    c = linear_case(M, K, N, dtype, residual=True, seed=3)
+    x = ref.act(c["x"].double(), x_act).to(dtype)
+    out, pre = block.vsa_linear(x, c["weight"], c["bias"], act, c["residual"], need_pre=True)
+    (want, _), (want_pre, _) = ref.linear(x, c["weight"], c["bias"], act, c["residual"])
+    assert off(out, want) <= step + 2.0 ** -10 and off(pre, want_pre) <= step + 2.0 ** -10
+    dout = randn(M, N, dtype=dtype, seed=70)
+    args = (dout, x, c["weight"], c["bias"], act, pre if act else None, x_act, c["x"] if x_act else None)
+    for n, got, (value, _) in zip(("dx", "dweight", "dbias"), block.vsa_linear_bwd(*args), ref.linear_bwd(*args)):
+        # (A rounding of dz is at most half a step of its value, 0.6 of one in the root of the mean square; with few
+        # terms the sums of signed errors may stand out, twice that covers them.)
+        bound = step + (2 * step if act and n != "dbias" else 0.0) + 2.0 ** -10
+        assert off(got, value) <= bound, (n, off(got, value), bound)
+
+
+@pytest.mark.parametrize("dtype,branch", [(FP32, BF16), (BF16, BF16)], ids=str)
+def test_gate_norm_long_video_in_the_norm(block, dtype, branch):
+    """A stream of thousands of tokens of a whole block's width, fp32 or bf16, forward and backward: each result is
+    off by half a step of its type in the norm, 2^-12 more for fp32."""
+    c, kind = norm_case(2, 8190, 1536, have="y gate weight bias scale shift", dtype=dtype, branch=branch, mod=FP32, wdtype=FP32)
+    x, h = forward(block, c, kind)
+    (want_x, _), (want_h, _) = ref.gate_norm(c["x"], *(c[n] for n in PARAMS), kind, 1e-6, 1e-6, branch)
+    assert off(x, want_x) <= ref.half_step(dtype) + 2.0 ** -12 and off(h, want_h) <= ref.half_step(branch) + 2.0 ** -12
+    dh, dx_out = randn(2, 8190, 1536, dtype=branch, seed=21), randn(2, 8190, 1536, dtype=dtype, seed=22)
+    args = (dh, dx_out, x, *(c[n] for n in PARAMS))
+    for n, got, want in zip(GRADS, block.vsa_gate_norm_bwd(*args), ref.gate_norm_bwd(*args, kind, 1e-6, 1e-6)):
+        if got is not None:
+            assert off(got, want[0]) <= ref.half_step(got.dtype) + 2.0 ** -12, n
+
+
+def test_gate_norm_inputs_that_are_broadcast(block):
+    """Tokens, entries and gradients of stride 0, and one tensor in several places."""
+    B, S, C = 3, 41, 264
+    one, row = randn(1, S, C, seed=1), randn(1, 1, C, seed=2)
+    gate, scale = randn(B, C, seed=3), randn(1, C, seed=4).expand(B, C)
+    w = randn(C, seed=5)
+    for x, y in ((one.expand(B, S, C), row.expand(B, S, C)), (row.expand(B, S, C), one.expand(B, S, C))):
+        args = (y, gate, None, w, w, scale, scale)
+        got = block.vsa_gate_norm(x, *args)
+        assert same_bits(got, block.vsa_gate_norm(x.contiguous(), y.contiguous(), *args[1:]))
+        bwd = block.vsa_gate_norm_bwd(y, x, x, *args)
+        assert same_bits(bwd, block.vsa_gate_norm_bwd(*(t.contiguous() for t in (y, x, x, y)), *args[1:]))
+    x = one.expand(B, S, C).contiguous()
+    assert same_bits(block.vsa_gate_norm(x, x, gate, scale=gate, shift=gate),
+                     block.vsa_gate_norm(x, x.clone(), gate, scale=gate.clone(), shift=gate.clone()))

@@ -237,3 +237,39 @@ def test_residual_of_other_leading_dimensions(autograd):
             for g in (dout, wide[..., 8:]):
                 got = torch.autograd.grad(f(r), (x, w1, r), g)
                 assert got[2].shape == shape and same(got[:2], want[:2]) and torch.equal(got[2].view_as(dout), want[2])
+
+
+def test_a_chain_of_the_operators_in_the_norm(autograd):
+    """Norm, two products and the gated sum with the next norm, against plain operations in 64 bits.  Some ten
+    bf16 results forward and as many back, half a step each, independent of one another: in the root of the sum of
+    squares sqrt(20) 2^-8, taken twice for the slopes, gates and 1 / deviations they pass through."""
+    B, S, C, W = 2, 150, 264, 1032
+    x, y = randn(B, S, C, dtype=FP32), randn(B, S, C, seed=1)
+    mods = [randn(B, C, seed=2 + i, scale=0.4) for i in range(6)]
+    w1, b1, w2, b2 = randn(W, C, seed=8, scale=C ** -0.5), randn(W, seed=9), randn(C, W, seed=10, scale=W ** -0.5), randn(C, seed=11)
+    nw, nb = randn(C, seed=12, scale=0.1) + 1, randn(C, seed=13, scale=0.1)
+    ts = leaves(x, y, *mods, w1, b1, w2, b2, nw, nb)
+    dx, dh = randn(B, S, C, dtype=FP32, seed=14), randn(B, S, C, seed=15)
+
+    def own(x, y, g1, s1, t1, g2, s2, t2, w1, b1, w2, b2, nw, nb):
+        x, h = autograd.gate_norm(x, y, g1, scale=s1, shift=t1)
+        return autograd.gate_norm(x, autograd.mlp(h, w1, b1, w2, b2, "gelu_tanh"), g2, weight=nw, bias=nb, scale=s2, shift=t2)
+
+    def plain(x, y, g1, s1, t1, g2, s2, t2, w1, b1, w2, b2, nw, nb):
+        def norm(x):
+            c = x - x.mean(-1, keepdim=True)
+            return c / torch.sqrt(c.square().mean(-1, keepdim=True) + 1e-6)
+        x = x + g1[:, None] * y
+        h = norm(x) * (1 + s1[:, None]) + t1[:, None]
+        x = x + g2[:, None] * (ref.act(h @ w1.T + b1, "gelu_tanh") @ w2.T + b2)
+        return x, (norm(x) * nw + nb) * (1 + s2[:, None]) + t2[:, None]
+
+    got = own(*ts)
+    wide = leaves(*(t.detach().double() for t in ts))
+    want = plain(*wide)
+    bound = 2 * 20 ** 0.5 * 2.0 ** -8
+    pairs = list(zip(got, want)) + list(zip(torch.autograd.grad(got, ts, [dx, dh]),
+                                            torch.autograd.grad(want, wide, [dx.double(), dh.double()])))
+    for i, (a, b) in enumerate(pairs):
+        error = ((a.detach().double() - b.detach()).norm() / b.detach().norm()).item()
+        assert error <= bound, (i, error, bound)
