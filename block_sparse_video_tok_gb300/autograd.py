@@ -281,7 +281,8 @@ def linear(x, weight, bias=None, act=None, residual=None):
 
 def mlp(x, w1, b1, w2, b2, act="gelu_tanh", residual=None):
     """act(x w1^T + b1) w2^T + b2 + residual, differentiable in all of them.  The backward keeps both
-    sides of the activation, [..., w1's rows] each."""
+    sides of the activation, [..., w1's rows] each; the gradient between them is rounded to x's type once,
+    and b1's sums it up so."""
     if act is None:
         raise ValueError("mlp needs an activation")
     return Mlp.apply(x, w1, b1, w2, b2, residual, act, torch.is_grad_enabled())

@@ -21,7 +21,8 @@
 // around it in the epilogue took 32760 x 512 -> 1536 from 42 us to 47, with a residual from 58 to 65.
 //
 // Bound by the tensor cores (91 % of their cycles): 32760 x 1536 x 6144 with bias and gelu_tanh 324 us in
-// bursts (1908 TFLOP/s, the measured burst rate; a plain library product 304), 131040 rows 1267; dx 328, dweight
+// bursts (1908 TFLOP/s, what the library reaches at 8192 x 8192 x 8192; at this size its plain product takes 304 us,
+// 2030 TFLOP/s), 131040 rows 1267 (the library's 1210 to 1230); dx 328, dweight
 // 305.  In runs of a second the power cap holds all of them to about 1650 TFLOP/s.  A residual or a
 // slope to read adds 27 us, pre to write 45: the operands take about 18 TB/s between L2 and the SMs, and what
 // the epilogue moves comes on top.  Four epilogue warps instead of eight: 455 us with bias and gelu_tanh.

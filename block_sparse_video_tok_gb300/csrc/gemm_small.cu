@@ -1,7 +1,9 @@
 // gemm_small.cu -- the products of vsa_linear where a tile of 256 x 256 results is too coarse: a CTA has
 // 128 x 64 results of one tile, and a cluster shares the tile along k.
 //
-// Such calls are bound by what comes before and after the products: a pair of CTAs of gemm.cu takes 6.7 us
+// Such calls are bound by what comes before and after the products and by single copies' time, not by traffic (1024 x
+// 1536 -> 1536: L2 to the SMs 23 % of its peak over the kernel, 36 % on the busiest SM; issue slots 9 %): a pair
+// of CTAs of gemm.cu takes 6.7 us
 // for a tile with 256 elements of k, of which its products are 0.4 (two cluster barriers, the epilogue
 // of 256 columns, TMA stores), and its tiles in parts a second kernel that adds them.  Here nothing is
 // persistent: two warps copy and multiply, then all eight write the results; the CTAs of a cluster leave
@@ -393,9 +395,9 @@ cudaError_t fill(Job* j, GemmOp op, const GemmArgs& a, const Plan& q) {
 
 // Where its CTAs fit on the GPU at once and its estimated time is the shorter.  Measured, us, here and
 // with gemm.cu's tiles (forward, rows x in -> out features):
-//   512 x 1536 -> 1536    9.0 and 11.5      512 x 4096 -> 1536   13.7 and 13.9
-//   1024 x 1536 -> 1536   9.6 and 13.0      512 x 6144 -> 1536   18.0 and 15.7
-//   256 x 1536 -> 9216   11.2 and 13.1      384 x 1536 -> 9216   18.2 and 13.8
+//   512 x 1536 -> 1536    8.0 and 11.2      512 x 4096 -> 1536   12.7 and 13.5
+//   1024 x 1536 -> 1536   9.0 and 11.9      512 x 6144 -> 1536   16.4 and 15.1
+//   256 x 1536 -> 9216   10.5 and 12.0      384 x 1536 -> 9216   17.8 and 12.5
 // The estimate: 3 us for a call, 1.5 for a cluster, and for a step of 64 elements of k 0.2 where an SM has one
 // CTA and 0.28 where it has two.
 bool use_gemm_small(int m, int n, int k) {
@@ -417,8 +419,8 @@ cudaError_t launch_gemm_small(GemmOp op, const GemmArgs& a, cudaStream_t stream)
   return a.dtype == VSA_BF16 ? launch_typed<__nv_bfloat16>(p, grid, stream) : launch_typed<__half>(p, grid, stream);
 }
 
-// Where the CTAs of both fit on the GPU at once (us on the GPU, in one launch and in two: 64 x 256 -> 256 5.0 and 6.9,
-// 512 x 512 -> 512 6.7 and 11.1, 1021 x 1000 -> 264 9.2 and 12.5; with 480 CTAs, 256 x 1536 -> 1536, 13.6 and 12.5).
+// Where the CTAs of both fit on the GPU at once (us on the GPU, in one launch and in two: 64 x 256 -> 256 4.5 and 6.7,
+// 512 x 512 -> 512 6.3 and 10.6, 1021 x 1000 -> 264 9.0 and 12.5; with 480 CTAs, 256 x 1536 -> 1536, 13.2 and 11.9).
 bool use_gemm_small_pair(const GemmArgs& a, const GemmArgs& b) {
   if (!use_gemm_small(a.m, a.n, a.k) || !use_gemm_small(b.m, b.n, b.k)) return false;
   const Plan q = plan_of(a.m, a.n, a.k), r = plan_of(b.m, b.n, b.k);
