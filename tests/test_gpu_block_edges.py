@@ -350,3 +350,25 @@ def test_gate_norm_bwd_memory_of_frozen_weights(block):
     assert torch.cuda.max_memory_allocated() - before <= 2 * got.numel() * got.element_size() + (1 << 20)
     want = ref.gate_norm_bwd(dh, None, x, None, None, None, w, None, scale.detach(), shift, "layer", 1e-6, 1e-6)[6]
     ref.check("dscale", got, *want)
+
+
+@pytest.mark.parametrize("case", [(2, 1, 1000, 400), (1, 7, 64, 700), (3, 43, 264, 86), (300, 1, 1536, 20), (1, 900, 1536, 900),
+                                  (1, 900, 128, 1800), (1, 300, 6152, 300)], ids=str)
+def test_gate_norm_bwd_of_some_parameters(block, case):
+    """Each parameter's gradient asked for alone, in pairs, and all but it, is what it is among all of them, but for
+    the order of fp32 sums (2^-15 of magnitudes that are at most some dozens of times the sums)."""
+    B, G, C, S = case
+    x, y, dh = (randn(B, S, C, seed=i) for i in range(3))
+    gate, scale, shift = (randn(*((B, C) if G == 1 else (B, G, C)), dtype=FP32, seed=10 + i, scale=0.4) for i in range(3))
+    post, w, b = (randn(C, dtype=FP32, seed=20 + i) for i in range(3))
+    args = (dh, None, x, y, gate, post, w, b, scale, shift)
+    every = block.vsa_gate_norm_bwd(*args)
+    some = [[i == j for j in range(6)] for i in range(6)] + [[i != j for j in range(6)] for i in range(6)]
+    some += [[j in (i, (i + 1) % 6) for j in range(6)] for i in range(6)] + [[True, False, False, False, True, True]]
+    for wanted in some:
+        got = block.vsa_gate_norm_bwd(*args, need_dparams=wanted)
+        assert same_bits(got[:2], every[:2])
+        for n, g, r in zip(wanted, got[2:], every[2:]):
+            assert (g is not None) == n
+            if n:
+                assert ((g.double() - r.double()).norm() / r.double().norm()).item() <= 2.0 ** -14
