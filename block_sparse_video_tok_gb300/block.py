@@ -19,6 +19,7 @@ from . import vsa
 from .layer import _DTYPES, _current, _on, _workspace
 
 KINDS = {"layer": 0, "rms": 1}
+MAX_TOKENS = 1 << 30      # and rows
 ACTS = {None: 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
 
 
@@ -244,6 +245,8 @@ def _gate_norm_op(x, branch, y, gate, post_weight, weight, bias, scale, shift, k
                         (dtype, " or 16-bit" if dtype is torch.float32 else "", branch))
     if C % 8 or not 8 <= C <= 8192:
         raise ValueError("channels must be a multiple of 8 up to 8192, got %d" % C)
+    if B * S > MAX_TOKENS:
+        raise ValueError("there may be up to 2^30 tokens, got %d" % (B * S))
     if kind not in KINDS:
         raise ValueError("kind must be one of %s, got %r" % (sorted(KINDS), kind))
     if y is None and (gate is not None or post_weight is not None):
@@ -427,7 +430,12 @@ def _linear_op(x, weight, bias, act):
         raise _misaligned("weight", weight)
     if step < K:
         raise ValueError("weight: the rows must not overlap (strides %s)" % (weight.stride(),))
-    return lambda rows: _pack_linear(rows, K, N, _DTYPES[dtype], _DTYPES[bdtype], ACTS[act], at, step, ptr), N, K
+
+    def make(rows):
+        if rows > MAX_TOKENS:
+            raise ValueError("there may be up to 2^30 rows, got %d" % rows)
+        return _pack_linear(rows, K, N, _DTYPES[dtype], _DTYPES[bdtype], ACTS[act], at, step, ptr)
+    return make, N, K
 
 
 @functools.lru_cache(maxsize=256)

@@ -5,6 +5,9 @@
 // dweight = dz^T x.  The pass is left out where there is neither an activation nor a bias; and a chain of two
 // products does not pay for it twice, as the second's dx goes on through the activation in its
 // epilogue (x_act).
+// dz is rounded to 16 bits there, as the tensor cores' operands are: dx and dweight are 0.00235 of their norm off in
+// bf16 (0.00029 in fp16) where the rounding of the results alone is 0.00166 (0.00021).  A second operand with
+// what the rounding lost would take both products twice as long.  dbias adds up dz before it is rounded.
 #include "act.cuh"
 #include "gemm.cuh"
 #include "vec8.cuh"

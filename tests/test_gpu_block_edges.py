@@ -372,3 +372,23 @@ def test_gate_norm_bwd_of_some_parameters(block, case):
             assert (g is not None) == n
             if n:
                 assert ((g.double() - r.double()).norm() / r.double().norm()).item() <= 2.0 ** -14
+
+
+def test_more_tokens_than_there_may_be(block):
+    """Sizes past 2^30 and past 2^31 are refused by name, before anything is allocated for them."""
+    for n in ((1 << 30) + 8, (1 << 31) + 8):
+        x = torch.zeros(1, 1, 8, dtype=BF16, device="cuda").expand(1, n, 8)
+        before = torch.cuda.max_memory_allocated()
+        with pytest.raises(ValueError):
+            block.vsa_gate_norm(x)
+        with pytest.raises(ValueError):
+            block.vsa_gate_norm_bwd(x, None, x)
+        assert torch.cuda.max_memory_allocated() == before
+        rows = torch.empty(n, 8, dtype=BF16, device="cuda")
+        w = torch.zeros(8, 8, dtype=BF16, device="cuda")
+        with pytest.raises(ValueError):
+            block.vsa_linear(rows, w)
+        with pytest.raises(ValueError):
+            block.vsa_linear_bwd(rows, rows, w)
+        del rows
+        torch.cuda.empty_cache()
